@@ -69,7 +69,9 @@ typedef enum {
     KDA_ERR_CUDA = -3
 } kda_status;
 
-typedef enum { KDA_DTYPE_BF16 = 0, KDA_DTYPE_FP32 = 1 } kda_dtype;
+/* KDA_DTYPE_FP16: the kda_kv4_* calls only (bf16 or fp16 there; a cache of 4
+ * bits has nothing for fp32 operands). */
+typedef enum { KDA_DTYPE_BF16 = 0, KDA_DTYPE_FP32 = 1, KDA_DTYPE_FP16 = 2 } kda_dtype;
 
 /* Bits OR-ed into *dev_err by kernels. */
 enum {
@@ -81,8 +83,10 @@ enum {
                                     chunk whose products could leave fp32 range (strong decays,
                                     positive gk, large k, v or state) through an fp32 recurrence
                                     instead of reporting it */
-    KDA_DEVERR_TIMEOUT = 16      /* a kernel's bounded wait on its own copies gave up (the unit
+    KDA_DEVERR_TIMEOUT = 16,     /* a kernel's bounded wait on its own copies gave up (the unit
                                     is abandoned, its slot is not written) */
+    KDA_DEVERR_PAGE_RANGE = 32,  /* a page number outside [0, num_pages) where a page is needed */
+    KDA_DEVERR_PAGES = 64        /* no free page left for a row, or a page freed that was free */
 };
 
 /* Largest number of layers (fold) or pools (slot copy) one call takes: the
@@ -432,6 +436,169 @@ KDA_API int kda_decode_fused(kda_dtype dt, int B, int H, int K, int V, const voi
  *               source and a destination in one call)
  */
 KDA_API int kda_slot_copy(int num_pools, float *const *pools, size_t slot_elems, int num_slots,
+                          const int32_t *src, const int32_t *dst, int n, int32_t *dev_err,
+                          void *stream);
+
+/*
+ * The paged 4-bit key/value cache of a hybrid model's full-attention layers.
+ * ---------------------------------------------------------------------------
+ * Next to the recurrent state pools ("Unified memory" and "Hybrid KDA Memory
+ * Management" of the same pages: one pool of memory behind slots and pages,
+ * copy-on-write, checkpoints at boundaries) such a model keeps the keys and
+ * values of its attention layers in pages.  One pool per layer:
+ *
+ *     uint8 [num_pages][H_kv][page_size / 16][18 D]
+ *
+ * A page holds page_size tokens (16, 32, 64, 128 or 256) of all H_kv heads, as
+ * tiles of 16 tokens: K codes [16][D/2], K scales [16][D/16], V codes [16][D/2],
+ * V scales [D/16][16].  Codes are e2m1, the even channel in the low nibble;
+ * scales are e4m3, one for 16 channels of one token; a value is
+ *     code x scale x k_scale (or v_scale).
+ * k_scale and v_scale are powers of two, so that they round nothing.  D is 64
+ * or 128.  16-byte aligned.
+ *
+ * Row b of page_table, device int32 [B][max_pages], names the pages of request
+ * b's tokens in order; entries past its pages are not read (-1 by convention).
+ * Requests' new tokens are packed: request b has tokens cu_seqlens[b] ..
+ * cu_seqlens[b+1] - 1 of [total_tokens][heads][D].
+ *
+ * Host checks, device error bits and ownership as above.  dtype: bf16 or fp16.
+ */
+
+/*
+ * kda_kv4_append -- store the new tokens' keys and values.
+ *
+ * Token i of request b goes to position start[b] + i, whose page the row must
+ * hold (kda_page_alloc) and share with no other row.  For each 16 channels
+ *     s = e4m3(max|x| / 6),  code = e2m1(x / s)    (0 where s = 0)
+ * both to nearest, ties to even, of x = value / k_scale (v_scale).  A NaN makes
+ * its block's scale NaN; beyond 2688 a block saturates.
+ *
+ *   k, v        device dtype [total_tokens][H_kv][D], token rows k_stride and
+ *               v_stride elements apart (>= H_kv D, multiples of 8; 16-byte
+ *               aligned): views of a fused projection's output
+ *   start       device int32 [B]
+ * A token whose page is missing or out of range, or past max_pages, is skipped
+ * (KDA_DEVERR_PAGE_RANGE, KDA_DEVERR_SEQLENS).
+ */
+KDA_API int kda_kv4_append(kda_dtype dt, int B, int total_tokens, int H_kv, int D, const void *k,
+                           long long k_stride, const void *v, long long v_stride,
+                           const int32_t *cu_seqlens, const int32_t *start,
+                           const int32_t *page_table, int max_pages, int page_size, void *pool,
+                           int num_pages, float k_scale, float v_scale, int32_t *dev_err,
+                           void *stream);
+
+/*
+ * kda_kv4_gather -- read tokens back as the values they stand for.
+ *
+ * The inverse of kda_kv4_append: positions start[b] + i into k, v
+ * [total_tokens][H_kv][D] (dense).  Exact while the scaled values stay in the
+ * type's range.  A token that cannot be read gets zeros and sets the bit.
+ */
+KDA_API int kda_kv4_gather(kda_dtype dt, int B, int total_tokens, int H_kv, int D, void *k,
+                           void *v, const int32_t *cu_seqlens, const int32_t *start,
+                           const int32_t *page_table, int max_pages, int page_size,
+                           const void *pool, int num_pages, float k_scale, float v_scale,
+                           int32_t *dev_err, void *stream);
+
+/* Bytes of the attention's workspace (one size for every call). */
+KDA_API size_t kda_kv4_workspace_bytes(void);
+
+/*
+ * kda_kv4_attention -- attention of each request's newest tokens over its cache.
+ *
+ * Decode (one token a request), verify (a few drafts) and prompts (a piece of
+ * any length on top of a prefix) are the same call.  Row i of a request with n
+ * new tokens and kv_lens[b] tokens in the cache, the new ones included, sees
+ * positions j <= kv_lens[b] - n + i and, where window > 0, j > kv_lens[b] - n +
+ * i - window.  H_q is a multiple of H_kv; query head h reads kv head
+ * h / (H_q / H_kv).
+ *     o   = sum_j softmax_j(scale q . k_j) v_j
+ *     lse = ln sum_j exp(scale q . k_j)
+ * A row that sees nothing has o = 0 and lse = -inf.  What lies in the pages at
+ * positions a row does not see has no influence, NaN included.
+ *
+ *   max_q       no request has more new tokens (host; sizes the launch)
+ *   q           device dtype [total_tokens][H_q][D], rows q_stride elements apart
+ *               (>= H_q D, a multiple of 8; 16-byte aligned)
+ *   o           device dtype [total_tokens][H_q][D]
+ *   lse         device float [total_tokens][H_q] or NULL
+ *   workspace   device, kda_kv4_workspace_bytes(), 16-byte aligned, zeroed before
+ *               its first call; calls that may run at the same time need one each
+ * A request with inconsistent cu_seqlens, more than max_q tokens or kv_lens out
+ * of [0, max_pages page_size] is skipped (KDA_DEVERR_SEQLENS, its rows are not
+ * written); tokens of a page that is out of range are left out
+ * (KDA_DEVERR_PAGE_RANGE).
+ */
+KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv,
+                              int D, const void *q, long long q_stride, const int32_t *cu_seqlens,
+                              const int32_t *kv_lens, const int32_t *page_table, int max_pages,
+                              int page_size, const void *pool, int num_pages, int window,
+                              float scale, float k_scale, float v_scale, void *o, float *lse,
+                              void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                              void *stream);
+
+/*
+ * Pages: refs, device int32 [num_pages], counts the rows that hold each page (a
+ * page set aside by the caller counts as held); a free page has 0.  Row b holds
+ * the first ceil(lens[b] / page_size) entries of its row of page_table; the
+ * others are -1.  Free pages are given out lowest number first, to rows in
+ * order: the result is the same on every run.  All of it stays on the device.
+ *
+ * kda_page_alloc -- lens[b] grows by grow[b] >= 0 tokens, with the pages that
+ * takes.  A row gets all of its pages or, when the pool runs out, none (its
+ * length stays, KDA_DEVERR_PAGES); later rows that need a page then get none
+ * either.
+ */
+KDA_API int kda_page_alloc(int B, int max_pages, int page_size, int num_pages, int32_t *refs,
+                           int32_t *page_table, int32_t *lens, const int32_t *grow,
+                           int32_t *dev_err, void *stream);
+
+/*
+ * kda_page_fork -- copy-on-write: row dst[i] becomes a second holder of row
+ * src[i]'s full pages, and gets a copy of its partial last page (in all pools).
+ * Row dst[i] is empty before (else KDA_DEVERR_SEQLENS, skipped) and is no source
+ * in the same call.  Where no page is left the fork is not made.
+ *
+ *   num_pools   P in [1, KDA_MAX_LAYERS]; pools host array [P] of device pools
+ *   page_bytes  bytes of one page in one pool, a multiple of 16
+ *   src, dst    device int32 [n]
+ *   workspace   device int32 [2 n]
+ */
+KDA_API int kda_page_fork(int num_pools, void *const *pools, size_t page_bytes, int B,
+                          int max_pages, int page_size, int num_pages, int32_t *refs,
+                          int32_t *page_table, int32_t *lens, const int32_t *src,
+                          const int32_t *dst, int n, int32_t *workspace, size_t workspace_ints,
+                          int32_t *dev_err, void *stream);
+
+/*
+ * kda_page_free -- rows (device int32 [n], distinct) let go of their pages: counts
+ * go down, their entries become -1 and their lengths 0.
+ */
+KDA_API int kda_page_free(int B, int max_pages, int page_size, int num_pages, int32_t *refs,
+                          int32_t *page_table, int32_t *lens, const int32_t *rows, int n,
+                          int32_t *dev_err, void *stream);
+
+/*
+ * kda_page_compact -- move the held pages numbered live .. num_pages - 1 (live:
+ * how many are held), in order, into the free pages below, lowest first, in all
+ * pools; refs and page_table follow, and *live is written.  Afterwards pages
+ * live .. are free and their memory can be given to state slots.  A caller's own
+ * copies of page numbers outside page_table do not follow.
+ *
+ *   live        device int32 [1]
+ *   workspace   device int32 [3 num_pages + 16]
+ */
+KDA_API int kda_page_compact(int num_pools, void *const *pools, size_t page_bytes, int B,
+                             int max_pages, int num_pages, int32_t *refs, int32_t *page_table,
+                             int32_t *live, int32_t *workspace, size_t workspace_ints,
+                             int32_t *dev_err, void *stream);
+
+/*
+ * kda_page_copy -- page dst[i] <- page src[i] in every pool (device int32 [n]; no
+ * page is both a source and a destination).
+ */
+KDA_API int kda_page_copy(int num_pools, void *const *pools, size_t page_bytes, int num_pages,
                           const int32_t *src, const int32_t *dst, int n, int32_t *dev_err,
                           void *stream);
 

@@ -5,11 +5,14 @@ The compute runs in hand-written sm_103a CUDA kernels behind the C ABI of
 """
 from .binding import (  # noqa: F401
     KDA_DEVERR_ACCEPT_RANGE,
+    KDA_DEVERR_PAGE_RANGE,
+    KDA_DEVERR_PAGES,
     KDA_DEVERR_RANGE,
     KDA_DEVERR_TIMEOUT,
     KDA_DEVERR_SEQLENS,
     KDA_DEVERR_SLOT_RANGE,
     KDA_DTYPE_BF16,
+    KDA_DTYPE_FP16,
     KDA_DTYPE_FP32,
     KDA_ERR_CUDA,
     KDA_ERR_INVALID_ARG,
@@ -24,6 +27,14 @@ from .binding import (  # noqa: F401
     kda_decode_fused,
     kda_decode_step,
     kda_gated_rmsnorm,
+    kda_kv4_append,
+    kda_kv4_attention,
+    kda_kv4_gather,
+    kda_page_alloc,
+    kda_page_compact,
+    kda_page_copy,
+    kda_page_fork,
+    kda_page_free,
     kda_replay_fold,
     kda_ring,
     kda_selftest_bounded_wait,
@@ -35,7 +46,11 @@ from .binding import (  # noqa: F401
     kda_verify_store_inputs_ragged,
     kda_verify_snapshot,
     lib,
+    kv4_tile_bytes,
+    kv4_workspace_bytes,
     make_conv_state,
+    make_kv4_pool,
+    make_kv4_workspace,
     make_ring,
     record_bytes,
     ring_len_for,

@@ -30,11 +30,14 @@ KDA_ERR_UNSUPPORTED = -2
 KDA_ERR_CUDA = -3
 KDA_DTYPE_BF16 = 0
 KDA_DTYPE_FP32 = 1
+KDA_DTYPE_FP16 = 2
 KDA_DEVERR_SLOT_RANGE = 1
 KDA_DEVERR_ACCEPT_RANGE = 2
 KDA_DEVERR_SEQLENS = 4
 KDA_DEVERR_RANGE = 8
 KDA_DEVERR_TIMEOUT = 16
+KDA_DEVERR_PAGE_RANGE = 32
+KDA_DEVERR_PAGES = 64
 KDA_MAX_LAYERS = 256
 K_DIM = 128
 V_DIM = 128
@@ -89,6 +92,20 @@ def lib() -> ctypes.CDLL:
                                        i, vp, f, f, f, ip, vp]
         L.kda_slot_copy.argtypes = [i, ctypes.POINTER(ctypes.c_void_p), ctypes.c_size_t, i, ip, ip,
                                     i, ip, vp]
+        vpp = ctypes.POINTER(ctypes.c_void_p)
+        sz = ctypes.c_size_t
+        L.kda_kv4_append.argtypes = [i, i, i, i, i, vp, ll, vp, ll, ip, ip, ip, i, i, vp, i, f, f, ip,
+                                     vp]
+        L.kda_kv4_gather.argtypes = [i, i, i, i, i, vp, vp, ip, ip, ip, i, i, vp, i, f, f, ip, vp]
+        L.kda_kv4_workspace_bytes.argtypes = []
+        L.kda_kv4_workspace_bytes.restype = sz
+        L.kda_kv4_attention.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, vp, i, i, f, f,
+                                        f, vp, vp, vp, sz, ip, vp]
+        L.kda_page_alloc.argtypes = [i, i, i, i, ip, ip, ip, ip, ip, vp]
+        L.kda_page_fork.argtypes = [i, vpp, sz, i, i, i, i, ip, ip, ip, ip, ip, i, vp, sz, ip, vp]
+        L.kda_page_free.argtypes = [i, i, i, i, ip, ip, ip, ip, i, ip, vp]
+        L.kda_page_compact.argtypes = [i, vpp, sz, i, i, i, ip, ip, ip, vp, sz, ip, vp]
+        L.kda_page_copy.argtypes = [i, vpp, sz, i, ip, ip, i, ip, vp]
         L.kda_selftest_bounded_wait.argtypes = [ip, i, vp]
         L.kda_selftest_prefill_wait.argtypes = [i, i, i, vp, vp, vp, vp, vp, ip, ip, vp, i, ip, ip,
                                                 vp, ip, i, vp]
@@ -96,6 +113,8 @@ def lib() -> ctypes.CDLL:
                    "kda_verify_store_inputs_ragged", "kda_verify_snapshot",
                    "kda_snapshot_commit", "kda_conv_prologue", "kda_gated_rmsnorm",
                    "kda_decode_fused",
+                   "kda_kv4_append", "kda_kv4_gather", "kda_kv4_attention", "kda_page_alloc",
+                   "kda_page_fork", "kda_page_free", "kda_page_compact", "kda_page_copy",
                    "kda_replay_fold", "kda_slot_copy", "kda_selftest_bounded_wait",
                    "kda_selftest_prefill_wait"):
             getattr(L, fn).restype = ctypes.c_int
@@ -601,6 +620,243 @@ def kda_slot_copy(pools, src, dst, dev_err=None, stream=None):
     slot_elems = pools[0][0].numel()
     _check("kda_slot_copy", lib().kda_slot_copy(
         P, ptrs, slot_elems, pools[0].shape[0], _p(src), _p(dst), src.numel(), _p(dev_err),
+        _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the paged 4-bit key/value cache
+# ---------------------------------------------------------------------------
+
+KV_TILE = 16          # tokens of a tile
+_KV_DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_FP16}
+
+
+def kv4_tile_bytes(D: int = K_DIM) -> int:
+    """Bytes of 16 tokens of one head: codes and scales of K and V (4.5 bits a value)."""
+    return 18 * int(D)
+
+
+def make_kv4_pool(num_pages: int, page_size: int, H_kv: int, D: int = K_DIM, device="cuda"):
+    """One layer's pool, uint8 [num_pages, H_kv, page_size / 16, 18 D]."""
+    if page_size not in (16, 32, 64, 128, 256):
+        raise ValueError("page_size is 16, 32, 64, 128 or 256, not %r" % (page_size,))
+    return torch.zeros(num_pages, H_kv, page_size // KV_TILE, kv4_tile_bytes(D), dtype=torch.uint8,
+                       device=device)
+
+
+def kv4_workspace_bytes() -> int:
+    return int(lib().kda_kv4_workspace_bytes())
+
+
+def make_kv4_workspace(device="cuda"):
+    """The attention's workspace, for one call at a time (zeroed, as its first call needs it)."""
+    return torch.zeros(kv4_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def _kv_dt(dtype):
+    if dtype not in _KV_DT:
+        raise TypeError("unsupported dtype %s (bf16 or fp16)" % dtype)
+    return _KV_DT[dtype]
+
+
+def _need_rows(t, name, shape, dtype=None, device=None):
+    """[tokens, heads, D] whose heads are dense and whose tokens may be strided.  Returns the
+    stride between tokens, in elements."""
+    _need(t, name, shape, dtype, device, dense=False)
+    T, H, D = t.shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError("%s: heads and channels must be dense (only tokens may be strided)" % name)
+    stride = t.stride(0) if T > 1 else H * D
+    if stride < H * D or stride % 8 != 0 or t.data_ptr() % 16 != 0:
+        raise ValueError("%s: tokens must start on 16-byte boundaries and not overlap" % name)
+    return stride
+
+
+def _need_pool(pool, D, device, name="pool"):
+    """uint8 [num_pages, H_kv, page_size / 16, 18 D].  Returns (num_pages, H_kv, page_size)."""
+    _need(pool, name, (None, None, None, 18 * D), torch.uint8, device)
+    return pool.shape[0], pool.shape[1], pool.shape[2] * KV_TILE
+
+
+def kda_kv4_append(k, v, cu_seqlens, start, page_table, pool, k_scale: float = 1.0,
+                   v_scale: float = 1.0, dev_err=None, stream=None):
+    """Store the packed new tokens' k, v [T, H_kv, D] (bf16 or fp16; tokens may be
+    strided) as 4-bit codes: token i of request b at position start[b] + i of the
+    pages that row b of page_table (int32 [B, max_pages]) names.  cu_seqlens int32
+    [B + 1], start int32 [B]; the scales are powers of two.  Writes the pool in place."""
+    _need(k, "k", (None, None, None), dense=False)
+    dt, dev = _kv_dt(k.dtype), k.device
+    T, H, D = k.shape
+    ks = _need_rows(k, "k", (T, H, D))
+    vs = _need_rows(v, "v", (T, H, D), k.dtype, dev)
+    pages, Hp, page_size = _need_pool(pool, D, dev)
+    if Hp != H:
+        raise ValueError("pool has %d heads, k has %d" % (Hp, H))
+    _need(page_table, "page_table", (None, None), I32, dev)
+    B = page_table.shape[0]
+    _need(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev)
+    _need(start, "start", (B,), I32, dev)
+    _need_err(dev_err, dev)
+    _check("kda_kv4_append", lib().kda_kv4_append(
+        dt, B, T, H, D, _p(k), ks, _p(v), vs, _p(cu_seqlens), _p(start), _p(page_table),
+        page_table.shape[1], page_size, _p(pool), pages, float(k_scale), float(v_scale),
+        _p(dev_err), _stream(stream)))
+
+
+def kda_kv4_gather(cu_seqlens, start, total_tokens: int, page_table, pool, dtype=torch.bfloat16,
+                   k=None, v=None, k_scale: float = 1.0, v_scale: float = 1.0, dev_err=None,
+                   stream=None):
+    """Read tokens back as the values they stand for: positions start[b] + i of request b
+    into packed k, v [total_tokens, H_kv, D].  Returns (k, v)."""
+    dt = _kv_dt(dtype)
+    _need(pool, "pool", (None, None, None, None), torch.uint8)
+    D, dev = pool.shape[3] // 18, pool.device
+    pages, H, page_size = _need_pool(pool, D, dev)
+    _need(page_table, "page_table", (None, None), I32, dev)
+    B, T = page_table.shape[0], int(total_tokens)
+    _need(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev)
+    _need(start, "start", (B,), I32, dev)
+    _need_err(dev_err, dev)
+    k = torch.empty(T, H, D, dtype=dtype, device=dev) if k is None else k
+    v = torch.empty(T, H, D, dtype=dtype, device=dev) if v is None else v
+    _need(k, "k", (T, H, D), dtype, dev)
+    _need(v, "v", (T, H, D), dtype, dev)
+    _check("kda_kv4_gather", lib().kda_kv4_gather(
+        dt, B, T, H, D, _p(k), _p(v), _p(cu_seqlens), _p(start), _p(page_table),
+        page_table.shape[1], page_size, _p(pool), pages, float(k_scale), float(v_scale),
+        _p(dev_err), _stream(stream)))
+    return k, v
+
+
+def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scale=None,
+                      window: int = 0, k_scale: float = 1.0, v_scale: float = 1.0, o=None, lse=None,
+                      workspace=None, dev_err=None, stream=None):
+    """Causal attention of the packed newest tokens' q [T, H_q, D] (bf16 or fp16; tokens
+    may be strided) over the cache; kv_lens int32 [B] counts each request's cached
+    tokens, the new ones included, and no request has more than max_q new ones.
+    ``window`` > 0 lets a token see that many positions, its own among them; ``scale``
+    defaults to D ** -0.5.  ``workspace``: ``make_kv4_workspace()``, kept by the caller
+    (one for each stream); a call without one makes its own.  Returns (o, lse), o in
+    q's dtype and lse fp32 [T, H_q]; a row that sees nothing has o = 0, lse = -inf."""
+    _need(q, "q", (None, None, None), dense=False)
+    dt, dev = _kv_dt(q.dtype), q.device
+    T, H, D = q.shape
+    qs = _need_rows(q, "q", (T, H, D))
+    pages, H_kv, page_size = _need_pool(pool, D, dev)
+    _need(page_table, "page_table", (None, None), I32, dev)
+    B = page_table.shape[0]
+    _need(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev)
+    _need(kv_lens, "kv_lens", (B,), I32, dev)
+    _need_err(dev_err, dev)
+    if o is None:
+        o = torch.empty(T, H, D, dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty(T, H, dtype=F32, device=dev)
+    if workspace is None:
+        workspace = make_kv4_workspace(dev)
+    _need(o, "o", (T, H, D), q.dtype, dev)
+    _need(lse, "lse", (T, H), F32, dev)
+    _need(workspace, "workspace", (None,), torch.uint8, dev)
+    _check("kda_kv4_attention", lib().kda_kv4_attention(
+        dt, B, T, int(max_q), H, H_kv, D, _p(q), qs, _p(cu_seqlens), _p(kv_lens), _p(page_table),
+        page_table.shape[1], page_size, _p(pool), pages, int(window),
+        float(D ** -0.5 if scale is None else scale), float(k_scale), float(v_scale), _p(o),
+        _p(lse), _p(workspace), workspace.numel(), _p(dev_err), _stream(stream)))
+    return o, lse
+
+
+def _need_pages(refs, page_table, lens, dev_err):
+    """refs int32 [num_pages], page_table int32 [B, max_pages], lens int32 [B].  Returns
+    (device, B, max_pages, num_pages)."""
+    _need(refs, "refs", (None,), I32)
+    dev = refs.device
+    _need(page_table, "page_table", (None, None), I32, dev)
+    B = page_table.shape[0]
+    if lens is not None:
+        _need(lens, "lens", (B,), I32, dev)
+    _need_err(dev_err, dev)
+    return dev, B, page_table.shape[1], refs.numel()
+
+
+def _need_page_pools(pools, num_pages, device):
+    """Layers' pools of one shape [num_pages, ...], any dtype.  Returns (pointers, bytes of a page)."""
+    if len(pools) == 0:
+        raise ValueError("pools must be a non-empty list")
+    for n, p in enumerate(pools):
+        _need(p, "pools[%d]" % n, device=device)
+        if p.dim() < 2 or p.shape[0] != num_pages or p.shape != pools[0].shape or p.dtype != pools[0].dtype:
+            raise ValueError("pools[%d]: every pool is [%d, ...] of one shape and dtype" % (n, num_pages))
+    ptrs = (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
+    return ptrs, pools[0].numel() // num_pages * pools[0].element_size()
+
+
+def kda_page_alloc(refs, page_table, lens, grow, page_size: int, dev_err=None, stream=None):
+    """Row b grows by grow[b] tokens (int32 [B]): the pages that takes are the lowest free
+    ones, rows in order.  refs int32 [num_pages] (holders of each page, 0: free),
+    page_table int32 [B, max_pages], lens int32 [B]; all three change in place."""
+    dev, B, M, N = _need_pages(refs, page_table, lens, dev_err)
+    _need(grow, "grow", (B,), I32, dev)
+    _check("kda_page_alloc", lib().kda_page_alloc(B, M, int(page_size), N, _p(refs), _p(page_table),
+                                                  _p(lens), _p(grow), _p(dev_err), _stream(stream)))
+
+
+def kda_page_fork(pools, refs, page_table, lens, src, dst, page_size: int, workspace=None,
+                  dev_err=None, stream=None):
+    """Copy-on-write: row dst[i] (empty) also holds row src[i]'s full pages, and gets a
+    copy of its partial last page in every pool of the list.  ``workspace``: int32, at
+    least 2 n; a call without one makes its own."""
+    dev, B, M, N = _need_pages(refs, page_table, lens, dev_err)
+    ptrs, page_bytes = _need_page_pools(pools, N, dev)
+    _need(src, "src", (None,), I32, dev)
+    n = src.numel()
+    _need(dst, "dst", (n,), I32, dev)
+    if workspace is None:
+        workspace = torch.empty(2 * n, dtype=I32, device=dev)
+    _need(workspace, "workspace", (None,), I32, dev)
+    _check("kda_page_fork", lib().kda_page_fork(
+        len(pools), ptrs, page_bytes, B, M, int(page_size), N, _p(refs), _p(page_table), _p(lens),
+        _p(src), _p(dst), n, _p(workspace), workspace.numel(), _p(dev_err), _stream(stream)))
+
+
+def kda_page_free(refs, page_table, lens, rows, page_size: int, dev_err=None, stream=None):
+    """Rows (int32 [n], distinct) let go of their pages; those nobody holds are free."""
+    dev, B, M, N = _need_pages(refs, page_table, lens, dev_err)
+    _need(rows, "rows", (None,), I32, dev)
+    _check("kda_page_free", lib().kda_page_free(B, M, int(page_size), N, _p(refs), _p(page_table),
+                                                _p(lens), _p(rows), rows.numel(), _p(dev_err),
+                                                _stream(stream)))
+
+
+def kda_page_compact(pools, refs, page_table, live=None, workspace=None, dev_err=None, stream=None):
+    """Move the held pages above the number of held pages into the free ones below, in
+    every pool; refs and page_table follow.  Returns live, int32 [1] on the device: the
+    pages from there on are free.  ``workspace``: int32, at least 3 num_pages + 16."""
+    dev, B, M, N = _need_pages(refs, page_table, None, dev_err)
+    ptrs, page_bytes = _need_page_pools(pools, N, dev)
+    if live is None:
+        live = torch.empty(1, dtype=I32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(3 * N + 16, dtype=I32, device=dev)
+    _need(live, "live", (1,), I32, dev)
+    _need(workspace, "workspace", (None,), I32, dev)
+    _check("kda_page_compact", lib().kda_page_compact(
+        len(pools), ptrs, page_bytes, B, M, N, _p(refs), _p(page_table), _p(live), _p(workspace),
+        workspace.numel(), _p(dev_err), _stream(stream)))
+    return live
+
+
+def kda_page_copy(pools, src, dst, dev_err=None, stream=None):
+    """Page dst[i] <- page src[i] in every pool of the list (int32 device index tensors)."""
+    if len(pools) == 0:
+        raise ValueError("pools must be a non-empty list")
+    _need(src, "src", (None,), I32)
+    dev = src.device
+    _need(dst, "dst", (src.numel(),), I32, dev)
+    _need_err(dev_err, dev)
+    _need(pools[0], "pools[0]", device=dev)
+    ptrs, page_bytes = _need_page_pools(pools, pools[0].shape[0], dev)
+    _check("kda_page_copy", lib().kda_page_copy(
+        len(pools), ptrs, page_bytes, pools[0].shape[0], _p(src), _p(dst), src.numel(), _p(dev_err),
         _stream(stream)))
 
 

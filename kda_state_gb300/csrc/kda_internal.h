@@ -8,6 +8,9 @@
 
 #include "../../include/kda.h"
 
+// Bytes of the cache attention's workspace: a counter and two partial results a CTA.
+#define KDA_KV4_WORKSPACE (16u << 20)
+
 namespace kda {
 
 struct DecodeArgs {
@@ -134,6 +137,55 @@ struct FusedDecodeArgs {
     int32_t *err;
 };
 
+// Append to and gather from one layer's 4-bit pool (kda_kv4.cuh: its layout).
+struct KvCacheArgs {
+    int dt, B, T, H, D, max_pages, page_shift, num_pages;
+    const void *k, *v;             // append: [T][H][D], tokens k_stride / v_stride elements apart
+    long long k_stride, v_stride;
+    void *k_out, *v_out;           // gather: [T][H][D]
+    const int32_t *cu, *start, *page_table;
+    uint8_t *pool;
+    float k_scale, v_scale, k_inv, v_inv;
+    int32_t *err;
+};
+
+struct KvAttentionArgs {
+    int dt, B, T, max_q, Hq, Hkv, D, max_pages, page_shift, num_pages, window;
+    const void *q;                 // [T][Hq][D], tokens q_stride elements apart
+    long long q_stride;
+    const int32_t *cu, *kv_lens, *page_table;
+    const uint8_t *pool;
+    float scale_k, v_scale;        // scale x k_scale x log2(e)
+    void *o;
+    float *lse;
+    uint8_t *ws;
+    int32_t *err;
+};
+
+// The page table's state: refs [num_pages], page_table [B][max_pages], lens [B].
+struct PageArgs {
+    int B, max_pages, page_shift, num_pages;
+    int32_t *refs, *page_table, *lens;
+    int32_t *err;
+};
+
+struct PageCopyParams {
+    int P, n, num_pages, step, chunks;
+    size_t page_bytes;
+    const int32_t *n_dev;          // the number of pairs on the device, or NULL: n
+    const int32_t *src, *dst;
+    int32_t *err;
+    uint8_t *pool[KDA_MAX_LAYERS];
+};
+
+cudaError_t launch_kv4_cache(const KvCacheArgs &a, bool append, cudaStream_t s);
+cudaError_t launch_kv4_attention(const KvAttentionArgs &a, cudaStream_t s);
+cudaError_t launch_page_alloc(const PageArgs &a, const int32_t *grow, cudaStream_t s);
+cudaError_t launch_page_fork(const PageArgs &a, const int32_t *src, const int32_t *dst, int n, PageCopyParams p,
+                             int32_t *ws, cudaStream_t s);
+cudaError_t launch_page_free(const PageArgs &a, const int32_t *rows, int n, cudaStream_t s);
+cudaError_t launch_page_compact(const PageArgs &a, PageCopyParams p, int32_t *ws, int32_t *live, cudaStream_t s);
+cudaError_t launch_page_copy(const PageCopyParams &p, cudaStream_t s);
 cudaError_t launch_conv_prologue(const PrologueArgs &a, cudaStream_t s);
 cudaError_t launch_gated_rmsnorm(const NormArgs &a, cudaStream_t s);
 cudaError_t launch_decode_fused(const FusedDecodeArgs &a, cudaStream_t s);

@@ -1,0 +1,152 @@
+// Append to and read back from the paged 4-bit cache.
+//
+// Append: for each 16 channels of a token's key or value
+//     s = e4m3(max|x| / 6),   code = e2m1(x / s)   (0 where s = 0)
+// One thread holds one block of 16 channels: 32 bytes in, 8 bytes of codes and
+// one scale out, no communication.  Both directions are bound by HBM for
+// prompts and by the launch for single tokens.
+#include "kda_internal.h"
+#include "kda_kv4.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int THREADS = 256;
+
+__device__ __forceinline__ void unpack16(const uint4 &w, float *x, __nv_bfloat16) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack16(const uint4 &w, float *x, __half) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = f16x2_to_float2(u[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// Where token t's head h lies: its tile, and its token in the tile; null with a bit set on bad input.
+template <int D>
+__device__ __forceinline__ uint8_t *locate(const KvCacheArgs &a, int t, int h, int &tok) {
+    const int b = owner_of(a.cu, a.B, t);
+    if (b < 0) {
+        report(a.err, DEVERR_SEQLENS);
+        return nullptr;
+    }
+    const long long pos = (long long)a.start[b] + (t - a.cu[b]);
+    if (pos < 0 || (pos >> a.page_shift) >= a.max_pages) {
+        report(a.err, DEVERR_SEQLENS);
+        return nullptr;
+    }
+    const int page = a.page_table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
+    if (page < 0 || page >= a.num_pages) {
+        report(a.err, DEVERR_PAGE_RANGE);
+        return nullptr;
+    }
+    const int in_page = (int)pos & ((1 << a.page_shift) - 1);
+    tok = in_page & (KV_TILE - 1);
+    return a.pool + ((((size_t)page * a.H + h) << (a.page_shift - 4)) + (in_page >> 4)) * KvTile<D>::BYTES;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS) append_kernel(const KvCacheArgs a) {
+    constexpr int NB = D / 16;
+    using L = KvTile<D>;
+    const long long id = (long long)blockIdx.x * THREADS + threadIdx.x;
+    const int blk = (int)(id % NB), side = (int)(id / NB & 1);
+    const long long th = id / (2 * NB);
+    const int h = (int)(th % a.H);
+    const int t = (int)(th / a.H);
+    if (t >= a.T) return;
+    const T *src = (side ? (const T *)a.v + t * a.v_stride : (const T *)a.k + t * a.k_stride) + h * D + blk * 16;
+    const uint4 w0 = __ldg(reinterpret_cast<const uint4 *>(src)), w1 = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+    int tok;
+    uint8_t *tile = locate<D>(a, t, h, tok);
+    if (!tile) return;
+    float x[16];
+    unpack16(w0, x, T());
+    unpack16(w1, x + 8, T());
+    const float inv = side ? a.v_inv : a.k_inv;      // a power of two: exact
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        x[i] *= inv;
+        top = max_nan(top, fabsf(x[i]));
+    }
+    const uint32_t sb = to_e4m3(__fdiv_rn(top, 6.f));
+    const float s = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x;
+    uint32_t code[2] = {0, 0};
+    if (sb != 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            code[i >> 2] |= to_e2m1x2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)) << (8 * (i & 3));
+    }
+    *reinterpret_cast<uint2 *>(tile + (side ? L::VC : L::KC) + tok * (D / 2) + blk * 8) = make_uint2(code[0], code[1]);
+    tile[side ? L::VS + blk * KV_TILE + tok : L::KS + tok * NB + blk] = (uint8_t)sb;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS) gather_kernel(const KvCacheArgs a) {
+    constexpr int NB = D / 16;
+    using L = KvTile<D>;
+    const long long id = (long long)blockIdx.x * THREADS + threadIdx.x;
+    const int blk = (int)(id % NB), side = (int)(id / NB & 1);
+    const long long th = id / (2 * NB);
+    const int h = (int)(th % a.H);
+    const int t = (int)(th / a.H);
+    if (t >= a.T) return;
+    int tok;
+    const uint8_t *tile = locate<D>(a, t, h, tok);
+    uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (tile) {
+        const uint2 code = *reinterpret_cast<const uint2 *>(tile + (side ? L::VC : L::KC) + tok * (D / 2) + blk * 8);
+        const uint32_t sb = tile[side ? L::VS + blk * KV_TILE + tok : L::KS + tok * NB + blk];
+        const float s = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x * (side ? a.v_scale : a.k_scale);
+        uint32_t h0[4], h1[4];
+        e2m1x8_to_f16x2(code.x, h0);
+        e2m1x8_to_f16x2(code.y, h1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = f16x2_to_float2(h0[i]), g = f16x2_to_float2(h1[i]);
+            out[i] = pack2(f.x * s, f.y * s, T());
+            out[i + 4] = pack2(g.x * s, g.y * s, T());
+        }
+    }
+    T *dst = (side ? (T *)a.v_out : (T *)a.k_out) + ((size_t)t * a.H + h) * D + blk * 16;
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+template <int D, typename T>
+cudaError_t launch(const KvCacheArgs &a, bool append, cudaStream_t s) {
+    const long long n = (long long)a.T * a.H * 2 * (D / 16);
+    const long long grid = (n + THREADS - 1) / THREADS;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (append) append_kernel<D, T><<<(unsigned)grid, THREADS, 0, s>>>(a);
+    else gather_kernel<D, T><<<(unsigned)grid, THREADS, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_cache(const KvCacheArgs &a, bool append, cudaStream_t s) {
+    if (a.dt == KDA_DTYPE_BF16)
+        return a.D == 128 ? launch<128, __nv_bfloat16>(a, append, s) : launch<64, __nv_bfloat16>(a, append, s);
+    return a.D == 128 ? launch<128, __half>(a, append, s) : launch<64, __half>(a, append, s);
+}
+
+}  // namespace kda
