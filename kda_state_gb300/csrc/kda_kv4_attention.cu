@@ -6,6 +6,7 @@
 //     o_i = sum_j softmax_j(scale q_i . k_j) v_j,   lse_i = ln sum_j exp(scale q_i . k_j)
 // A row that sees nothing has o = 0 and lse = -inf.
 #include "kda_kv4_decode.cuh"
+#include "kda_kv4_tiles.cuh"
 
 namespace kda {
 namespace {
@@ -14,7 +15,11 @@ template <int D, typename T>
 cudaError_t launch(const KvAttentionArgs &a, cudaStream_t s) {
     const long long rows = (long long)a.max_q * (a.Hq / a.Hkv);
     if (rows <= 8) return kv4::launch_decode_attention<D, 1, T>(a, s);
-    return kv4::launch_decode_attention<D, 2, T>(a, s);
+    if (rows <= 16) return kv4::launch_decode_attention<D, 2, T>(a, s);
+    // 256 rows a part where that still makes enough parts for the SMs
+    const long long parts = (long long)a.T * (a.Hq / a.Hkv) / 256 * a.Hkv;
+    if (parts >= 2 * kv4::SMS) return kv4::launch_tile_attention<D, 2, T>(a, s);
+    return kv4::launch_tile_attention<D, 1, T>(a, s);
 }
 
 }  // namespace

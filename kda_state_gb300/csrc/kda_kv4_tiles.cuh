@@ -1,0 +1,775 @@
+// Attention over the 4-bit cache for many query rows: prompts, long drafts.
+//
+// One CTA an SM works on 128 query rows of a kv head at a time (QT = 1) or 256
+// (QT = 2), a row being one (token, query head of the group), against tiles of
+// 128 cached tokens.  Three kinds of warps hand tiles on through mbarriers:
+//
+//   unpack  (warps 8-11)  a tile's codes, read from the pages one tile ahead into
+//                         registers, become fp16 K [token][channel] and V^T
+//                         [channel][token] in shared memory (both K-major, 128-byte
+//                         swizzle): one conversion and one product with the scale
+//                         for two values, exact; V pairs neighbouring tokens by
+//                         interleaving their nibbles before the conversion
+//   product (warp 12)     S = Q K^T and O += P V on tcgen05 (fp16, fp32 sums): S, P
+//                         and O stay in TMEM, P over S's columns
+//   softmax (warps 0-7)   two groups of four warps, a thread a row: the running
+//                         maximum (it moves only when a score passes it by 2^6, so O
+//                         is seldom rescaled), the weights as fp16 into TMEM, the sum
+//
+// The two groups alternate on the tensor cores: one's softmax runs beside the
+// other's products.  With QT = 2 they hold different rows and share each tile
+// (two products for each unpacked tile); with QT = 1 the same rows and every other
+// tile, joined at the end.  Queries are scaled by powers of two and weights held
+// 2^9 above the maximum as in the kernel for few rows.
+//
+// Parts of the work are dealt to the CTAs in turn.  If there are fewer (request,
+// rows, head) than SMs, each is cut along the tokens; the last part to arrive
+// joins the results in order.
+#pragma once
+
+#include "kda_kv4_decode.cuh"
+
+namespace kda {
+namespace kv4 {
+
+constexpr int TT = 128;                // tokens of a tile
+constexpr int TILE_THREADS = 13 * 32;
+constexpr int SMS = 152;
+constexpr int SPLIT_PARTS = 126;       // a cut aims at this many parts: at most twice as many arise
+
+template <int D, int QT>
+struct TileShape {
+    static constexpr int STAGES = QT == 1 ? 3 : 2;
+    static constexpr int QBYTES = 128 * D * 2;
+    static constexpr int KBYTES = TT * D * 2;
+    static constexpr int STAGE = 2 * KBYTES;
+    static constexpr int RING = QT * QBYTES;
+    static constexpr int META = RING + STAGES * STAGE;   // barriers and small arrays
+    static constexpr int SMEM = META + 3072;
+    static constexpr int PARTIAL = 128 * (D + 2);        // floats
+    static constexpr uint32_t O_COL = 256;
+};
+
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {   // K-major, 128-byte swizzle, 8-row groups 1 KB apart
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)64 << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
+}
+constexpr uint32_t idesc_f16(int M, int N) {                      // fp16 operands, fp32 sums, both K-major
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_done(uint32_t bar) {          // arrives when every MMA issued so far is complete
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void group_sync(uint32_t id, uint32_t count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// A bounded wait; once one has given up (*dead), none waits any longer and the CTA runs out on what it has.
+__device__ __forceinline__ void wait_or_dead(uint32_t bar, uint32_t parity, volatile int *dead) {
+    if (barrier_test(bar, parity)) return;
+    const uint64_t t0 = global_timer();
+    while (!*dead) {
+        if (barrier_test(bar, parity)) return;
+        if (global_timer() - t0 > ASYNC_WAIT_NS) *dead = 1;
+    }
+}
+
+// A piece of work: rows of one kv head of one request against tiles of its cache.
+struct Part {
+    int b, h, row0, rows, q0, n, len;
+    int tile0, tiles;                  // of TT tokens; tiles may be 0
+    int pieces, slot0, piece;          // how many parts share the rows; their first slot
+};
+
+// Finds parts by number, in ascending order, 32 requests at a time; every lane of a warp calls it.
+template <int QT>
+struct Walker {
+    int b0, parts_upto, slots_upto, before, slots_before, cut;
+    Request q;
+    int mine, my_slots, incl, slots_incl;
+
+    // Tiles that no part of the request exceeds.
+    __device__ __forceinline__ static int most_tiles(const KvAttentionArgs &a, const Request &q) {
+        const int all = (q.len + TT - 1) / TT;
+        if (a.window <= 0) return max(all, 1);
+        const long long near = ((long long)a.window + 128 * QT) / TT + 2;
+        return max((int)min((long long)all, near), 1);
+    }
+    __device__ __forceinline__ int pieces_of(const KvAttentionArgs &a, const Request &r) const {
+        return cut > 0 ? (most_tiles(a, r) + cut - 1) / cut : 1;
+    }
+    __device__ __forceinline__ void load(const KvAttentionArgs &a) {
+        const int lane = threadIdx.x & 31, b = b0 + lane;
+        mine = my_slots = 0;
+        if (b < a.B) {
+            q = request_of(a, b, 128 * QT, false);
+            const int pieces = q.row_blocks ? pieces_of(a, q) : 0;
+            mine = q.row_blocks * a.Hkv * pieces;
+            my_slots = pieces > 1 ? mine : 0;
+        }
+        incl = mine, slots_incl = my_slots;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(~0u, incl, o), y = __shfl_up_sync(~0u, slots_incl, o);
+            if (lane >= o) incl += x, slots_incl += y;
+        }
+    }
+    __device__ __forceinline__ void start(const KvAttentionArgs &a, int cut_) {
+        cut = cut_;
+        b0 = before = slots_before = 0;
+        load(a);
+    }
+    __device__ __forceinline__ bool find(const KvAttentionArgs &a, int p, Part &out) {
+        while (true) {
+            const int total = __shfl_sync(~0u, incl, 31);
+            if (p < before + total) break;
+            b0 += 32;
+            if (b0 >= a.B) return false;
+            before += total;
+            slots_before += __shfl_sync(~0u, slots_incl, 31);
+            load(a);
+        }
+        const int src = __ffs(__ballot_sync(~0u, before + incl > p)) - 1;
+        const int index = p - (before + __shfl_sync(~0u, incl - mine, src));
+        out.b = b0 + src;
+        out.q0 = __shfl_sync(~0u, q.q0, src);
+        out.n = __shfl_sync(~0u, q.n, src);
+        out.len = __shfl_sync(~0u, q.len, src);
+        const int blocks = __shfl_sync(~0u, q.row_blocks, src);
+        Request r;
+        r.len = out.len;
+        out.pieces = pieces_of(a, r);
+        out.piece = index % out.pieces;
+        const int unit = index / out.pieces;
+        out.slot0 = slots_before + __shfl_sync(~0u, slots_incl - my_slots, src) + unit * out.pieces;
+        out.h = unit / blocks;
+        // the rows that see most come first
+        out.row0 = (blocks - 1 - unit % blocks) * 128 * QT;
+        const int G = a.Hq / a.Hkv;
+        out.rows = min(128 * QT, out.n * G - out.row0);
+        const int i0 = out.row0 / G, i1 = (out.row0 + out.rows - 1) / G;
+        const int lo = a.window > 0 ? max(0, out.len - out.n + i0 + 1 - a.window) / TT : 0;
+        const int hi = (max(out.len - out.n + i1 + 1, 0) + TT - 1) / TT;
+        const long long tiles = max(hi - lo, 1);
+        out.tile0 = lo + (int)(tiles * out.piece / out.pieces);
+        out.tiles = lo + (int)(tiles * (out.piece + 1) / out.pieces) - out.tile0;
+        return true;
+    }
+};
+
+// Byte of the 16-byte chunk (8 fp16 of the contraction axis) of a row in a K-major tile of `rows` rows.
+__device__ __forceinline__ uint32_t chunk_at(int row, int chunk, int rows) {
+    return (uint32_t)((chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+// The first and last tokens row `row` of a part sees (last < first: none).
+__device__ __forceinline__ int2 sight(const KvAttentionArgs &a, const Part &p, int row) {
+    if (row >= p.rows) return make_int2(0, -1);
+    const int last = p.len - p.n + (p.row0 + row) / (a.Hq / a.Hkv);
+    return make_int2(a.window > 0 ? max(0, last + 1 - a.window) : 0, last);
+}
+
+template <int D, int QT, typename T>
+__global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const KvAttentionArgs a) {
+    using L = KvTile<D>;
+    using S = TileShape<D, QT>;
+    constexpr int ST = S::STAGES;
+    extern __shared__ __align__(1024) uint8_t tile_smem[];
+    uint8_t *const smem = tile_smem;
+    uint8_t *const meta = smem + S::META;
+    float2 *const ml_s = reinterpret_cast<float2 *>(meta);                  // [2][128] maximum and sum (QT = 1)
+    uint8_t *const nan_s = meta + 2048;                                     // [ST][8 blocks][16 groups of 8 tokens]
+    uint8_t *const miss_s = nan_s + 3 * 128;                                // [ST][16] groups whose page is missing
+    uint32_t *const nan_any = reinterpret_cast<uint32_t *>(miss_s + 3 * 16);// [ST] a byte for each unpacking warp
+    volatile int *const dead = reinterpret_cast<volatile int *>(nan_any + 4);
+    volatile uint32_t *const misc = nan_any + 5;                            // TMEM base, a flag
+    uint8_t *const nan_row = meta + 2048 + 384 + 48 + 32;                   // [2][128] blocks with a NaN value (QT = 1)
+    const uint32_t bar = shared_addr(nan_row + 256);
+    const uint32_t Q_FULL = bar, S_FULL = bar + 16, P_FULL = bar + 32, PV_DONE = bar + 48, FINISHED = bar + 64, KV_FULL = bar + 72,
+                   KV_FREE = KV_FULL + 8 * ST;
+    static_assert(2048 + 384 + 48 + 32 + 256 + 72 + 16 * 3 <= 3072, "the small arrays");
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int G = a.Hq / a.Hkv;
+
+    if (w == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(shared_addr(const_cast<uint32_t *>(misc))) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int g = 0; g < 2; ++g) {
+            barrier_init(Q_FULL + 8 * g, 4);
+            barrier_init(S_FULL + 8 * g, 1);
+            barrier_init(P_FULL + 8 * g, 4);
+            barrier_init(PV_DONE + 8 * g, 1);
+        }
+        for (int s = 0; s < ST; ++s) {
+            barrier_init(KV_FULL + 8 * s, 4);
+            barrier_init(KV_FREE + 8 * s, 1);
+        }
+        barrier_init(FINISHED, 1);
+        *dead = 0;
+    }
+    tmem_before_sync();
+    __syncthreads();
+    tmem_after_sync();
+    const uint32_t tmem = misc[0];
+
+    // ---- how the work is cut: only where there are fewer parts than SMs (QT = 1) -----------------------
+    int cut = 0;
+    {
+        long long units = 0, tiles = 0;
+        for (int b = lane; b < a.B; b += 32) {
+            const Request q = request_of(a, b, 128 * QT, blockIdx.x == 0 && w == 0);
+            units += (long long)q.row_blocks * a.Hkv;
+            if (q.row_blocks) tiles += (long long)q.row_blocks * a.Hkv * Walker<QT>::most_tiles(a, q);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            units += __shfl_xor_sync(~0u, units, o);
+            tiles += __shfl_xor_sync(~0u, tiles, o);
+        }
+        if (QT == 1 && units < SMS) cut = (int)max((tiles + SPLIT_PARTS - 1) / SPLIT_PARTS, 2LL);
+    }
+    Walker<QT> walk;
+    walk.start(a, cut);
+    Part p;
+
+    if (w < 8) {
+        // ================================ softmax ======================================================
+        const int g = w >> 2, row = tid & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
+        const uint32_t s_col = lanes + g * 128, o_col = lanes + S::O_COL + g * D;
+        uint8_t *const q_tile = smem + (QT == 2 ? g : 0) * S::QBYTES;
+        const int my_row = (QT == 2 ? g * 128 : 0) + row;      // of the part
+        uint32_t done = 0;             // this group's tiles so far
+        uint32_t kv = 0;               // tiles so far
+        for (int pi = blockIdx.x; walk.find(a, pi, p); pi += gridDim.x) {
+            // queries: scaled by a power of two, so that the largest of a row is in [1, 2)
+            float factor;
+            {
+                uint32_t qw[D / 2];
+                float top = 0.f;
+                if (my_row < p.rows) {
+                    const int rr = p.row0 + my_row;
+                    const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + (long long)(p.q0 + rr / G) * a.q_stride +
+                                                                       (p.h * G + rr % G) * D);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = __ldg(src + i);
+                        qw[4 * i] = v.x, qw[4 * i + 1] = v.y, qw[4 * i + 2] = v.z, qw[4 * i + 3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 2; ++i) qw[i] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 2; ++i) {
+                    const float2 f = pair_of<T>(qw[i]);
+                    top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
+                }
+                const int e = min(max((int)(__float_as_uint(top) >> 23 & 255), 1), 253);
+                const float down = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), a.scale_k);
+                factor = fabsf(a.scale_k) * __uint_as_float((uint32_t)e << 23);
+                if (QT == 2 || g == 0) {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = pair_of<T>(qw[4 * i + k]);
+                            x[k] = half_pair(f.x * down, f.y * down);
+                        }
+                        *reinterpret_cast<uint4 *>(q_tile + chunk_at(row, i, 128)) = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(Q_FULL + 8 * g);
+                }
+            }
+            const int2 see = sight(a, p, my_row);
+            // every row of this group sees a tile whole if it lies between these
+            int all_first, all_last;
+            {
+                const int2 x = sight(a, p, QT == 2 ? g * 128 : 0);
+                const int2 y = sight(a, p, min(QT == 2 ? g * 128 + 127 : 127, p.rows - 1));
+                all_first = y.x, all_last = x.y;
+            }
+            float m = NOTHING, l = 0.f;
+            uint32_t nan_blocks = 0;
+            int mine = 0;              // tiles of this part that this group has done
+            for (int j = QT == 2 ? 0 : g; j < p.tiles; j += QT == 2 ? 1 : 2) {
+                const int stage = (kv + j) % ST, pos0 = (p.tile0 + j) * TT;
+                wait_or_dead(S_FULL + 8 * g, done & 1, dead);
+                tmem_after_sync();
+                const uint4 miss = *reinterpret_cast<const uint4 *>(miss_s + stage * 16);
+                const bool some = pos0 < all_first || pos0 + TT - 1 > all_last || (miss.x | miss.y | miss.z | miss.w) != 0;
+                const uint32_t gone[4] = {miss.x, miss.y, miss.z, miss.w};
+                auto visible = [&](int c) -> uint32_t {        // of tokens 32 c .. 32 c + 31
+                    const int lo = see.x - (pos0 + 32 * c), hi = see.y - (pos0 + 32 * c);
+                    uint32_t v = hi < 0 ? 0u : hi >= 31 ? ~0u : (2u << hi) - 1;
+                    v &= lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
+                    return v & ~gone[c];
+                };
+                float top = -INFINITY;
+                uint32_t x[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32(s_col + 32 * c, x);
+                    if (some) {
+                        const uint32_t v = visible(c);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (v >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+                    }
+                }
+                top = top == -INFINITY ? top : top * factor;
+                if (__any_sync(~0u, top - m > MOVE)) {
+                    const float to = fmaxf(m, top - HEADROOM), keep = exp2_fast(m - to);
+                    m = to;
+                    l *= keep;
+                    if (mine > 0) {
+                        wait_or_dead(PV_DONE + 8 * g, (done - 1) & 1, dead);
+                        tmem_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            tmem_ld32(o_col + 32 * c, x);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
+                            tmem_st32(o_col + 32 * c, x);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32(s_col + 32 * c, x);
+                    uint32_t pk[16];
+                    const uint32_t v = some ? visible(c) : ~0u;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), factor, -m));
+                        float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), factor, -m));
+                        if (some) {
+                            p0 = v >> e & 1 ? p0 : 0.f;
+                            p1 = v >> (e + 1) & 1 ? p1 : 0.f;
+                        }
+                        l += p0 + p1;
+                        pk[e / 2] = half_pair(p0, p1);
+                    }
+                    tmem_st16(s_col + 16 * c, pk);
+                }
+                if (nan_any[stage]) {                          // NaN values: they reach the rows that see them
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t v = visible(c);
+#pragma unroll 1
+                        for (int blk = 0; blk < D / 16; ++blk) {
+                            const int unpacker = (blk >> 2) * 2 + (c >> 1);
+                            if (!(nan_any[stage] >> (8 * unpacker) & 255)) continue;
+                            if (v & *reinterpret_cast<const uint32_t *>(nan_s + stage * 128 + blk * 16 + 4 * c)) nan_blocks |= 1u << blk;
+                        }
+                    }
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tmem_before_sync();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(P_FULL + 8 * g);
+                ++done;
+                ++mine;
+            }
+            kv += p.tiles;
+            if (mine > 0) wait_or_dead(PV_DONE + 8 * g, (done - 1) & 1, dead);
+            tmem_after_sync();
+
+            const int rr = p.row0 + my_row;
+            const size_t at_row = (size_t)(p.q0 + rr / G) * a.Hq + p.h * G + rr % G;
+            constexpr float LN2 = 0.69314718055994531f;
+            if (QT == 2) {
+                const float f = l == 0.f ? 0.f : a.v_scale / l;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32(o_col + 32 * c, x);
+                    if (my_row < p.rows && !*dead) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            const bool bad = nan_blocks >> (2 * c + e / 16) & 1;
+                            uint32_t y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float u = __uint_as_float(x[e + 2 * k]) * f, v = __uint_as_float(x[e + 2 * k + 1]) * f;
+                                y[k] = bad ? 0x7fff7fffu : l == 0.f ? 0u : pack_of<T>(u, v);
+                            }
+                            *reinterpret_cast<uint4 *>((T *)a.o + at_row * D + 32 * c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                }
+                if (my_row < p.rows && a.lse && !*dead) a.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+                tmem_before_sync();
+            } else {
+                // both groups hold the same rows: each joins half of the channels
+                ml_s[g * 128 + row] = make_float2(m, l);
+                nan_row[g * 128 + row] = (uint8_t)nan_blocks;
+                tmem_before_sync();
+                group_sync(1, 256);
+                tmem_after_sync();
+                const float2 ml0 = ml_s[row], ml1 = ml_s[128 + row];
+                nan_blocks = nan_row[row] | nan_row[128 + row];
+                const float both = fmaxf(ml0.x, ml1.x);
+                const float k0 = exp2_fast(ml0.x - both), k1 = exp2_fast(ml1.x - both), sum = ml0.y * k0 + ml1.y * k1;
+                const bool have0 = p.tiles > 0, have1 = p.tiles > 1, split = p.pieces > 1;
+                const float f = split ? 1.f : sum == 0.f ? 0.f : a.v_scale / sum;
+                float *const partials = reinterpret_cast<float *>(a.ws + MAX_CTAS * 4);
+                float *const my_part = partials + (size_t)(p.slot0 + p.piece) * S::PARTIAL;
+#pragma unroll 1
+                for (int c = g * (D / 64); c < (g + 1) * (D / 64); ++c) {
+                    uint32_t x0[32], x1[32];
+                    tmem_ld32(lanes + S::O_COL + 32 * c, x0);
+                    tmem_ld32(lanes + S::O_COL + D + 32 * c, x1);
+                    if (my_row >= p.rows || *dead) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float v = (have0 ? __uint_as_float(x0[e]) * k0 : 0.f) + (have1 ? __uint_as_float(x1[e]) * k1 : 0.f);
+                        if (nan_blocks >> (2 * c + e / 16) & 1) v = __uint_as_float(0x7fffffffu);
+                        x0[e] = __float_as_uint(split || sum != 0.f ? v * f : 0.f);
+                    }
+                    if (split) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            __stcg(reinterpret_cast<uint4 *>(my_part + row * D + 32 * c + e), make_uint4(x0[e], x0[e + 1], x0[e + 2], x0[e + 3]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] = pack_of<T>(__uint_as_float(x0[e + 2 * k]), __uint_as_float(x0[e + 2 * k + 1]));
+                            *reinterpret_cast<uint4 *>((T *)a.o + at_row * D + 32 * c + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                }
+                if (g == 0 && my_row < p.rows && !*dead) {
+                    if (split) __stcg(reinterpret_cast<float2 *>(my_part + 128 * D + 2 * row), make_float2(both, sum));
+                    else if (a.lse) a.lse[at_row] = sum == 0.f ? -INFINITY : (both + log2f(sum)) * LN2;
+                }
+                if (split) {
+                    __threadfence();
+                    group_sync(1, 256);
+                    if (tid == 0) {
+                        int *const counter = reinterpret_cast<int *>(a.ws) + p.slot0;
+                        const bool last = atomicAdd(counter, 1) == p.pieces - 1;
+                        if (last) *counter = 0;                // as the next call needs it
+                        misc[1] = last;
+                    }
+                    group_sync(1, 256);
+                    if (misc[1] && !*dead) {
+                        __threadfence();
+                        for (int i = tid; i < p.rows * (D / 4); i += 256) {
+                            const int col = i / (D / 4), d = i % (D / 4) * 4;
+                            float to = NOTHING, total = 0.f;
+                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (int x = 0; x < p.pieces; ++x) {
+                                const float *src = partials + (size_t)(p.slot0 + x) * S::PARTIAL;
+                                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + 128 * D + 2 * col));
+                                const float4 u = __ldcg(reinterpret_cast<const float4 *>(src + col * D + d));
+                                const float up = fmaxf(to, ml.x), keep = exp2_fast(to - up), add = exp2_fast(ml.x - up);
+                                to = up;
+                                total = total * keep + ml.y * add;
+                                v.x = v.x * keep + u.x * add, v.y = v.y * keep + u.y * add;
+                                v.z = v.z * keep + u.z * add, v.w = v.w * keep + u.w * add;
+                            }
+                            const int orow = p.row0 + col;
+                            const size_t at = (size_t)(p.q0 + orow / G) * a.Hq + p.h * G + orow % G;
+                            const float fo = total == 0.f ? 0.f : a.v_scale / total;
+                            *reinterpret_cast<uint2 *>((T *)a.o + at * D + d) =
+                                total == 0.f ? make_uint2(0, 0) : make_uint2(pack_of<T>(v.x * fo, v.y * fo), pack_of<T>(v.z * fo, v.w * fo));
+                            if (d == 0 && a.lse) a.lse[at] = total == 0.f ? -INFINITY : (to + log2f(total)) * LN2;
+                        }
+                    }
+                }
+                tmem_before_sync();
+                group_sync(1, 256);    // both have read O, the maxima and sums
+            }
+        }
+    } else if (w < 12) {
+        // ================================ unpack =======================================================
+        const int uw = w - 8, ut = tid - 256;
+        const int box = uw & 1, grp = lane & 7, blk = (uw >> 1) * 4 + (lane >> 3);
+        const bool has_v = blk < D / 16;
+        const int v_tok = box * 64 + grp * 8;                  // of the tile: this thread's 8 tokens of V
+        struct Raw {
+            uint4 k[D / 32];
+            uint2 v[8];
+            uint2 ks, vs;
+            uint32_t missing;
+        };
+        struct Spot {                                          // a tile, and the pages this thread reads of it
+            int pi, j, page_k, page_v, pos0, h, len;
+            bool valid;
+        };
+        auto next = [&](Spot &s) {
+            ++s.j;
+            while (s.valid && s.j >= p.tiles) {
+                s.pi += gridDim.x;
+                s.j = 0;
+                s.valid = walk.find(a, s.pi, p);
+            }
+            if (!s.valid) return;
+            s.pos0 = (p.tile0 + s.j) * TT;
+            s.h = p.h;
+            s.len = p.len;
+            const int32_t *const pages = a.page_table + (size_t)p.b * a.max_pages;
+            s.page_k = s.pos0 + ut < p.len ? pages[(s.pos0 + ut) >> a.page_shift] : -2;
+            s.page_v = s.pos0 + v_tok < p.len ? pages[(s.pos0 + v_tok) >> a.page_shift] : -2;
+        };
+        auto tile_of = [&](int page, int h, int pos) {
+            const int in_page = pos & ((1 << a.page_shift) - 1);
+            return a.pool + ((((size_t)page * a.Hkv + h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
+        };
+        auto load = [&](const Spot &s, Raw &r) {
+            if (s.page_k >= 0 && s.page_k < a.num_pages) {
+                const int pos = s.pos0 + ut, tok = pos & 15;
+                const uint8_t *t = tile_of(s.page_k, s.h, pos);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) r.k[i] = __ldg(reinterpret_cast<const uint4 *>(t + tok * (D / 2)) + i);
+                if constexpr (D == 128) r.ks = __ldg(reinterpret_cast<const uint2 *>(t + L::KS + tok * 8));
+                else r.ks = make_uint2(__ldg(reinterpret_cast<const uint32_t *>(t + L::KS + tok * 4)), 0);
+            } else {
+                if (s.page_k != -2) report(a.err, DEVERR_PAGE_RANGE);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) r.k[i] = make_uint4(0, 0, 0, 0);
+                r.ks = make_uint2(0, 0);
+            }
+            r.missing = s.page_v != -2 && (s.page_v < 0 || s.page_v >= a.num_pages) ? 255u : 0u;
+            if (has_v && s.page_v >= 0 && s.page_v < a.num_pages) {
+                const int pos = s.pos0 + v_tok, tok = pos & 15;
+                const uint8_t *t = tile_of(s.page_v, s.h, pos);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r.v[i] = __ldg(reinterpret_cast<const uint2 *>(t + L::VC + (tok + i) * (D / 2) + blk * 8));
+                r.vs = __ldg(reinterpret_cast<const uint2 *>(t + L::VS + blk * KV_TILE + tok));
+                // scales of tokens past the end: 0
+                const int live = s.len - pos;
+                if (live < 4) r.vs.x &= (1u << (8 * live)) - 1;
+                if (live < 8) r.vs.y &= live <= 4 ? 0u : (1u << (8 * (live - 4))) - 1;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r.v[i] = make_uint2(0, 0);
+                r.vs = make_uint2(0, 0);
+            }
+        };
+        auto unpack = [&](const Raw &r, uint8_t *k_tile, uint8_t *v_tile, int stage) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {                  // 8 channels: one word
+                const uint4 &four = r.k[i / 4];
+                const uint32_t word = (i & 3) == 0 ? four.x : (i & 3) == 1 ? four.y : (i & 3) == 2 ? four.z : four.w;
+                const uint32_t two = e4m3x2_to_f16x2((i < 8 ? r.ks.x : r.ks.y) >> (i & 4 ? 16 : 0) & 0xffffu);
+                const uint32_t sc = __byte_perm(two, 0, i & 2 ? 0x3232 : 0x1010);
+                uint32_t f[4];
+                e2m1x8_to_f16x2(word, f);
+                *reinterpret_cast<uint4 *>(k_tile + chunk_at(ut, i, TT)) =
+                    make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
+            }
+            uint2 vs = r.vs;
+            const uint32_t n0 = ((vs.x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u, n1 = ((vs.y & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            const bool any = __any_sync(~0u, (n0 | n1) != 0);
+            if (any) {                                         // NaN scales: 0 here, noted for the softmax
+                vs.x &= ~((n0 >> 7) * 255u);
+                vs.y &= ~((n1 >> 7) * 255u);
+                // bits 0, 8, 16, 24 to bits 0..3
+                const uint32_t b0 = (n0 >> 7) * 0x01020408u >> 24 & 15u, b1 = (n1 >> 7) * 0x01020408u >> 24 & 15u;
+                if (has_v) nan_s[stage * 128 + blk * 16 + box * 8 + grp] = (uint8_t)(b0 | b1 << 4);
+            }
+            if (lane == 0) reinterpret_cast<uint8_t *>(nan_any + stage)[uw] = any;
+            if (blk == 0) miss_s[stage * 16 + box * 8 + grp] = (uint8_t)r.missing;
+            if (has_v) {
+                const uint32_t sc[4] = {e4m3x2_to_f16x2(vs.x & 0xffffu), e4m3x2_to_f16x2(vs.x >> 16), e4m3x2_to_f16x2(vs.y & 0xffffu),
+                                        e4m3x2_to_f16x2(vs.y >> 16)};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {                  // 8 channels of 8 tokens
+                    constexpr uint32_t LOW = 0x0f0f0f0fu;
+                    uint32_t even[4][4], odd[4][4];            // [pair of tokens][channel pair]
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t x = q ? r.v[2 * t].y : r.v[2 * t].x, y = q ? r.v[2 * t + 1].y : r.v[2 * t + 1].x;
+                        e2m1x8_to_f16x2((x & LOW) | ((y << 4) & ~LOW), even[t]);
+                        e2m1x8_to_f16x2(((x >> 4) & LOW) | (y & ~LOW), odd[t]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int ch = blk * 16 + q * 8 + 2 * i;
+                        *reinterpret_cast<uint4 *>(v_tile + chunk_at(ch, box * 8 + grp, D)) =
+                            make_uint4(hmul2(even[0][i], sc[0]), hmul2(even[1][i], sc[1]), hmul2(even[2][i], sc[2]), hmul2(even[3][i], sc[3]));
+                        *reinterpret_cast<uint4 *>(v_tile + chunk_at(ch + 1, box * 8 + grp, D)) =
+                            make_uint4(hmul2(odd[0][i], sc[0]), hmul2(odd[1][i], sc[1]), hmul2(odd[2][i], sc[2]), hmul2(odd[3][i], sc[3]));
+                    }
+                }
+            }
+        };
+        Spot spot;
+        spot.pi = blockIdx.x;
+        spot.j = -1;
+        spot.valid = walk.find(a, spot.pi, p);
+        Raw now, then;
+        next(spot);
+        bool have = spot.valid;
+        if (have) {
+            load(spot, now);
+            next(spot);
+        }
+        for (uint32_t n = 0; have; ++n) {
+            const bool more = spot.valid;
+            if (more) {
+                load(spot, then);
+                next(spot);
+            }
+            const int stage = n % ST;
+            if (n >= ST) wait_or_dead(KV_FREE + 8 * stage, (n / ST - 1) & 1, dead);
+            uint8_t *const k_tile = smem + S::RING + stage * S::STAGE;
+            unpack(now, k_tile, k_tile + S::KBYTES, stage);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) barrier_arrive(KV_FULL + 8 * stage);
+            now = then;
+            have = more;
+        }
+    } else {
+        // ================================ products =====================================================
+        constexpr uint32_t ID_S = idesc_f16(128, TT), ID_O = idesc_f16(128, D);
+        const uint32_t base = shared_addr(smem);
+        uint32_t done[2] = {0, 0}, kv = 0, parts = 0;
+        for (int pi = blockIdx.x; walk.find(a, pi, p); pi += gridDim.x) {
+            if (lane == 0) {
+                auto kv_wait = [&](int j) { wait_or_dead(KV_FULL + 8 * ((kv + j) % ST), (kv + j) / ST & 1, dead); };
+                auto scores = [&](int g, int j) {
+                    const uint64_t dq = tile_desc(base + (QT == 2 ? g : 0) * S::QBYTES), dk = tile_desc(base + S::RING + (kv + j) % ST * S::STAGE);
+                    tmem_after_sync();
+                    if (!*dead) {
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s) {
+                            const uint64_t at = (uint64_t)(((s >> 2) * 16384 + (s & 3) * 32) >> 4);
+                            mma_f16_ss(tmem + g * 128, dq + at, dk + at, ID_S, s > 0);
+                        }
+                    }
+                    mma_done(S_FULL + 8 * g);
+                };
+                auto values = [&](int g, int j, bool first) {
+                    wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
+                    ++done[g];
+                    const uint64_t dv = tile_desc(base + S::RING + (kv + j) % ST * S::STAGE + S::KBYTES);
+                    tmem_after_sync();
+                    if (!*dead) {
+#pragma unroll
+                        for (int s = 0; s < TT / 16; ++s) {
+                            const uint64_t at = (uint64_t)(((s >> 2) * D * 128 + (s & 3) * 32) >> 4);
+                            mma_f16_ts(tmem + S::O_COL + g * D, tmem + g * 128 + 8 * s, dv + at, ID_O, s > 0 || !first);
+                        }
+                    }
+                    mma_done(PV_DONE + 8 * g);
+                };
+                const int tiles = p.tiles;
+                wait_or_dead(Q_FULL, parts & 1, dead);
+                if (QT == 2) {
+                    wait_or_dead(Q_FULL + 8, parts & 1, dead);
+                    kv_wait(0);
+                    scores(0, 0);
+                    scores(1, 0);
+                    for (int j = 0; j < tiles; ++j) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            values(g, j, j == 0);
+                            if (g == 1) mma_done(KV_FREE + 8 * ((kv + j) % ST));
+                            if (j + 1 < tiles) {
+                                if (g == 0) kv_wait(j + 1);
+                                scores(g, j + 1);
+                            }
+                        }
+                    }
+                } else {
+                    for (int j = 0; j < min(tiles, 2); ++j) {
+                        kv_wait(j);
+                        scores(j, j);
+                    }
+                    for (int j = 0; j < tiles; ++j) {
+                        values(j & 1, j, j < 2);
+                        mma_done(KV_FREE + 8 * ((kv + j) % ST));
+                        if (j + 2 < tiles) {
+                            kv_wait(j + 2);
+                            scores(j & 1, j + 2);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            kv += p.tiles;
+            ++parts;
+        }
+        if (lane == 0) {
+            mma_done(FINISHED);
+            barrier_wait(FINISHED, 0);
+        }
+        __syncwarp();
+    }
+
+    tmem_before_sync();
+    __syncthreads();
+    if (tid == 0 && *dead) report(a.err, DEVERR_TIMEOUT);
+    if (w == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int D, int QT, typename T>
+cudaError_t launch_tile_attention(const KvAttentionArgs &a, cudaStream_t s) {
+    using Sh = TileShape<D, QT>;
+    static_assert((size_t)MAX_CTAS * 4 + 2 * SPLIT_PARTS * (size_t)Sh::PARTIAL * 4 <= KDA_KV4_WORKSPACE, "workspace");
+    static const cudaError_t set =
+        cudaFuncSetAttribute(tile_attention_kernel<D, QT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+    if (set != cudaSuccess) return set;
+    tile_attention_kernel<D, QT, T><<<SMS, TILE_THREADS, Sh::SMEM, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace kv4
+}  // namespace kda
