@@ -4,13 +4,13 @@
 // (QT = 2), a row being one (token, query head of the group), against tiles of
 // 128 cached tokens.  Three kinds of warps hand tiles on through mbarriers:
 //
-//   unpack  (warps 8-11)  a tile's codes, read from the pages one tile ahead into
+//   unpack  (warps 8-15)  a tile's codes, read from the pages one tile ahead into
 //                         registers, become fp16 K [token][channel] and V^T
 //                         [channel][token] in shared memory (both K-major, 128-byte
 //                         swizzle): one conversion and one product with the scale
 //                         for two values, exact; V pairs neighbouring tokens by
 //                         interleaving their nibbles before the conversion
-//   product (warp 12)     S = Q K^T and O += P V on tcgen05 (fp16, fp32 sums): S, P
+//   product (warp 16)     S = Q K^T and O += P V on tcgen05 (fp16, fp32 sums): S, P
 //                         and O stay in TMEM, P over S's columns
 //   softmax (warps 0-7)   two groups of four warps, a thread a row: the running
 //                         maximum (it moves only when a score passes it by 2^6, so O
@@ -33,7 +33,9 @@ namespace kda {
 namespace kv4 {
 
 constexpr int TT = 128;                // tokens of a tile
-constexpr int TILE_THREADS = 13 * 32;
+constexpr int TILE_THREADS = 20 * 32;   // softmax 0-7, unpack 8-15, product 16 (17-19 are idle: registers are dealt by four warps)
+constexpr int REGS_SOFTMAX = 160, REGS_UNPACK = 64, REGS_PRODUCT = 32;   // 640 threads are launched with 96
+static_assert(256 * REGS_SOFTMAX + 256 * REGS_UNPACK + 128 * REGS_PRODUCT <= TILE_THREADS * 96, "register split");
 constexpr int SMS = 152;
 constexpr int SPLIT_PARTS = 126;       // a cut aims at this many parts: at most twice as many arise
 
@@ -72,11 +74,11 @@ __device__ __forceinline__ void mma_done(uint32_t bar) {          // arrives whe
 }
 __device__ __forceinline__ void tmem_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+// 32 columns of this thread's lane; the registers hold them after tmem_ld_wait().
+__device__ __forceinline__ void tmem_ld32_async(uint32_t at, uint32_t *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
         "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
@@ -84,16 +86,35 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
         : "r"(at)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(at),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+// The wait names the registers, so that nothing reads them before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+    tmem_ld32_async(at, r);
+    tmem_ld_wait(r);
+}
+// (x0, x1) * f + c, on pairs of fp32
+__device__ __forceinline__ void fma_pair(uint32_t &x0, uint32_t &x1, uint64_t f, uint64_t c) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(x0), "r"(x1));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(f), "l"(c));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(x0), "=r"(x1) : "l"(v));
+}
+__device__ __forceinline__ uint64_t pair_of_floats(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile(
@@ -102,6 +123,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) 
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// One lane of the warp, chosen so that the compiler knows it is one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one;
 }
 __device__ __forceinline__ void group_sync(uint32_t id, uint32_t count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
@@ -223,18 +267,18 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
     float2 *const ml_s = reinterpret_cast<float2 *>(meta);                  // [2][128] maximum and sum (QT = 1)
     uint8_t *const nan_s = meta + 2048;                                     // [ST][8 blocks][16 groups of 8 tokens]
     uint8_t *const miss_s = nan_s + 3 * 128;                                // [ST][16] groups whose page is missing
-    uint32_t *const nan_any = reinterpret_cast<uint32_t *>(miss_s + 3 * 16);// [ST] a byte for each unpacking warp
-    volatile int *const dead = reinterpret_cast<volatile int *>(nan_any + 4);
-    volatile uint32_t *const misc = nan_any + 5;                            // TMEM base, a flag
-    uint8_t *const nan_row = meta + 2048 + 384 + 48 + 32;                   // [2][128] blocks with a NaN value (QT = 1)
+    uint32_t *const nan_any = reinterpret_cast<uint32_t *>(miss_s + 3 * 16);// [ST][2] a byte for each unpacking warp
+    volatile int *const dead = reinterpret_cast<volatile int *>(nan_any + 6);
+    volatile uint32_t *const misc = nan_any + 7;                            // TMEM base, a flag
+    uint8_t *const nan_row = meta + 2048 + 384 + 48 + 48;                   // [2][128] blocks with a NaN value (QT = 1)
     const uint32_t bar = shared_addr(nan_row + 256);
     const uint32_t Q_FULL = bar, S_FULL = bar + 16, P_FULL = bar + 32, PV_DONE = bar + 48, FINISHED = bar + 64, KV_FULL = bar + 72,
                    KV_FREE = KV_FULL + 8 * ST;
-    static_assert(2048 + 384 + 48 + 32 + 256 + 72 + 16 * 3 <= 3072, "the small arrays");
+    static_assert(2048 + 384 + 48 + 48 + 256 + 72 + 16 * 3 <= 3072, "the small arrays");
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int G = a.Hq / a.Hkv;
 
-    if (w == 12) {
+    if (w == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(shared_addr(const_cast<uint32_t *>(misc))) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
@@ -246,7 +290,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             barrier_init(PV_DONE + 8 * g, 1);
         }
         for (int s = 0; s < ST; ++s) {
-            barrier_init(KV_FULL + 8 * s, 4);
+            barrier_init(KV_FULL + 8 * s, 8);
             barrier_init(KV_FREE + 8 * s, 1);
         }
         barrier_init(FINISHED, 1);
@@ -278,6 +322,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
     Part p;
 
     if (w < 8) {
+        take_registers<REGS_SOFTMAX>();
         // ================================ softmax ======================================================
         const int g = w >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
@@ -353,21 +398,29 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     v &= lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
                     return v & ~gone[c];
                 };
-                float top = -INFINITY;
-                uint32_t x[32];
+                uint32_t x[TT];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(s_col + 32 * c, x);
-                    if (some) {
+                for (int c = 0; c < 4; ++c) tmem_ld32_async(s_col + 32 * c, x + 32 * c);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_wait(x + 32 * c);
+                if (some) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
                         const uint32_t v = visible(c);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (v >> e & 1) top = fmaxf(top, __uint_as_float(x[e]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+                            if (!(v >> e & 1)) x[32 * c + e] = 0xff800000u;
                     }
                 }
+                float tops[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tops[c] = __uint_as_float(x[c]);
+#pragma unroll
+                    for (int e = c + 4; e < TT; e += 8)
+                        tops[c] = max3(tops[c], __uint_as_float(x[e]), e + 4 < TT ? __uint_as_float(x[e + 4]) : -INFINITY);
+                }
+                float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
                 top = top == -INFINITY ? top : top * factor;
                 if (__any_sync(~0u, top - m > MOVE)) {
                     const float to = fmaxf(m, top - HEADROOM), keep = exp2_fast(m - to);
@@ -377,40 +430,54 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         wait_or_dead(PV_DONE + 8 * g, (done - 1) & 1, dead);
                         tmem_after_sync();
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            tmem_ld32(o_col + 32 * c, x);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t y[16];
+                            tmem_ld16(o_col + 16 * c, y);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
-                            tmem_st32(o_col + 32 * c, x);
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
+                            tmem_st16(o_col + 16 * c, y);
                         }
                     }
                 }
+                const uint64_t ff = pair_of_floats(factor, factor), mm = pair_of_floats(-m, -m);
+                uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(s_col + 32 * c, x);
                     uint32_t pk[16];
                     const uint32_t v = some ? visible(c) : ~0u;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float p0 = exp2_fast(fmaf(__uint_as_float(x[e]), factor, -m));
-                        float p1 = exp2_fast(fmaf(__uint_as_float(x[e + 1]), factor, -m));
-                        if (some) {
-                            p0 = v >> e & 1 ? p0 : 0.f;
-                            p1 = v >> (e + 1) & 1 ? p1 : 0.f;
-                        }
-                        l += p0 + p1;
-                        pk[e / 2] = half_pair(p0, p1);
+                        uint32_t &x0 = x[32 * c + e], &x1 = x[32 * c + e + 1];
+                        fma_pair(x0, x1, ff, mm);
+                        const float p0 = exp2_fast(__uint_as_float(x0)), p1 = exp2_fast(__uint_as_float(x1));
+                        x0 = __float_as_uint(p0), x1 = __float_as_uint(p1);
+                    }
+                    if (some) {            // a masked score times a scale of 0 is a NaN: the mask has the last word
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(v >> e & 1)) x[32 * c + e] = 0;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const uint64_t u0 = pair_of_floats(__uint_as_float(x[32 * c + e]), __uint_as_float(x[32 * c + e + 1]));
+                        const uint64_t u1 = pair_of_floats(__uint_as_float(x[32 * c + e + 2]), __uint_as_float(x[32 * c + e + 3]));
+                        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(u0));
+                        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(u1));
+                        pk[e / 2] = half_pair(__uint_as_float(x[32 * c + e]), __uint_as_float(x[32 * c + e + 1]));
+                        pk[e / 2 + 1] = half_pair(__uint_as_float(x[32 * c + e + 2]), __uint_as_float(x[32 * c + e + 3]));
                     }
                     tmem_st16(s_col + 16 * c, pk);
                 }
-                if (nan_any[stage]) {                          // NaN values: they reach the rows that see them
+                l += (__uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32))) +
+                     (__uint_as_float((uint32_t)sum1) + __uint_as_float((uint32_t)(sum1 >> 32)));
+                if (nan_any[2 * stage] | nan_any[2 * stage + 1]) {   // NaN values: they reach the rows that see them
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t v = visible(c);
 #pragma unroll 1
                         for (int blk = 0; blk < D / 16; ++blk) {
-                            const int unpacker = (blk >> 2) * 2 + (c >> 1);
-                            if (!(nan_any[stage] >> (8 * unpacker) & 255)) continue;
+                            const int unpacker = (blk >> 1) * 2 + (c >> 1);
+                            if (!reinterpret_cast<const uint8_t *>(nan_any + 2 * stage)[unpacker]) continue;
                             if (v & *reinterpret_cast<const uint32_t *>(nan_s + stage * 128 + blk * 16 + 4 * c)) nan_blocks |= 1u << blk;
                         }
                     }
@@ -535,18 +602,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 group_sync(1, 256);    // both have read O, the maxima and sums
             }
         }
-    } else if (w < 12) {
+    } else if (w < 16) {
+        give_registers<REGS_UNPACK>();
         // ================================ unpack =======================================================
         const int uw = w - 8, ut = tid - 256;
-        const int box = uw & 1, grp = lane & 7, blk = (uw >> 1) * 4 + (lane >> 3);
+        const int k_tok = ut & 127, k_half = ut >> 7;          // K: half the channels of one token
+        // V: 8 channels (one word, of scale block blk) of 8 tokens; the lanes' 8 token groups fill one 128-byte row
+        const int box = uw & 1, grp = lane & 7, word = (uw >> 1) * 4 + (lane >> 3), blk = word >> 1;
         const bool has_v = blk < D / 16;
-        const int v_tok = box * 64 + grp * 8;                  // of the tile: this thread's 8 tokens of V
-        struct Raw {
-            uint4 k[D / 32];
-            uint2 v[8];
-            uint2 ks, vs;
-            uint32_t missing;
-        };
+        const int v_tok = box * 64 + grp * 8;
         struct Spot {                                          // a tile, and the pages this thread reads of it
             int pi, j, page_k, page_v, pos0, h, len;
             bool valid;
@@ -563,57 +627,64 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             s.h = p.h;
             s.len = p.len;
             const int32_t *const pages = a.page_table + (size_t)p.b * a.max_pages;
-            s.page_k = s.pos0 + ut < p.len ? pages[(s.pos0 + ut) >> a.page_shift] : -2;
+            s.page_k = s.pos0 + k_tok < p.len ? pages[(s.pos0 + k_tok) >> a.page_shift] : -2;
             s.page_v = s.pos0 + v_tok < p.len ? pages[(s.pos0 + v_tok) >> a.page_shift] : -2;
         };
         auto tile_of = [&](int page, int h, int pos) {
             const int in_page = pos & ((1 << a.page_shift) - 1);
             return a.pool + ((((size_t)page * a.Hkv + h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
         };
-        auto load = [&](const Spot &s, Raw &r) {
+        constexpr int KW = D / 16;                             // words of half a K row
+        uint32_t kr[KW], kscale, vr[8], missing;
+        uint2 vscale;
+        auto load_k = [&](const Spot &s) {
             if (s.page_k >= 0 && s.page_k < a.num_pages) {
-                const int pos = s.pos0 + ut, tok = pos & 15;
+                const int pos = s.pos0 + k_tok, tok = pos & 15;
                 const uint8_t *t = tile_of(s.page_k, s.h, pos);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) r.k[i] = __ldg(reinterpret_cast<const uint4 *>(t + tok * (D / 2)) + i);
-                if constexpr (D == 128) r.ks = __ldg(reinterpret_cast<const uint2 *>(t + L::KS + tok * 8));
-                else r.ks = make_uint2(__ldg(reinterpret_cast<const uint32_t *>(t + L::KS + tok * 4)), 0);
+                for (int i = 0; i < KW / 4; ++i) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(t + tok * (D / 2) + k_half * (D / 4)) + i);
+                    kr[4 * i] = x.x, kr[4 * i + 1] = x.y, kr[4 * i + 2] = x.z, kr[4 * i + 3] = x.w;
+                }
+                if constexpr (D == 128) kscale = __ldg(reinterpret_cast<const uint32_t *>(t + L::KS + tok * 8 + k_half * 4));
+                else kscale = __ldg(reinterpret_cast<const uint16_t *>(t + L::KS + tok * 4 + k_half * 2));
             } else {
                 if (s.page_k != -2) report(a.err, DEVERR_PAGE_RANGE);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) r.k[i] = make_uint4(0, 0, 0, 0);
-                r.ks = make_uint2(0, 0);
+                for (int i = 0; i < KW; ++i) kr[i] = 0;
+                kscale = 0;
             }
-            r.missing = s.page_v != -2 && (s.page_v < 0 || s.page_v >= a.num_pages) ? 255u : 0u;
+        };
+        auto load_v = [&](const Spot &s) {
+            missing = s.page_v != -2 && (s.page_v < 0 || s.page_v >= a.num_pages) ? 255u : 0u;
             if (has_v && s.page_v >= 0 && s.page_v < a.num_pages) {
                 const int pos = s.pos0 + v_tok, tok = pos & 15;
                 const uint8_t *t = tile_of(s.page_v, s.h, pos);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) r.v[i] = __ldg(reinterpret_cast<const uint2 *>(t + L::VC + (tok + i) * (D / 2) + blk * 8));
-                r.vs = __ldg(reinterpret_cast<const uint2 *>(t + L::VS + blk * KV_TILE + tok));
-                // scales of tokens past the end: 0
-                const int live = s.len - pos;
-                if (live < 4) r.vs.x &= (1u << (8 * live)) - 1;
-                if (live < 8) r.vs.y &= live <= 4 ? 0u : (1u << (8 * (live - 4))) - 1;
+                for (int i = 0; i < 8; ++i) vr[i] = __ldg(reinterpret_cast<const uint32_t *>(t + L::VC + (tok + i) * (D / 2) + word * 4));
+                vscale = __ldg(reinterpret_cast<const uint2 *>(t + L::VS + blk * KV_TILE + tok));
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) r.v[i] = make_uint2(0, 0);
-                r.vs = make_uint2(0, 0);
+                for (int i = 0; i < 8; ++i) vr[i] = 0;
+                vscale = make_uint2(0, 0);
             }
         };
-        auto unpack = [&](const Raw &r, uint8_t *k_tile, uint8_t *v_tile, int stage) {
+        auto unpack_k = [&](uint8_t *tile) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {                  // 8 channels: one word
-                const uint4 &four = r.k[i / 4];
-                const uint32_t word = (i & 3) == 0 ? four.x : (i & 3) == 1 ? four.y : (i & 3) == 2 ? four.z : four.w;
-                const uint32_t two = e4m3x2_to_f16x2((i < 8 ? r.ks.x : r.ks.y) >> (i & 4 ? 16 : 0) & 0xffffu);
+            for (int i = 0; i < KW; ++i) {                     // 8 channels: one word, half a scale block
+                const uint32_t two = e4m3x2_to_f16x2(kscale >> (i & 4 ? 16 : 0) & 0xffffu);
                 const uint32_t sc = __byte_perm(two, 0, i & 2 ? 0x3232 : 0x1010);
                 uint32_t f[4];
-                e2m1x8_to_f16x2(word, f);
-                *reinterpret_cast<uint4 *>(k_tile + chunk_at(ut, i, TT)) =
+                e2m1x8_to_f16x2(kr[i], f);
+                *reinterpret_cast<uint4 *>(tile + chunk_at(k_tok, k_half * KW + i, TT)) =
                     make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
             }
-            uint2 vs = r.vs;
+        };
+        auto unpack_v = [&](uint8_t *tile, int stage, int live) {
+            uint2 vs = vscale;
+            // scales of tokens past the end: 0
+            if (live < 4) vs.x &= live <= 0 ? 0u : (1u << (8 * live)) - 1;
+            if (live < 8) vs.y &= live <= 4 ? 0u : (1u << (8 * (live - 4))) - 1;
             const uint32_t n0 = ((vs.x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u, n1 = ((vs.y & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
             const bool any = __any_sync(~0u, (n0 | n1) != 0);
             if (any) {                                         // NaN scales: 0 here, noted for the softmax
@@ -623,29 +694,24 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 const uint32_t b0 = (n0 >> 7) * 0x01020408u >> 24 & 15u, b1 = (n1 >> 7) * 0x01020408u >> 24 & 15u;
                 if (has_v) nan_s[stage * 128 + blk * 16 + box * 8 + grp] = (uint8_t)(b0 | b1 << 4);
             }
-            if (lane == 0) reinterpret_cast<uint8_t *>(nan_any + stage)[uw] = any;
-            if (blk == 0) miss_s[stage * 16 + box * 8 + grp] = (uint8_t)r.missing;
+            if (lane == 0) reinterpret_cast<uint8_t *>(nan_any + 2 * stage)[uw] = any;
+            if (word == 0) miss_s[stage * 16 + box * 8 + grp] = (uint8_t)missing;
             if (has_v) {
                 const uint32_t sc[4] = {e4m3x2_to_f16x2(vs.x & 0xffffu), e4m3x2_to_f16x2(vs.x >> 16), e4m3x2_to_f16x2(vs.y & 0xffffu),
                                         e4m3x2_to_f16x2(vs.y >> 16)};
+                constexpr uint32_t LOW = 0x0f0f0f0fu;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {                  // 8 channels of 8 tokens
-                    constexpr uint32_t LOW = 0x0f0f0f0fu;
-                    uint32_t even[4][4], odd[4][4];            // [pair of tokens][channel pair]
+                for (int odd = 0; odd < 2; ++odd) {            // channels 0, 2, 4, 6 of the word, then 1, 3, 5, 7
+                    uint32_t f[4][4];                          // [pair of tokens][channel]
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const uint32_t x = q ? r.v[2 * t].y : r.v[2 * t].x, y = q ? r.v[2 * t + 1].y : r.v[2 * t + 1].x;
-                        e2m1x8_to_f16x2((x & LOW) | ((y << 4) & ~LOW), even[t]);
-                        e2m1x8_to_f16x2(((x >> 4) & LOW) | (y & ~LOW), odd[t]);
+                        const uint32_t x = vr[2 * t], y = vr[2 * t + 1];
+                        e2m1x8_to_f16x2(odd ? ((x >> 4) & LOW) | (y & ~LOW) : (x & LOW) | ((y << 4) & ~LOW), f[t]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ch = blk * 16 + q * 8 + 2 * i;
-                        *reinterpret_cast<uint4 *>(v_tile + chunk_at(ch, box * 8 + grp, D)) =
-                            make_uint4(hmul2(even[0][i], sc[0]), hmul2(even[1][i], sc[1]), hmul2(even[2][i], sc[2]), hmul2(even[3][i], sc[3]));
-                        *reinterpret_cast<uint4 *>(v_tile + chunk_at(ch + 1, box * 8 + grp, D)) =
-                            make_uint4(hmul2(odd[0][i], sc[0]), hmul2(odd[1][i], sc[1]), hmul2(odd[2][i], sc[2]), hmul2(odd[3][i], sc[3]));
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(tile + chunk_at(word * 8 + 2 * i + odd, box * 8 + grp, D)) =
+                            make_uint4(hmul2(f[0][i], sc[0]), hmul2(f[1][i], sc[1]), hmul2(f[2][i], sc[2]), hmul2(f[3][i], sc[3]));
                 }
             }
         };
@@ -653,62 +719,72 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
         spot.pi = blockIdx.x;
         spot.j = -1;
         spot.valid = walk.find(a, spot.pi, p);
-        Raw now, then;
         next(spot);
         bool have = spot.valid;
+        int live = 0;                                          // of this thread's V tokens, those before the end
         if (have) {
-            load(spot, now);
+            load_k(spot);
+            load_v(spot);
+            live = spot.len - (spot.pos0 + v_tok);
             next(spot);
         }
-        for (uint32_t n = 0; have; ++n) {
-            const bool more = spot.valid;
-            if (more) {
-                load(spot, then);
+        // the next tile's codes are asked for as soon as this one's registers are free
+        uint32_t stage = 0, round = 0;
+        while (have) {
+            have = spot.valid;
+            if (round > 0) wait_or_dead(KV_FREE + 8 * stage, (round - 1) & 1, dead);
+            uint8_t *const k_tile = smem + S::RING + stage * S::STAGE;
+            unpack_k(k_tile);
+            if (have) load_k(spot);
+            unpack_v(k_tile + S::KBYTES, stage, live);
+            if (have) {
+                load_v(spot);
+                live = spot.len - (spot.pos0 + v_tok);
                 next(spot);
             }
-            const int stage = n % ST;
-            if (n >= ST) wait_or_dead(KV_FREE + 8 * stage, (n / ST - 1) & 1, dead);
-            uint8_t *const k_tile = smem + S::RING + stage * S::STAGE;
-            unpack(now, k_tile, k_tile + S::KBYTES, stage);
             fence_async_shared();
             __syncwarp();
             if (lane == 0) barrier_arrive(KV_FULL + 8 * stage);
-            now = then;
-            have = more;
+            if (++stage == ST) stage = 0, ++round;
         }
     } else {
+        give_registers<REGS_PRODUCT>();
+        if (w == 16) {
         // ================================ products =====================================================
         constexpr uint32_t ID_S = idesc_f16(128, TT), ID_O = idesc_f16(128, D);
         const uint32_t base = shared_addr(smem);
         uint32_t done[2] = {0, 0}, kv = 0, parts = 0;
         for (int pi = blockIdx.x; walk.find(a, pi, p); pi += gridDim.x) {
-            if (lane == 0) {
+            {
                 auto kv_wait = [&](int j) { wait_or_dead(KV_FULL + 8 * ((kv + j) % ST), (kv + j) / ST & 1, dead); };
                 auto scores = [&](int g, int j) {
                     const uint64_t dq = tile_desc(base + (QT == 2 ? g : 0) * S::QBYTES), dk = tile_desc(base + S::RING + (kv + j) % ST * S::STAGE);
                     tmem_after_sync();
-                    if (!*dead) {
+                    if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < D / 16; ++s) {
                             const uint64_t at = (uint64_t)(((s >> 2) * 16384 + (s & 3) * 32) >> 4);
                             mma_f16_ss(tmem + g * 128, dq + at, dk + at, ID_S, s > 0);
                         }
+                        mma_done(S_FULL + 8 * g);
                     }
-                    mma_done(S_FULL + 8 * g);
+                    __syncwarp();
                 };
-                auto values = [&](int g, int j, bool first) {
+                auto values = [&](int g, int j, bool first, bool frees) {
                     wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
                     ++done[g];
                     const uint64_t dv = tile_desc(base + S::RING + (kv + j) % ST * S::STAGE + S::KBYTES);
                     tmem_after_sync();
-                    if (!*dead) {
+                    if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < TT / 16; ++s) {
                             const uint64_t at = (uint64_t)(((s >> 2) * D * 128 + (s & 3) * 32) >> 4);
                             mma_f16_ts(tmem + S::O_COL + g * D, tmem + g * 128 + 8 * s, dv + at, ID_O, s > 0 || !first);
                         }
+                        mma_done(PV_DONE + 8 * g);
+                        if (frees) mma_done(KV_FREE + 8 * ((kv + j) % ST));
                     }
-                    mma_done(PV_DONE + 8 * g);
+                    __syncwarp();
                 };
                 const int tiles = p.tiles;
                 wait_or_dead(Q_FULL, parts & 1, dead);
@@ -720,8 +796,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     for (int j = 0; j < tiles; ++j) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            values(g, j, j == 0);
-                            if (g == 1) mma_done(KV_FREE + 8 * ((kv + j) % ST));
+                            values(g, j, j == 0, g == 1);
                             if (j + 1 < tiles) {
                                 if (g == 0) kv_wait(j + 1);
                                 scores(g, j + 1);
@@ -734,8 +809,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         scores(j, j);
                     }
                     for (int j = 0; j < tiles; ++j) {
-                        values(j & 1, j, j < 2);
-                        mma_done(KV_FREE + 8 * ((kv + j) % ST));
+                        values(j & 1, j, j < 2, true);
                         if (j + 2 < tiles) {
                             kv_wait(j + 2);
                             scores(j & 1, j + 2);
@@ -747,17 +821,18 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             kv += p.tiles;
             ++parts;
         }
-        if (lane == 0) {
+        if (elect_one()) {
             mma_done(FINISHED);
             barrier_wait(FINISHED, 0);
         }
         __syncwarp();
+        }
     }
 
     tmem_before_sync();
     __syncthreads();
     if (tid == 0 && *dead) report(a.err, DEVERR_TIMEOUT);
-    if (w == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (w == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 template <int D, int QT, typename T>

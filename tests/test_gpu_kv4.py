@@ -147,6 +147,27 @@ def test_attention(ws, shape, window, dtype):
     check(o, lse, expected(q[:, :Hq], news, lens, pool, table, P, window, D ** -0.5), dtype)
 
 
+@pytest.mark.parametrize("D,P,window,dtype", [(128, 64, 0, BF), (64, 16, 100, FP)])
+def test_large_prompts(ws, D, P, window, dtype):
+    """Enough rows that a part of the work holds 256 of them; some of the rows against the oracle."""
+    news, lens, Hq, Hkv = [700, 1, 599], [900, 77, 599], 64, 8
+    pool, table = make_cache(lens, Hkv, D, P, 17)
+    ref.store(pool, table[2], 300, np.full((Hkv, D), np.nan), np.full((Hkv, D), np.nan), P)   # rows 300.. of request 2
+    q = packed_q(news, Hq, D, dtype, 18, 2.0)
+    o, lse, err = attend(pool, table, news, lens, q, Hq, ws, window)
+    assert err == 0
+    o2, lse2, _ = attend(pool, table, news, lens, q, Hq, ws, window)
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16))
+    at = 0
+    for b, n in enumerate(news):
+        for i in sorted({0, 1, n // 3, n // 2, 299, 300, 399, 400, n - 2, n - 1} & set(range(n))):
+            seen = lens[b] - n + i + 1
+            t = at + i
+            want = expected(q[t:t + 1], [1], [seen], pool, table[b:b + 1], P, window, D ** -0.5)
+            check(o[t:t + 1], lse[t:t + 1], want, dtype)
+        at += n
+
+
 @pytest.mark.parametrize("news", [[1, 1, 1], [6, 6, 2], [90, 20, 64]])
 def test_scales_of_every_size(ws, news):
     """Tensor scales, large scores (one token takes all), a negative scale, queries near the type's ends."""
