@@ -2,14 +2,17 @@
 //
 // One CTA an SM works on 128 query rows of a kv head at a time (QT = 1) or 256
 // (QT = 2), a row being one (token, query head of the group), against tiles of
-// 128 cached tokens.  Three kinds of warps hand tiles on through mbarriers:
+// 128 cached tokens.  Four kinds of warps hand work on through mbarriers:
 //
-//   unpack  (warps 8-15)  a tile's codes, read from the pages one tile ahead into
-//                         registers, become fp16 K [token][channel] and V^T
-//                         [channel][token] in shared memory (both K-major, 128-byte
-//                         swizzle): one conversion and one product with the scale
-//                         for two values, exact; V pairs neighbouring tokens by
-//                         interleaving their nibbles before the conversion
+//   load    (warp 17)     claims the next part of the work and describes it to the
+//                         others; looks up pages and asks for their codes by bulk
+//                         copies, 64 tokens to a stage of a ring
+//   unpack  (warps 8-15)  codes to fp16 K [token][channel] and V^T [channel][token],
+//                         both K-major with the 128-byte swizzle: one conversion and
+//                         one product with the scale for two values, exact.  V is
+//                         turned by transposing matrix stores; a lane takes its
+//                         bytes in an order of its own, so that the eight rows of
+//                         each stored matrix lie in different banks
 //   product (warp 16)     S = Q K^T and O += P V on tcgen05 (fp16, fp32 sums): S, P
 //                         and O stay in TMEM, P over S's columns
 //   softmax (warps 0-7)   two groups of four warps, a thread a row: the running
@@ -22,9 +25,9 @@
 // tile, joined at the end.  Queries are scaled by powers of two and weights held
 // 2^9 above the maximum as in the kernel for few rows.
 //
-// Parts of the work are dealt to the CTAs in turn.  If there are fewer (request,
-// rows, head) than SMs, each is cut along the tokens; the last part to arrive
-// joins the results in order.
+// If there are fewer (request, rows, head) than SMs, each is cut along the tokens;
+// the last part to arrive joins the results in order, so they do not depend on
+// which CTA claimed what.
 #pragma once
 
 #include "kda_kv4_decode.cuh"
@@ -33,23 +36,46 @@ namespace kda {
 namespace kv4 {
 
 constexpr int TT = 128;                // tokens of a tile
-constexpr int TILE_THREADS = 20 * 32;   // softmax 0-7, unpack 8-15, product 16 (17-19 are idle: registers are dealt by four warps)
-constexpr int REGS_SOFTMAX = 160, REGS_UNPACK = 64, REGS_PRODUCT = 32;   // 640 threads are launched with 96
-static_assert(256 * REGS_SOFTMAX + 256 * REGS_UNPACK + 128 * REGS_PRODUCT <= TILE_THREADS * 96, "register split");
+constexpr int BOX = 64;                // tokens of a stage of codes: half a tile
+constexpr int TILE_THREADS = 20 * 32;  // warps 18 and 19 are idle: registers are dealt by four warps
+constexpr int REGS_SOFTMAX = 168, REGS_UNPACK = 48, REGS_OTHER = 48;   // 640 threads are launched with 96
+static_assert(256 * REGS_SOFTMAX + 256 * REGS_UNPACK + 128 * REGS_OTHER <= TILE_THREADS * 96, "register split");
 constexpr int SMS = 152;
 constexpr int SPLIT_PARTS = 126;       // a cut aims at this many parts: at most twice as many arise
+constexpr int NEXT_PART = 2 * SPLIT_PARTS + 2, CTAS_DONE = NEXT_PART + 1;   // counters behind the joins'
+static_assert(CTAS_DONE < MAX_CTAS, "counters");
+
+// A piece of work: rows of one kv head of one request against tiles of its cache.
+struct Part {
+    int b, h, row0, rows, q0, n, len;
+    int tile0, tiles;                  // of TT tokens; tiles may be 0, and is -1 after the last part
+    int pieces, slot0, piece;          // how many parts share the rows; their first slot
+};
 
 template <int D, int QT>
 struct TileShape {
-    static constexpr int STAGES = QT == 1 ? 3 : 2;
+    static constexpr int RAW = QT == 1 ? 6 : 3;          // stages of BOX tokens' codes
+    static constexpr int RAW_BYTES = BOX / KV_TILE * KvTile<D>::BYTES;
     static constexpr int QBYTES = 128 * D * 2;
-    static constexpr int KBYTES = TT * D * 2;
-    static constexpr int STAGE = 2 * KBYTES;
-    static constexpr int RING = QT * QBYTES;
-    static constexpr int META = RING + STAGES * STAGE;   // barriers and small arrays
-    static constexpr int SMEM = META + 3072;
+    static constexpr int KBYTES = TT * D * 2;            // of a tile of K, and of V^T: two stages each
+    static constexpr int K_AT = QT * QBYTES, V_AT = K_AT + 2 * KBYTES, RAW_AT = V_AT + 2 * KBYTES;
+    static constexpr int META = RAW_AT + RAW * RAW_BYTES;
     static constexpr int PARTIAL = 128 * (D + 2);        // floats
     static constexpr uint32_t O_COL = 256;
+};
+
+// The small shared arrays behind the tiles.
+struct alignas(16) TileMeta {
+    float2 ml[2][128];                 // maximum and sum of the groups' rows (QT = 1)
+    uint8_t nan_row[2][128];           // scale blocks in which a row met a NaN value (QT = 1)
+    uint8_t nan_value[4][16][8];       // by tile & 3, group of 8 tokens, block: tokens whose V scale is NaN
+    uint8_t nan_group[4][16];          // whether that group has any (else its bytes above are old)
+    uint8_t missing[4][16];            // 255: the group's page is out of range
+    Part parts[4];
+    int raw_live[8], raw_bad[8];       // by stage of codes: tokens before the end; a bit a run of 16 out of range
+    uint32_t tmem;
+    int last, dead;
+    uint64_t bars[25 + 2 * 6];
 };
 
 __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {   // K-major, 128-byte swizzle, 8-row groups 1 KB apart
@@ -151,22 +177,24 @@ __device__ __forceinline__ void group_sync(uint32_t id, uint32_t count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// A bounded wait; once one has given up (*dead), none waits any longer and the CTA runs out on what it has.
+// A warp's bounded wait; once one has given up (*dead), none waits any longer and the CTA runs out on what it has.
 __device__ __forceinline__ void wait_or_dead(uint32_t bar, uint32_t parity, volatile int *dead) {
-    if (barrier_test(bar, parity)) return;
-    const uint64_t t0 = global_timer();
-    while (!*dead) {
-        if (barrier_test(bar, parity)) return;
-        if (global_timer() - t0 > ASYNC_WAIT_NS) *dead = 1;
+    if (!barrier_test(bar, parity)) {
+        const uint64_t t0 = global_timer();
+        while (!*dead && !barrier_test(bar, parity))
+            if (global_timer() - t0 > ASYNC_WAIT_NS) *dead = 1;
     }
+    __syncwarp();
 }
-
-// A piece of work: rows of one kv head of one request against tiles of its cache.
-struct Part {
-    int b, h, row0, rows, q0, n, len;
-    int tile0, tiles;                  // of TT tokens; tiles may be 0
-    int pieces, slot0, piece;          // how many parts share the rows; their first slot
-};
+// Whether any thread of the named barrier's says so.
+__device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool mine) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)mine), "r"(id), "r"(count)
+                 : "memory");
+    return r;
+}
 
 // Finds parts by number, in ascending order, 32 requests at a time; every lane of a warp calls it.
 template <int QT>
@@ -256,70 +284,57 @@ __device__ __forceinline__ int2 sight(const KvAttentionArgs &a, const Part &p, i
     return make_int2(a.window > 0 ? max(0, last + 1 - a.window) : 0, last);
 }
 
+// Four 8 x 8 matrices of fp16, each stored transposed; lane 8 m + r gives the address of row r of matrix m.
+__device__ __forceinline__ void store_transposed(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 template <int D, int QT, typename T>
 __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const KvAttentionArgs a) {
     using L = KvTile<D>;
     using S = TileShape<D, QT>;
-    constexpr int ST = S::STAGES;
     extern __shared__ __align__(1024) uint8_t tile_smem[];
     uint8_t *const smem = tile_smem;
-    uint8_t *const meta = smem + S::META;
-    float2 *const ml_s = reinterpret_cast<float2 *>(meta);                  // [2][128] maximum and sum (QT = 1)
-    uint8_t *const nan_s = meta + 2048;                                     // [ST][8 blocks][16 groups of 8 tokens]
-    uint8_t *const miss_s = nan_s + 3 * 128;                                // [ST][16] groups whose page is missing
-    uint32_t *const nan_any = reinterpret_cast<uint32_t *>(miss_s + 3 * 16);// [ST][2] a byte for each unpacking warp
-    volatile int *const dead = reinterpret_cast<volatile int *>(nan_any + 6);
-    volatile uint32_t *const misc = nan_any + 7;                            // TMEM base, a flag
-    uint8_t *const nan_row = meta + 2048 + 384 + 48 + 48;                   // [2][128] blocks with a NaN value (QT = 1)
-    const uint32_t bar = shared_addr(nan_row + 256);
-    const uint32_t Q_FULL = bar, S_FULL = bar + 16, P_FULL = bar + 32, PV_DONE = bar + 48, FINISHED = bar + 64, KV_FULL = bar + 72,
-                   KV_FREE = KV_FULL + 8 * ST;
-    static_assert(2048 + 384 + 48 + 48 + 256 + 72 + 16 * 3 <= 3072, "the small arrays");
+    TileMeta &meta = *reinterpret_cast<TileMeta *>(smem + S::META);
+    volatile int *const dead = &meta.dead;
+    const uint32_t bar = shared_addr(meta.bars);
+    const uint32_t PART_FULL = bar, PART_FREE = bar + 32, Q_FULL = bar + 64, S_FULL = bar + 80, P_FULL = bar + 96, PV_DONE = bar + 112,
+                   K_FULL = bar + 128, K_FREE = bar + 144, V_FULL = bar + 160, V_FREE = bar + 176, FINISHED = bar + 192,
+                   RAW_FULL = bar + 200, RAW_FREE = RAW_FULL + 8 * S::RAW;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int G = a.Hq / a.Hkv;
 
     if (w == 16) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(shared_addr(const_cast<uint32_t *>(misc))) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(shared_addr(&meta.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int g = 0; g < 2; ++g) {
-            barrier_init(Q_FULL + 8 * g, 4);
-            barrier_init(S_FULL + 8 * g, 1);
-            barrier_init(P_FULL + 8 * g, 4);
-            barrier_init(PV_DONE + 8 * g, 1);
+        for (int i = 0; i < 4; ++i) {
+            barrier_init(PART_FULL + 8 * i, 1);
+            barrier_init(PART_FREE + 8 * i, 9);        // the softmax and product warps
         }
-        for (int s = 0; s < ST; ++s) {
-            barrier_init(KV_FULL + 8 * s, 8);
-            barrier_init(KV_FREE + 8 * s, 1);
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(Q_FULL + 8 * i, 4);
+            barrier_init(S_FULL + 8 * i, 1);
+            barrier_init(P_FULL + 8 * i, 4);
+            barrier_init(PV_DONE + 8 * i, 1);
+            barrier_init(K_FULL + 8 * i, 8);
+            barrier_init(K_FREE + 8 * i, 1);
+            barrier_init(V_FULL + 8 * i, 8);
+            barrier_init(V_FREE + 8 * i, 1);
+        }
+        for (int i = 0; i < S::RAW; ++i) {
+            barrier_init(RAW_FULL + 8 * i, 1);
+            barrier_init(RAW_FREE + 8 * i, 8);
         }
         barrier_init(FINISHED, 1);
-        *dead = 0;
+        meta.dead = 0;
     }
     tmem_before_sync();
     __syncthreads();
     tmem_after_sync();
-    const uint32_t tmem = misc[0];
-
-    // ---- how the work is cut: only where there are fewer parts than SMs (QT = 1) -----------------------
-    int cut = 0;
-    {
-        long long units = 0, tiles = 0;
-        for (int b = lane; b < a.B; b += 32) {
-            const Request q = request_of(a, b, 128 * QT, blockIdx.x == 0 && w == 0);
-            units += (long long)q.row_blocks * a.Hkv;
-            if (q.row_blocks) tiles += (long long)q.row_blocks * a.Hkv * Walker<QT>::most_tiles(a, q);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            units += __shfl_xor_sync(~0u, units, o);
-            tiles += __shfl_xor_sync(~0u, tiles, o);
-        }
-        if (QT == 1 && units < SMS) cut = (int)max((tiles + SPLIT_PARTS - 1) / SPLIT_PARTS, 2LL);
-    }
-    Walker<QT> walk;
-    walk.start(a, cut);
-    Part p;
+    const uint32_t tmem = meta.tmem;
 
     if (w < 8) {
         take_registers<REGS_SOFTMAX>();
@@ -331,7 +346,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
         const int my_row = (QT == 2 ? g * 128 : 0) + row;      // of the part
         uint32_t done = 0;             // this group's tiles so far
         uint32_t kv = 0;               // tiles so far
-        for (int pi = blockIdx.x; walk.find(a, pi, p); pi += gridDim.x) {
+        for (uint32_t part = 0;; ++part) {
+            wait_or_dead(PART_FULL + 8 * (part & 3), part >> 2 & 1, dead);
+            const Part &p = meta.parts[part & 3];
+            const int tiles = __shfl_sync(~0u, p.tiles, 0), tile0 = p.tile0;
+            // all that meet at a barrier below leave together
+            const bool leave = tiles < 0 || *dead;
+            if (QT == 1 ? group_any(1, 256, leave) : (bool)__any_sync(~0u, leave)) break;
             // queries: scaled by a power of two, so that the largest of a row is in [1, 2)
             float factor;
             {
@@ -385,18 +406,21 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             float m = NOTHING, l = 0.f;
             uint32_t nan_blocks = 0;
             int mine = 0;              // tiles of this part that this group has done
-            for (int j = QT == 2 ? 0 : g; j < p.tiles; j += QT == 2 ? 1 : 2) {
-                const int stage = (kv + j) % ST, pos0 = (p.tile0 + j) * TT;
+#pragma unroll 1
+            for (int j = QT == 2 ? 0 : g; j < tiles; j += QT == 2 ? 1 : 2) {
+                const int pos0 = (tile0 + j) * TT, ring = (kv + j) & 3;
                 wait_or_dead(S_FULL + 8 * g, done & 1, dead);
                 tmem_after_sync();
-                const uint4 miss = *reinterpret_cast<const uint4 *>(miss_s + stage * 16);
+                const uint4 miss = *reinterpret_cast<const uint4 *>(meta.missing[ring]);
+                const uint4 nans = *reinterpret_cast<const uint4 *>(meta.nan_group[ring]);
+                const bool any_nan = (nans.x | nans.y | nans.z | nans.w) != 0;
                 const bool some = pos0 < all_first || pos0 + TT - 1 > all_last || (miss.x | miss.y | miss.z | miss.w) != 0;
-                const uint32_t gone[4] = {miss.x, miss.y, miss.z, miss.w};
                 auto visible = [&](int c) -> uint32_t {        // of tokens 32 c .. 32 c + 31
                     const int lo = see.x - (pos0 + 32 * c), hi = see.y - (pos0 + 32 * c);
                     uint32_t v = hi < 0 ? 0u : hi >= 31 ? ~0u : (2u << hi) - 1;
                     v &= lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
-                    return v & ~gone[c];
+                    const uint32_t gone = reinterpret_cast<const uint32_t *>(meta.missing[ring])[c];
+                    return v & ~gone;
                 };
                 uint32_t x[TT];
 #pragma unroll
@@ -470,15 +494,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 }
                 l += (__uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32))) +
                      (__uint_as_float((uint32_t)sum1) + __uint_as_float((uint32_t)(sum1 >> 32)));
-                if (nan_any[2 * stage] | nan_any[2 * stage + 1]) {   // NaN values: they reach the rows that see them
+                if (any_nan) {                                 // NaN values: they reach the rows that see them
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         const uint32_t v = visible(c);
 #pragma unroll 1
-                        for (int blk = 0; blk < D / 16; ++blk) {
-                            const int unpacker = (blk >> 1) * 2 + (c >> 1);
-                            if (!reinterpret_cast<const uint8_t *>(nan_any + 2 * stage)[unpacker]) continue;
-                            if (v & *reinterpret_cast<const uint32_t *>(nan_s + stage * 128 + blk * 16 + 4 * c)) nan_blocks |= 1u << blk;
+                        for (int i = 0; i < 4; ++i) {
+                            if (!meta.nan_group[ring][4 * c + i]) continue;
+#pragma unroll 1
+                            for (int blk = 0; blk < D / 16; ++blk)
+                                if (v >> (8 * i) & meta.nan_value[ring][4 * c + i][blk]) nan_blocks |= 1u << blk;
                         }
                     }
                 }
@@ -489,7 +514,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 ++done;
                 ++mine;
             }
-            kv += p.tiles;
+            kv += tiles;
             if (mine > 0) wait_or_dead(PV_DONE + 8 * g, (done - 1) & 1, dead);
             tmem_after_sync();
 
@@ -520,16 +545,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 tmem_before_sync();
             } else {
                 // both groups hold the same rows: each joins half of the channels
-                ml_s[g * 128 + row] = make_float2(m, l);
-                nan_row[g * 128 + row] = (uint8_t)nan_blocks;
+                meta.ml[g][row] = make_float2(m, l);
+                meta.nan_row[g][row] = (uint8_t)nan_blocks;
                 tmem_before_sync();
                 group_sync(1, 256);
                 tmem_after_sync();
-                const float2 ml0 = ml_s[row], ml1 = ml_s[128 + row];
-                nan_blocks = nan_row[row] | nan_row[128 + row];
+                const float2 ml0 = meta.ml[0][row], ml1 = meta.ml[1][row];
+                nan_blocks = meta.nan_row[0][row] | meta.nan_row[1][row];
                 const float both = fmaxf(ml0.x, ml1.x);
                 const float k0 = exp2_fast(ml0.x - both), k1 = exp2_fast(ml1.x - both), sum = ml0.y * k0 + ml1.y * k1;
-                const bool have0 = p.tiles > 0, have1 = p.tiles > 1, split = p.pieces > 1;
+                const bool have0 = tiles > 0, have1 = tiles > 1, split = p.pieces > 1;
                 const float f = split ? 1.f : sum == 0.f ? 0.f : a.v_scale / sum;
                 float *const partials = reinterpret_cast<float *>(a.ws + MAX_CTAS * 4);
                 float *const my_part = partials + (size_t)(p.slot0 + p.piece) * S::PARTIAL;
@@ -570,10 +595,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         int *const counter = reinterpret_cast<int *>(a.ws) + p.slot0;
                         const bool last = atomicAdd(counter, 1) == p.pieces - 1;
                         if (last) *counter = 0;                // as the next call needs it
-                        misc[1] = last;
+                        meta.last = last;
                     }
                     group_sync(1, 256);
-                    if (misc[1] && !*dead) {
+                    if (*(volatile int *)&meta.last && !*dead) {
                         __threadfence();
                         for (int i = tid; i < p.rows * (D / 4); i += 256) {
                             const int col = i / (D / 4), d = i % (D / 4) * 4;
@@ -601,164 +626,135 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 tmem_before_sync();
                 group_sync(1, 256);    // both have read O, the maxima and sums
             }
+            __syncwarp();
+            if (lane == 0) barrier_arrive(PART_FREE + 8 * (part & 3));
         }
     } else if (w < 16) {
         give_registers<REGS_UNPACK>();
         // ================================ unpack =======================================================
-        const int uw = w - 8, ut = tid - 256;
-        const int k_tok = ut & 127, k_half = ut >> 7;          // K: half the channels of one token
-        // V: 8 channels (one word, of scale block blk) of 8 tokens; the lanes' 8 token groups fill one 128-byte row
-        const int box = uw & 1, grp = lane & 7, word = (uw >> 1) * 4 + (lane >> 3), blk = word >> 1;
-        const bool has_v = blk < D / 16;
-        const int v_tok = box * 64 + grp * 8;
-        struct Spot {                                          // a tile, and the pages this thread reads of it
-            int pi, j, page_k, page_v, pos0, h, len;
-            bool valid;
-        };
-        auto next = [&](Spot &s) {
-            ++s.j;
-            while (s.valid && s.j >= p.tiles) {
-                s.pi += gridDim.x;
-                s.j = 0;
-                s.valid = walk.find(a, s.pi, p);
-            }
-            if (!s.valid) return;
-            s.pos0 = (p.tile0 + s.j) * TT;
-            s.h = p.h;
-            s.len = p.len;
-            const int32_t *const pages = a.page_table + (size_t)p.b * a.max_pages;
-            s.page_k = s.pos0 + k_tok < p.len ? pages[(s.pos0 + k_tok) >> a.page_shift] : -2;
-            s.page_v = s.pos0 + v_tok < p.len ? pages[(s.pos0 + v_tok) >> a.page_shift] : -2;
-        };
-        auto tile_of = [&](int page, int h, int pos) {
-            const int in_page = pos & ((1 << a.page_shift) - 1);
-            return a.pool + ((((size_t)page * a.Hkv + h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
-        };
-        constexpr int KW = D / 16;                             // words of half a K row
-        uint32_t kr[KW], kscale, vr[8], missing;
-        uint2 vscale;
-        auto load_k = [&](const Spot &s) {
-            if (s.page_k >= 0 && s.page_k < a.num_pages) {
-                const int pos = s.pos0 + k_tok, tok = pos & 15;
-                const uint8_t *t = tile_of(s.page_k, s.h, pos);
-#pragma unroll
-                for (int i = 0; i < KW / 4; ++i) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(t + tok * (D / 2) + k_half * (D / 4)) + i);
-                    kr[4 * i] = x.x, kr[4 * i + 1] = x.y, kr[4 * i + 2] = x.z, kr[4 * i + 3] = x.w;
+        // A lane holds, of token 8 uw + lane / 4 of 64, a quarter of the channels of K and then of V.
+        constexpr int W = D / 32;                              // words of a lane
+        const int uw = w - 8, c = lane & 3, tok = uw * 8 + (lane >> 2);
+        const uint32_t in_box = (uint32_t)((tok >> 4) * L::BYTES);
+        const uint32_t base = shared_addr(smem);
+        uint32_t raw = 0, raw_round = 0;
+        for (uint32_t n = 0;; ++n) {                           // tiles
+            const uint32_t stage = n & 1, round = n >> 1, ring = n & 3;
+            bool end = false;
+            if (round > 0) wait_or_dead(K_FREE + 8 * stage, (round - 1) & 1, dead);
+            uint32_t r = raw, rr = raw_round;
+#pragma unroll 1
+            for (int box = 0; box < 2; ++box) {
+                wait_or_dead(RAW_FULL + 8 * r, rr & 1, dead);
+                const int live = meta.raw_live[r], bad = meta.raw_bad[r];
+                if (__any_sync(~0u, live < 0 || *dead)) {
+                    end = true;
+                    break;
                 }
-                if constexpr (D == 128) kscale = __ldg(reinterpret_cast<const uint32_t *>(t + L::KS + tok * 8 + k_half * 4));
-                else kscale = __ldg(reinterpret_cast<const uint16_t *>(t + L::KS + tok * 4 + k_half * 2));
-            } else {
-                if (s.page_k != -2) report(a.err, DEVERR_PAGE_RANGE);
+                const uint8_t *t = smem + S::RAW_AT + r * S::RAW_BYTES + in_box;
+                uint32_t k[W], scale;
+                if constexpr (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(t + (tok & 15) * 64 + c * 16);
+                    // lanes 2 and 3 of four take their words in the order 2, 3, 0, 1: no bank conflicts below
+                    k[0] = c & 2 ? x.z : x.x, k[1] = c & 2 ? x.w : x.y, k[2] = c & 2 ? x.x : x.z, k[3] = c & 2 ? x.y : x.w;
+                    scale = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(t + L::KS + (tok & 15) * 8 + c * 2));
+                    if (c & 2) scale = __byte_perm(scale, 0, 0x1032);
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(t + (tok & 15) * 32 + c * 8);
+                    k[0] = x.x, k[1] = x.y;
+                    scale = e4m3x2_to_f16x2(t[L::KS + (tok & 15) * 4 + c]);
+                }
+                uint8_t *const tile = smem + S::K_AT + stage * S::KBYTES;
 #pragma unroll
-                for (int i = 0; i < KW; ++i) kr[i] = 0;
-                kscale = 0;
-            }
-        };
-        auto load_v = [&](const Spot &s) {
-            missing = s.page_v != -2 && (s.page_v < 0 || s.page_v >= a.num_pages) ? 255u : 0u;
-            if (has_v && s.page_v >= 0 && s.page_v < a.num_pages) {
-                const int pos = s.pos0 + v_tok, tok = pos & 15;
-                const uint8_t *t = tile_of(s.page_v, s.h, pos);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) vr[i] = __ldg(reinterpret_cast<const uint32_t *>(t + L::VC + (tok + i) * (D / 2) + word * 4));
-                vscale = __ldg(reinterpret_cast<const uint2 *>(t + L::VS + blk * KV_TILE + tok));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) vr[i] = 0;
-                vscale = make_uint2(0, 0);
-            }
-        };
-        auto unpack_k = [&](uint8_t *tile) {
-#pragma unroll
-            for (int i = 0; i < KW; ++i) {                     // 8 channels: one word, half a scale block
-                const uint32_t two = e4m3x2_to_f16x2(kscale >> (i & 4 ? 16 : 0) & 0xffffu);
-                const uint32_t sc = __byte_perm(two, 0, i & 2 ? 0x3232 : 0x1010);
-                uint32_t f[4];
-                e2m1x8_to_f16x2(kr[i], f);
-                *reinterpret_cast<uint4 *>(tile + chunk_at(k_tok, k_half * KW + i, TT)) =
-                    make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
-            }
-        };
-        auto unpack_v = [&](uint8_t *tile, int stage, int live) {
-            uint2 vs = vscale;
-            // scales of tokens past the end: 0
-            if (live < 4) vs.x &= live <= 0 ? 0u : (1u << (8 * live)) - 1;
-            if (live < 8) vs.y &= live <= 4 ? 0u : (1u << (8 * (live - 4))) - 1;
-            const uint32_t n0 = ((vs.x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u, n1 = ((vs.y & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            const bool any = __any_sync(~0u, (n0 | n1) != 0);
-            if (any) {                                         // NaN scales: 0 here, noted for the softmax
-                vs.x &= ~((n0 >> 7) * 255u);
-                vs.y &= ~((n1 >> 7) * 255u);
-                // bits 0, 8, 16, 24 to bits 0..3
-                const uint32_t b0 = (n0 >> 7) * 0x01020408u >> 24 & 15u, b1 = (n1 >> 7) * 0x01020408u >> 24 & 15u;
-                if (has_v) nan_s[stage * 128 + blk * 16 + box * 8 + grp] = (uint8_t)(b0 | b1 << 4);
-            }
-            if (lane == 0) reinterpret_cast<uint8_t *>(nan_any + 2 * stage)[uw] = any;
-            if (word == 0) miss_s[stage * 16 + box * 8 + grp] = (uint8_t)missing;
-            if (has_v) {
-                const uint32_t sc[4] = {e4m3x2_to_f16x2(vs.x & 0xffffu), e4m3x2_to_f16x2(vs.x >> 16), e4m3x2_to_f16x2(vs.y & 0xffffu),
-                                        e4m3x2_to_f16x2(vs.y >> 16)};
-                constexpr uint32_t LOW = 0x0f0f0f0fu;
-#pragma unroll
-                for (int odd = 0; odd < 2; ++odd) {            // channels 0, 2, 4, 6 of the word, then 1, 3, 5, 7
-                    uint32_t f[4][4];                          // [pair of tokens][channel]
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t x = vr[2 * t], y = vr[2 * t + 1];
-                        e2m1x8_to_f16x2(odd ? ((x >> 4) & LOW) | (y & ~LOW) : (x & LOW) | ((y << 4) & ~LOW), f[t]);
+                for (int i = 0; i < W; ++i) {
+                    const uint32_t sc = __byte_perm(scale, 0, i >= 2 ? 0x3232 : 0x1010);
+                    const int chunk = W * c + (D == 128 ? i ^ (c & 2) : i);
+                    uint32_t f[4];
+                    e2m1x8_to_f16x2(k[i], f);
+                    *reinterpret_cast<uint4 *>(tile + chunk_at(box * BOX + tok, chunk, TT)) =
+                        make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
+                }
+                // what the softmax has to know of these 8 tokens: a page out of range, NaN values
+                const bool gone = bad >> (tok >> 4) & 1, off = gone || tok >= live;
+                uint32_t vs0 = 0, vs1 = 0;
+                if (!off) {
+                    vs0 = t[L::VS + (D == 128 ? 2 * c : c) * KV_TILE + (tok & 15)];
+                    if (D == 128) vs1 = t[L::VS + (2 * c + 1) * KV_TILE + (tok & 15)];
+                }
+                const uint32_t n0 = __ballot_sync(~0u, (vs0 & 127) == 127), n1 = __ballot_sync(~0u, (vs1 & 127) == 127);
+                if ((n0 | n1) && lane < 4) {
+                    uint32_t x0 = 0, x1 = 0;
+                    for (int i = 0; i < 8; ++i) {
+                        x0 |= (n0 >> (4 * i + c) & 1) << i;
+                        x1 |= (n1 >> (4 * i + c) & 1) << i;
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4 *>(tile + chunk_at(word * 8 + 2 * i + odd, box * 8 + grp, D)) =
-                            make_uint4(hmul2(f[0][i], sc[0]), hmul2(f[1][i], sc[1]), hmul2(f[2][i], sc[2]), hmul2(f[3][i], sc[3]));
+                    meta.nan_value[ring][box * 8 + uw][D == 128 ? 2 * c : c] = (uint8_t)x0;
+                    if (D == 128) meta.nan_value[ring][box * 8 + uw][2 * c + 1] = (uint8_t)x1;
                 }
+                if (lane == 0) {
+                    meta.nan_group[ring][box * 8 + uw] = (n0 | n1) != 0;
+                    meta.missing[ring][box * 8 + uw] = gone ? 255 : 0;
+                }
+                if (++r == S::RAW) r = 0, ++rr;
             }
-        };
-        Spot spot;
-        spot.pi = blockIdx.x;
-        spot.j = -1;
-        spot.valid = walk.find(a, spot.pi, p);
-        next(spot);
-        bool have = spot.valid;
-        int live = 0;                                          // of this thread's V tokens, those before the end
-        if (have) {
-            load_k(spot);
-            load_v(spot);
-            live = spot.len - (spot.pos0 + v_tok);
-            next(spot);
-        }
-        // the next tile's codes are asked for as soon as this one's registers are free
-        uint32_t stage = 0, round = 0;
-        while (have) {
-            have = spot.valid;
-            if (round > 0) wait_or_dead(KV_FREE + 8 * stage, (round - 1) & 1, dead);
-            uint8_t *const k_tile = smem + S::RING + stage * S::STAGE;
-            unpack_k(k_tile);
-            if (have) load_k(spot);
-            unpack_v(k_tile + S::KBYTES, stage, live);
-            if (have) {
-                load_v(spot);
-                live = spot.len - (spot.pos0 + v_tok);
-                next(spot);
+            if (end) break;
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) barrier_arrive(K_FULL + 8 * stage);
+
+            if (round > 0) wait_or_dead(V_FREE + 8 * stage, (round - 1) & 1, dead);
+            const uint32_t v_tile = base + S::V_AT + stage * S::KBYTES;
+#pragma unroll 1
+            for (int box = 0; box < 2; ++box) {
+                const int live = meta.raw_live[raw], bad = meta.raw_bad[raw];
+                const bool off = (bad >> (tok >> 4) & 1) || tok >= live;
+                const uint8_t *t = smem + S::RAW_AT + raw * S::RAW_BYTES + in_box;
+                uint32_t v[W], sc[W / 2];
+                if constexpr (D == 128) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(t + L::VC + (tok & 15) * 64 + c * 16);
+                    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(t + L::VC + (tok & 15) * 32 + c * 8);
+                    v[0] = x.x, v[1] = x.y;
+                }
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i) {              // NaN scales and tokens past the end: 0
+                    const uint32_t byte = t[L::VS + (W / 2 * c + i) * KV_TILE + (tok & 15)];
+                    sc[i] = __byte_perm(e4m3x2_to_f16x2(off || (byte & 127) == 127 ? 0u : byte), 0, 0x1010);
+                }
+                // this lane's address: row r of matrix m is the channel that lane quarter r / 2 put there
+                const int am = lane >> 3, ac = lane >> 1 & 3;
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    uint32_t f[4];
+                    e2m1x8_to_f16x2(__funnelshift_r(v[i], v[i], 8 * c), f);
+                    const int ch = 8 * (W * ac + i) + 2 * ((am + ac) & 3) + (lane & 1);
+                    store_transposed(v_tile + chunk_at(ch, box * 8 + uw, D), hmul2(f[0], sc[i / 2]), hmul2(f[1], sc[i / 2]),
+                                     hmul2(f[2], sc[i / 2]), hmul2(f[3], sc[i / 2]));
+                }
+                __syncwarp();
+                if (lane == 0) barrier_arrive(RAW_FREE + 8 * raw);
+                if (++raw == S::RAW) raw = 0, ++raw_round;
             }
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) barrier_arrive(KV_FULL + 8 * stage);
-            if (++stage == ST) stage = 0, ++round;
+            if (lane == 0) barrier_arrive(V_FULL + 8 * stage);
         }
     } else {
-        give_registers<REGS_PRODUCT>();
+        give_registers<REGS_OTHER>();
         if (w == 16) {
-        // ================================ products =====================================================
-        constexpr uint32_t ID_S = idesc_f16(128, TT), ID_O = idesc_f16(128, D);
-        const uint32_t base = shared_addr(smem);
-        uint32_t done[2] = {0, 0}, kv = 0, parts = 0;
-        for (int pi = blockIdx.x; walk.find(a, pi, p); pi += gridDim.x) {
-            {
-                auto kv_wait = [&](int j) { wait_or_dead(KV_FULL + 8 * ((kv + j) % ST), (kv + j) / ST & 1, dead); };
-                auto scores = [&](int g, int j) {
-                    const uint64_t dq = tile_desc(base + (QT == 2 ? g : 0) * S::QBYTES), dk = tile_desc(base + S::RING + (kv + j) % ST * S::STAGE);
+            // ============================ products =====================================================
+            constexpr uint32_t ID_S = idesc_f16(128, TT), ID_O = idesc_f16(128, D);
+            const uint32_t base = shared_addr(smem);
+            uint32_t done[2] = {0, 0}, kv = 0;
+            for (uint32_t part = 0;; ++part) {
+                wait_or_dead(PART_FULL + 8 * (part & 3), part >> 2 & 1, dead);
+                const int tiles = __shfl_sync(~0u, meta.parts[part & 3].tiles, 0);
+                if (__any_sync(~0u, tiles < 0 || *dead)) break;
+                if (lane == 0) barrier_arrive(PART_FREE + 8 * (part & 3));
+                auto scores = [&](int g, int j, bool frees) {
+                    const uint32_t n = kv + j;
+                    const uint64_t dq = tile_desc(base + (QT == 2 ? g : 0) * S::QBYTES), dk = tile_desc(base + S::K_AT + (n & 1) * S::KBYTES);
                     tmem_after_sync();
                     if (elect_one()) {
 #pragma unroll
@@ -767,13 +763,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                             mma_f16_ss(tmem + g * 128, dq + at, dk + at, ID_S, s > 0);
                         }
                         mma_done(S_FULL + 8 * g);
+                        if (frees) mma_done(K_FREE + 8 * (n & 1));
                     }
                     __syncwarp();
                 };
                 auto values = [&](int g, int j, bool first, bool frees) {
+                    const uint32_t n = kv + j;
                     wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
                     ++done[g];
-                    const uint64_t dv = tile_desc(base + S::RING + (kv + j) % ST * S::STAGE + S::KBYTES);
+                    const uint64_t dv = tile_desc(base + S::V_AT + (n & 1) * S::KBYTES);
                     tmem_after_sync();
                     if (elect_one()) {
 #pragma unroll
@@ -782,50 +780,135 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                             mma_f16_ts(tmem + S::O_COL + g * D, tmem + g * 128 + 8 * s, dv + at, ID_O, s > 0 || !first);
                         }
                         mma_done(PV_DONE + 8 * g);
-                        if (frees) mma_done(KV_FREE + 8 * ((kv + j) % ST));
+                        if (frees) mma_done(V_FREE + 8 * (n & 1));
                     }
                     __syncwarp();
                 };
-                const int tiles = p.tiles;
-                wait_or_dead(Q_FULL, parts & 1, dead);
+                auto k_wait = [&](int j) { wait_or_dead(K_FULL + 8 * ((kv + j) & 1), (kv + j) >> 1 & 1, dead); };
+                auto v_wait = [&](int j) { wait_or_dead(V_FULL + 8 * ((kv + j) & 1), (kv + j) >> 1 & 1, dead); };
+                wait_or_dead(Q_FULL, part & 1, dead);
                 if (QT == 2) {
-                    wait_or_dead(Q_FULL + 8, parts & 1, dead);
-                    kv_wait(0);
-                    scores(0, 0);
-                    scores(1, 0);
+                    wait_or_dead(Q_FULL + 8, part & 1, dead);
+                    k_wait(0);
+                    scores(0, 0, false);
+                    scores(1, 0, true);
+#pragma unroll 1
                     for (int j = 0; j < tiles; ++j) {
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            values(g, j, j == 0, g == 1);
-                            if (j + 1 < tiles) {
-                                if (g == 0) kv_wait(j + 1);
-                                scores(g, j + 1);
-                            }
+                        v_wait(j);
+                        values(0, j, j == 0, false);
+                        if (j + 1 < tiles) {
+                            k_wait(j + 1);
+                            scores(0, j + 1, false);
                         }
+                        values(1, j, j == 0, true);
+                        if (j + 1 < tiles) scores(1, j + 1, true);
                     }
                 } else {
                     for (int j = 0; j < min(tiles, 2); ++j) {
-                        kv_wait(j);
-                        scores(j, j);
+                        k_wait(j);
+                        scores(j, j, true);
                     }
+#pragma unroll 1
                     for (int j = 0; j < tiles; ++j) {
+                        v_wait(j);
                         values(j & 1, j, j < 2, true);
                         if (j + 2 < tiles) {
-                            kv_wait(j + 2);
-                            scores(j & 1, j + 2);
+                            k_wait(j + 2);
+                            scores(j & 1, j + 2, true);
                         }
                     }
                 }
+                kv += tiles;
+            }
+            if (elect_one()) {
+                mma_done(FINISHED);
+                barrier_wait(FINISHED, 0);
             }
             __syncwarp();
-            kv += p.tiles;
-            ++parts;
-        }
-        if (elect_one()) {
-            mma_done(FINISHED);
-            barrier_wait(FINISHED, 0);
-        }
-        __syncwarp();
+        } else if (w == 17) {
+            // ============================ load =========================================================
+            // how the work is cut: only where there are fewer parts than SMs
+            int cut = 0;
+            {
+                long long units = 0, all = 0;
+                for (int b = lane; b < a.B; b += 32) {
+                    const Request q = request_of(a, b, 128 * QT, blockIdx.x == 0);
+                    units += (long long)q.row_blocks * a.Hkv;
+                    if (q.row_blocks) all += (long long)q.row_blocks * a.Hkv * Walker<QT>::most_tiles(a, q);
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    units += __shfl_xor_sync(~0u, units, o);
+                    all += __shfl_xor_sync(~0u, all, o);
+                }
+                if (QT == 1 && units < SMS) cut = (int)max((all + SPLIT_PARTS - 1) / SPLIT_PARTS, 2LL);
+            }
+            int *const counters = reinterpret_cast<int *>(a.ws);
+            Walker<QT> walk;
+            walk.start(a, cut);
+            uint32_t raw = 0, raw_round = 0;
+            for (uint32_t part = 0;; ++part) {
+                int pi = 0;
+                if (lane == 0) pi = atomicAdd(counters + NEXT_PART, 1);
+                pi = __shfl_sync(~0u, pi, 0);
+                Part p;
+                const bool found = walk.find(a, pi, p) && !__any_sync(~0u, *dead);
+                if (part >= 4) wait_or_dead(PART_FREE + 8 * (part & 3), ((part >> 2) - 1) & 1, dead);
+                if (lane == 0) {
+                    if (found) meta.parts[part & 3] = p;
+                    else meta.parts[part & 3].tiles = -1;
+                    barrier_arrive(PART_FULL + 8 * (part & 3));
+                }
+                __syncwarp();
+                if (!found) break;
+                const int32_t *const pages = a.page_table + (size_t)p.b * a.max_pages;
+                const int boxes = 2 * p.tiles, from = p.tile0 * TT;
+                auto look = [&](int i) {               // the page of the i-th 16 tokens of the part; -2 past the end
+                    const long long pos = (long long)from + (long long)i * KV_TILE;
+                    return i < boxes * 4 && pos < p.len ? pages[pos >> a.page_shift] : -2;
+                };
+                int now = look(lane), then = look(32 + lane);
+                for (int i = 0; i < boxes; ++i) {
+                    if (i > 0 && (i & 7) == 0) {
+                        now = then;
+                        then = look((i + 8) * 4 + lane);
+                    }
+                    if (raw_round > 0) wait_or_dead(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead);
+                    // lanes 0..3: one run of 16 tokens each
+                    const int page = __shfl_sync(~0u, now, (i & 7) * 4 + (lane & 3));
+                    const bool ok = page >= 0 && page < a.num_pages;
+                    const uint32_t oks = __ballot_sync(~0u, ok) & 15u, gone = __ballot_sync(~0u, !ok && page != -2) & 15u;
+                    if (lane == 0) {
+                        meta.raw_live[raw] = (int)min(max((long long)p.len - from - (long long)i * BOX, 0LL), (long long)BOX);
+                        meta.raw_bad[raw] = gone;
+                        if (gone) report(a.err, DEVERR_PAGE_RANGE);
+                        barrier_expect(RAW_FULL + 8 * raw, __popc(oks) * L::BYTES);
+                    }
+                    __syncwarp();
+                    if (lane < 4 && ok) {
+                        const int in_page = (from + i * BOX + lane * KV_TILE) & ((1 << a.page_shift) - 1);
+                        bulk_copy(smem + S::RAW_AT + raw * S::RAW_BYTES + lane * L::BYTES,
+                                  a.pool + ((((size_t)page * a.Hkv + p.h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES, L::BYTES,
+                                  RAW_FULL + 8 * raw);
+                    }
+                    if (++raw == S::RAW) raw = 0, ++raw_round;
+                }
+            }
+            // after a wait that gave up: the copies that were asked for may still be on their way
+            if (__any_sync(~0u, *dead)) {
+                for (uint32_t i = 0; i < S::RAW; ++i)
+                    if (i < raw || raw_round > 0) barrier_wait(RAW_FULL + 8 * i, (i < raw ? raw_round : raw_round - 1) & 1);
+            }
+            // the end, for the unpacking warps; the last CTA leaves the counters as the next call needs them
+            if (raw_round > 0) wait_or_dead(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead);
+            if (lane == 0) {
+                meta.raw_live[raw] = -1;
+                barrier_arrive(RAW_FULL + 8 * raw);
+                if (atomicAdd(counters + CTAS_DONE, 1) == (int)gridDim.x - 1) {
+                    counters[NEXT_PART] = 0;
+                    counters[CTAS_DONE] = 0;
+                }
+            }
         }
     }
 
@@ -838,11 +921,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
 template <int D, int QT, typename T>
 cudaError_t launch_tile_attention(const KvAttentionArgs &a, cudaStream_t s) {
     using Sh = TileShape<D, QT>;
+    constexpr int SMEM = Sh::META + sizeof(TileMeta);
+    static_assert(SMEM <= 232448, "shared memory");
     static_assert((size_t)MAX_CTAS * 4 + 2 * SPLIT_PARTS * (size_t)Sh::PARTIAL * 4 <= KDA_KV4_WORKSPACE, "workspace");
     static const cudaError_t set =
-        cudaFuncSetAttribute(tile_attention_kernel<D, QT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+        cudaFuncSetAttribute(tile_attention_kernel<D, QT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (set != cudaSuccess) return set;
-    tile_attention_kernel<D, QT, T><<<SMS, TILE_THREADS, Sh::SMEM, s>>>(a);
+    tile_attention_kernel<D, QT, T><<<SMS, TILE_THREADS, SMEM, s>>>(a);
     return cudaGetLastError();
 }
 
