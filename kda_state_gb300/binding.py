@@ -16,6 +16,7 @@ without a report.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 
@@ -627,8 +628,13 @@ def kda_slot_copy(pools, src, dst, dev_err=None, stream=None):
 # the paged 4-bit key/value cache
 # ---------------------------------------------------------------------------
 
+# These calls are short next to the host's share of them: each argument is checked with a few
+# attribute reads, and only one that fails goes through _need for its message.
+
 KV_TILE = 16          # tokens of a tile
 _KV_DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_FP16}
+_U8 = torch.uint8
+_KIND = operator.attrgetter("dtype", "shape")
 
 
 def kv4_tile_bytes(D: int = K_DIM) -> int:
@@ -659,23 +665,68 @@ def _kv_dt(dtype):
     return _KV_DT[dtype]
 
 
-def _need_rows(t, name, shape, dtype=None, device=None):
+def _ptr(t, name, shape, dtype, first):
+    """The address of a dense tensor of this shape and dtype on first's device."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and
+                t.get_device() == first.get_device()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, shape, dtype, first.device)
+    return t.data_ptr()
+
+
+def _err_ptr(dev_err, first):
+    if dev_err is None:
+        return None
+    _need_err(dev_err, first.device)
+    return dev_err.data_ptr()
+
+
+def _stream_of(stream, first):
+    """The stream argument as a handle: by default the current one of the operands' device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(first.get_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _first(t, name, dims):
+    """The operand that sets the device: a CUDA tensor of ``dims`` dimensions."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != dims:
+        _need(t, name, (None,) * dims, dense=False)
+
+
+def _rows(t, name, dtype, shape, first):
     """[tokens, heads, D] whose heads are dense and whose tokens may be strided.  Returns the
-    stride between tokens, in elements."""
-    _need(t, name, shape, dtype, device, dense=False)
-    T, H, D = t.shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    address and the stride between tokens, in elements."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != first.get_device():
+        _need(t, name, shape, dtype, first.device, dense=False)
+    T, H, D = shape
+    stride, head, one = t.stride()
+    if T <= 1:
+        stride = H * D
+    at = t.data_ptr()
+    if one != 1 or (H > 1 and head != D):
         raise ValueError("%s: heads and channels must be dense (only tokens may be strided)" % name)
-    stride = t.stride(0) if T > 1 else H * D
-    if stride < H * D or stride % 8 != 0 or t.data_ptr() % 16 != 0:
+    if stride < H * D or stride % 8 != 0 or at % 16 != 0:
         raise ValueError("%s: tokens must start on 16-byte boundaries and not overlap" % name)
-    return stride
+    return at, stride
 
 
-def _need_pool(pool, D, device, name="pool"):
-    """uint8 [num_pages, H_kv, page_size / 16, 18 D].  Returns (num_pages, H_kv, page_size)."""
-    _need(pool, name, (None, None, None, 18 * D), torch.uint8, device)
-    return pool.shape[0], pool.shape[1], pool.shape[2] * KV_TILE
+def _pool(pool, D, first):
+    """uint8 [num_pages, H_kv, page_size / 16, 18 D].  Returns (address, num_pages, H_kv, page_size)."""
+    shape = pool.shape if isinstance(pool, torch.Tensor) else ()
+    if len(shape) != 4 or shape[3] != 18 * D:
+        _need(pool, "pool", (None, None, None, 18 * D), _U8, first.device)
+    return _ptr(pool, "pool", shape, _U8, first), shape[0], shape[1], shape[2] * KV_TILE
+
+
+def _table(page_table, first):
+    """int32 [B, max_pages].  Returns (address, B, max_pages)."""
+    _first(page_table, "page_table", 2)
+    B, M = page_table.shape
+    return _ptr(page_table, "page_table", (B, M), I32, first), B, M
 
 
 def kda_kv4_append(k, v, cu_seqlens, start, page_table, pool, k_scale: float = 1.0,
@@ -684,23 +735,21 @@ def kda_kv4_append(k, v, cu_seqlens, start, page_table, pool, k_scale: float = 1
     strided) as 4-bit codes: token i of request b at position start[b] + i of the
     pages that row b of page_table (int32 [B, max_pages]) names.  cu_seqlens int32
     [B + 1], start int32 [B]; the scales are powers of two.  Writes the pool in place."""
-    _need(k, "k", (None, None, None), dense=False)
-    dt, dev = _kv_dt(k.dtype), k.device
-    T, H, D = k.shape
-    ks = _need_rows(k, "k", (T, H, D))
-    vs = _need_rows(v, "v", (T, H, D), k.dtype, dev)
-    pages, Hp, page_size = _need_pool(pool, D, dev)
+    _first(k, "k", 3)
+    dt, shape = _kv_dt(k.dtype), k.shape
+    T, H, D = shape
+    ka, ks = _rows(k, "k", k.dtype, shape, k)
+    _first(v, "v", 3)
+    va, vs = _rows(v, "v", k.dtype, shape, k)
+    pa, pages, Hp, page_size = _pool(pool, D, k)
     if Hp != H:
         raise ValueError("pool has %d heads, k has %d" % (Hp, H))
-    _need(page_table, "page_table", (None, None), I32, dev)
-    B = page_table.shape[0]
-    _need(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev)
-    _need(start, "start", (B,), I32, dev)
-    _need_err(dev_err, dev)
-    _check("kda_kv4_append", lib().kda_kv4_append(
-        dt, B, T, H, D, _p(k), ks, _p(v), vs, _p(cu_seqlens), _p(start), _p(page_table),
-        page_table.shape[1], page_size, _p(pool), pages, float(k_scale), float(v_scale),
-        _p(dev_err), _stream(stream)))
+    ta, B, M = _table(page_table, k)
+    status = lib().kda_kv4_append(
+        dt, B, T, H, D, ka, ks, va, vs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, k),
+        _ptr(start, "start", (B,), I32, k), ta, M, page_size, pa, pages, k_scale, v_scale,
+        _err_ptr(dev_err, k), _stream_of(stream, k))
+    _check("kda_kv4_append", status)
 
 
 def kda_kv4_gather(cu_seqlens, start, total_tokens: int, page_table, pool, dtype=torch.bfloat16,
@@ -709,22 +758,20 @@ def kda_kv4_gather(cu_seqlens, start, total_tokens: int, page_table, pool, dtype
     """Read tokens back as the values they stand for: positions start[b] + i of request b
     into packed k, v [total_tokens, H_kv, D].  Returns (k, v)."""
     dt = _kv_dt(dtype)
-    _need(pool, "pool", (None, None, None, None), torch.uint8)
-    D, dev = pool.shape[3] // 18, pool.device
-    pages, H, page_size = _need_pool(pool, D, dev)
-    _need(page_table, "page_table", (None, None), I32, dev)
-    B, T = page_table.shape[0], int(total_tokens)
-    _need(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev)
-    _need(start, "start", (B,), I32, dev)
-    _need_err(dev_err, dev)
-    k = torch.empty(T, H, D, dtype=dtype, device=dev) if k is None else k
-    v = torch.empty(T, H, D, dtype=dtype, device=dev) if v is None else v
-    _need(k, "k", (T, H, D), dtype, dev)
-    _need(v, "v", (T, H, D), dtype, dev)
-    _check("kda_kv4_gather", lib().kda_kv4_gather(
-        dt, B, T, H, D, _p(k), _p(v), _p(cu_seqlens), _p(start), _p(page_table),
-        page_table.shape[1], page_size, _p(pool), pages, float(k_scale), float(v_scale),
-        _p(dev_err), _stream(stream)))
+    _first(pool, "pool", 4)
+    D, T = pool.shape[3] // 18, int(total_tokens)
+    pa, pages, H, page_size = _pool(pool, D, pool)
+    ta, B, M = _table(page_table, pool)
+    if k is None:
+        k = torch.empty(T, H, D, dtype=dtype, device=pool.device)
+    if v is None:
+        v = torch.empty(T, H, D, dtype=dtype, device=pool.device)
+    status = lib().kda_kv4_gather(
+        dt, B, T, H, D, _ptr(k, "k", (T, H, D), dtype, pool), _ptr(v, "v", (T, H, D), dtype, pool),
+        _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, pool), _ptr(start, "start", (B,), I32, pool),
+        ta, M, page_size, pa, pages, k_scale, v_scale, _err_ptr(dev_err, pool),
+        _stream_of(stream, pool))
+    _check("kda_kv4_gather", status)
     return k, v
 
 
@@ -738,66 +785,71 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
     defaults to D ** -0.5.  ``workspace``: ``make_kv4_workspace()``, kept by the caller
     (one for each stream); a call without one makes its own.  Returns (o, lse), o in
     q's dtype and lse fp32 [T, H_q]; a row that sees nothing has o = 0, lse = -inf."""
-    _need(q, "q", (None, None, None), dense=False)
-    dt, dev = _kv_dt(q.dtype), q.device
-    T, H, D = q.shape
-    qs = _need_rows(q, "q", (T, H, D))
-    pages, H_kv, page_size = _need_pool(pool, D, dev)
-    _need(page_table, "page_table", (None, None), I32, dev)
-    B = page_table.shape[0]
-    _need(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev)
-    _need(kv_lens, "kv_lens", (B,), I32, dev)
-    _need_err(dev_err, dev)
+    _first(q, "q", 3)
+    dtype, shape = q.dtype, q.shape
+    dt = _kv_dt(dtype)
+    T, H, D = shape
+    qa, qs = _rows(q, "q", dtype, shape, q)
+    pa, pages, H_kv, page_size = _pool(pool, D, q)
+    ta, B, M = _table(page_table, q)
     if o is None:
-        o = torch.empty(T, H, D, dtype=q.dtype, device=dev)
+        o = torch.empty(T, H, D, dtype=dtype, device=q.device)
     if lse is None:
-        lse = torch.empty(T, H, dtype=F32, device=dev)
+        lse = torch.empty(T, H, dtype=F32, device=q.device)
     if workspace is None:
-        workspace = make_kv4_workspace(dev)
-    _need(o, "o", (T, H, D), q.dtype, dev)
-    _need(lse, "lse", (T, H), F32, dev)
-    _need(workspace, "workspace", (None,), torch.uint8, dev)
-    _check("kda_kv4_attention", lib().kda_kv4_attention(
-        dt, B, T, int(max_q), H, H_kv, D, _p(q), qs, _p(cu_seqlens), _p(kv_lens), _p(page_table),
-        page_table.shape[1], page_size, _p(pool), pages, int(window),
-        float(D ** -0.5 if scale is None else scale), float(k_scale), float(v_scale), _p(o),
-        _p(lse), _p(workspace), workspace.numel(), _p(dev_err), _stream(stream)))
+        workspace = make_kv4_workspace(q.device)
+    _first(workspace, "workspace", 1)
+    wb = workspace.numel()
+    status = lib().kda_kv4_attention(
+        dt, B, T, max_q, H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, q),
+        _ptr(kv_lens, "kv_lens", (B,), I32, q), ta, M, page_size, pa, pages, window,
+        D ** -0.5 if scale is None else scale, k_scale, v_scale, _ptr(o, "o", shape, dtype, q),
+        _ptr(lse, "lse", (T, H), F32, q), _ptr(workspace, "workspace", (wb,), _U8, q), wb,
+        _err_ptr(dev_err, q), _stream_of(stream, q))
+    _check("kda_kv4_attention", status)
     return o, lse
 
 
-def _need_pages(refs, page_table, lens, dev_err):
-    """refs int32 [num_pages], page_table int32 [B, max_pages], lens int32 [B].  Returns
-    (device, B, max_pages, num_pages)."""
-    _need(refs, "refs", (None,), I32)
-    dev = refs.device
-    _need(page_table, "page_table", (None, None), I32, dev)
-    B = page_table.shape[0]
-    if lens is not None:
-        _need(lens, "lens", (B,), I32, dev)
-    _need_err(dev_err, dev)
-    return dev, B, page_table.shape[1], refs.numel()
+def _page_state(refs, page_table, lens):
+    """refs int32 [num_pages], page_table int32 [B, max_pages], lens int32 [B].  Returns their
+    addresses and (B, max_pages, num_pages)."""
+    _first(refs, "refs", 1)
+    N = refs.numel()
+    ta, B, M = _table(page_table, refs)
+    return (_ptr(refs, "refs", (N,), I32, refs), ta,
+            None if lens is None else _ptr(lens, "lens", (B,), I32, refs), B, M, N)
 
 
-def _need_page_pools(pools, num_pages, device):
-    """Layers' pools of one shape [num_pages, ...], any dtype.  Returns (pointers, bytes of a page)."""
+def _page_pools(pools, num_pages, first):
+    """Layers' pools of one dtype and shape [num_pages, ...].  Returns (addresses, bytes of a page)."""
     if len(pools) == 0:
         raise ValueError("pools must be a non-empty list")
-    for n, p in enumerate(pools):
-        _need(p, "pools[%d]" % n, device=device)
-        if p.dim() < 2 or p.shape[0] != num_pages or p.shape != pools[0].shape or p.dtype != pools[0].dtype:
-            raise ValueError("pools[%d]: every pool is [%d, ...] of one shape and dtype" % (n, num_pages))
-    ptrs = (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
-    return ptrs, pools[0].numel() // num_pages * pools[0].element_size()
+    p = pools[0]
+    one = isinstance(p, torch.Tensor) and p.dim() >= 2 and p.shape[0] == num_pages
+    if one and all(map(torch.is_tensor, pools)):
+        one = (set(map(_KIND, pools)) == {(p.dtype, p.shape)} and
+               set(map(torch.Tensor.get_device, pools)) == {first.get_device()} and
+               all(map(torch.Tensor.is_contiguous, pools)))
+    else:
+        one = False
+    if not one:
+        for n, q in enumerate(pools):
+            _need(q, "pools[%d]" % n, device=first.device)
+            if q.dim() < 2 or q.shape[0] != num_pages or q.shape != p.shape or q.dtype != p.dtype:
+                raise ValueError("pools[%d]: every pool is [%d, ...] of one shape and dtype" % (
+                    n, num_pages))
+    ptrs = (ctypes.c_void_p * len(pools))(*map(torch.Tensor.data_ptr, pools))
+    return ptrs, p.numel() // num_pages * p.element_size()
 
 
 def kda_page_alloc(refs, page_table, lens, grow, page_size: int, dev_err=None, stream=None):
     """Row b grows by grow[b] tokens (int32 [B]): the pages that takes are the lowest free
     ones, rows in order.  refs int32 [num_pages] (holders of each page, 0: free),
     page_table int32 [B, max_pages], lens int32 [B]; all three change in place."""
-    dev, B, M, N = _need_pages(refs, page_table, lens, dev_err)
-    _need(grow, "grow", (B,), I32, dev)
-    _check("kda_page_alloc", lib().kda_page_alloc(B, M, int(page_size), N, _p(refs), _p(page_table),
-                                                  _p(lens), _p(grow), _p(dev_err), _stream(stream)))
+    ra, ta, la, B, M, N = _page_state(refs, page_table, lens)
+    status = lib().kda_page_alloc(B, M, page_size, N, ra, ta, la, _ptr(grow, "grow", (B,), I32, refs),
+                                  _err_ptr(dev_err, refs), _stream_of(stream, refs))
+    _check("kda_page_alloc", status)
 
 
 def kda_page_fork(pools, refs, page_table, lens, src, dst, page_size: int, workspace=None,
@@ -805,43 +857,48 @@ def kda_page_fork(pools, refs, page_table, lens, src, dst, page_size: int, works
     """Copy-on-write: row dst[i] (empty) also holds row src[i]'s full pages, and gets a
     copy of its partial last page in every pool of the list.  ``workspace``: int32, at
     least 2 n; a call without one makes its own."""
-    dev, B, M, N = _need_pages(refs, page_table, lens, dev_err)
-    ptrs, page_bytes = _need_page_pools(pools, N, dev)
-    _need(src, "src", (None,), I32, dev)
+    ra, ta, la, B, M, N = _page_state(refs, page_table, lens)
+    ptrs, page_bytes = _page_pools(pools, N, refs)
+    _first(src, "src", 1)
     n = src.numel()
-    _need(dst, "dst", (n,), I32, dev)
     if workspace is None:
-        workspace = torch.empty(2 * n, dtype=I32, device=dev)
-    _need(workspace, "workspace", (None,), I32, dev)
-    _check("kda_page_fork", lib().kda_page_fork(
-        len(pools), ptrs, page_bytes, B, M, int(page_size), N, _p(refs), _p(page_table), _p(lens),
-        _p(src), _p(dst), n, _p(workspace), workspace.numel(), _p(dev_err), _stream(stream)))
+        workspace = torch.empty(2 * n, dtype=I32, device=refs.device)
+    _first(workspace, "workspace", 1)
+    wn = workspace.numel()
+    status = lib().kda_page_fork(
+        len(pools), ptrs, page_bytes, B, M, page_size, N, ra, ta, la, _ptr(src, "src", (n,), I32, refs),
+        _ptr(dst, "dst", (n,), I32, refs), n, _ptr(workspace, "workspace", (wn,), I32, refs), wn,
+        _err_ptr(dev_err, refs), _stream_of(stream, refs))
+    _check("kda_page_fork", status)
 
 
 def kda_page_free(refs, page_table, lens, rows, page_size: int, dev_err=None, stream=None):
     """Rows (int32 [n], distinct) let go of their pages; those nobody holds are free."""
-    dev, B, M, N = _need_pages(refs, page_table, lens, dev_err)
-    _need(rows, "rows", (None,), I32, dev)
-    _check("kda_page_free", lib().kda_page_free(B, M, int(page_size), N, _p(refs), _p(page_table),
-                                                _p(lens), _p(rows), rows.numel(), _p(dev_err),
-                                                _stream(stream)))
+    ra, ta, la, B, M, N = _page_state(refs, page_table, lens)
+    _first(rows, "rows", 1)
+    n = rows.numel()
+    status = lib().kda_page_free(B, M, page_size, N, ra, ta, la, _ptr(rows, "rows", (n,), I32, refs), n,
+                                 _err_ptr(dev_err, refs), _stream_of(stream, refs))
+    _check("kda_page_free", status)
 
 
 def kda_page_compact(pools, refs, page_table, live=None, workspace=None, dev_err=None, stream=None):
     """Move the held pages above the number of held pages into the free ones below, in
     every pool; refs and page_table follow.  Returns live, int32 [1] on the device: the
     pages from there on are free.  ``workspace``: int32, at least 3 num_pages + 16."""
-    dev, B, M, N = _need_pages(refs, page_table, None, dev_err)
-    ptrs, page_bytes = _need_page_pools(pools, N, dev)
+    ra, ta, _, B, M, N = _page_state(refs, page_table, None)
+    ptrs, page_bytes = _page_pools(pools, N, refs)
     if live is None:
-        live = torch.empty(1, dtype=I32, device=dev)
+        live = torch.empty(1, dtype=I32, device=refs.device)
     if workspace is None:
-        workspace = torch.empty(3 * N + 16, dtype=I32, device=dev)
-    _need(live, "live", (1,), I32, dev)
-    _need(workspace, "workspace", (None,), I32, dev)
-    _check("kda_page_compact", lib().kda_page_compact(
-        len(pools), ptrs, page_bytes, B, M, N, _p(refs), _p(page_table), _p(live), _p(workspace),
-        workspace.numel(), _p(dev_err), _stream(stream)))
+        workspace = torch.empty(3 * N + 16, dtype=I32, device=refs.device)
+    _first(workspace, "workspace", 1)
+    wn = workspace.numel()
+    status = lib().kda_page_compact(
+        len(pools), ptrs, page_bytes, B, M, N, ra, ta, _ptr(live, "live", (1,), I32, refs),
+        _ptr(workspace, "workspace", (wn,), I32, refs), wn, _err_ptr(dev_err, refs),
+        _stream_of(stream, refs))
+    _check("kda_page_compact", status)
     return live
 
 
@@ -849,15 +906,15 @@ def kda_page_copy(pools, src, dst, dev_err=None, stream=None):
     """Page dst[i] <- page src[i] in every pool of the list (int32 device index tensors)."""
     if len(pools) == 0:
         raise ValueError("pools must be a non-empty list")
-    _need(src, "src", (None,), I32)
-    dev = src.device
-    _need(dst, "dst", (src.numel(),), I32, dev)
-    _need_err(dev_err, dev)
-    _need(pools[0], "pools[0]", device=dev)
-    ptrs, page_bytes = _need_page_pools(pools, pools[0].shape[0], dev)
-    _check("kda_page_copy", lib().kda_page_copy(
-        len(pools), ptrs, page_bytes, pools[0].shape[0], _p(src), _p(dst), src.numel(), _p(dev_err),
-        _stream(stream)))
+    _first(src, "src", 1)
+    n = src.numel()
+    _need(pools[0], "pools[0]", device=src.device)
+    N = pools[0].shape[0]
+    ptrs, page_bytes = _page_pools(pools, N, src)
+    status = lib().kda_page_copy(
+        len(pools), ptrs, page_bytes, N, _ptr(src, "src", (n,), I32, src),
+        _ptr(dst, "dst", (n,), I32, src), n, _err_ptr(dev_err, src), _stream_of(stream, src))
+    _check("kda_page_copy", status)
 
 
 def kda_selftest_bounded_wait(dev_err, wait_us: int = 2000, stream=None):

@@ -18,13 +18,15 @@
 // largest, and most steps rescale nothing.
 //
 // Work is the list of all (request, block of rows, kv head, 32 tokens), cut into
-// equal contiguous ranges, one a CTA: a ragged batch and one long request are
-// balanced alike.  A range that ends inside a (request, rows, head) leaves a
-// partial result; the last of its CTAs to arrive joins them in order, so results
-// do not depend on timing.
+// equal contiguous ranges, one a warp: a ragged batch and one long request are
+// balanced alike, and a warp writes out by itself every (request, rows, head) that
+// lies in its range.  One that it shares leaves a partial result, joined by the CTA
+// once all its warps are done, or, where several CTAs share it, by the last of them
+// to arrive; in order, so results do not depend on timing.
 //
-// Each warp takes every eighth 32 tokens of its CTA's range through a ring of its
-// own, filled by bulk copies (one contiguous block of 18 D bytes for 16 tokens).
+// A warp's tokens come through a ring of its own, filled by bulk copies (one
+// contiguous block of 18 D bytes for 16 tokens); the next unit's are asked for
+// before the last one's result leaves.
 #pragma once
 
 #include "kda_async.cuh"
@@ -42,6 +44,17 @@ constexpr float HEADROOM = 9.f;        // log2 of a weight at the running maximu
 constexpr float MOVE = HEADROOM + 6.f; // a score this far above m makes the maximum move
 constexpr float NOTHING = -1e30f;      // the running maximum before any score
 
+constexpr float LN2 = 0.69314718055994531f;
+
+// What a warp leaves of a unit that it does not have all of (rows = 0: none).
+struct Piece {
+    long long begin, end;
+    int q0, h, row0, rows;
+};
+struct WarpPieces {
+    Piece first, last;
+};
+
 template <int D, int NT>
 struct DecodeShape {
     static constexpr int ROWS = 8 * NT;
@@ -50,7 +63,9 @@ struct DecodeShape {
     static constexpr int OSTRIDE = D + 4;
     static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
     static constexpr int OUT = WARPS * ROWS * OSTRIDE * 4;
-    static constexpr int SMEM = RING + OUT + WARPS * ROWS * 8 + WARPS * STAGES * 8 + 64;
+    static constexpr int ML = 2 * WARPS * ROWS * 8;
+    static constexpr int SMEM = RING + OUT + ML + WARPS * STAGES * 8 + 16 + WARPS * sizeof(WarpPieces);
+    static_assert(STAGES == 2 && ROWS * OSTRIDE * 4 <= STAGES * STAGE_BYTES, "a warp's last piece lies over its ring");
     static constexpr int PARTIAL = ROWS * (D + 2);         // floats
 };
 
@@ -137,9 +152,10 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     constexpr int LW = D / 32;             // 32-bit words of a lane's share of a K row
     extern __shared__ __align__(128) uint8_t smem[];
     float *const out_s = reinterpret_cast<float *>(smem + S::RING);                  // [WARPS][ROWS][OSTRIDE]
-    float2 *const ml_s = reinterpret_cast<float2 *>(smem + S::RING + S::OUT);        // [WARPS][ROWS]
-    uint8_t *const bars = smem + S::RING + S::OUT + WARPS * S::ROWS * 8;
+    float2 *const ml_s = reinterpret_cast<float2 *>(smem + S::RING + S::OUT);        // [2][WARPS][ROWS]
+    uint8_t *const bars = smem + S::RING + S::OUT + S::ML;
     int *const shared = reinterpret_cast<int *>(bars + WARPS * S::STAGES * 8);
+    WarpPieces *const pieces = reinterpret_cast<WarpPieces *>(bars + WARPS * S::STAGES * 8 + 16);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int G = a.Hq / a.Hkv;
 
@@ -200,44 +216,104 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
 
     uint8_t *const ring = smem + w * S::STAGES * S::STAGE_BYTES;
     const uint32_t bar0 = shared_addr(bars + w * S::STAGES * 8);
-    uint32_t phases = 0;                   // the parity that each stage waits for next
-    bool dead = false;                     // a wait gave up: nothing more is read
+    uint32_t asked = 0, taken = 0;         // chunks that went through the ring
+    bool dead = false;                     // a wait gave up: nothing more is read or written
     const int tA = 4 * (r >> 1) + (r & 1), tB = tA + 2;    // the tokens of this lane's MMA rows r and r + 8
 
+    // ---- this warp's share of the range: contiguous, so that most of its units are its own ------
+    long long at = begin + (end - begin) * w / WARPS;
+    const long long stop = begin + (end - begin) * (w + 1) / WARPS;
     Request rq = request_of(a, b, S::ROWS, false);
-    long long at = begin;
-    while (at < end) {
-        // ---- the next (request, rows, head) of the range ---------------------------------------
+    // A unit: the rows of one (request, block of rows, kv head), and the chunks of it that are this warp's.
+    struct Unit {
+        long long begin, end;
+        int b, q0, n, len, h, row0, rows, c0, count;
+    } u;
+    auto plan = [&]() {                    // of the unit at `at`
         while (at >= base + (long long)rq.chunks * rq.row_blocks * a.Hkv) {
             base += (long long)rq.chunks * rq.row_blocks * a.Hkv;
             rq = request_of(a, ++b, S::ROWS, false);
         }
-        const int unit = (int)((at - base) / rq.chunks);
-        const long long unit_begin = base + (long long)unit * rq.chunks, unit_end = unit_begin + rq.chunks;
-        const int h = unit % a.Hkv, row0 = unit / a.Hkv * S::ROWS, rows = min(S::ROWS, rq.n * G - row0);
-        const int c0 = rq.first_chunk + (int)(at - unit_begin);
-        const int c1 = rq.first_chunk + (int)(min(end, unit_end) - unit_begin);
-        const int32_t *const pages = a.page_table + (size_t)b * a.max_pages;
+        const int index = (int)((at - base) / rq.chunks);
+        u.begin = base + (long long)index * rq.chunks;
+        u.end = u.begin + rq.chunks;
+        u.b = b, u.q0 = rq.q0, u.n = rq.n, u.len = rq.len;
+        u.h = index % a.Hkv;
+        u.row0 = index / a.Hkv * S::ROWS;
+        u.rows = min(S::ROWS, rq.n * G - u.row0);
+        u.c0 = rq.first_chunk + (int)(at - u.begin);
+        u.count = (int)(min(stop, u.end) - at);
+    };
+    int page0 = -2, page1 = -2;            // pages of the two tiles of chunk (32-fold part) + lane; -2: past the end
+    uint32_t here = 0;                     // two bits a stage: which tiles of it were loaded
+    auto fetch = [&](int k) {              // the unit's k-th chunk
+        if ((k & 31) == 0) {
+            const int32_t *const pages = a.page_table + (size_t)u.b * a.max_pages;
+            const int kk = k + lane;
+            const long long t0 = (long long)(u.c0 + kk) * CHUNK, t1 = t0 + KV_TILE;
+            page0 = kk < u.count && t0 < u.len ? pages[t0 >> a.page_shift] : -2;
+            page1 = kk < u.count && t1 < u.len ? pages[t1 >> a.page_shift] : -2;
+            if ((page0 != -2 && (page0 < 0 || page0 >= a.num_pages)) || (page1 != -2 && (page1 < 0 || page1 >= a.num_pages)))
+                report(a.err, DEVERR_PAGE_RANGE);
+        }
+        const int s = asked++ & 1;
+        const int p0 = __shfl_sync(~0u, page0, k & 31), p1 = __shfl_sync(~0u, page1, k & 31);
+        const bool ok0 = p0 >= 0 && p0 < a.num_pages, ok1 = p1 >= 0 && p1 < a.num_pages;
+        here = (here & ~(3u << (2 * s))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * s);
+        if (lane == 0) {
+            const int t0 = (u.c0 + k) * CHUNK, in_page = t0 & ((1 << a.page_shift) - 1);
+            const uint32_t bar = bar0 + 8 * s;
+            uint8_t *dst = ring + s * S::STAGE_BYTES;
+            const uint8_t *src0 = a.pool + ((((size_t)p0 * a.Hkv + u.h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
+            barrier_expect(bar, (ok0 ? L::BYTES : 0) + (ok1 ? L::BYTES : 0));
+            if (ok0 && ok1 && a.page_shift > 4) {          // one page: 32 tokens in a row
+                bulk_copy(dst, src0, 2 * L::BYTES, bar);
+            } else {
+                if (ok0) bulk_copy(dst, src0, L::BYTES, bar);
+                if (ok1) {
+                    const int in1 = (t0 + KV_TILE) & ((1 << a.page_shift) - 1);
+                    bulk_copy(dst + L::BYTES,
+                              a.pool + ((((size_t)p1 * a.Hkv + u.h) << (a.page_shift - 4)) + (in1 >> 4)) * L::BYTES, L::BYTES, bar);
+                }
+            }
+        }
+    };
+    // A result that is part of its unit's: maximum, sum and weighted values of its rows.  Of a warp's
+    // range only the first unit (begun by another warp) and the last (not ended) are such: the first
+    // goes to out_s, the last over the ring, which is empty by then.
+    auto row_of = [&](const Unit &x, int col) {
+        const int row = x.row0 + col;
+        return (size_t)(x.q0 + row / G) * a.Hq + x.h * G + row % G;
+    };
+    if (lane == 0) pieces[w].first.rows = pieces[w].last.rows = 0;
 
+    bool more = at < stop;
+    if (more) {
+        plan();
+#pragma unroll
+        for (int i = 0; i < S::STAGES; ++i)
+            if (i < u.count) fetch(i);
+    }
+    while (more) {
         // ---- queries, as B fragments, and what their rows see -----------------------------------
         uint32_t qf[NT][2 * KS];
         float factor[NT][2];
         int last[NT][2];
         int last_min, first_max;
         {
-            const int i0 = row0 / G, i1 = (row0 + rows - 1) / G;
-            last_min = rq.len - rq.n + i0;
-            first_max = a.window > 0 ? rq.len - rq.n + i1 + 1 - a.window : 0;
+            const int i0 = u.row0 / G, i1 = (u.row0 + u.rows - 1) / G;
+            last_min = u.len - u.n + i0;
+            first_max = a.window > 0 ? u.len - u.n + i1 + 1 - a.window : 0;
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int row = row0 + t * 8 + r;
+            const int row = u.row0 + t * 8 + r;
             float top = 0.f, x[D / 4];
 #pragma unroll
             for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
-            if (t * 8 + r < rows) {
-                const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + (long long)(rq.q0 + row / G) * a.q_stride +
-                                                                   (h * G + row % G) * D + c * (D / 4));
+            if (t * 8 + r < u.rows) {
+                const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + (long long)(u.q0 + row / G) * a.q_stride +
+                                                                   (u.h * G + row % G) * D + c * (D / 4));
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     const uint4 v = __ldg(src + i);
@@ -264,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             for (int k = 0; k < 2; ++k) {
                 factor[t][k] = __shfl_sync(~0u, f, (2 * c + k) * 4);
                 const int col = t * 8 + 2 * c + k;
-                last[t][k] = col < rows ? rq.len - rq.n + (row0 + col) / G : -1;
+                last[t][k] = col < u.rows ? u.len - u.n + (u.row0 + col) / G : -1;
             }
         }
 
@@ -277,57 +353,17 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             l[t][0] = l[t][1] = 0.f;
         }
 
-        // ---- this warp's chunks: c0 + w, c0 + w + WARPS, ... ------------------------------------
-        const int count = c1 - c0 > w ? (c1 - c0 - w + WARPS - 1) / WARPS : 0;
-        int page0 = -1, page1 = -1;        // pages of the two tiles of chunk (32-fold part) + lane
-        uint32_t here = 0;                 // two bits a stage: which tiles of it were loaded
-        auto fetch = [&](int k) {
-            if ((k & 31) == 0) {
-                const int kk = k + lane, t0 = (c0 + w + kk * WARPS) * CHUNK, t1 = t0 + KV_TILE;
-                page0 = kk < count && t0 < rq.len ? pages[t0 >> a.page_shift] : -2;
-                page1 = kk < count && t1 < rq.len ? pages[t1 >> a.page_shift] : -2;
-                if ((page0 != -2 && (page0 < 0 || page0 >= a.num_pages)) ||
-                    (page1 != -2 && (page1 < 0 || page1 >= a.num_pages)))
-                    report(a.err, DEVERR_PAGE_RANGE);
-            }
-            const int s = k % S::STAGES;
-            const int p0 = __shfl_sync(~0u, page0, k & 31), p1 = __shfl_sync(~0u, page1, k & 31);
-            const bool ok0 = p0 >= 0 && p0 < a.num_pages, ok1 = p1 >= 0 && p1 < a.num_pages;
-            here = (here & ~(3u << (2 * s))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * s);
-            if (lane == 0) {
-                const int t0 = (c0 + w + k * WARPS) * CHUNK, in_page = t0 & ((1 << a.page_shift) - 1);
-                const uint32_t bar = bar0 + 8 * s;
-                uint8_t *dst = ring + s * S::STAGE_BYTES;
-                const uint8_t *src0 = a.pool + ((((size_t)p0 * a.Hkv + h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
-                barrier_expect(bar, (ok0 ? L::BYTES : 0) + (ok1 ? L::BYTES : 0));
-                if (ok0 && ok1 && p0 == p1 && a.page_shift > 4) {
-                    bulk_copy(dst, src0, 2 * L::BYTES, bar);
-                } else {
-                    if (ok0) bulk_copy(dst, src0, L::BYTES, bar);
-                    if (ok1) {
-                        const int in1 = (t0 + KV_TILE) & ((1 << a.page_shift) - 1);
-                        bulk_copy(dst + L::BYTES,
-                                  a.pool + ((((size_t)p1 * a.Hkv + h) << (a.page_shift - 4)) + (in1 >> 4)) * L::BYTES,
-                                  L::BYTES, bar);
-                    }
-                }
-            }
-        };
-        if (!dead) {
-#pragma unroll
-            for (int s = 0; s < S::STAGES; ++s)
-                if (s < count) fetch(s);
-        }
 
-        for (int k = 0; k < count && !dead; ++k) {
-            const int s = k % S::STAGES, t0 = (c0 + w + k * WARPS) * CHUNK;
-            if (!__all_sync(~0u, barrier_test(bar0 + 8 * s, phases >> s & 1) || barrier_wait(bar0 + 8 * s, phases >> s & 1))) {
-                barrier_wait(bar0 + 8 * (1 - s), phases >> (1 - s) & 1);
+        for (int k = 0; k < u.count && !dead; ++k) {
+            const int s = taken & 1, t0 = (u.c0 + k) * CHUNK;
+            const uint32_t parity = taken >> 1 & 1;
+            if (!__all_sync(~0u, barrier_test(bar0 + 8 * s, parity) || barrier_wait(bar0 + 8 * s, parity))) {
+                if (asked - taken > 1) barrier_wait(bar0 + 8 * (1 - s), (taken + 1) >> 1 & 1);
                 if (lane == 0) report(a.err, DEVERR_TIMEOUT);
                 dead = true;
                 break;
             }
-            phases ^= 1u << s;
+            ++taken;
             const uint8_t *stage = ring + s * S::STAGE_BYTES;
             const uint32_t loaded = here >> (2 * s) & 3u;
             const bool whole = loaded == 3u && t0 >= first_max && t0 + CHUNK - 1 <= last_min;
@@ -481,13 +517,26 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                 }
             }
             __syncwarp();                  // all lanes have read the stage
-            if (k + S::STAGES < count) {
+            if (k + S::STAGES < u.count) {
                 fence_async_shared();
                 fetch(k + S::STAGES);
             }
         }
 
-        // ---- join the warps ---------------------------------------------------------------------
+        // ---- the unit's end: the next one's codes are asked for, then its results leave ----------
+        const Unit x = u;
+        const bool begun = at == x.begin, ended = at + x.count == x.end;
+        at += x.count;
+        more = at < stop;
+        if (more) {
+            plan();
+            if (!dead) {
+                fence_async_shared();
+#pragma unroll
+                for (int i = 0; i < S::STAGES; ++i)
+                    if (i < u.count) fetch(i);
+            }
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -497,45 +546,80 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                 sum += __shfl_xor_sync(~0u, sum, 8);
                 sum += __shfl_xor_sync(~0u, sum, 16);
                 const int col = t * 8 + 2 * c + k2;
-                if (r == 0) ml_s[w * S::ROWS + col] = make_float2(m[t][k2], sum);
-                float *dst = out_s + (w * S::ROWS + col) * S::OSTRIDE + r * (D / 8);
+                if (begun && ended) {
+                    if (col >= x.rows || dead) continue;
+                    const size_t row = row_of(x, col);
+                    const float f = sum == 0.f ? 0.f : a.v_scale / sum;
+                    if (r == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (m[t][k2] + log2f(sum)) * LN2;
+                    uint32_t y[KS];
 #pragma unroll
-                for (int j = 0; j < KS; j += 2)
-                    *reinterpret_cast<float4 *>(dst + 2 * j) =
-                        make_float4(o[t][j][k2], o[t][j][k2 + 2], o[t][j + 1][k2], o[t][j + 1][k2 + 2]);
+                    for (int j = 0; j < KS; ++j)
+                        y[j] = sum == 0.f ? 0u : pack_of<T>(o[t][j][k2] * f, o[t][j][k2 + 2] * f);
+                    uint4 *dst = reinterpret_cast<uint4 *>((T *)a.o + row * D + r * (D / 8));
+#pragma unroll
+                    for (int j = 0; j < KS / 4; ++j) dst[j] = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                } else {
+                    if (r == 0) ml_s[((begun ? WARPS : 0) + w) * S::ROWS + col] = make_float2(m[t][k2], sum);
+                    float *dst = (begun ? reinterpret_cast<float *>(ring) : out_s + w * S::ROWS * S::OSTRIDE) + col * S::OSTRIDE + r * (D / 8);
+#pragma unroll
+                    for (int j = 0; j < KS; j += 2)
+                        *reinterpret_cast<float4 *>(dst + 2 * j) =
+                            make_float4(o[t][j][k2], o[t][j][k2 + 2], o[t][j + 1][k2], o[t][j + 1][k2 + 2]);
+                }
             }
-        __syncthreads();
-        const bool complete = unit_begin >= begin && unit_end <= end;
-        const int cta0 = (int)(unit_begin / per), cta1 = (int)((unit_end - 1) / per);
-        float *const partials = reinterpret_cast<float *>(a.ws + MAX_CTAS * 4);
-        constexpr int QUADS = S::ROWS * D / 4;
+        if (!(begun && ended) && lane == 0) {
+            Piece &y = begun ? pieces[w].last : pieces[w].first;
+            y.begin = x.begin, y.end = x.end, y.q0 = x.q0, y.h = x.h, y.row0 = x.row0, y.rows = x.rows;
+        }
+    }
+
+    // ---- join what the warps have of one unit ------------------------------------------------------
+    __syncthreads();
+    float *const partials = reinterpret_cast<float *>(a.ws + MAX_CTAS * 4);
+    constexpr int QUADS = S::ROWS * D / 4;
+    for (int from = 0; from < 2 * WARPS; ++from) {
+        // a unit begins with a warp's last piece, or before this CTA (then the first warp with a share has its
+        // first piece of it); it goes on in the first pieces of the warps behind
+        const bool is_last = from & 1;
+        const int w0 = from >> 1;
+        const Piece &x = is_last ? pieces[w0].last : pieces[w0].first;
+        if (x.rows == 0) continue;
+        if (!is_last) {
+            bool behind = x.begin >= begin;
+            for (int y = 0; y < w0; ++y) behind |= pieces[y].first.rows != 0;
+            if (behind) continue;
+        }
+        const bool complete = x.begin >= begin && x.end <= end;
+        const int cta0 = (int)(x.begin / per), cta1 = (int)((x.end - 1) / per);
         auto finish = [&](int col, int d, float4 v, float top, float sum) {
-            const int row = row0 + col;
-            const size_t at_row = (size_t)(rq.q0 + row / G) * a.Hq + h * G + row % G;
+            const int row = x.row0 + col;
+            const size_t at_row = (size_t)(x.q0 + row / G) * a.Hq + x.h * G + row % G;
             const float f = sum == 0.f ? 0.f : a.v_scale / sum;
-            uint32_t *dst = reinterpret_cast<uint32_t *>((T *)a.o + at_row * D + d);
-            *reinterpret_cast<uint2 *>(dst) = sum == 0.f ? make_uint2(0, 0) : make_uint2(pack_of<T>(v.x * f, v.y * f), pack_of<T>(v.z * f, v.w * f));
-            if (d == 0 && a.lse) a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+            *reinterpret_cast<uint2 *>((T *)a.o + at_row * D + d) =
+                sum == 0.f ? make_uint2(0, 0) : make_uint2(pack_of<T>(v.x * f, v.y * f), pack_of<T>(v.z * f, v.w * f));
+            if (d == 0 && a.lse) a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * LN2;
         };
         for (int i = tid; i < QUADS; i += THREADS) {
             const int col = i / (D / 4), d = i % (D / 4) * 4;
-            float top = NOTHING;
-#pragma unroll
-            for (int x = 0; x < WARPS; ++x) top = max_nan(top, ml_s[x * S::ROWS + col].x);
-            float sum = 0.f;
+            if (col >= x.rows) continue;
+            float top = NOTHING, sum = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int x = 0; x < WARPS; ++x) {
-                const float2 ml = ml_s[x * S::ROWS + col];
-                const float keep = exp2_fast(ml.x - top);
-                const float4 u = *reinterpret_cast<const float4 *>(out_s + (x * S::ROWS + col) * S::OSTRIDE + d);
-                sum += ml.y * keep;
-                v.x += u.x * keep, v.y += u.y * keep, v.z += u.z * keep, v.w += u.w * keep;
+            for (int y = w0; y < WARPS; ++y) {
+                const bool over_ring = is_last && y == w0;
+                if (!over_ring && !(pieces[y].first.rows && pieces[y].first.begin == x.begin)) continue;
+                const float2 ml = ml_s[((over_ring ? WARPS : 0) + y) * S::ROWS + col];
+                const float *src = over_ring ? reinterpret_cast<const float *>(smem + y * S::STAGES * S::STAGE_BYTES)
+                                             : out_s + y * S::ROWS * S::OSTRIDE;
+                const float4 z = *reinterpret_cast<const float4 *>(src + col * S::OSTRIDE + d);
+                const float to = max_nan(top, ml.x), keep = exp2_fast(top - to), add = exp2_fast(ml.x - to);
+                top = to;
+                sum = sum * keep + ml.y * add;
+                v.x = v.x * keep + z.x * add, v.y = v.y * keep + z.y * add;
+                v.z = v.z * keep + z.z * add, v.w = v.w * keep + z.w * add;
             }
-            if (complete) {
-                if (col < rows) finish(col, d, v, top, sum);
-            } else {
-                float *dst = partials + (size_t)(2 * blockIdx.x + (at == unit_begin)) * S::PARTIAL;
+            if (complete) finish(col, d, v, top, sum);
+            else {
+                float *dst = partials + (size_t)(2 * blockIdx.x + (x.begin >= begin)) * S::PARTIAL;
                 __stcg(reinterpret_cast<float4 *>(dst + col * D + d), v);
                 if (d == 0) __stcg(reinterpret_cast<float2 *>(dst + S::ROWS * D + 2 * col), make_float2(top, sum));
             }
@@ -555,25 +639,23 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                 __threadfence();
                 for (int i = tid; i < QUADS; i += THREADS) {
                     const int col = i / (D / 4), d = i % (D / 4) * 4;
-                    if (col >= rows) continue;
+                    if (col >= x.rows) continue;
                     float top = NOTHING, sum = 0.f;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int x = cta0; x <= cta1; ++x) {
-                        const float *src = partials + (size_t)(2 * x + (x == cta0)) * S::PARTIAL;
+                    for (int y = cta0; y <= cta1; ++y) {
+                        const float *src = partials + (size_t)(2 * y + (y == cta0)) * S::PARTIAL;
                         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + S::ROWS * D + 2 * col));
-                        const float4 u = __ldcg(reinterpret_cast<const float4 *>(src + col * D + d));
+                        const float4 z = __ldcg(reinterpret_cast<const float4 *>(src + col * D + d));
                         const float to = max_nan(top, ml.x), keep = exp2_fast(top - to), add = exp2_fast(ml.x - to);
                         top = to;
                         sum = sum * keep + ml.y * add;
-                        v.x = v.x * keep + u.x * add, v.y = v.y * keep + u.y * add;
-                        v.z = v.z * keep + u.z * add, v.w = v.w * keep + u.w * add;
+                        v.x = v.x * keep + z.x * add, v.y = v.y * keep + z.y * add;
+                        v.z = v.z * keep + z.z * add, v.w = v.w * keep + z.w * add;
                     }
                     finish(col, d, v, top, sum);
                 }
             }
         }
-        __syncthreads();                   // the joined results are read; the next segment writes over them
-        at = min(end, unit_end);
     }
 }
 

@@ -520,7 +520,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
 
             const int rr = p.row0 + my_row;
             const size_t at_row = (size_t)(p.q0 + rr / G) * a.Hq + p.h * G + rr % G;
-            constexpr float LN2 = 0.69314718055994531f;
             if (QT == 2) {
                 const float f = l == 0.f ? 0.f : a.v_scale / l;
 #pragma unroll 1
