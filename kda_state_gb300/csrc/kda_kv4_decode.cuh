@@ -86,6 +86,17 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+// a times one half of b
+__device__ __forceinline__ uint32_t hmul2_by(uint32_t a, uint32_t b, bool high) {
+    const __half2 x = *reinterpret_cast<const __half2 *>(&a), y = *reinterpret_cast<const __half2 *>(&b);
+    const __half2 d = __hmul2_rn(x, high ? __high2half2(y) : __low2half2(y));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -331,11 +342,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             top = max_nan(top, __shfl_xor_sync(~0u, top, 1));
             top = max_nan(top, __shfl_xor_sync(~0u, top, 2));
             const int e = min(max((int)(__float_as_uint(top) >> 23 & 255), 1), 253);
-            const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
+            const float down = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), a.scale_k), up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
             for (int i = 0; i < 2 * KS; ++i) qf[t][i] = half_pair(x[2 * i] * down, x[2 * i + 1] * down);
             // scores come back by columns: this lane holds those of rows 2 c and 2 c + 1
-            const float f = a.scale_k * up;
+            const float f = fabsf(a.scale_k) * up;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 factor[t][k] = __shfl_sync(~0u, f, (2 * c + k) * 4);
@@ -368,69 +379,103 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             const uint32_t loaded = here >> (2 * s) & 3u;
             const bool whole = loaded == 3u && t0 >= first_max && t0 + CHUNK - 1 <= last_min;
 
-            // scores of 32 tokens
+            // scores of 32 tokens: the two tiles' products alternate, so that neither waits for its own sums
             float y[2][NT][4];
+            {
+                uint32_t ka[2][LW], kb[2][LW], sa[2], sb[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t *tile = stage + i * L::BYTES;
-                uint32_t ka[LW], kb[LW], sa[2], sb[2];
-                if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(tile + tA * 64 + c * 16);
-                    const uint4 z = *reinterpret_cast<const uint4 *>(tile + tB * 64 + c * 16);
-                    ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
-                    kb[0] = z.x, kb[1] = z.y, kb[2] = z.z, kb[3] = z.w;
-                    const uint32_t fa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(tile + L::KS + tA * 8 + c * 2));
-                    const uint32_t fb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(tile + L::KS + tB * 8 + c * 2));
-                    sa[0] = __byte_perm(fa, 0, 0x1010), sa[1] = __byte_perm(fa, 0, 0x3232);
-                    sb[0] = __byte_perm(fb, 0, 0x1010), sb[1] = __byte_perm(fb, 0, 0x3232);
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(tile + tA * 32 + c * 8);
-                    const uint2 z = *reinterpret_cast<const uint2 *>(tile + tB * 32 + c * 8);
-                    ka[0] = x.x, ka[1] = x.y;
-                    kb[0] = z.x, kb[1] = z.y;
-                    sa[0] = sa[1] = __byte_perm(e4m3x2_to_f16x2(tile[L::KS + tA * 4 + c]), 0, 0x1010);
-                    sb[0] = sb[1] = __byte_perm(e4m3x2_to_f16x2(tile[L::KS + tB * 4 + c]), 0, 0x1010);
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t *tile = stage + i * L::BYTES;
+                    if constexpr (D == 128) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(tile + tA * 64 + c * 16);
+                        const uint4 z = *reinterpret_cast<const uint4 *>(tile + tB * 64 + c * 16);
+                        ka[i][0] = x.x, ka[i][1] = x.y, ka[i][LW - 2] = x.z, ka[i][LW - 1] = x.w;
+                        kb[i][0] = z.x, kb[i][1] = z.y, kb[i][LW - 2] = z.z, kb[i][LW - 1] = z.w;
+                        sa[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(tile + L::KS + tA * 8 + c * 2));
+                        sb[i] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(tile + L::KS + tB * 8 + c * 2));
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(tile + tA * 32 + c * 8);
+                        const uint2 z = *reinterpret_cast<const uint2 *>(tile + tB * 32 + c * 8);
+                        ka[i][0] = x.x, ka[i][1] = x.y;
+                        kb[i][0] = z.x, kb[i][1] = z.y;
+                        sa[i] = e4m3x2_to_f16x2(tile[L::KS + tA * 4 + c]);
+                        sb[i] = e4m3x2_to_f16x2(tile[L::KS + tB * 4 + c]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) y[i][t][0] = y[i][t][1] = y[i][t][2] = y[i][t][3] = 0.f;
                 }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) y[i][t][0] = y[i][t][1] = y[i][t][2] = y[i][t][3] = 0.f;
 #pragma unroll
                 for (int q = 0; q < LW; ++q) {
-                    uint32_t fa[4], fb[4];
-                    e2m1x8_to_f16x2(ka[q], fa);
-                    e2m1x8_to_f16x2(kb[q], fb);
-                    const int blk = D == 128 ? q / 2 : 0;
+                    uint32_t fa[2][4], fb[2][4];
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const uint32_t a0 = hmul2(fa[2 * z], sa[blk]), a1 = hmul2(fb[2 * z], sb[blk]);
-                        const uint32_t a2 = hmul2(fa[2 * z + 1], sa[blk]), a3 = hmul2(fb[2 * z + 1], sb[blk]);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            mma_16816(y[i][t], a0, a1, a2, a3, qf[t][4 * q + 2 * z], qf[t][4 * q + 2 * z + 1]);
+                    for (int i = 0; i < 2; ++i) {
+                        e2m1x8_to_f16x2(ka[i][q], fa[i]);
+                        e2m1x8_to_f16x2(kb[i][q], fb[i]);
                     }
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t a0 = hmul2_by(fa[i][2 * z], sa[i], D == 128 && q >= 2), a1 = hmul2_by(fb[i][2 * z], sb[i], D == 128 && q >= 2);
+                            const uint32_t a2 = hmul2_by(fa[i][2 * z + 1], sa[i], D == 128 && q >= 2), a3 = hmul2_by(fb[i][2 * z + 1], sb[i], D == 128 && q >= 2);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                mma_16816(y[i][t], a0, a1, a2, a3, qf[t][4 * q + 2 * z], qf[t][4 * q + 2 * z + 1]);
+                        }
                 }
             }
-            // y <- the scores, in units of log2; the maximum moves if a weight is too large
-            bool move = false;
+            // x: log2 of the weights; the maximum moves if one is too large
+            uint32_t seen = ~0u;               // a bit a score
+            if (!whole) {
+                seen = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int pos = t0 + i * KV_TILE + (e < 2 ? tA : tB), end_at = last[t][e & 1];
+                            if ((loaded >> i & 1) && pos <= end_at && (a.window <= 0 || pos > end_at - a.window))
+                                seen |= 1u << ((i * NT + t) * 4 + e);
+                        }
+            }
+            float x[2][NT][4];
+            auto weigh = [&]() {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[i][t][e] = fmaf(y[i][t][e], factor[t][e & 1], -m[t][e & 1]);
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!(seen >> ((i * NT + t) * 4 + e) & 1)) x[i][t][e] = -INFINITY;
+                }
+            };
+            weigh();
+            float high = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[i][t][e] *= factor[t][e & 1];
-                        if (!whole) {
-                            const int pos = t0 + i * KV_TILE + (e < 2 ? tA : tB), end_at = last[t][e & 1];
-                            if (!(loaded >> i & 1) || pos > end_at || (a.window > 0 && pos <= end_at - a.window))
-                                y[i][t][e] = -INFINITY;
-                        }
-                        move |= y[i][t][e] - m[t][e & 1] > MOVE;
-                    }
-            if (__any_sync(~0u, move)) {
+                    for (int e = 0; e < 4; e += 2) high = max3(high, x[i][t][e], x[i][t][e + 1]);
+            if (__any_sync(~0u, high > MOVE)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {
-                        float top = fmaxf(fmaxf(y[0][t][k2], y[0][t][k2 + 2]), fmaxf(y[1][t][k2], y[1][t][k2 + 2]));
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = k2; e < 4; e += 2)
+                                if (seen >> ((i * NT + t) * 4 + e) & 1) top = fmaxf(top, y[i][t][e] * factor[t][k2]);
                         top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
@@ -443,6 +488,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                             o[t][j][k2 + 2] *= keep;
                         }
                     }
+                weigh();
             }
             // values of 32 tokens
 #pragma unroll
@@ -454,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[e] = exp2_fast(y[i][t][e] - m[t][e & 1]);
+                        p[e] = exp2_fast(x[i][t][e]);
                         l[t][e & 1] += p[e];
                     }
                     pb[t][0] = transpose8(half_pair(p[0], p[1]));
@@ -473,7 +519,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                         for (int t = 0; t < NT; ++t) {
                             float hit[4] = {0.f, 0.f, 0.f, 0.f}, sees[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) sees[e] = y[i][t][e] == -INFINITY ? 0.f : 1.f;
+                            for (int e = 0; e < 4; ++e) sees[e] = seen >> ((i * NT + t) * 4 + e) & 1 ? 1.f : 0.f;
                             seen_b[t][0] = transpose8(half_pair(sees[0], sees[1]));
                             seen_b[t][1] = transpose8(half_pair(sees[2], sees[3]));
                             mma_16816(hit, n01, n01, n23, n23, seen_b[t][0], seen_b[t][1]);

@@ -137,11 +137,6 @@ __device__ __forceinline__ uint64_t pair_of_floats(float a, float b) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
     return v;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
