@@ -72,7 +72,7 @@ struct alignas(16) TileMeta {
     uint8_t nan_group[4][16];          // whether that group has any (else its bytes above are old)
     uint8_t missing[4][16];            // 255: the group's page is out of range
     Part parts[4];
-    int raw_live[8], raw_bad[8];       // by stage of codes: tokens before the end; a bit a run of 16 out of range
+    int2 raw_about[8];                 // by stage of codes: tokens before the end; a bit a run of 16 out of range
     uint32_t tmem;
     int last, dead;
     uint64_t bars[25 + 2 * 6];
@@ -144,6 +144,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) 
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
     asm volatile(
@@ -458,34 +463,33 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         }
                     }
                 }
-                const uint64_t ff = pair_of_floats(factor, factor), mm = pair_of_floats(-m, -m);
+                // a masked score is -inf here: its weight is 0 unless the factor is (then NaN: 0 in its place)
+                const float by = some && factor == 0.f ? 1.f : factor;
+                if (some && factor == 0.f) {
+#pragma unroll
+                    for (int e = 0; e < TT; ++e)
+                        if (x[e] != 0xff800000u) x[e] = __float_as_uint(__uint_as_float(x[e]) * factor);
+                }
+                const uint64_t ff = pair_of_floats(by, by), mm = pair_of_floats(-m, -m);
                 uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-                    const uint32_t v = some ? visible(c) : ~0u;
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t pk[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        uint32_t &x0 = x[32 * c + e], &x1 = x[32 * c + e + 1];
-                        fma_pair(x0, x1, ff, mm);
-                        const float p0 = exp2_fast(__uint_as_float(x0)), p1 = exp2_fast(__uint_as_float(x1));
-                        x0 = __float_as_uint(p0), x1 = __float_as_uint(p1);
-                    }
-                    if (some) {            // a masked score times a scale of 0 is a NaN: the mask has the last word
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(v >> e & 1)) x[32 * c + e] = 0;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const uint64_t u0 = pair_of_floats(__uint_as_float(x[32 * c + e]), __uint_as_float(x[32 * c + e + 1]));
-                        const uint64_t u1 = pair_of_floats(__uint_as_float(x[32 * c + e + 2]), __uint_as_float(x[32 * c + e + 3]));
+                    for (int e = 0; e < 16; e += 4) {
+                        uint64_t u0, u1;
+                        uint32_t *const z = x + 16 * c + e;
+                        fma_pair(z[0], z[1], ff, mm);
+                        fma_pair(z[2], z[3], ff, mm);
+                        const float p0 = exp2_fast(__uint_as_float(z[0])), p1 = exp2_fast(__uint_as_float(z[1]));
+                        const float p2 = exp2_fast(__uint_as_float(z[2])), p3 = exp2_fast(__uint_as_float(z[3]));
+                        u0 = pair_of_floats(p0, p1), u1 = pair_of_floats(p2, p3);
                         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(u0));
                         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(u1));
-                        pk[e / 2] = half_pair(__uint_as_float(x[32 * c + e]), __uint_as_float(x[32 * c + e + 1]));
-                        pk[e / 2 + 1] = half_pair(__uint_as_float(x[32 * c + e + 2]), __uint_as_float(x[32 * c + e + 3]));
+                        pk[e / 2] = half_pair(p0, p1);
+                        pk[e / 2 + 1] = half_pair(p2, p3);
                     }
-                    tmem_st16(s_col + 16 * c, pk);
+                    tmem_st8(s_col + 8 * c, pk);
                 }
                 l += (__uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32))) +
                      (__uint_as_float((uint32_t)sum1) + __uint_as_float((uint32_t)(sum1 >> 32)));
@@ -626,109 +630,106 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
     } else if (w < 16) {
         give_registers<REGS_UNPACK>();
         // ================================ unpack =======================================================
-        // A lane holds, of token 8 uw + lane / 4 of 64, a quarter of the channels of K and then of V.
+        // A lane holds, of token 8 uw + lane / 4 of each half tile, a quarter of the channels of K and of V: all of a
+        // tile's codes are in registers, and their stages free again, before the first is converted.
         constexpr int W = D / 32;                              // words of a lane
         const int uw = w - 8, c = lane & 3, tok = uw * 8 + (lane >> 2);
-        const uint32_t in_box = (uint32_t)((tok >> 4) * L::BYTES);
+        const uint8_t *const codes = smem + S::RAW_AT + (tok >> 4) * L::BYTES;
+        const int in_tile = tok & 15;
         const uint32_t base = shared_addr(smem);
-        uint32_t raw = 0, raw_round = 0;
+        // V: row r of stored matrix m is the channel that lane quarter r / 2 put there
+        const int am = lane >> 3, ac = lane >> 1 & 3;
+        const int v_channel = 8 * W * ac + 2 * ((am + ac) & 3) + (lane & 1);
+        uint32_t raw = 0, raw_parity = 0;
         for (uint32_t n = 0;; ++n) {                           // tiles
             const uint32_t stage = n & 1, round = n >> 1, ring = n & 3;
+            uint32_t k[2][W], v[2][W], ks[2], vs[2], gone = 0;
             bool end = false;
-            if (round > 0) wait_or_dead(K_FREE + 8 * stage, (round - 1) & 1, dead);
-            uint32_t r = raw, rr = raw_round;
-#pragma unroll 1
+#pragma unroll
             for (int box = 0; box < 2; ++box) {
-                wait_or_dead(RAW_FULL + 8 * r, rr & 1, dead);
-                const int live = meta.raw_live[r], bad = meta.raw_bad[r];
-                if (__any_sync(~0u, live < 0 || *dead)) {
-                    end = true;
-                    break;
-                }
-                const uint8_t *t = smem + S::RAW_AT + r * S::RAW_BYTES + in_box;
-                uint32_t k[W], scale;
+                wait_or_dead(RAW_FULL + 8 * raw, raw_parity, dead);
+                const int2 about = meta.raw_about[raw];        // tokens before the end; runs of 16 out of range
+                end |= about.x < 0;
+                const uint8_t *t = codes + raw * S::RAW_BYTES;
                 if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(t + (tok & 15) * 64 + c * 16);
-                    // lanes 2 and 3 of four take their words in the order 2, 3, 0, 1: no bank conflicts below
-                    k[0] = c & 2 ? x.z : x.x, k[1] = c & 2 ? x.w : x.y, k[2] = c & 2 ? x.x : x.z, k[3] = c & 2 ? x.y : x.w;
-                    scale = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(t + L::KS + (tok & 15) * 8 + c * 2));
-                    if (c & 2) scale = __byte_perm(scale, 0, 0x1032);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(t + in_tile * 64 + c * 16);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(t + L::VC + in_tile * 64 + c * 16);
+                    ks[box] = *reinterpret_cast<const uint16_t *>(t + L::KS + in_tile * 8 + c * 2);
+                    vs[box] = t[L::VS + 2 * c * KV_TILE + in_tile] | (uint32_t)t[L::VS + (2 * c + 1) * KV_TILE + in_tile] << 8;
+                    // lanes 2 and 3 of four take K's words in the order 2, 3, 0, 1: no bank conflicts below
+                    k[box][0] = c & 2 ? x.z : x.x, k[box][1] = c & 2 ? x.w : x.y;
+                    k[box][W - 2] = c & 2 ? x.x : x.z, k[box][W - 1] = c & 2 ? x.y : x.w;
+                    v[box][0] = y.x, v[box][1] = y.y, v[box][W - 2] = y.z, v[box][W - 1] = y.w;
+                    if (c & 2) ks[box] = __byte_perm(ks[box], 0, 0x4401);
                 } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(t + (tok & 15) * 32 + c * 8);
-                    k[0] = x.x, k[1] = x.y;
-                    scale = e4m3x2_to_f16x2(t[L::KS + (tok & 15) * 4 + c]);
+                    const uint2 x = *reinterpret_cast<const uint2 *>(t + in_tile * 32 + c * 8);
+                    const uint2 y = *reinterpret_cast<const uint2 *>(t + L::VC + in_tile * 32 + c * 8);
+                    ks[box] = t[L::KS + in_tile * 4 + c];
+                    vs[box] = t[L::VS + c * KV_TILE + in_tile];
+                    k[box][0] = x.x, k[box][1] = x.y;
+                    v[box][0] = y.x, v[box][1] = y.y;
                 }
-                uint8_t *const tile = smem + S::K_AT + stage * S::KBYTES;
+                const bool away = about.y >> (tok >> 4) & 1;
+                gone |= (uint32_t)away << box;
+                if (away || tok >= about.x) vs[box] = 0;       // nothing that no row sees goes into a product
+                __syncwarp();
+                if (lane == 0) barrier_arrive(RAW_FREE + 8 * raw);
+                if (++raw == S::RAW) raw = 0, raw_parity ^= 1;
+            }
+            if (__any_sync(~0u, end || *dead)) break;
+            // what the softmax has to know of these tokens: a page out of range, NaN values (their scales: 0 here)
+            const uint32_t both = vs[0] | vs[1] << 16, nan4 = (((both & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+            const bool any = __any_sync(~0u, nan4 != 0);
+            if (round > 0) wait_or_dead(K_FREE + 8 * stage, (round - 1) & 1, dead);
+            if (any) {
+#pragma unroll
+                for (int box = 0; box < 2; ++box) {
+                    const uint32_t n0 = __ballot_sync(~0u, nan4 >> (16 * box) & 1), n1 = __ballot_sync(~0u, nan4 >> (16 * box + 8) & 1);
+                    if (lane < 4) {
+                        uint32_t x0 = 0, x1 = 0;
+                        for (int i = 0; i < 8; ++i) {
+                            x0 |= (n0 >> (4 * i + c) & 1) << i;
+                            x1 |= (n1 >> (4 * i + c) & 1) << i;
+                        }
+                        meta.nan_value[ring][box * 8 + uw][D == 128 ? 2 * c : c] = (uint8_t)x0;
+                        if (D == 128) meta.nan_value[ring][box * 8 + uw][2 * c + 1] = (uint8_t)x1;
+                    }
+                }
+                vs[0] &= ~(nan4 * 255u);
+                vs[1] &= ~((nan4 >> 16) * 255u);
+            }
+            if (lane < 2) {                                    // a lane a half tile
+                meta.nan_group[ring][lane * 8 + uw] = any;
+                meta.missing[ring][lane * 8 + uw] = gone >> lane & 1 ? 255 : 0;
+            }
+#pragma unroll
+            for (int box = 0; box < 2; ++box) {
+                const uint32_t two = e4m3x2_to_f16x2(ks[box]);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    const uint32_t sc = __byte_perm(scale, 0, i >= 2 ? 0x3232 : 0x1010);
                     const int chunk = W * c + (D == 128 ? i ^ (c & 2) : i);
                     uint32_t f[4];
-                    e2m1x8_to_f16x2(k[i], f);
-                    *reinterpret_cast<uint4 *>(tile + chunk_at(box * BOX + tok, chunk, TT)) =
-                        make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
+                    e2m1x8_to_f16x2(k[box][i], f);
+                    *reinterpret_cast<uint4 *>(smem + S::K_AT + stage * S::KBYTES + chunk_at(box * BOX + tok, chunk, TT)) =
+                        make_uint4(hmul2_by(f[0], two, i >= 2), hmul2_by(f[1], two, i >= 2), hmul2_by(f[2], two, i >= 2), hmul2_by(f[3], two, i >= 2));
                 }
-                // what the softmax has to know of these 8 tokens: a page out of range, NaN values
-                const bool gone = bad >> (tok >> 4) & 1, off = gone || tok >= live;
-                uint32_t vs0 = 0, vs1 = 0;
-                if (!off) {
-                    vs0 = t[L::VS + (D == 128 ? 2 * c : c) * KV_TILE + (tok & 15)];
-                    if (D == 128) vs1 = t[L::VS + (2 * c + 1) * KV_TILE + (tok & 15)];
-                }
-                const uint32_t n0 = __ballot_sync(~0u, (vs0 & 127) == 127), n1 = __ballot_sync(~0u, (vs1 & 127) == 127);
-                if ((n0 | n1) && lane < 4) {
-                    uint32_t x0 = 0, x1 = 0;
-                    for (int i = 0; i < 8; ++i) {
-                        x0 |= (n0 >> (4 * i + c) & 1) << i;
-                        x1 |= (n1 >> (4 * i + c) & 1) << i;
-                    }
-                    meta.nan_value[ring][box * 8 + uw][D == 128 ? 2 * c : c] = (uint8_t)x0;
-                    if (D == 128) meta.nan_value[ring][box * 8 + uw][2 * c + 1] = (uint8_t)x1;
-                }
-                if (lane == 0) {
-                    meta.nan_group[ring][box * 8 + uw] = (n0 | n1) != 0;
-                    meta.missing[ring][box * 8 + uw] = gone ? 255 : 0;
-                }
-                if (++r == S::RAW) r = 0, ++rr;
             }
-            if (end) break;
             fence_async_shared();
             __syncwarp();
             if (lane == 0) barrier_arrive(K_FULL + 8 * stage);
 
             if (round > 0) wait_or_dead(V_FREE + 8 * stage, (round - 1) & 1, dead);
             const uint32_t v_tile = base + S::V_AT + stage * S::KBYTES;
-#pragma unroll 1
-            for (int box = 0; box < 2; ++box) {
-                const int live = meta.raw_live[raw], bad = meta.raw_bad[raw];
-                const bool off = (bad >> (tok >> 4) & 1) || tok >= live;
-                const uint8_t *t = smem + S::RAW_AT + raw * S::RAW_BYTES + in_box;
-                uint32_t v[W], sc[W / 2];
-                if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(t + L::VC + (tok & 15) * 64 + c * 16);
-                    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(t + L::VC + (tok & 15) * 32 + c * 8);
-                    v[0] = x.x, v[1] = x.y;
-                }
 #pragma unroll
-                for (int i = 0; i < W / 2; ++i) {              // NaN scales and tokens past the end: 0
-                    const uint32_t byte = t[L::VS + (W / 2 * c + i) * KV_TILE + (tok & 15)];
-                    sc[i] = __byte_perm(e4m3x2_to_f16x2(off || (byte & 127) == 127 ? 0u : byte), 0, 0x1010);
-                }
-                // this lane's address: row r of matrix m is the channel that lane quarter r / 2 put there
-                const int am = lane >> 3, ac = lane >> 1 & 3;
+            for (int box = 0; box < 2; ++box) {
+                const uint32_t two = e4m3x2_to_f16x2(vs[box]);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     uint32_t f[4];
-                    e2m1x8_to_f16x2(__funnelshift_r(v[i], v[i], 8 * c), f);
-                    const int ch = 8 * (W * ac + i) + 2 * ((am + ac) & 3) + (lane & 1);
-                    store_transposed(v_tile + chunk_at(ch, box * 8 + uw, D), hmul2(f[0], sc[i / 2]), hmul2(f[1], sc[i / 2]),
-                                     hmul2(f[2], sc[i / 2]), hmul2(f[3], sc[i / 2]));
+                    e2m1x8_to_f16x2(__funnelshift_r(v[box][i], v[box][i], 8 * c), f);
+                    store_transposed(v_tile + chunk_at(v_channel + 8 * i, box * 8 + uw, D), hmul2_by(f[0], two, i >= 2), hmul2_by(f[1], two, i >= 2),
+                                     hmul2_by(f[2], two, i >= 2), hmul2_by(f[3], two, i >= 2));
                 }
-                __syncwarp();
-                if (lane == 0) barrier_arrive(RAW_FREE + 8 * raw);
-                if (++raw == S::RAW) raw = 0, ++raw_round;
             }
             fence_async_shared();
             __syncwarp();
@@ -873,8 +874,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     const bool ok = page >= 0 && page < a.num_pages;
                     const uint32_t oks = __ballot_sync(~0u, ok) & 15u, gone = __ballot_sync(~0u, !ok && page != -2) & 15u;
                     if (lane == 0) {
-                        meta.raw_live[raw] = (int)min(max((long long)p.len - from - (long long)i * BOX, 0LL), (long long)BOX);
-                        meta.raw_bad[raw] = gone;
+                        meta.raw_about[raw] = make_int2((int)min(max((long long)p.len - from - (long long)i * BOX, 0LL), (long long)BOX), gone);
                         if (gone) report(a.err, DEVERR_PAGE_RANGE);
                         barrier_expect(RAW_FULL + 8 * raw, __popc(oks) * L::BYTES);
                     }
@@ -894,10 +894,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     if (i < raw || raw_round > 0) barrier_wait(RAW_FULL + 8 * i, (i < raw ? raw_round : raw_round - 1) & 1);
             }
             // the end, for the unpacking warps; the last CTA leaves the counters as the next call needs them
-            if (raw_round > 0) wait_or_dead(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead);
+            for (int i = 0; i < 2; ++i) {              // (they look at two stages at a time)
+                if (raw_round > 0) wait_or_dead(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead);
+                if (lane == 0) {
+                    meta.raw_about[raw] = make_int2(-1, 0);
+                    barrier_arrive(RAW_FULL + 8 * raw);
+                }
+                if (++raw == S::RAW) raw = 0, ++raw_round;
+            }
             if (lane == 0) {
-                meta.raw_live[raw] = -1;
-                barrier_arrive(RAW_FULL + 8 * raw);
                 if (atomicAdd(counters + CTAS_DONE, 1) == (int)gridDim.x - 1) {
                     counters[NEXT_PART] = 0;
                     counters[CTAS_DONE] = 0;
