@@ -871,34 +871,35 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 if (!found) break;
                 const int32_t *const pages = a.page_table + (size_t)p.b * a.max_pages;
                 const int boxes = 2 * p.tiles, from = p.tile0 * TT;
-                auto look = [&](int i) {               // the page of the i-th 16 tokens of the part; -2 past the end
+                // a lane looks up one run of 16 tokens of each 8 stages, and asks for it when its stage's turn comes
+                auto look = [&](int i) {               // the page of the part's i-th run; -2 past the end
                     const long long pos = (long long)from + (long long)i * KV_TILE;
                     return i < boxes * 4 && pos < p.len ? pages[pos >> a.page_shift] : -2;
                 };
-                int now = look(lane), then = look(32 + lane);
-                for (int i = 0; i < boxes; ++i) {
-                    if (i > 0 && (i & 7) == 0) {
-                        now = then;
-                        then = look((i + 8) * 4 + lane);
-                    }
-                    if (raw_round > 0) wait_or_dead(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead);
-                    // lanes 0..3: one run of 16 tokens each
-                    const int page = __shfl_sync(~0u, now, (i & 7) * 4 + (lane & 3));
+                const bool one_copy = a.page_shift >= 6;       // a stage lies in one page
+                int then = look(lane);
+                for (int i0 = 0; i0 < boxes; i0 += 8) {
+                    const int page = then;
+                    then = look((i0 + 8) * 4 + lane);
                     const bool ok = page >= 0 && page < a.num_pages;
-                    const uint32_t oks = __ballot_sync(~0u, ok) & 15u, gone = __ballot_sync(~0u, !ok && page != -2) & 15u;
-                    if (lane == 0) {
-                        meta.raw_about[raw] = make_int2((int)min(max((long long)p.len - from - (long long)i * BOX, 0LL), (long long)BOX), gone);
-                        if (gone) report(a.err, DEVERR_PAGE_RANGE);
-                        barrier_expect(RAW_FULL + 8 * raw, __popc(oks) * L::BYTES);
+                    const uint32_t oks = __ballot_sync(~0u, ok), gone = __ballot_sync(~0u, !ok && page != -2);
+                    if (gone && lane == 0) report(a.err, DEVERR_PAGE_RANGE);
+                    const int in_page = (from + (i0 * 4 + lane) * KV_TILE) & ((1 << a.page_shift) - 1);
+                    const uint8_t *const src = a.pool + ((((size_t)page * a.Hkv + p.h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
+                    const int mine = lane & 3, left = p.len - from - i0 * BOX;
+                    for (int i = 0; i < min(8, boxes - i0); ++i) {
+                        if (raw_round > 0) wait_or_dead(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead);
+                        const int runs = __popc(oks >> (4 * i) & 15u);
+                        if (lane == 4 * i) {
+                            meta.raw_about[raw] = make_int2(min(max(left - i * BOX, 0), BOX), gone >> (4 * i) & 15u);
+                            barrier_expect(RAW_FULL + 8 * raw, runs * L::BYTES);
+                        }
+                        __syncwarp();
+                        if (lane >> 2 == i && ok && (mine == 0 || !one_copy))
+                            bulk_copy(smem + S::RAW_AT + raw * S::RAW_BYTES + mine * L::BYTES, src, one_copy ? runs * L::BYTES : L::BYTES,
+                                      RAW_FULL + 8 * raw);
+                        if (++raw == S::RAW) raw = 0, ++raw_round;
                     }
-                    __syncwarp();
-                    if (lane < 4 && ok) {
-                        const int in_page = (from + i * BOX + lane * KV_TILE) & ((1 << a.page_shift) - 1);
-                        bulk_copy(smem + S::RAW_AT + raw * S::RAW_BYTES + lane * L::BYTES,
-                                  a.pool + ((((size_t)page * a.Hkv + p.h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES, L::BYTES,
-                                  RAW_FULL + 8 * raw);
-                    }
-                    if (++raw == S::RAW) raw = 0, ++raw_round;
                 }
             }
             // after a wait that gave up: the copies that were asked for may still be on their way
