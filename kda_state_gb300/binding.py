@@ -15,8 +15,8 @@ without a report.
 """
 from __future__ import annotations
 
+import array
 import ctypes
-import operator
 import os
 from dataclasses import dataclass
 
@@ -93,7 +93,6 @@ def lib() -> ctypes.CDLL:
                                        i, vp, f, f, f, ip, vp]
         L.kda_slot_copy.argtypes = [i, ctypes.POINTER(ctypes.c_void_p), ctypes.c_size_t, i, ip, ip,
                                     i, ip, vp]
-        vpp = ctypes.POINTER(ctypes.c_void_p)
         sz = ctypes.c_size_t
         L.kda_kv4_append.argtypes = [i, i, i, i, i, vp, ll, vp, ll, ip, ip, ip, i, i, vp, i, f, f, ip,
                                      vp]
@@ -103,10 +102,10 @@ def lib() -> ctypes.CDLL:
         L.kda_kv4_attention.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, vp, i, i, f, f,
                                         f, vp, vp, vp, sz, ip, vp]
         L.kda_page_alloc.argtypes = [i, i, i, i, ip, ip, ip, ip, ip, vp]
-        L.kda_page_fork.argtypes = [i, vpp, sz, i, i, i, i, ip, ip, ip, ip, ip, i, vp, sz, ip, vp]
+        L.kda_page_fork.argtypes = [i, vp, sz, i, i, i, i, ip, ip, ip, ip, ip, i, vp, sz, ip, vp]
         L.kda_page_free.argtypes = [i, i, i, i, ip, ip, ip, ip, i, ip, vp]
-        L.kda_page_compact.argtypes = [i, vpp, sz, i, i, i, ip, ip, ip, vp, sz, ip, vp]
-        L.kda_page_copy.argtypes = [i, vpp, sz, i, ip, ip, i, ip, vp]
+        L.kda_page_compact.argtypes = [i, vp, sz, i, i, i, ip, ip, ip, vp, sz, ip, vp]
+        L.kda_page_copy.argtypes = [i, vp, sz, i, ip, ip, i, ip, vp]
         L.kda_selftest_bounded_wait.argtypes = [ip, i, vp]
         L.kda_selftest_prefill_wait.argtypes = [i, i, i, vp, vp, vp, vp, vp, ip, ip, vp, i, ip, ip,
                                                 vp, ip, i, vp]
@@ -634,7 +633,8 @@ def kda_slot_copy(pools, src, dst, dev_err=None, stream=None):
 KV_TILE = 16          # tokens of a tile
 _KV_DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_FP16}
 _U8 = torch.uint8
-_KIND = operator.attrgetter("dtype", "shape")
+_width, _device_of = torch.Tensor.element_size, torch.Tensor.get_device
+_dense, _address = torch.Tensor.is_contiguous, torch.Tensor.data_ptr
 
 
 def kv4_tile_bytes(D: int = K_DIM) -> int:
@@ -764,10 +764,16 @@ def kda_kv4_gather(cu_seqlens, start, total_tokens: int, page_table, pool, dtype
     ta, B, M = _table(page_table, pool)
     if k is None:
         k = torch.empty(T, H, D, dtype=dtype, device=pool.device)
+        ka = k.data_ptr()
+    else:
+        ka = _ptr(k, "k", (T, H, D), dtype, pool)
     if v is None:
         v = torch.empty(T, H, D, dtype=dtype, device=pool.device)
+        va = v.data_ptr()
+    else:
+        va = _ptr(v, "v", (T, H, D), dtype, pool)
     status = lib().kda_kv4_gather(
-        dt, B, T, H, D, _ptr(k, "k", (T, H, D), dtype, pool), _ptr(v, "v", (T, H, D), dtype, pool),
+        dt, B, T, H, D, ka, va,
         _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, pool), _ptr(start, "start", (B,), I32, pool),
         ta, M, page_size, pa, pages, k_scale, v_scale, _err_ptr(dev_err, pool),
         _stream_of(stream, pool))
@@ -794,8 +800,14 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
     ta, B, M = _table(page_table, q)
     if o is None:
         o = torch.empty(T, H, D, dtype=dtype, device=q.device)
+        oa = o.data_ptr()
+    else:
+        oa = _ptr(o, "o", shape, dtype, q)
     if lse is None:
         lse = torch.empty(T, H, dtype=F32, device=q.device)
+        la = lse.data_ptr()
+    else:
+        la = _ptr(lse, "lse", (T, H), F32, q)
     if workspace is None:
         workspace = make_kv4_workspace(q.device)
     _first(workspace, "workspace", 1)
@@ -803,8 +815,8 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
     status = lib().kda_kv4_attention(
         dt, B, T, max_q, H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, q),
         _ptr(kv_lens, "kv_lens", (B,), I32, q), ta, M, page_size, pa, pages, window,
-        D ** -0.5 if scale is None else scale, k_scale, v_scale, _ptr(o, "o", shape, dtype, q),
-        _ptr(lse, "lse", (T, H), F32, q), _ptr(workspace, "workspace", (wb,), _U8, q), wb,
+        D ** -0.5 if scale is None else scale, k_scale, v_scale, oa, la,
+        _ptr(workspace, "workspace", (wb,), _U8, q), wb,
         _err_ptr(dev_err, q), _stream_of(stream, q))
     _check("kda_kv4_attention", status)
     return o, lse
@@ -821,25 +833,27 @@ def _page_state(refs, page_table, lens):
 
 
 def _page_pools(pools, num_pages, first):
-    """Layers' pools of one dtype and shape [num_pages, ...].  Returns (addresses, bytes of a page)."""
+    """Layers' pools [num_pages, ...] with pages of one size.  Returns (the array of their
+    addresses, its address, bytes of a page); the array has to outlive the call."""
     if len(pools) == 0:
         raise ValueError("pools must be a non-empty list")
-    p = pools[0]
-    one = isinstance(p, torch.Tensor) and p.dim() >= 2 and p.shape[0] == num_pages
-    if one and all(map(torch.is_tensor, pools)):
-        one = (set(map(_KIND, pools)) == {(p.dtype, p.shape)} and
-               set(map(torch.Tensor.get_device, pools)) == {first.get_device()} and
-               all(map(torch.Tensor.is_contiguous, pools)))
-    else:
+    try:
+        shapes, widths = [p.shape for p in pools], list(map(_width, pools))
+        one = (shapes.count(shapes[0]) == widths.count(widths[0]) == len(pools) and
+               len(shapes[0]) >= 2 and shapes[0][0] == num_pages and
+               set(map(_device_of, pools)) == {first.get_device()} and all(map(_dense, pools)))
+    except (AttributeError, TypeError):
         one = False
     if not one:
         for n, q in enumerate(pools):
             _need(q, "pools[%d]" % n, device=first.device)
-            if q.dim() < 2 or q.shape[0] != num_pages or q.shape != p.shape or q.dtype != p.dtype:
+            if q.dim() < 2 or q.shape[0] != num_pages or q.shape != pools[0].shape or (
+                    q.dtype != pools[0].dtype):
                 raise ValueError("pools[%d]: every pool is [%d, ...] of one shape and dtype" % (
                     n, num_pages))
-    ptrs = (ctypes.c_void_p * len(pools))(*map(torch.Tensor.data_ptr, pools))
-    return ptrs, p.numel() // num_pages * p.element_size()
+    ptrs = array.array("Q", map(_address, pools))
+    p = pools[0]
+    return ptrs, ptrs.buffer_info()[0], p.numel() // num_pages * p.element_size()
 
 
 def kda_page_alloc(refs, page_table, lens, grow, page_size: int, dev_err=None, stream=None):
@@ -858,7 +872,7 @@ def kda_page_fork(pools, refs, page_table, lens, src, dst, page_size: int, works
     copy of its partial last page in every pool of the list.  ``workspace``: int32, at
     least 2 n; a call without one makes its own."""
     ra, ta, la, B, M, N = _page_state(refs, page_table, lens)
-    ptrs, page_bytes = _page_pools(pools, N, refs)
+    keep, ptrs, page_bytes = _page_pools(pools, N, refs)
     _first(src, "src", 1)
     n = src.numel()
     if workspace is None:
@@ -887,7 +901,7 @@ def kda_page_compact(pools, refs, page_table, live=None, workspace=None, dev_err
     every pool; refs and page_table follow.  Returns live, int32 [1] on the device: the
     pages from there on are free.  ``workspace``: int32, at least 3 num_pages + 16."""
     ra, ta, _, B, M, N = _page_state(refs, page_table, None)
-    ptrs, page_bytes = _page_pools(pools, N, refs)
+    keep, ptrs, page_bytes = _page_pools(pools, N, refs)
     if live is None:
         live = torch.empty(1, dtype=I32, device=refs.device)
     if workspace is None:
@@ -910,7 +924,7 @@ def kda_page_copy(pools, src, dst, dev_err=None, stream=None):
     n = src.numel()
     _need(pools[0], "pools[0]", device=src.device)
     N = pools[0].shape[0]
-    ptrs, page_bytes = _page_pools(pools, N, src)
+    keep, ptrs, page_bytes = _page_pools(pools, N, src)
     status = lib().kda_page_copy(
         len(pools), ptrs, page_bytes, N, _ptr(src, "src", (n,), I32, src),
         _ptr(dst, "dst", (n,), I32, src), n, _err_ptr(dev_err, src), _stream_of(stream, src))

@@ -174,6 +174,9 @@ struct PageCopyParams {
     size_t page_bytes;
     const int32_t *n_dev;          // the number of pairs on the device, or NULL: n
     const int32_t *src, *dst;
+    long long cells;               // a compaction's page table entries, sent through map; or 0
+    int32_t *table;
+    const int32_t *map;
     int32_t *err;
     uint8_t *pool[KDA_MAX_LAYERS];
 };

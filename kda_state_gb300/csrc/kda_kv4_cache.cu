@@ -5,6 +5,12 @@
 // One thread holds one block of 16 channels: 32 bytes in, 8 bytes of codes and
 // one scale out, no communication.  Both directions are bound by HBM for
 // prompts and by the launch for single tokens.
+//
+// The quotients are products with a reciprocal, rounded to 18 bits.  What comes of
+// them changes only at ties of the two small types, values of at most 5 bits: an
+// exact quotient of x (8 or 11 bits) that is no tie is at least 2^-16 of it away
+// from one, and the product is off by less than 2^-22, so rounding to 18 bits puts
+// ties on themselves and takes nothing across.
 #include "kda_internal.h"
 #include "kda_kv4.cuh"
 
@@ -39,10 +45,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
+__device__ __forceinline__ float to_18_bits(float x) {
+    return __uint_as_float((__float_as_uint(x) + 0x20u) & ~0x3fu);
+}
+
 // Where token t's head h lies: its tile, and its token in the tile; null with a bit set on bad input.
 template <int D>
 __device__ __forceinline__ uint8_t *locate(const KvCacheArgs &a, int t, int h, int &tok) {
     const int b = owner_of(a.cu, a.B, t);
+    if (t >= a.T) return nullptr;
     if (b < 0) {
         report(a.err, DEVERR_SEQLENS);
         return nullptr;
@@ -71,9 +82,12 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const KvCacheArgs a) {
     const long long th = id / (2 * NB);
     const int h = (int)(th % a.H);
     const int t = (int)(th / a.H);
-    if (t >= a.T) return;
-    const T *src = (side ? (const T *)a.v + t * a.v_stride : (const T *)a.k + t * a.k_stride) + h * D + blk * 16;
-    const uint4 w0 = __ldg(reinterpret_cast<const uint4 *>(src)), w1 = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+    if (t < a.T) {
+        const T *src = (side ? (const T *)a.v + t * a.v_stride : (const T *)a.k + t * a.k_stride) + h * D + blk * 16;
+        w0 = __ldg(reinterpret_cast<const uint4 *>(src));
+        w1 = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+    }
     int tok;
     uint8_t *tile = locate<D>(a, t, h, tok);
     if (!tile) return;
@@ -87,13 +101,14 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const KvCacheArgs a) {
         x[i] *= inv;
         top = max_nan(top, fabsf(x[i]));
     }
-    const uint32_t sb = to_e4m3(__fdiv_rn(top, 6.f));
+    const uint32_t sb = to_e4m3(isnan(top) ? top : to_18_bits(top * (1.f / 6.f)));
     const float s = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x;
     uint32_t code[2] = {0, 0};
     if (sb != 0) {
+        const float one_over = __frcp_rn(s);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            code[i >> 2] |= to_e2m1x2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)) << (8 * (i & 3));
+            code[i >> 2] |= to_e2m1x2(to_18_bits(x[2 * i] * one_over), to_18_bits(x[2 * i + 1] * one_over)) << (8 * (i & 3));
     }
     *reinterpret_cast<uint2 *>(tile + (side ? L::VC : L::KC) + tok * (D / 2) + blk * 8) = make_uint2(code[0], code[1]);
     tile[side ? L::VS + blk * KV_TILE + tok : L::KS + tok * NB + blk] = (uint8_t)sb;
@@ -108,9 +123,9 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const KvCacheArgs a) {
     const long long th = id / (2 * NB);
     const int h = (int)(th % a.H);
     const int t = (int)(th / a.H);
-    if (t >= a.T) return;
     int tok;
     const uint8_t *tile = locate<D>(a, t, h, tok);
+    if (t >= a.T) return;
     uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (tile) {
         const uint2 code = *reinterpret_cast<const uint2 *>(tile + (side ? L::VC : L::KC) + tok * (D / 2) + blk * 8);

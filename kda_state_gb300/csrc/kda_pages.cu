@@ -47,6 +47,20 @@ __device__ __forceinline__ int cta_scan(int x, int &total) {
     return warp_sum[w] + in - x;
 }
 
+// refs of pages p0 .. p0 + PER - 1 (p0 a multiple of PER); `past` beyond the last page.
+__device__ __forceinline__ void load_refs(const int32_t *refs, int num_pages, int p0, int past, int (&r)[PER]) {
+    if (p0 + PER <= num_pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+            const int4 x = *reinterpret_cast<const int4 *>(refs + p0 + i);
+            r[i] = x.x, r[i + 1] = x.y, r[i + 2] = x.z, r[i + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) r[i] = p0 + i < num_pages ? refs[p0 + i] : past;
+    }
+}
+
 // Hands out `want` free pages from page `cursor` on, lowest first: take(k, page)
 // is called for the k-th, by any thread.  Returns how many there were, and leaves
 // the cursor at the step that may have more (the caller has counted those it took
@@ -58,11 +72,9 @@ __device__ int hand_out(const int32_t *refs, int num_pages, int &cursor, int wan
         const int p0 = cursor + (int)threadIdx.x * PER;
         int r[PER];
         int free_here = 0;
+        load_refs(refs, num_pages, p0, 1, r);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            r[i] = p0 + i < num_pages ? refs[p0 + i] : 1;
-            free_here += r[i] == 0;
-        }
+        for (int i = 0; i < PER; ++i) free_here += r[i] == 0;
         int total;
         int k = cta_scan(free_here, total) + got;
 #pragma unroll
@@ -143,6 +155,7 @@ __global__ void __launch_bounds__(SCAN) alloc_kernel(const PageArgs a, const int
 __global__ void __launch_bounds__(SCAN) fork_kernel(const PageArgs a, const int32_t *__restrict__ src,
                                                     const int32_t *__restrict__ dst, int n_forks, int32_t *moves) {
     __shared__ int upto[SCAN], fresh_s[SCAN];
+    __shared__ int4 share_s[SCAN];     // of each fork that is made: from row, to row, full pages, pages
     int cursor = 0;
     bool out = false;
     for (int f0 = 0; f0 < n_forks; f0 += SCAN) {
@@ -194,20 +207,20 @@ __global__ void __launch_bounds__(SCAN) fork_kernel(const PageArgs a, const int3
             moves[2 * f] = from;
             moves[2 * f + 1] = to;
         }
+        share_s[threadIdx.x] = served ? make_int4(s, d, full, full + need) : make_int4(-1, 0, 0, 0);
+        __syncthreads();
         // the full pages are shared: a warp copies one row's entries at a time
-        const int lane = threadIdx.x & 31;
-        for (int i = 0; i < 32; ++i) {
-            const int ok = __shfl_sync(~0u, (int)served, i), si = __shfl_sync(~0u, s, i), di = __shfl_sync(~0u, d, i),
-                      fi = __shfl_sync(~0u, full, i), used = fi + __shfl_sync(~0u, need, i);
-            if (!ok) continue;
-            for (int j = lane; j < a.max_pages; j += 32) {
-                if (j < fi) {
-                    const int page = a.page_table[(size_t)si * a.max_pages + j];
-                    a.page_table[(size_t)di * a.max_pages + j] = page;
+        for (int i = threadIdx.x >> 5; i < n; i += SCAN / 32) {
+            const int4 x = share_s[i];
+            if (x.x < 0) continue;
+            for (int j = threadIdx.x & 31; j < a.max_pages; j += 32) {
+                if (j < x.z) {
+                    const int page = a.page_table[(size_t)x.x * a.max_pages + j];
+                    a.page_table[(size_t)x.y * a.max_pages + j] = page;
                     if (page < 0 || page >= a.num_pages) report(a.err, DEVERR_PAGE_RANGE);
                     else atomicAdd(&a.refs[page], 1);
-                } else if (j >= used) {
-                    a.page_table[(size_t)di * a.max_pages + j] = -1;
+                } else if (j >= x.w) {
+                    a.page_table[(size_t)x.y * a.max_pages + j] = -1;
                 }
             }
         }
@@ -252,33 +265,40 @@ __global__ void __launch_bounds__(SCAN) compact_plan_kernel(const PageArgs a, in
     int live = 0;
     {
         int mine = 0;
-        for (int p = threadIdx.x; p < N; p += SCAN) mine += a.refs[p] != 0;
+        for (int p0 = (int)threadIdx.x * PER; p0 < N; p0 += SCAN * PER) {
+            int r[PER];
+            load_refs(a.refs, N, p0, 0, r);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mine += r[i] != 0;
+        }
         cta_scan(mine, live);
     }
-    int holes = 0, movers = 0;         // found so far
+    int holes = 0, movers = 0;         // found so far; one scan counts both, 16384 at most of each in a step
     for (int p0 = 0; p0 < N; p0 += SCAN * PER) {
         const int p1 = p0 + (int)threadIdx.x * PER;
         int r[PER], h = 0, m = 0;
+        load_refs(a.refs, N, p1, 0, r);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int p = p1 + i;
-            r[i] = p < N ? a.refs[p] : 0;
-            if (p < N) {
-                h += r[i] == 0 && p < live;
-                m += r[i] != 0 && p >= live;
-            }
+            h += r[i] == 0 && p < live;
+            m += r[i] != 0 && p >= live;
         }
-        int th, tm;
-        int kh = holes + cta_scan(h, th), km = movers + cta_scan(m, tm);
+        int both;
+        const int before = cta_scan(h | m << 16, both);
+        int kh = holes + (before & 0xffff), km = movers + (before >> 16);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int p = p1 + i;
             if (p >= N) continue;
             if (r[i] == 0 && p < live) moves[2 * kh++ + 1] = p;
-            if (r[i] != 0 && p >= live) moves[2 * km++] = p;
+            if (p >= live) {
+                if (r[i] != 0) moves[2 * km++] = p;
+                else map[p] = p;               // free: an entry that names it all the same stays
+            }
         }
-        holes += th;
-        movers += tm;
+        holes += both & 0xffff;
+        movers += both >> 16;
     }
     __syncthreads();
     for (int k = threadIdx.x; k < movers; k += SCAN) {
@@ -294,22 +314,18 @@ __global__ void __launch_bounds__(SCAN) compact_plan_kernel(const PageArgs a, in
     }
 }
 
-__global__ void __launch_bounds__(256) remap_kernel(const PageArgs a, const int32_t *ws) {
-    const int32_t *map = ws + 16 + 2 * (size_t)a.num_pages;
-    const int live = ws[1];
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= (long long)a.B * a.max_pages) return;
-    const int p = a.page_table[i];
-    if (p >= a.num_pages) report(a.err, DEVERR_PAGE_RANGE);
-    else if (p >= live) a.page_table[i] = map[p];
-}
-
 constexpr int COPY_THREADS = 256;
 constexpr int COPY_VEC = 8;
 constexpr size_t COPY_CHUNK = (size_t)COPY_THREADS * COPY_VEC * 16;     // bytes per CTA and step
 
 // dst page <- src page in every pool: pair i at src[i * step], dst[i * step]; n from the device where n_dev is given.
+// A compaction's page table follows in the same launch: entries past the live pages go through the plan's map.
 __global__ void __launch_bounds__(COPY_THREADS) page_copy_kernel(const __grid_constant__ PageCopyParams p) {
+    for (long long i = (long long)blockIdx.x * COPY_THREADS + threadIdx.x; i < p.cells; i += (long long)gridDim.x * COPY_THREADS) {
+        const int page = p.table[i];
+        if (page >= p.num_pages) report(p.err, DEVERR_PAGE_RANGE);
+        else if (page >= p.n_dev[1]) p.table[i] = p.map[page];
+    }
     const long long n = p.n_dev ? *p.n_dev : p.n;
     const long long units = n * p.P * p.chunks;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
@@ -325,8 +341,9 @@ __global__ void __launch_bounds__(COPY_THREADS) page_copy_kernel(const __grid_co
         }
         const uint4 *from = reinterpret_cast<const uint4 *>(p.pool[pool] + (size_t)s * p.page_bytes);
         uint4 *to = reinterpret_cast<uint4 *>(p.pool[pool] + (size_t)d * p.page_bytes);
-        const size_t nvec = p.page_bytes / 16;
-        const size_t v0 = (size_t)chunk * (COPY_CHUNK / 16) + threadIdx.x;
+        // the chunks of a page are of one size
+        const size_t all = p.page_bytes / 16, part = (all + p.chunks - 1) / p.chunks;
+        const size_t nvec = min(all, (chunk + 1) * part), v0 = chunk * part + threadIdx.x;
         uint4 buf[COPY_VEC];
 #pragma unroll
         for (int j = 0; j < COPY_VEC; ++j) {
@@ -380,12 +397,9 @@ cudaError_t launch_page_compact(const PageArgs &a, PageCopyParams p, int32_t *ws
     compact_plan_kernel<<<1, SCAN, 0, s>>>(a, ws, live);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const long long cells = (long long)a.B * a.max_pages;
-    if (cells > 0) {
-        remap_kernel<<<(unsigned)((cells + 255) / 256), 256, 0, s>>>(a, ws);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
+    p.cells = (long long)a.B * a.max_pages;
+    p.table = a.page_table;
+    p.map = ws + 16 + 2 * (size_t)a.num_pages;
     p.n_dev = ws;
     p.src = ws + 16;
     p.dst = ws + 17;
