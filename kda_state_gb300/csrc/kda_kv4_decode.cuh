@@ -38,7 +38,6 @@ namespace kv4 {
 
 constexpr int WARPS = 8;
 constexpr int THREADS = WARPS * 32;
-constexpr int CHUNK = 32;              // tokens of one step of a warp
 constexpr int MAX_CTAS = 152 * 2;
 constexpr float HEADROOM = 9.f;        // log2 of a weight at the running maximum
 constexpr float MOVE = HEADROOM + 6.f; // a score this far above m makes the maximum move
@@ -58,8 +57,10 @@ struct WarpPieces {
 template <int D, int NT>
 struct DecodeShape {
     static constexpr int ROWS = 8 * NT;
+    static constexpr int TILES = D == 128 ? 2 : 4;       // of 16 tokens: a chunk, one step of a warp
+    static constexpr int CHUNK = TILES * KV_TILE;
     static constexpr int STAGES = 2;
-    static constexpr int STAGE_BYTES = 2 * KvTile<D>::BYTES;
+    static constexpr int STAGE_BYTES = TILES * KvTile<D>::BYTES;
     static constexpr int OSTRIDE = D + 4;
     static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
     static constexpr int OUT = WARPS * ROWS * OSTRIDE * 4;
@@ -135,7 +136,7 @@ __device__ __forceinline__ uint32_t pack_of<__half>(float a, float b) {
 struct Request {
     int q0, n, len, first_chunk, chunks, row_blocks;
 };
-__device__ __forceinline__ Request request_of(const KvAttentionArgs &a, int b, int rows, bool tell) {
+__device__ __forceinline__ Request request_of(const KvAttentionArgs &a, int b, int rows, int chunk, bool tell) {
     Request r;
     r.q0 = a.cu[b];
     r.n = a.cu[b + 1] - r.q0;
@@ -149,10 +150,15 @@ __device__ __forceinline__ Request request_of(const KvAttentionArgs &a, int b, i
     }
     if (r.n == 0) return r;
     const int first = a.window > 0 ? max(0, min(r.len, r.len - r.n + 1) - a.window) : 0;
-    r.first_chunk = first / CHUNK;
-    r.chunks = max(1, (r.len + CHUNK - 1) / CHUNK - r.first_chunk);
+    r.first_chunk = first / chunk;
+    r.chunks = max(1, (int)(((long long)r.len + chunk - 1) / chunk) - r.first_chunk);
     r.row_blocks = (r.n * (a.Hq / a.Hkv) + rows - 1) / rows;
     return r;
+}
+
+// x / y (x >= 0, y > 0), which is short where x has 32 bits
+__device__ __forceinline__ long long divide(long long x, int y) {
+    return x >> 32 == 0 ? (long long)((unsigned)x / (unsigned)y) : x / y;
 }
 
 template <int D, int NT, typename T>
@@ -160,6 +166,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     using L = KvTile<D>;
     using S = DecodeShape<D, NT>;
     constexpr int KS = D / 16;             // MMA steps of a score; also V's tiles of 16 channels
+    constexpr int TILES = S::TILES, CHUNK = S::CHUNK;
     constexpr int LW = D / 32;             // 32-bit words of a lane's share of a K row
     extern __shared__ __align__(128) uint8_t smem[];
     float *const out_s = reinterpret_cast<float *>(smem + S::RING);                  // [WARPS][ROWS][OSTRIDE]
@@ -173,15 +180,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     // ---- the work's total and this CTA's range -------------------------------------------------
     long long begin, end, per, base;       // base: where request b's work begins
     int b;
+    Request rq;                            // request b
     {
         __shared__ long long scan_s[WARPS + 1];
-        __shared__ long long found_s[2];
+        __shared__ long long found_s;
+        __shared__ int found_b;
+        __shared__ Request found_rq;
         const int share = (a.B + THREADS - 1) / THREADS;
         long long mine = 0;
         for (int i = 0; i < share; ++i) {
             const int bb = tid * share + i;
             if (bb >= a.B) break;
-            const Request q = request_of(a, bb, S::ROWS, blockIdx.x == 0);
+            const Request q = request_of(a, bb, S::ROWS, CHUNK, blockIdx.x == 0);
             mine += (long long)q.chunks * q.row_blocks * a.Hkv;
         }
         long long in = mine;
@@ -203,26 +213,28 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             total += scan_s[i];
         }
         before += in - mine;
-        per = max((total + gridDim.x - 1) / gridDim.x, (long long)WARPS);
+        per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)WARPS);
         begin = blockIdx.x * per;
         end = min(begin + per, total);
         if (begin >= total) return;
         if (begin >= before && begin < before + mine) {
             for (int i = 0; i < share; ++i) {
                 const int bb = tid * share + i;
-                const Request q = request_of(a, bb, S::ROWS, false);
+                const Request q = request_of(a, bb, S::ROWS, CHUNK, false);
                 const long long here = (long long)q.chunks * q.row_blocks * a.Hkv;
                 if (begin < before + here) {
-                    found_s[0] = bb;
-                    found_s[1] = before;
+                    found_b = bb;
+                    found_s = before;
+                    found_rq = q;
                     break;
                 }
                 before += here;
             }
         }
         __syncthreads();
-        b = (int)found_s[0];
-        base = found_s[1];
+        b = found_b;
+        base = found_s;
+        rq = found_rq;
     }
 
     uint8_t *const ring = smem + w * S::STAGES * S::STAGE_BYTES;
@@ -234,7 +246,6 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     // ---- this warp's share of the range: contiguous, so that most of its units are its own ------
     long long at = begin + (end - begin) * w / WARPS;
     const long long stop = begin + (end - begin) * (w + 1) / WARPS;
-    Request rq = request_of(a, b, S::ROWS, false);
     // A unit: the rows of one (request, block of rows, kv head), and the chunks of it that are this warp's.
     struct Unit {
         long long begin, end;
@@ -243,9 +254,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     auto plan = [&]() {                    // of the unit at `at`
         while (at >= base + (long long)rq.chunks * rq.row_blocks * a.Hkv) {
             base += (long long)rq.chunks * rq.row_blocks * a.Hkv;
-            rq = request_of(a, ++b, S::ROWS, false);
+            rq = request_of(a, ++b, S::ROWS, CHUNK, false);
         }
-        const int index = (int)((at - base) / rq.chunks);
+        const int index = (int)divide(at - base, rq.chunks);
         u.begin = base + (long long)index * rq.chunks;
         u.end = u.begin + rq.chunks;
         u.b = b, u.q0 = rq.q0, u.n = rq.n, u.len = rq.len;
@@ -255,38 +266,54 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         u.c0 = rq.first_chunk + (int)(at - u.begin);
         u.count = (int)(min(stop, u.end) - at);
     };
-    int page0 = -2, page1 = -2;            // pages of the two tiles of chunk (32-fold part) + lane; -2: past the end
-    uint32_t here = 0;                     // two bits a stage: which tiles of it were loaded
-    auto fetch = [&](int k) {              // the unit's k-th chunk
-        if ((k & 31) == 0) {
-            const int32_t *const pages = a.page_table + (size_t)u.b * a.max_pages;
-            const int kk = k + lane;
-            const long long t0 = (long long)(u.c0 + kk) * CHUNK, t1 = t0 + KV_TILE;
-            page0 = kk < u.count && t0 < u.len ? pages[t0 >> a.page_shift] : -2;
-            page1 = kk < u.count && t1 < u.len ? pages[t1 >> a.page_shift] : -2;
-            if ((page0 != -2 && (page0 < 0 || page0 >= a.num_pages)) || (page1 != -2 && (page1 < 0 || page1 >= a.num_pages)))
-                report(a.err, DEVERR_PAGE_RANGE);
-        }
-        const int s = asked++ & 1;
-        const int p0 = __shfl_sync(~0u, page0, k & 31), p1 = __shfl_sync(~0u, page1, k & 31);
-        const bool ok0 = p0 >= 0 && p0 < a.num_pages, ok1 = p1 >= 0 && p1 < a.num_pages;
-        here = (here & ~(3u << (2 * s))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * s);
-        if (lane == 0) {
-            const int t0 = (u.c0 + k) * CHUNK, in_page = t0 & ((1 << a.page_shift) - 1);
-            const uint32_t bar = bar0 + 8 * s;
-            uint8_t *dst = ring + s * S::STAGE_BYTES;
-            const uint8_t *src0 = a.pool + ((((size_t)p0 * a.Hkv + u.h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
-            barrier_expect(bar, (ok0 ? L::BYTES : 0) + (ok1 ? L::BYTES : 0));
-            if (ok0 && ok1 && a.page_shift > 4) {          // one page: 32 tokens in a row
-                bulk_copy(dst, src0, 2 * L::BYTES, bar);
-            } else {
-                if (ok0) bulk_copy(dst, src0, L::BYTES, bar);
-                if (ok1) {
-                    const int in1 = (t0 + KV_TILE) & ((1 << a.page_shift) - 1);
-                    bulk_copy(dst + L::BYTES,
-                              a.pool + ((((size_t)p1 * a.Hkv + u.h) << (a.page_shift - 4)) + (in1 >> 4)) * L::BYTES, L::BYTES, bar);
-                }
+    uint32_t q_raw[NT][D / 8];             // this lane's quarter of row r of each 8, as it was given
+    auto ask_q = [&]() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int row = u.row0 + t * 8 + r;
+            const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + (long long)(u.q0 + row / G) * a.q_stride +
+                                                               (u.h * G + row % G) * D + c * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 v = t * 8 + r < u.rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                q_raw[t][4 * i] = v.x, q_raw[t][4 * i + 1] = v.y, q_raw[t][4 * i + 2] = v.z, q_raw[t][4 * i + 3] = v.w;
             }
+        }
+    };
+    // Pages are looked up for 32 tiles at a time, one by a lane, and 32 ahead; each lane asks for its own tile
+    // when its chunk's turn comes, or one lane for all of a chunk that lies in one page.
+    constexpr int WINDOW = 32 / TILES;     // chunks
+    const bool one_copy = 1 << a.page_shift >= CHUNK;
+    int page_next = -2;                    // -2: past the end
+    const uint8_t *source = nullptr;
+    uint32_t oks = 0, here = 0;            // tiles of the window whose page is good; of each stage, those loaded
+    auto look = [&](int k) {
+        const long long t = ((long long)(u.c0 + k) * TILES + lane) * KV_TILE;
+        return k + lane / TILES < u.count && t < u.len ? a.page_table[(size_t)u.b * a.max_pages + (t >> a.page_shift)] : -2;
+    };
+    auto fetch = [&](int k) {              // the unit's k-th chunk
+        const int j = k % WINDOW;
+        if (j == 0) {
+            const int page = k == 0 ? look(0) : page_next;
+            page_next = look(k + WINDOW);
+            const bool ok = page >= 0 && page < a.num_pages;
+            oks = __ballot_sync(~0u, ok);
+            if (!ok && page != -2) report(a.err, DEVERR_PAGE_RANGE);
+            const int in_page = (int)((unsigned)((u.c0 + k) * TILES + lane) * KV_TILE) & ((1 << a.page_shift) - 1);
+            source = a.pool + ((((size_t)page * a.Hkv + u.h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
+        }
+        const int s = asked++ % S::STAGES;
+        const uint32_t run = oks >> (TILES * j) & ((1u << TILES) - 1), bar = bar0 + 8 * s;
+        here = (here & ~(((1u << TILES) - 1) << (TILES * s))) | run << (TILES * s);
+        uint8_t *const dst = ring + s * S::STAGE_BYTES;
+        if (lane == TILES * j) {
+            barrier_expect(bar, __popc(run) * L::BYTES);
+            if (one_copy && run) bulk_copy(dst, source, __popc(run) * L::BYTES, bar);
+        }
+        if (!one_copy) {
+            __syncwarp();
+            const int i = lane - TILES * j;
+            if (i >= 0 && i < TILES && (run >> i & 1)) bulk_copy(dst + i * L::BYTES, source, L::BYTES, bar);
         }
     };
     // A result that is part of its unit's: maximum, sum and weighted values of its rows.  Of a warp's
@@ -301,6 +328,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     bool more = at < stop;
     if (more) {
         plan();
+        ask_q();
 #pragma unroll
         for (int i = 0; i < S::STAGES; ++i)
             if (i < u.count) fetch(i);
@@ -318,33 +346,21 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int row = u.row0 + t * 8 + r;
-            float top = 0.f, x[D / 4];
+            float top = 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
-            if (t * 8 + r < u.rows) {
-                const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + (long long)(u.q0 + row / G) * a.q_stride +
-                                                                   (u.h * G + row % G) * D + c * (D / 4));
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint4 v = __ldg(src + i);
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = pair_of<T>(u[k]);
-                        x[8 * i + 2 * k] = f.x;
-                        x[8 * i + 2 * k + 1] = f.y;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < D / 4; ++i) top = max_nan(top, fabsf(x[i]));
+            for (int i = 0; i < D / 8; ++i) {
+                const float2 f = pair_of<T>(q_raw[t][i]);
+                top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
             }
             top = max_nan(top, __shfl_xor_sync(~0u, top, 1));
             top = max_nan(top, __shfl_xor_sync(~0u, top, 2));
             const int e = min(max((int)(__float_as_uint(top) >> 23 & 255), 1), 253);
             const float down = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), a.scale_k), up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
-            for (int i = 0; i < 2 * KS; ++i) qf[t][i] = half_pair(x[2 * i] * down, x[2 * i + 1] * down);
+            for (int i = 0; i < D / 8; ++i) {
+                const float2 f = pair_of<T>(q_raw[t][i]);
+                qf[t][i] = half_pair(f.x * down, f.y * down);
+            }
             // scores come back by columns: this lane holds those of rows 2 c and 2 c + 1
             const float f = fabsf(a.scale_k) * up;
 #pragma unroll
@@ -376,15 +392,15 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             }
             ++taken;
             const uint8_t *stage = ring + s * S::STAGE_BYTES;
-            const uint32_t loaded = here >> (2 * s) & 3u;
-            const bool whole = loaded == 3u && t0 >= first_max && t0 + CHUNK - 1 <= last_min;
+            const uint32_t loaded = here >> (TILES * s) & ((1u << TILES) - 1);
+            const bool whole = loaded == (1u << TILES) - 1 && t0 >= first_max && t0 + CHUNK - 1 <= last_min;
 
-            // scores of 32 tokens: the two tiles' products alternate, so that neither waits for its own sums
-            float y[2][NT][4];
+            // scores: the tiles' products alternate, so that none waits for its own sums
+            float y[TILES][NT][4];
             {
-                uint32_t ka[2][LW], kb[2][LW], sa[2], sb[2];
+                uint32_t ka[TILES][LW], kb[TILES][LW], sa[TILES], sb[TILES];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < TILES; ++i) {
                     const uint8_t *tile = stage + i * L::BYTES;
                     if constexpr (D == 128) {
                         const uint4 x = *reinterpret_cast<const uint4 *>(tile + tA * 64 + c * 16);
@@ -406,16 +422,16 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                 }
 #pragma unroll
                 for (int q = 0; q < LW; ++q) {
-                    uint32_t fa[2][4], fb[2][4];
+                    uint32_t fa[TILES][4], fb[TILES][4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < TILES; ++i) {
                         e2m1x8_to_f16x2(ka[i][q], fa[i]);
                         e2m1x8_to_f16x2(kb[i][q], fb[i]);
                     }
 #pragma unroll
                     for (int z = 0; z < 2; ++z)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < TILES; ++i) {
                             const uint32_t a0 = hmul2_by(fa[i][2 * z], sa[i], D == 128 && q >= 2), a1 = hmul2_by(fb[i][2 * z], sb[i], D == 128 && q >= 2);
                             const uint32_t a2 = hmul2_by(fa[i][2 * z + 1], sa[i], D == 128 && q >= 2), a3 = hmul2_by(fb[i][2 * z + 1], sb[i], D == 128 && q >= 2);
 #pragma unroll
@@ -429,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             if (!whole) {
                 seen = 0;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < TILES; ++i)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -439,17 +455,17 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                                 seen |= 1u << ((i * NT + t) * 4 + e);
                         }
             }
-            float x[2][NT][4];
+            float x[TILES][NT][4];
             auto weigh = [&]() {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < TILES; ++i)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[i][t][e] = fmaf(y[i][t][e], factor[t][e & 1], -m[t][e & 1]);
                 if (!whole) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < TILES; ++i)
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -460,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             weigh();
             float high = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < TILES; ++i)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -472,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                     for (int k2 = 0; k2 < 2; ++k2) {
                         float top = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                        for (int i = 0; i < TILES; ++i)
 #pragma unroll
                             for (int e = k2; e < 4; e += 2)
                                 if (seen >> ((i * NT + t) * 4 + e) & 1) top = fmaxf(top, y[i][t][e] * factor[t][k2]);
@@ -490,9 +506,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                     }
                 weigh();
             }
-            // values of 32 tokens
+            // values
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < TILES; ++i) {
                 const uint8_t *tile = stage + i * L::BYTES;
                 uint32_t pb[NT][2], seen_b[NT][2];
 #pragma unroll
@@ -576,6 +592,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         more = at < stop;
         if (more) {
             plan();
+            ask_q();
             if (!dead) {
                 fence_async_shared();
 #pragma unroll
@@ -620,88 +637,133 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     }
 
     // ---- join what the warps have of one unit ------------------------------------------------------
+    // A unit begins with a warp's last piece, or before this CTA (then the first warp with a share has its
+    // first piece of it), and goes on in the first pieces of the warps behind.
     __syncthreads();
-    float *const partials = reinterpret_cast<float *>(a.ws + MAX_CTAS * 4);
     constexpr int QUADS = S::ROWS * D / 4;
-    for (int from = 0; from < 2 * WARPS; ++from) {
-        // a unit begins with a warp's last piece, or before this CTA (then the first warp with a share has its
-        // first piece of it); it goes on in the first pieces of the warps behind
-        const bool is_last = from & 1;
-        const int w0 = from >> 1;
-        const Piece &x = is_last ? pieces[w0].last : pieces[w0].first;
-        if (x.rows == 0) continue;
-        if (!is_last) {
-            bool behind = x.begin >= begin;
-            for (int y = 0; y < w0; ++y) behind |= pieces[y].first.rows != 0;
-            if (behind) continue;
-        }
-        const bool complete = x.begin >= begin && x.end <= end;
-        const int cta0 = (int)(x.begin / per), cta1 = (int)((x.end - 1) / per);
-        auto finish = [&](int col, int d, float4 v, float top, float sum) {
-            const int row = x.row0 + col;
-            const size_t at_row = (size_t)(x.q0 + row / G) * a.Hq + x.h * G + row % G;
-            const float f = sum == 0.f ? 0.f : a.v_scale / sum;
-            *reinterpret_cast<uint2 *>((T *)a.o + at_row * D + d) =
-                sum == 0.f ? make_uint2(0, 0) : make_uint2(pack_of<T>(v.x * f, v.y * f), pack_of<T>(v.z * f, v.w * f));
-            if (d == 0 && a.lse) a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * LN2;
-        };
-        for (int i = tid; i < QUADS; i += THREADS) {
+    auto finish = [&](const Piece &x, int col, int d, float4 v, float top, float sum) {
+        const int row = x.row0 + col;
+        const size_t at_row = (size_t)(x.q0 + row / G) * a.Hq + x.h * G + row % G;
+        const float f = sum == 0.f ? 0.f : a.v_scale / sum;
+        *reinterpret_cast<uint2 *>((T *)a.o + at_row * D + d) =
+            sum == 0.f ? make_uint2(0, 0) : make_uint2(pack_of<T>(v.x * f, v.y * f), pack_of<T>(v.z * f, v.w * f));
+        if (d == 0 && a.lse) a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * LN2;
+    };
+    auto add = [](float4 &v, float &top, float &sum, const float4 &z, const float2 &ml) {
+        const float to = max_nan(top, ml.x), keep = exp2_fast(top - to), by = exp2_fast(ml.x - to);
+        top = to;
+        sum = sum * keep + ml.y * by;
+        v.x = v.x * keep + z.x * by, v.y = v.y * keep + z.y * by;
+        v.z = v.z * keep + z.z * by, v.w = v.w * keep + z.w * by;
+    };
+    // four channels of a row over this CTA's pieces of the unit x that begins in warp w0's first or last piece
+    auto gather = [&](const Piece &x, int w0, bool with_last, int col, int d, float &top, float &sum) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        top = NOTHING, sum = 0.f;
+        if (with_last)
+            add(v, top, sum, *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w0 * S::STAGES * S::STAGE_BYTES) +
+                                                               col * S::OSTRIDE + d),
+                ml_s[(WARPS + w0) * S::ROWS + col]);
+        for (int y = with_last ? w0 + 1 : w0; y < WARPS; ++y)
+            if (pieces[y].first.rows && pieces[y].first.begin == x.begin)
+                add(v, top, sum, *reinterpret_cast<const float4 *>(out_s + (y * S::ROWS + col) * S::OSTRIDE + d), ml_s[y * S::ROWS + col]);
+        return v;
+    };
+    // units that begin and end in this CTA: a warp each
+    if (pieces[w].last.rows && pieces[w].last.end <= end) {
+        const Piece x = pieces[w].last;
+        for (int i = lane; i < x.rows * (D / 4); i += 32) {
             const int col = i / (D / 4), d = i % (D / 4) * 4;
-            if (col >= x.rows) continue;
-            float top = NOTHING, sum = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int y = w0; y < WARPS; ++y) {
-                const bool over_ring = is_last && y == w0;
-                if (!over_ring && !(pieces[y].first.rows && pieces[y].first.begin == x.begin)) continue;
-                const float2 ml = ml_s[((over_ring ? WARPS : 0) + y) * S::ROWS + col];
-                const float *src = over_ring ? reinterpret_cast<const float *>(smem + y * S::STAGES * S::STAGE_BYTES)
-                                             : out_s + y * S::ROWS * S::OSTRIDE;
-                const float4 z = *reinterpret_cast<const float4 *>(src + col * S::OSTRIDE + d);
-                const float to = max_nan(top, ml.x), keep = exp2_fast(top - to), add = exp2_fast(ml.x - to);
-                top = to;
-                sum = sum * keep + ml.y * add;
-                v.x = v.x * keep + z.x * add, v.y = v.y * keep + z.y * add;
-                v.z = v.z * keep + z.z * add, v.w = v.w * keep + z.w * add;
-            }
-            if (complete) finish(col, d, v, top, sum);
-            else {
-                float *dst = partials + (size_t)(2 * blockIdx.x + (x.begin >= begin)) * S::PARTIAL;
-                __stcg(reinterpret_cast<float4 *>(dst + col * D + d), v);
-                if (d == 0) __stcg(reinterpret_cast<float2 *>(dst + S::ROWS * D + 2 * col), make_float2(top, sum));
+            float top, sum;
+            const float4 v = gather(x, w, true, col, d, top, sum);
+            finish(x, col, d, v, top, sum);
+        }
+    }
+    // the two that other CTAs share: four warps each, one for the unit that began before, one for that which goes on
+    const int side = w >> 2, st = tid & 127;
+    int w0 = -1;
+    if (side == 0) {
+        for (int y = WARPS - 1; y >= 0; --y)
+            if (pieces[y].first.rows || pieces[y].last.rows) w0 = y;
+        if (w0 >= 0 && !(pieces[w0].first.rows && pieces[w0].first.begin < begin)) w0 = -1;
+    } else {
+        for (int y = 0; y < WARPS; ++y)
+            if (pieces[y].last.rows && pieces[y].last.end > end) w0 = y;
+    }
+    float *const partials = reinterpret_cast<float *>(a.ws + MAX_CTAS * 4);
+    Piece x;
+    x.rows = 0;
+    if (w0 >= 0) {
+        x = side ? pieces[w0].last : pieces[w0].first;
+        float *const dst = partials + (size_t)(2 * blockIdx.x + side) * S::PARTIAL;
+        for (int i = st; i < x.rows * (D / 4); i += 128) {
+            const int col = i / (D / 4), d = i % (D / 4) * 4;
+            float top, sum;
+            const float4 v = gather(x, w0, side, col, d, top, sum);
+            __stcg(reinterpret_cast<float4 *>(dst + col * D + d), v);
+            if (d == 0) __stcg(reinterpret_cast<float2 *>(dst + S::ROWS * D + 2 * col), make_float2(top, sum));
+        }
+    }
+    __syncthreads();
+    const int cta0 = w0 >= 0 ? (int)divide(x.begin, (int)per) : 0, cta1 = w0 >= 0 ? (int)divide(x.end - 1, (int)per) : 0;
+    if (st == 0) {
+        bool arrived = false;
+        if (w0 >= 0) {
+            // the last of the unit's CTAs to arrive joins their results, in order
+            int *const counter = reinterpret_cast<int *>(a.ws) + cta0;
+            __threadfence();
+            arrived = atomicAdd(counter, 1) == cta1 - cta0;
+            if (arrived) {
+                *counter = 0;              // as the next call needs it
+                __threadfence();
             }
         }
-        if (!complete) {
-            // the last of the unit's CTAs to arrive joins their results, in order
-            __threadfence();
-            __syncthreads();
-            int *const counter = reinterpret_cast<int *>(a.ws) + cta0;
-            if (tid == 0) {
-                const int arrived = atomicAdd(counter, 1) == cta1 - cta0;
-                if (arrived) *counter = 0;     // as the next call needs it
-                *shared = arrived;
-            }
-            __syncthreads();
-            if (*shared) {
-                __threadfence();
-                for (int i = tid; i < QUADS; i += THREADS) {
-                    const int col = i / (D / 4), d = i % (D / 4) * 4;
-                    if (col >= x.rows) continue;
-                    float top = NOTHING, sum = 0.f;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int y = cta0; y <= cta1; ++y) {
-                        const float *src = partials + (size_t)(2 * y + (y == cta0)) * S::PARTIAL;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + S::ROWS * D + 2 * col));
-                        const float4 z = __ldcg(reinterpret_cast<const float4 *>(src + col * D + d));
-                        const float to = max_nan(top, ml.x), keep = exp2_fast(top - to), add = exp2_fast(ml.x - to);
-                        top = to;
-                        sum = sum * keep + ml.y * add;
-                        v.x = v.x * keep + z.x * add, v.y = v.y * keep + z.y * add;
-                        v.z = v.z * keep + z.z * add, v.w = v.w * keep + z.w * add;
-                    }
-                    finish(col, d, v, top, sum);
+        shared[side] = arrived;
+    }
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + side) : "memory");
+    if (!shared[side]) return;
+    // each warp takes every fourth result, a lane QUADS / 32 times four channels of it
+    {
+        constexpr int N = QUADS / 32;
+        float4 v[N];
+        float top[N], sum[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f), top[k] = NOTHING, sum[k] = 0.f;
+#pragma unroll 2
+        for (int y = cta0 + (w & 3); y <= cta1; y += 4) {
+            const float *src = partials + (size_t)(2 * y + (y == cta0)) * S::PARTIAL;
+            float4 z[N];
+            float2 ml[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int i = 32 * k + lane, col = i / (D / 4);
+                z[k] = make_float4(0.f, 0.f, 0.f, 0.f), ml[k] = make_float2(NOTHING, 0.f);
+                if (col < x.rows) {
+                    z[k] = __ldcg(reinterpret_cast<const float4 *>(src) + i);
+                    ml[k] = __ldcg(reinterpret_cast<const float2 *>(src + S::ROWS * D) + col);
                 }
             }
+#pragma unroll
+            for (int k = 0; k < N; ++k) add(v[k], top[k], sum[k], z[k], ml[k]);
         }
+        // (both sides' pieces in out_s have been read)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = 32 * k + lane, col = i / (D / 4), d = i % (D / 4) * 4;
+            *reinterpret_cast<float4 *>(out_s + (w * S::ROWS + col) * S::OSTRIDE + d) = v[k];
+            if (d == 0) ml_s[w * S::ROWS + col] = make_float2(top[k], sum[k]);
+        }
+    }
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + side) : "memory");
+    for (int i = st; i < x.rows * (D / 4); i += 128) {
+        const int col = i / (D / 4), d = i % (D / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top = NOTHING, sum = 0.f;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            add(v, top, sum, *reinterpret_cast<const float4 *>(out_s + ((4 * side + y) * S::ROWS + col) * S::OSTRIDE + d),
+                ml_s[(4 * side + y) * S::ROWS + col]);
+        finish(x, col, d, v, top, sum);
     }
 }
 

@@ -218,7 +218,7 @@ struct Walker {
     __device__ __forceinline__ void load(const KvAttentionArgs &a) {
         const int lane = threadIdx.x & 31, b = b0 + lane;
         mine = my_slots = 0;
-        if (b < a.B) q = request_of(a, b, 128 * QT, false);
+        if (b < a.B) q = request_of(a, b, 128 * QT, TT, false);
         if (b < a.B && q.row_blocks && (int)((long long)(longest - most_tiles(a, q)) * classes / longest) == cls) {
             const int pieces = q.row_blocks ? pieces_of(a, q) : 0;
             mine = q.row_blocks * a.Hkv * pieces;
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             {
                 long long units = 0, all = 0;
                 for (int b = lane; b < a.B; b += 32) {
-                    const Request q = request_of(a, b, 128 * QT, blockIdx.x == 0);
+                    const Request q = request_of(a, b, 128 * QT, TT, blockIdx.x == 0);
                     units += (long long)q.row_blocks * a.Hkv;
                     if (q.row_blocks) {
                         const int tiles = Walker<QT>::most_tiles(a, q);
