@@ -592,7 +592,6 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         more = at < stop;
         if (more) {
             plan();
-            ask_q();
             if (!dead) {
                 fence_async_shared();
 #pragma unroll
@@ -634,6 +633,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             Piece &y = begun ? pieces[w].last : pieces[w].first;
             y.begin = x.begin, y.end = x.end, y.q0 = x.q0, y.h = x.h, y.row0 = x.row0, y.rows = x.rows;
         }
+        if (more) ask_q();
     }
 
     // ---- join what the warps have of one unit ------------------------------------------------------
