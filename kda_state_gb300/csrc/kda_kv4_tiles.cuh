@@ -196,34 +196,45 @@ __device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool mine
     return r;
 }
 
+__device__ __forceinline__ int tiles_of(int tokens) { return tokens / TT + (tokens % TT != 0); }
+
 // Finds parts by number, in ascending order, 32 requests at a time; every lane of a warp calls it.
-// Requests come by classes of their length, the longest first, so that the last parts claimed are
-// short ones (64 requests of 0.5 to 6 K tokens, 8 new each: 172 -> 157 us).
+// Up to 128 requests come by classes of their length, the longest first, so that the last parts
+// claimed are short ones (64 requests of 0.5 to 6 K tokens, 8 new each: 172 -> 157 us); what is
+// needed of them is kept, a lane a request of each 32.
 template <int QT>
 struct Walker {
-    int b0, before, slots_before, cut, classes, cls, longest;
-    Request q;
+    static constexpr int GROUPS = 4;
+    int b0, before, slots_before, cut, classes, cls;
+    int parts[GROUPS], cls_of[GROUPS];     // of requests lane, lane + 32, ...: parts (negative: cut ones), class
     int mine, my_slots, incl, slots_incl;
 
     // Tiles that no part of the request exceeds.
-    __device__ __forceinline__ static int most_tiles(const KvAttentionArgs &a, const Request &q) {
-        const int all = (q.len + TT - 1) / TT;
+    __device__ __forceinline__ static int most_tiles(const KvAttentionArgs &a, int len) {
+        const int all = tiles_of(len);
         if (a.window <= 0) return max(all, 1);
         const long long near = ((long long)a.window + 128 * QT) / TT + 2;
         return max((int)min((long long)all, near), 1);
     }
-    __device__ __forceinline__ int pieces_of(const KvAttentionArgs &a, const Request &r) const {
-        return cut > 0 ? (most_tiles(a, r) + cut - 1) / cut : 1;
+    __device__ __forceinline__ int pieces_of(const KvAttentionArgs &a, int len) const {
+        return cut > 0 ? (most_tiles(a, len) + cut - 1) / cut : 1;
+    }
+    __device__ __forceinline__ int parts_of(const KvAttentionArgs &a, const Request &q) const {
+        const int pieces = pieces_of(a, q.len), n = q.row_blocks * a.Hkv * pieces;
+        return pieces > 1 ? -n : n;
     }
     __device__ __forceinline__ void load(const KvAttentionArgs &a) {
-        const int lane = threadIdx.x & 31, b = b0 + lane;
-        mine = my_slots = 0;
-        if (b < a.B) q = request_of(a, b, 128 * QT, TT, false);
-        if (b < a.B && q.row_blocks && (int)((long long)(longest - most_tiles(a, q)) * classes / longest) == cls) {
-            const int pieces = q.row_blocks ? pieces_of(a, q) : 0;
-            mine = q.row_blocks * a.Hkv * pieces;
-            my_slots = pieces > 1 ? mine : 0;
+        const int lane = threadIdx.x & 31;
+        int n = 0;
+        if (classes > 1) {
+#pragma unroll
+            for (int i = 0; i < GROUPS; ++i)
+                if (b0 == 32 * i && cls_of[i] == cls) n = parts[i];
+        } else if (b0 + lane < a.B) {
+            n = parts_of(a, request_of(a, b0 + lane, 128 * QT, TT, false));
         }
+        mine = abs(n);
+        my_slots = n < 0 ? -n : 0;
         incl = mine, slots_incl = my_slots;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -231,11 +242,20 @@ struct Walker {
             if (lane >= o) incl += x, slots_incl += y;
         }
     }
-    __device__ __forceinline__ void start(const KvAttentionArgs &a, int cut_, int longest_) {
+    __device__ __forceinline__ void start(const KvAttentionArgs &a, int cut_, int longest) {
         cut = cut_;
-        longest = longest_;
-        classes = a.B > 1 && a.B <= 256 ? 8 : 1;       // (each class goes through all requests once more)
+        classes = a.B > 1 && a.B <= 32 * GROUPS ? 8 : 1;
         b0 = before = slots_before = cls = 0;
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+            const int b = 32 * i + (threadIdx.x & 31);
+            parts[i] = cls_of[i] = 0;
+            if (classes > 1 && b < a.B) {
+                const Request q = request_of(a, b, 128 * QT, TT, false);
+                parts[i] = parts_of(a, q);
+                cls_of[i] = q.row_blocks ? (int)((long long)(longest - most_tiles(a, q.len)) * classes / longest) : 0;
+            }
+        }
         load(a);
     }
     __device__ __forceinline__ bool find(const KvAttentionArgs &a, int p, Part &out) {
@@ -255,13 +275,10 @@ struct Walker {
         const int src = __ffs(__ballot_sync(~0u, before + incl > p)) - 1;
         const int index = p - (before + __shfl_sync(~0u, incl - mine, src));
         out.b = b0 + src;
-        out.q0 = __shfl_sync(~0u, q.q0, src);
-        out.n = __shfl_sync(~0u, q.n, src);
-        out.len = __shfl_sync(~0u, q.len, src);
-        const int blocks = __shfl_sync(~0u, q.row_blocks, src);
-        Request r;
-        r.len = out.len;
-        out.pieces = pieces_of(a, r);
+        const Request q = request_of(a, out.b, 128 * QT, TT, false);
+        const int blocks = q.row_blocks;
+        out.q0 = q.q0, out.n = q.n, out.len = q.len;
+        out.pieces = pieces_of(a, q.len);
         out.piece = index % out.pieces;
         const int unit = index / out.pieces;
         out.slot0 = slots_before + __shfl_sync(~0u, slots_incl - my_slots, src) + unit * out.pieces;
@@ -272,7 +289,7 @@ struct Walker {
         out.rows = min(128 * QT, out.n * G - out.row0);
         const int i0 = out.row0 / G, i1 = (out.row0 + out.rows - 1) / G;
         const int lo = a.window > 0 ? max(0, out.len - out.n + i0 + 1 - a.window) / TT : 0;
-        const int hi = (max(out.len - out.n + i1 + 1, 0) + TT - 1) / TT;
+        const int hi = tiles_of(max(out.len - out.n + i1 + 1, 0));
         const long long tiles = max(hi - lo, 1);
         out.tile0 = lo + (int)(tiles * out.piece / out.pieces);
         out.tiles = lo + (int)(tiles * (out.piece + 1) / out.pieces) - out.tile0;
@@ -354,22 +371,22 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
         const int my_row = (QT == 2 ? g * 128 : 0) + row;      // of the part
         uint32_t done = 0;             // this group's tiles so far
         uint32_t kv = 0;               // tiles so far
-        for (uint32_t part = 0;; ++part) {
+        // The next part: its queries go out, and its tiles are returned, or -1 after the last one.
+        float factor = 0.f, next_factor = 0.f;
+        auto take = [&](uint32_t part, float &factor) {
             wait_or_dead(PART_FULL + 8 * (part & 3), part >> 2 & 1, dead);
             const Part &p = meta.parts[part & 3];
-            const int tiles = __shfl_sync(~0u, p.tiles, 0), tile0 = p.tile0;
+            const int tiles = __shfl_sync(~0u, p.tiles, 0);
             // all that meet at a barrier below leave together
             const bool leave = tiles < 0 || *dead;
-            if (QT == 1 ? group_any(1, 256, leave) : (bool)__any_sync(~0u, leave)) break;
+            if (QT == 1 ? group_any(1, 256, leave) : (bool)__any_sync(~0u, leave)) return -1;
             // queries: scaled by a power of two, so that the largest of a row is in [1, 2)
-            float factor;
             {
-                uint32_t qw[D / 2];
-                float top = 0.f;
-                if (my_row < p.rows) {
-                    const int rr = p.row0 + my_row;
-                    const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + (long long)(p.q0 + rr / G) * a.q_stride +
-                                                                       (p.h * G + rr % G) * D);
+                uint32_t qw[D / 2], most = 0;
+                const int rr = p.row0 + min(my_row, p.rows - 1);       // (rows past the last are computed like it)
+                const uint4 *src = reinterpret_cast<const uint4 *>((const T *)a.q + (long long)(p.q0 + rr / G) * a.q_stride +
+                                                                   (p.h * G + rr % G) * D);
+                if ((my_row & ~31) < p.rows) {
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) {
                         const uint4 v = __ldg(src + i);
@@ -379,15 +396,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
 #pragma unroll
                     for (int i = 0; i < D / 2; ++i) qw[i] = 0;
                 }
+                // magnitudes of both types order as their bits do, NaN last
 #pragma unroll
-                for (int i = 0; i < D / 2; ++i) {
-                    const float2 f = pair_of<T>(qw[i]);
-                    top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
-                }
+                for (int i = 0; i < D / 2; ++i) most = __vmaxu2(most, qw[i] & 0x7fff7fffu);
+                const float2 tops = pair_of<T>(most);
+                const float top = max_nan(tops.x, tops.y);
                 const int e = min(max((int)(__float_as_uint(top) >> 23 & 255), 1), 253);
                 const float down = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), a.scale_k);
                 factor = fabsf(a.scale_k) * __uint_as_float((uint32_t)e << 23);
                 if (QT == 2 || g == 0) {
+                    if ((my_row & ~31) < p.rows)
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) {
                         uint32_t x[4];
@@ -403,6 +421,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     if (lane == 0) barrier_arrive(Q_FULL + 8 * g);
                 }
             }
+            return tiles;
+        };
+        int tiles = take(0, factor), next_tiles = -1;
+        for (uint32_t part = 0; tiles >= 0; ++part, tiles = next_tiles, factor = next_factor) {
+            const Part &p = meta.parts[part & 3];
+            const int tile0 = p.tile0;
             const int2 see = sight(a, p, my_row);
             // every row of this group sees a tile whole if it lies between these
             int all_first, all_last;
@@ -411,6 +435,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 const int2 y = sight(a, p, min(QT == 2 ? g * 128 + 127 : 127, p.rows - 1));
                 all_first = y.x, all_last = x.y;
             }
+            // a warp without rows leaves its lanes of Q and P as they are: they reach nothing but its lanes of O
+            const bool no_rows = QT == 1 && (my_row & ~31) >= p.rows;
             float m = NOTHING, l = 0.f;
             uint32_t nan_blocks = 0;
             int mine = 0;              // tiles of this part that this group has done
@@ -419,6 +445,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 const int pos0 = (tile0 + j) * TT, ring = (kv + j) & 3;
                 wait_or_dead(S_FULL + 8 * g, done & 1, dead);
                 tmem_after_sync();
+                if (no_rows) {
+                    if (lane == 0) barrier_arrive(P_FULL + 8 * g);
+                    ++done;
+                    ++mine;
+                    continue;
+                }
                 const uint4 miss = *reinterpret_cast<const uint4 *>(meta.missing[ring]);
                 const uint4 nans = *reinterpret_cast<const uint4 *>(meta.nan_group[ring]);
                 const bool any_nan = (nans.x | nans.y | nans.z | nans.w) != 0;
@@ -560,21 +592,28 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 nan_blocks = meta.nan_row[0][row] | meta.nan_row[1][row];
                 const float both = fmaxf(ml0.x, ml1.x);
                 const float k0 = exp2_fast(ml0.x - both), k1 = exp2_fast(ml1.x - both), sum = ml0.y * k0 + ml1.y * k1;
-                const bool have0 = tiles > 0, have1 = tiles > 1, split = p.pieces > 1;
-                const float f = split ? 1.f : sum == 0.f ? 0.f : a.v_scale / sum;
+                const bool split = p.pieces > 1;
+                const float f = split ? 1.f : sum == 0.f ? 0.f : a.v_scale / sum, f0 = k0 * f, f1 = k1 * f;
                 float *const partials = reinterpret_cast<float *>(a.ws + MAX_CTAS * 4);
                 float *const my_part = partials + (size_t)(p.slot0 + p.piece) * S::PARTIAL;
 #pragma unroll 1
-                for (int c = g * (D / 64); c < (g + 1) * (D / 64); ++c) {
+                for (int c = no_rows ? D / 32 : g * (D / 64); c < (g + 1) * (D / 64); ++c) {
                     uint32_t x0[32], x1[32];
-                    tmem_ld32(lanes + S::O_COL + 32 * c, x0);
-                    tmem_ld32(lanes + S::O_COL + D + 32 * c, x1);
+                    tmem_ld32_async(lanes + S::O_COL + 32 * c, x0);
+                    tmem_ld32_async(lanes + S::O_COL + D + 32 * c, x1);
+                    tmem_ld_wait(x0);
+                    tmem_ld_wait(x1);
+                    if (tiles < 2) {       // a group without a tile has made no O
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x0[e] = tiles < 1 ? 0 : x0[e], x1[e] = 0;
+                    }
                     if (my_row >= p.rows || *dead) continue;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float v = (have0 ? __uint_as_float(x0[e]) * k0 : 0.f) + (have1 ? __uint_as_float(x1[e]) * k1 : 0.f);
-                        if (nan_blocks >> (2 * c + e / 16) & 1) v = __uint_as_float(0x7fffffffu);
-                        x0[e] = __float_as_uint(split || sum != 0.f ? v * f : 0.f);
+                    for (int e = 0; e < 32; ++e) x0[e] = __float_as_uint(fmaf(__uint_as_float(x0[e]), f0, __uint_as_float(x1[e]) * f1));
+                    if (nan_blocks >> (2 * c) & 3) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (nan_blocks >> (2 * c + e / 16) & 1) x0[e] = 0x7fffffffu;
                     }
                     if (split) {
 #pragma unroll
@@ -634,6 +673,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             }
             __syncwarp();
             if (lane == 0) barrier_arrive(PART_FREE + 8 * (part & 3));
+            next_tiles = take(part + 1, next_factor);
         }
     } else if (w < 16) {
         give_registers<REGS_UNPACK>();
@@ -838,7 +878,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     const Request q = request_of(a, b, 128 * QT, TT, blockIdx.x == 0);
                     units += (long long)q.row_blocks * a.Hkv;
                     if (q.row_blocks) {
-                        const int tiles = Walker<QT>::most_tiles(a, q);
+                        const int tiles = Walker<QT>::most_tiles(a, q.len);
                         all += (long long)q.row_blocks * a.Hkv * tiles;
                         longest = max(longest, tiles);
                     }
