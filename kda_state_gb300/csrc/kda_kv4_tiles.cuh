@@ -41,8 +41,8 @@ constexpr int TILE_THREADS = 20 * 32;  // warps 18 and 19 are idle: registers ar
 constexpr int REGS_SOFTMAX = 168, REGS_UNPACK = 40, REGS_OTHER = 64;   // 640 threads are launched with 96
 static_assert(256 * REGS_SOFTMAX + 256 * REGS_UNPACK + 128 * REGS_OTHER <= TILE_THREADS * 96, "register split");
 constexpr int SMS = 152;
-constexpr int SPLIT_PARTS = 126;       // a cut aims at this many parts: at most twice as many arise
-constexpr int NEXT_PART = 2 * SPLIT_PARTS + 2, CTAS_DONE = NEXT_PART + 1;   // counters behind the joins'
+constexpr int MAX_SLOTS = 252;         // partial results, as the workspace holds
+constexpr int NEXT_PART = MAX_SLOTS, CTAS_DONE = NEXT_PART + 1;        // counters behind the joins'
 static_assert(CTAS_DONE < MAX_CTAS, "counters");
 
 // A piece of work: rows of one kv head of one request against tiles of its cache.
@@ -74,7 +74,7 @@ struct alignas(16) TileMeta {
     Part parts[4];
     int2 raw_about[8];                 // by stage of codes: tokens before the end; a bit a run of 16 out of range
     uint32_t tmem;
-    int last, dead;
+    int last, dead, cut;
     uint64_t bars[25 + 2 * 6];
 };
 
@@ -231,7 +231,7 @@ struct Walker {
             for (int i = 0; i < GROUPS; ++i)
                 if (b0 == 32 * i && cls_of[i] == cls) n = parts[i];
         } else if (b0 + lane < a.B) {
-            n = parts_of(a, request_of(a, b0 + lane, 128 * QT, TT, false));
+            n = parts_of(a, request_of(a, b0 + lane, 128 * QT, TT, blockIdx.x == 0));
         }
         mine = abs(n);
         my_slots = n < 0 ? -n : 0;
@@ -242,7 +242,7 @@ struct Walker {
             if (lane >= o) incl += x, slots_incl += y;
         }
     }
-    __device__ __forceinline__ void start(const KvAttentionArgs &a, int cut_, int longest) {
+    __device__ __forceinline__ void start(const KvAttentionArgs &a, int cut_) {
         cut = cut_;
         classes = a.B > 1 && a.B <= 32 * GROUPS ? 8 : 1;
         b0 = before = slots_before = cls = 0;
@@ -251,11 +251,18 @@ struct Walker {
             const int b = 32 * i + (threadIdx.x & 31);
             parts[i] = cls_of[i] = 0;
             if (classes > 1 && b < a.B) {
-                const Request q = request_of(a, b, 128 * QT, TT, false);
+                const Request q = request_of(a, b, 128 * QT, TT, blockIdx.x == 0);
                 parts[i] = parts_of(a, q);
-                cls_of[i] = q.row_blocks ? (int)((long long)(longest - most_tiles(a, q.len)) * classes / longest) : 0;
+                cls_of[i] = q.row_blocks ? most_tiles(a, q.len) : 0;      // tiles first
             }
         }
+        int longest = 1;
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) longest = max(longest, cls_of[i]);
+        longest = __reduce_max_sync(~0u, longest);
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i)
+            cls_of[i] = cls_of[i] ? (int)((long long)(longest - cls_of[i]) * classes / longest) : 0;
         load(a);
     }
     __device__ __forceinline__ bool find(const KvAttentionArgs &a, int p, Part &out) {
@@ -296,6 +303,46 @@ struct Walker {
         return true;
     }
 };
+
+// How the work is cut along the tokens (0: not at all); a whole warp calls it.
+// Only fewer units than SMs are cut, into the shortest pieces (of two tiles at least) that make one part an SM at most:
+// with more parts some SMs would work on two while others wait (one request of 100 new tokens over 3259, 56 units: 168 parts
+// 54 us, 112 parts 41 us).
+template <int QT>
+__device__ __noinline__ int cut_of(const KvAttentionArgs &a) {
+    constexpr int GROUPS = 5;              // larger batches are not cut
+    const int lane = threadIdx.x & 31;
+    int n_of[GROUPS], tiles_in[GROUPS];
+    long long units = 0, all = 0;
+    int longest = 1;
+    for (int i = 0; i < GROUPS; ++i) n_of[i] = 0, tiles_in[i] = 1;
+    for (int b = lane, i = 0; b < a.B; b += 32, ++i) {
+        const Request q = request_of(a, b, 128 * QT, TT, false);
+        if (!q.row_blocks) continue;
+        const int tiles = Walker<QT>::most_tiles(a, q.len);
+        units += (long long)q.row_blocks * a.Hkv;
+        all += (long long)q.row_blocks * a.Hkv * tiles;
+        longest = max(longest, tiles);
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k)
+            if (i == k) n_of[k] = q.row_blocks * a.Hkv, tiles_in[k] = tiles;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        units += __shfl_xor_sync(~0u, units, o);
+        all += __shfl_xor_sync(~0u, all, o);
+        longest = max(longest, __shfl_xor_sync(~0u, longest, o));
+    }
+    if (units >= SMS || a.B > 32 * GROUPS) return 0;
+    int cut = (int)max((all + SMS - 1) / SMS, 2LL);
+    for (; cut < longest; cut += max(cut / 8, 1)) {
+        int parts = 0;
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) parts += n_of[k] * ((tiles_in[k] + cut - 1) / cut);
+        if (__reduce_add_sync(~0u, parts) <= SMS) break;
+    }
+    return cut;
+}
 
 // Byte of the 16-byte chunk (8 fp16 of the contraction axis) of a row in a K-major tile of `rows` rows.
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk, int rows) {
@@ -355,6 +402,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
         }
         barrier_init(FINISHED, 1);
         meta.dead = 0;
+    }
+    if (QT == 1 && w == 17) {
+        const int cut = cut_of<QT>(a);
+        if (lane == 0) meta.cut = cut;
     }
     tmem_before_sync();
     __syncthreads();
@@ -645,26 +696,40 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     group_sync(1, 256);
                     if (*(volatile int *)&meta.last && !*dead) {
                         __threadfence();
-                        for (int i = tid; i < p.rows * (D / 4); i += 256) {
-                            const int col = i / (D / 4), d = i % (D / 4) * 4;
-                            float to = NOTHING, total = 0.f;
-                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        // four times four channels a thread, so that many loads are on their way
+                        constexpr int N = 4;
+                        for (int i0 = tid; i0 < p.rows * (D / 4); i0 += N * 256) {
+                            float to[N], total[N];
+                            float4 v[N];
+#pragma unroll
+                            for (int k = 0; k < N; ++k) to[k] = NOTHING, total[k] = 0.f, v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                             for (int x = 0; x < p.pieces; ++x) {
                                 const float *src = partials + (size_t)(p.slot0 + x) * S::PARTIAL;
-                                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + 128 * D + 2 * col));
-                                const float4 u = __ldcg(reinterpret_cast<const float4 *>(src + col * D + d));
-                                const float up = fmaxf(to, ml.x), keep = exp2_fast(to - up), add = exp2_fast(ml.x - up);
-                                to = up;
-                                total = total * keep + ml.y * add;
-                                v.x = v.x * keep + u.x * add, v.y = v.y * keep + u.y * add;
-                                v.z = v.z * keep + u.z * add, v.w = v.w * keep + u.w * add;
+#pragma unroll
+                                for (int k = 0; k < N; ++k) {
+                                    const int i = min(i0 + k * 256, p.rows * (D / 4) - 1);
+                                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(src + 128 * D) + i / (D / 4));
+                                    const float4 u = __ldcg(reinterpret_cast<const float4 *>(src) + i);
+                                    const float up = fmaxf(to[k], ml.x), keep = exp2_fast(to[k] - up), add = exp2_fast(ml.x - up);
+                                    to[k] = up;
+                                    total[k] = total[k] * keep + ml.y * add;
+                                    v[k].x = v[k].x * keep + u.x * add, v[k].y = v[k].y * keep + u.y * add;
+                                    v[k].z = v[k].z * keep + u.z * add, v[k].w = v[k].w * keep + u.w * add;
+                                }
                             }
-                            const int orow = p.row0 + col;
-                            const size_t at = (size_t)(p.q0 + orow / G) * a.Hq + p.h * G + orow % G;
-                            const float fo = total == 0.f ? 0.f : a.v_scale / total;
-                            *reinterpret_cast<uint2 *>((T *)a.o + at * D + d) =
-                                total == 0.f ? make_uint2(0, 0) : make_uint2(pack_of<T>(v.x * fo, v.y * fo), pack_of<T>(v.z * fo, v.w * fo));
-                            if (d == 0 && a.lse) a.lse[at] = total == 0.f ? -INFINITY : (to + log2f(total)) * LN2;
+#pragma unroll
+                            for (int k = 0; k < N; ++k) {
+                                const int i = i0 + k * 256, col = i / (D / 4), d = i % (D / 4) * 4;
+                                if (col >= p.rows) continue;
+                                const int orow = p.row0 + col;
+                                const size_t at = (size_t)(p.q0 + orow / G) * a.Hq + p.h * G + orow % G;
+                                const float fo = total[k] == 0.f ? 0.f : a.v_scale / total[k];
+                                *reinterpret_cast<uint2 *>((T *)a.o + at * D + d) =
+                                    total[k] == 0.f ? make_uint2(0, 0)
+                                                    : make_uint2(pack_of<T>(v[k].x * fo, v[k].y * fo), pack_of<T>(v[k].z * fo, v[k].w * fo));
+                                if (d == 0 && a.lse) a.lse[at] = total[k] == 0.f ? -INFINITY : (to[k] + log2f(total[k])) * LN2;
+                            }
                         }
                     }
                 }
@@ -870,30 +935,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             __syncwarp();
         } else if (w == 17) {
             // ============================ load =========================================================
-            // how the work is cut: only where there are fewer parts than SMs
-            int cut = 0, longest = 1;
-            {
-                long long units = 0, all = 0;
-                for (int b = lane; b < a.B; b += 32) {
-                    const Request q = request_of(a, b, 128 * QT, TT, blockIdx.x == 0);
-                    units += (long long)q.row_blocks * a.Hkv;
-                    if (q.row_blocks) {
-                        const int tiles = Walker<QT>::most_tiles(a, q.len);
-                        all += (long long)q.row_blocks * a.Hkv * tiles;
-                        longest = max(longest, tiles);
-                    }
-                }
-#pragma unroll
-                for (int o = 16; o; o >>= 1) {
-                    units += __shfl_xor_sync(~0u, units, o);
-                    all += __shfl_xor_sync(~0u, all, o);
-                    longest = max(longest, __shfl_xor_sync(~0u, longest, o));
-                }
-                if (QT == 1 && units < SMS) cut = (int)max((all + SPLIT_PARTS - 1) / SPLIT_PARTS, 2LL);
-            }
             int *const counters = reinterpret_cast<int *>(a.ws);
             Walker<QT> walk;
-            walk.start(a, cut, longest);
+            walk.start(a, QT == 1 ? meta.cut : 0);
             uint32_t raw = 0, raw_round = 0;
             for (uint32_t part = 0;; ++part) {
                 int pi = 0;
@@ -976,7 +1020,7 @@ cudaError_t launch_tile_attention(const KvAttentionArgs &a, cudaStream_t s) {
     using Sh = TileShape<D, QT>;
     constexpr int SMEM = Sh::META + sizeof(TileMeta);
     static_assert(SMEM <= 232448, "shared memory");
-    static_assert((size_t)MAX_CTAS * 4 + 2 * SPLIT_PARTS * (size_t)Sh::PARTIAL * 4 <= KDA_KV4_WORKSPACE, "workspace");
+    static_assert((size_t)MAX_CTAS * 4 + MAX_SLOTS * (size_t)Sh::PARTIAL * 4 <= KDA_KV4_WORKSPACE, "workspace");
     static const cudaError_t set =
         cudaFuncSetAttribute(tile_attention_kernel<D, QT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (set != cudaSuccess) return set;
