@@ -14,12 +14,24 @@ namespace {
 template <int D, typename T>
 cudaError_t launch(const KvAttentionArgs &a, cudaStream_t s) {
     const long long rows = (long long)a.max_q * (a.Hq / a.Hkv);
+    // Few rows: the kernel that reads the cache once, 8 or 16 rows at a time.  64 requests of 0.5 to 6 K tokens, D = 128,
+    // 8 kv heads: 16 rows 90 us against 128 us in tiles, 24 rows 148 against 129, 64 rows 279 against 134.
     if (rows <= 8) return kv4::launch_decode_attention<D, 1, T>(a, s);
     if (rows <= 16) return kv4::launch_decode_attention<D, 2, T>(a, s);
-    // 256 rows a part where that still makes enough parts for the SMs
-    const long long parts = (long long)a.T * (a.Hq / a.Hkv) / 256 * a.Hkv;
-    if (parts >= 2 * kv4::SMS) return kv4::launch_tile_attention<D, 2, T>(a, s);
-    return kv4::launch_tile_attention<D, 1, T>(a, s);
+    // Tiles with 256 rows a part make half as many parts, which take 1.3 times as long (3470 cycles a tile against 2700)
+    // and are not cut.  One request: as the waves of parts come out (300 new tokens of 8 x 8 heads over 3259: 43 us with
+    // 128 rows, one wave; 340: 58 with 256 rows, 75 with 128 in two waves).  Several, of unknown lengths: 256 rows where
+    // the average request fills them and there are a quarter more parts than SMs (218 parts: 96 us against 111; 109
+    // parts: 73 against 69).
+    const long long all = (long long)a.T * (a.Hq / a.Hkv);
+    bool wide;
+    if (a.B == 1) {
+        const long long w1 = ((all + 127) / 128 * a.Hkv + kv4::SMS - 1) / kv4::SMS, w2 = ((all + 255) / 256 * a.Hkv + kv4::SMS - 1) / kv4::SMS;
+        wide = 13 * w2 < 10 * w1;
+    } else {
+        wide = all >= 256LL * a.B && all / 256 * a.Hkv >= kv4::SMS * 5 / 4;
+    }
+    return wide ? kv4::launch_tile_attention<D, 2, T>(a, s) : kv4::launch_tile_attention<D, 1, T>(a, s);
 }
 
 }  // namespace
