@@ -528,7 +528,8 @@ KDA_API size_t kda_kv4_workspace_bytes(void);
  * A request with inconsistent cu_seqlens, more than max_q tokens or kv_lens out
  * of [0, max_pages page_size] is skipped (KDA_DEVERR_SEQLENS, its rows are not
  * written); tokens of a page that is out of range are left out
- * (KDA_DEVERR_PAGE_RANGE).
+ * (KDA_DEVERR_PAGE_RANGE).  After KDA_DEVERR_TIMEOUT the outputs of the call are
+ * not valid, and the workspace has to be zeroed.
  */
 KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv,
                               int D, const void *q, long long q_stride, const int32_t *cu_seqlens,
@@ -545,10 +546,12 @@ KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, 
  * others are -1.  Free pages are given out lowest number first, to rows in
  * order: the result is the same on every run.  All of it stays on the device.
  *
- * kda_page_alloc -- lens[b] grows by grow[b] >= 0 tokens, with the pages that
- * takes.  A row gets all of its pages or, when the pool runs out, none (its
- * length stays, KDA_DEVERR_PAGES); later rows that need a page then get none
- * either.
+ * kda_page_alloc -- lens[b] grows by grow[b] tokens, with the pages that takes.
+ * A row gets all of its pages or, when the pool runs out, none (its length stays,
+ * KDA_DEVERR_PAGES); later rows that need a page then get none either.  A
+ * negative grow takes tokens back (drafts that were not accepted) and lets go of
+ * the pages behind the new end, before any are given out; into a page that
+ * another row holds too a row cannot shrink (KDA_DEVERR_PAGES, it stays).
  */
 KDA_API int kda_page_alloc(int B, int max_pages, int page_size, int num_pages, int32_t *refs,
                            int32_t *page_table, int32_t *lens, const int32_t *grow,

@@ -858,7 +858,7 @@ def _page_pools(pools, num_pages, first):
 
 def kda_page_alloc(refs, page_table, lens, grow, page_size: int, dev_err=None, stream=None):
     """Row b grows by grow[b] tokens (int32 [B]): the pages that takes are the lowest free
-    ones, rows in order.  refs int32 [num_pages] (holders of each page, 0: free),
+    ones, rows in order; a negative grow takes tokens back and lets go of their pages.  refs int32 [num_pages] (holders of each page, 0: free),
     page_table int32 [B, max_pages], lens int32 [B]; all three change in place."""
     ra, ta, la, B, M, N = _page_state(refs, page_table, lens)
     status = lib().kda_page_alloc(B, M, page_size, N, ra, ta, la, _ptr(grow, "grow", (B,), I32, refs),
@@ -922,7 +922,8 @@ def kda_page_copy(pools, src, dst, dev_err=None, stream=None):
         raise ValueError("pools must be a non-empty list")
     _first(src, "src", 1)
     n = src.numel()
-    _need(pools[0], "pools[0]", device=src.device)
+    if not isinstance(pools[0], torch.Tensor) or pools[0].dim() < 1:
+        raise ValueError("pools[0] needs a page axis")
     N = pools[0].shape[0]
     keep, ptrs, page_bytes = _page_pools(pools, N, src)
     status = lib().kda_page_copy(

@@ -70,6 +70,16 @@ struct DecodeShape {
     static constexpr int PARTIAL = ROWS * (D + 2);         // floats
 };
 
+// Whether the phase with the given parity is complete (it may wait a short time).
+__device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok;
+}
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
     asm volatile(
@@ -771,8 +781,7 @@ template <int D, int NT, typename T>
 cudaError_t launch_decode_attention(const KvAttentionArgs &a, cudaStream_t s) {
     using Sh = DecodeShape<D, NT>;
     static_assert((size_t)MAX_CTAS * (4 + 2 * Sh::PARTIAL * 4) <= KDA_KV4_WORKSPACE, "workspace");
-    static const cudaError_t set = cudaFuncSetAttribute(decode_attention_kernel<D, NT, T>,
-                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+    const cudaError_t set = cudaFuncSetAttribute(decode_attention_kernel<D, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
     if (set != cudaSuccess) return set;
     decode_attention_kernel<D, NT, T><<<NT == 1 ? MAX_CTAS : MAX_CTAS / 2, THREADS, Sh::SMEM, s>>>(a);
     return cudaGetLastError();

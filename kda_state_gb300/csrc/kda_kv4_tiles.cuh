@@ -1021,7 +1021,7 @@ cudaError_t launch_tile_attention(const KvAttentionArgs &a, cudaStream_t s) {
     constexpr int SMEM = Sh::META + sizeof(TileMeta);
     static_assert(SMEM <= 232448, "shared memory");
     static_assert((size_t)MAX_CTAS * 4 + MAX_SLOTS * (size_t)Sh::PARTIAL * 4 <= KDA_KV4_WORKSPACE, "workspace");
-    static const cudaError_t set =
+    const cudaError_t set =
         cudaFuncSetAttribute(tile_attention_kernel<D, QT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (set != cudaSuccess) return set;
     tile_attention_kernel<D, QT, T><<<SMS, TILE_THREADS, SMEM, s>>>(a);

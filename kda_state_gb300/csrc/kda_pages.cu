@@ -103,9 +103,59 @@ __device__ __forceinline__ int pages_of(int tokens, int shift) {
     return (int)(((long long)tokens + (1 << shift) - 1) >> shift);
 }
 
+// One holder less of the page that a table's entry names; the entry becomes -1.
+__device__ __forceinline__ void let_go(const PageArgs &a, int32_t *entry) {
+    const int page = *entry;
+    if (page < 0 || page >= a.num_pages) report(a.err, DEVERR_PAGE_RANGE);
+    else if (atomicSub(&a.refs[page], 1) <= 0) {           // it was free already
+        atomicAdd(&a.refs[page], 1);
+        report(a.err, DEVERR_PAGES);
+    }
+    *entry = -1;
+}
+
 __global__ void __launch_bounds__(SCAN) alloc_kernel(const PageArgs a, const int32_t *__restrict__ grow) {
     __shared__ int upto[SCAN], have_s[SCAN], need_s[SCAN];
     int cursor = 0;
+    // Rows that shrink come first: all of them are looked at before any lets go of a page, so that what a row may do
+    // does not depend on when another's count went down.  (65536 rows in one go: a bit each of a thread's 64.)
+    bool any = false;
+    for (int b = threadIdx.x; b < a.B; b += SCAN) any |= grow[b] < 0;
+    if (__syncthreads_or(any)) {
+        for (int g0 = 0; g0 < a.B; g0 += 64 * SCAN) {
+            unsigned long long shrinks = 0;
+            for (int i = 0; i < 64; ++i) {
+                const int b = g0 + i * SCAN + (int)threadIdx.x;
+                if (b >= a.B || grow[b] >= 0) continue;
+                const int len = a.lens[b];
+                const long long to = (long long)len + grow[b];
+                if (to < 0 || (long long)len > ((long long)a.max_pages << a.page_shift)) {
+                    report(a.err, DEVERR_SEQLENS);
+                    continue;
+                }
+                if (to & ((1 << a.page_shift) - 1)) {      // its new last page is one it will write to: not a shared one
+                    const int page = a.page_table[(size_t)b * a.max_pages + (to >> a.page_shift)];
+                    if (page < 0 || page >= a.num_pages) {
+                        report(a.err, DEVERR_PAGE_RANGE);
+                        continue;
+                    }
+                    if (a.refs[page] > 1) {
+                        report(a.err, DEVERR_PAGES);
+                        continue;
+                    }
+                }
+                shrinks |= 1ull << i;
+            }
+            __syncthreads();
+            for (int i = 0; i < 64; ++i) {
+                if (!(shrinks >> i & 1)) continue;
+                const int b = g0 + i * SCAN + (int)threadIdx.x, len = a.lens[b], to = len + grow[b];
+                for (int j = pages_of(to, a.page_shift); j < pages_of(len, a.page_shift); ++j) let_go(a, a.page_table + (size_t)b * a.max_pages + j);
+                a.lens[b] = to;
+            }
+            __syncthreads();
+        }
+    }
     bool out = false;                  // the pool has run out: later rows that need pages get none
     for (int b0 = 0; b0 < a.B; b0 += SCAN) {
         const int b = b0 + threadIdx.x, n = min(SCAN, a.B - b0);
@@ -115,9 +165,10 @@ __global__ void __launch_bounds__(SCAN) alloc_kernel(const PageArgs a, const int
             const int len = a.lens[b];
             g = grow[b];
             const long long to = (long long)len + g;
-            bad = len < 0 || g < 0 || to > ((long long)a.max_pages << a.page_shift);
-            if (bad) report(a.err, DEVERR_SEQLENS);
-            else {
+            bad = g < 0 || len < 0 || to > ((long long)a.max_pages << a.page_shift);
+            if (bad) {
+                if (g >= 0) report(a.err, DEVERR_SEQLENS);
+            } else {
                 have = pages_of(len, a.page_shift);
                 need = pages_of((int)to, a.page_shift) - have;
             }
@@ -244,15 +295,8 @@ __global__ void __launch_bounds__(128) free_kernel(const PageArgs a, const int32
     const int held = pages_of(len, a.page_shift);
     for (int j = threadIdx.x; j < a.max_pages; j += blockDim.x) {
         int32_t *entry = a.page_table + (size_t)b * a.max_pages + j;
-        if (j < held) {
-            const int page = *entry;
-            if (page < 0 || page >= a.num_pages) report(a.err, DEVERR_PAGE_RANGE);
-            else if (atomicSub(&a.refs[page], 1) <= 0) {   // it was free already
-                atomicAdd(&a.refs[page], 1);
-                report(a.err, DEVERR_PAGES);
-            }
-        }
-        *entry = -1;
+        if (j < held) let_go(a, entry);
+        else *entry = -1;
     }
     __syncthreads();
     if (threadIdx.x == 0) a.lens[b] = 0;

@@ -116,8 +116,23 @@ class Pages:
         return [p for p, r in enumerate(self.refs) if r == 0]
 
     def alloc(self, grow):
-        out = False
+        out = refused = False
+        may = [g < 0 and (not (self.lens[b] + g) % self.P or self.refs[self.table[b][(self.lens[b] + g) // self.P]] == 1)
+               for b, g in enumerate(grow)]
         for b, g in enumerate(grow):
+            if g >= 0:
+                continue
+            if not may[b]:
+                refused = True
+                continue
+            keep = -(-(self.lens[b] + g) // self.P)
+            for j in range(keep, self.held(b)):
+                self.refs[self.table[b][j]] -= 1
+                self.table[b][j] = -1
+            self.lens[b] += g
+        for b, g in enumerate(grow):
+            if g < 0:
+                continue
             have = self.held(b)
             need = -(-(self.lens[b] + g) // self.P) - have
             free = self._free()
@@ -128,7 +143,7 @@ class Pages:
                 self.table[b][have + j] = free[j]
                 self.refs[free[j]] = 1
             self.lens[b] += g
-        return out
+        return out or refused
 
     def fork(self, src, dst, data):
         """data: list of arrays [num_pages, ...].  Returns True when pages ran out."""

@@ -115,6 +115,36 @@ def test_random_steps(seed):
             s.compact()
 
 
+def test_rows_shrink():
+    s = Both(12, 4, 6, 16)
+    s.alloc([40, 33, 16, 0])
+    s.alloc([-7, -33, -1, 0])          # a page back, all of them, none
+    s.alloc([-1, 0, -15, 96])          # what shrinking frees is there for the growing row
+    s.alloc([0, 20, 0, -90])
+    s.fork([0], [2])                   # rows 0 and 2 share two full pages
+    s.alloc([-3, 0, 5, 0])             # row 0 would write into a shared one: refused
+    s.alloc([-16, 0, -21, 0])          # to a border: allowed; row 2 to its own page's start
+    s.alloc([-16, 0, 0, 0])
+    s.alloc([0, 0, -3, 0])             # now row 2 holds its pages alone
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_random_steps_with_drafts(seed):
+    """Growth by drafts, and back by those not accepted, between forks and ends."""
+    rng = np.random.default_rng(50 + seed)
+    rows, P = [7, 60, 1100][seed], [16, 32, 16][seed]
+    s = Both([40, 200, 4000][seed], rows, 10, P, seed=seed)
+    for step in range(25):
+        s.alloc([int(rng.integers(1, 9)) if n < 8 * P else 0 for n in s.o.lens])
+        s.alloc([-int(rng.integers(0, min(n, 8) + 1)) if rng.random() < .8 else int(n < 8 * P) for n in s.o.lens])
+        full = [b for b in range(rows) if s.o.lens[b]]
+        s.free([int(x) for x in rng.permutation(full)[:max(1, len(full) // 6)]])
+        full = [b for b in range(rows) if s.o.lens[b]]
+        empty = [b for b in range(rows) if not s.o.lens[b]]
+        if full and empty:
+            s.fork([full[0]] * len(empty[:3]), empty[:3])
+
+
 def test_large_tables_cross_the_scan_steps():
     """More pages than one scan step (16384), more rows than one block (1024)."""
     s = Both(50000, 2500, 20, 16, layers=1, page_shape=(16,))
@@ -159,7 +189,7 @@ def test_bad_rows_change_nothing():
     for rows, bit in (([6], 1), ([-1], 1)):
         call(kda().kda_page_free, *s.state(), i32(rows), 16)
         s.same(bit)
-    for grow in ([0, 0, 81, 0, 0, 0], [0, -1, 0, 0, 0, 0], [0, 0, 0, 2 ** 31 - 1, 0, 0]):
+    for grow in ([0, 0, 81, 0, 0, 0], [0, -34, 0, 0, 0, 0], [0, 0, -1, 0, 0, 0], [0, 0, 0, 2 ** 31 - 1, 0, 0]):
         call(kda().kda_page_alloc, *s.state(), i32(grow), 16)
         s.same(4)
     # an entry that names no page: flagged, the rest of the row goes on

@@ -84,7 +84,7 @@ def test_pages_keep_counts():
     for step in range(200):
         op = rng.integers(4)
         if op == 0:
-            p.alloc([int(rng.integers(0, 20)) if p.lens[b] < 70 else 0 for b in range(8)])
+            p.alloc([int(rng.integers(-min(9, p.lens[b]), 20)) if p.lens[b] < 70 else 0 for b in range(8)])
         elif op == 1:
             src = [b for b in range(8) if p.lens[b]]
             dst = [b for b in range(8) if not p.lens[b]]
