@@ -77,11 +77,11 @@ template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) append_kernel(const KvCacheArgs a) {
     constexpr int NB = D / 16;
     using L = KvTile<D>;
-    const long long id = (long long)blockIdx.x * THREADS + threadIdx.x;
-    const int blk = (int)(id % NB), side = (int)(id / NB & 1);
-    const long long th = id / (2 * NB);
-    const int h = (int)(th % a.H);
-    const int t = (int)(th / a.H);
+    // (token, head) pairs have 31 bits; a CTA holds a whole number of them
+    constexpr int PAIRS = THREADS / (2 * NB);
+    const int blk = threadIdx.x % NB, side = threadIdx.x / NB & 1;
+    const unsigned pair = blockIdx.x * (unsigned)PAIRS + threadIdx.x / (2 * NB);
+    const int t = (int)(pair / (unsigned)a.H), h = (int)(pair - (unsigned)t * a.H);
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
     if (t < a.T) {
         const T *src = (side ? (const T *)a.v + t * a.v_stride : (const T *)a.k + t * a.k_stride) + h * D + blk * 16;
@@ -118,11 +118,11 @@ template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) gather_kernel(const KvCacheArgs a) {
     constexpr int NB = D / 16;
     using L = KvTile<D>;
-    const long long id = (long long)blockIdx.x * THREADS + threadIdx.x;
-    const int blk = (int)(id % NB), side = (int)(id / NB & 1);
-    const long long th = id / (2 * NB);
-    const int h = (int)(th % a.H);
-    const int t = (int)(th / a.H);
+    // (token, head) pairs have 31 bits; a CTA holds a whole number of them
+    constexpr int PAIRS = THREADS / (2 * NB);
+    const int blk = threadIdx.x % NB, side = threadIdx.x / NB & 1;
+    const unsigned pair = blockIdx.x * (unsigned)PAIRS + threadIdx.x / (2 * NB);
+    const int t = (int)(pair / (unsigned)a.H), h = (int)(pair - (unsigned)t * a.H);
     int tok;
     const uint8_t *tile = locate<D>(a, t, h, tok);
     if (t >= a.T) return;
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const KvCacheArgs a) {
 
 template <int D, typename T>
 cudaError_t launch(const KvCacheArgs &a, bool append, cudaStream_t s) {
-    const long long n = (long long)a.T * a.H * 2 * (D / 16);
-    const long long grid = (n + THREADS - 1) / THREADS;
+    constexpr int PAIRS = THREADS / (2 * (D / 16));
+    const long long grid = ((long long)a.T * a.H + PAIRS - 1) / PAIRS;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if (append) append_kernel<D, T><<<(unsigned)grid, THREADS, 0, s>>>(a);
     else gather_kernel<D, T><<<(unsigned)grid, THREADS, 0, s>>>(a);
