@@ -633,7 +633,7 @@ def kda_slot_copy(pools, src, dst, dev_err=None, stream=None):
 KV_TILE = 16          # tokens of a tile
 _KV_DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_FP16}
 _U8 = torch.uint8
-_width, _device_of = torch.Tensor.element_size, torch.Tensor.get_device
+_numel, _width, _device_of = torch.Tensor.numel, torch.Tensor.element_size, torch.Tensor.get_device
 _dense, _address = torch.Tensor.is_contiguous, torch.Tensor.data_ptr
 
 
@@ -665,43 +665,48 @@ def _kv_dt(dtype):
     return _KV_DT[dtype]
 
 
-def _ptr(t, name, shape, dtype, first):
-    """The address of a dense tensor of this shape and dtype on first's device."""
+def _ptr(t, name, shape, dtype, dev):
+    """The address of a dense tensor of this shape and dtype on CUDA device number dev."""
     try:
-        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and
-                t.get_device() == first.get_device()):
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
         pass
-    _need(t, name, shape, dtype, first.device)
+    _need(t, name, shape, dtype, torch.device("cuda", dev))
     return t.data_ptr()
 
 
-def _err_ptr(dev_err, first):
+def _err_ptr(dev_err, dev):
     if dev_err is None:
         return None
-    _need_err(dev_err, first.device)
+    _need_err(dev_err, torch.device("cuda", dev))
     return dev_err.data_ptr()
 
 
-def _stream_of(stream, first):
+def _stream_of(stream, dev):
     """The stream argument as a handle: by default the current one of the operands' device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(first.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _first(t, name, dims):
-    """The operand that sets the device: a CUDA tensor of ``dims`` dimensions."""
+    """The operand that sets the device, a CUDA tensor of ``dims`` dimensions.  Returns its shape and
+    the device's number."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != dims:
         _need(t, name, (None,) * dims, dense=False)
+    return t.shape, t.get_device()
 
 
-def _rows(t, name, dtype, shape, first):
+def _rows(t, name, dtype, shape, dev):
     """[tokens, heads, D] whose heads are dense and whose tokens may be strided.  Returns the
     address and the stride between tokens, in elements."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != first.get_device():
-        _need(t, name, shape, dtype, first.device, dense=False)
+    try:
+        same = t.dtype is dtype and t.shape == shape and t.get_device() == dev
+    except AttributeError:
+        same = False
+    if not same:
+        _need(t, name, shape, dtype, torch.device("cuda", dev), dense=False)
     T, H, D = shape
     stride, head, one = t.stride()
     if T <= 1:
@@ -714,19 +719,20 @@ def _rows(t, name, dtype, shape, first):
     return at, stride
 
 
-def _pool(pool, D, first):
+def _pool(pool, D, dev):
     """uint8 [num_pages, H_kv, page_size / 16, 18 D].  Returns (address, num_pages, H_kv, page_size)."""
     shape = pool.shape if isinstance(pool, torch.Tensor) else ()
     if len(shape) != 4 or shape[3] != 18 * D:
-        _need(pool, "pool", (None, None, None, 18 * D), _U8, first.device)
-    return _ptr(pool, "pool", shape, _U8, first), shape[0], shape[1], shape[2] * KV_TILE
+        _need(pool, "pool", (None, None, None, 18 * D), _U8, torch.device("cuda", dev))
+    return _ptr(pool, "pool", shape, _U8, dev), shape[0], shape[1], shape[2] * KV_TILE
 
 
-def _table(page_table, first):
+def _table(page_table, dev):
     """int32 [B, max_pages].  Returns (address, B, max_pages)."""
-    _first(page_table, "page_table", 2)
-    B, M = page_table.shape
-    return _ptr(page_table, "page_table", (B, M), I32, first), B, M
+    shape = page_table.shape if isinstance(page_table, torch.Tensor) else ()
+    if len(shape) != 2:
+        shape = (None, None)
+    return (_ptr(page_table, "page_table", shape, I32, dev),) + tuple(shape)
 
 
 def kda_kv4_append(k, v, cu_seqlens, start, page_table, pool, k_scale: float = 1.0,
@@ -735,20 +741,20 @@ def kda_kv4_append(k, v, cu_seqlens, start, page_table, pool, k_scale: float = 1
     strided) as 4-bit codes: token i of request b at position start[b] + i of the
     pages that row b of page_table (int32 [B, max_pages]) names.  cu_seqlens int32
     [B + 1], start int32 [B]; the scales are powers of two.  Writes the pool in place."""
-    _first(k, "k", 3)
-    dt, shape = _kv_dt(k.dtype), k.shape
+    shape, dev = _first(k, "k", 3)
+    dtype = k.dtype
+    dt = _kv_dt(dtype)
     T, H, D = shape
-    ka, ks = _rows(k, "k", k.dtype, shape, k)
-    _first(v, "v", 3)
-    va, vs = _rows(v, "v", k.dtype, shape, k)
-    pa, pages, Hp, page_size = _pool(pool, D, k)
+    ka, ks = _rows(k, "k", dtype, shape, dev)
+    va, vs = _rows(v, "v", dtype, shape, dev)
+    pa, pages, Hp, page_size = _pool(pool, D, dev)
     if Hp != H:
         raise ValueError("pool has %d heads, k has %d" % (Hp, H))
-    ta, B, M = _table(page_table, k)
+    ta, B, M = _table(page_table, dev)
     status = lib().kda_kv4_append(
-        dt, B, T, H, D, ka, ks, va, vs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, k),
-        _ptr(start, "start", (B,), I32, k), ta, M, page_size, pa, pages, k_scale, v_scale,
-        _err_ptr(dev_err, k), _stream_of(stream, k))
+        dt, B, T, H, D, ka, ks, va, vs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(start, "start", (B,), I32, dev), ta, M, page_size, pa, pages, k_scale, v_scale,
+        _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_kv4_append", status)
 
 
@@ -758,25 +764,25 @@ def kda_kv4_gather(cu_seqlens, start, total_tokens: int, page_table, pool, dtype
     """Read tokens back as the values they stand for: positions start[b] + i of request b
     into packed k, v [total_tokens, H_kv, D].  Returns (k, v)."""
     dt = _kv_dt(dtype)
-    _first(pool, "pool", 4)
-    D, T = pool.shape[3] // 18, int(total_tokens)
-    pa, pages, H, page_size = _pool(pool, D, pool)
-    ta, B, M = _table(page_table, pool)
+    shape, dev = _first(pool, "pool", 4)
+    D, T = shape[3] // 18, int(total_tokens)
+    pa, pages, H, page_size = _pool(pool, D, dev)
+    ta, B, M = _table(page_table, dev)
     if k is None:
         k = torch.empty(T, H, D, dtype=dtype, device=pool.device)
         ka = k.data_ptr()
     else:
-        ka = _ptr(k, "k", (T, H, D), dtype, pool)
+        ka = _ptr(k, "k", (T, H, D), dtype, dev)
     if v is None:
         v = torch.empty(T, H, D, dtype=dtype, device=pool.device)
         va = v.data_ptr()
     else:
-        va = _ptr(v, "v", (T, H, D), dtype, pool)
+        va = _ptr(v, "v", (T, H, D), dtype, dev)
     status = lib().kda_kv4_gather(
         dt, B, T, H, D, ka, va,
-        _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, pool), _ptr(start, "start", (B,), I32, pool),
-        ta, M, page_size, pa, pages, k_scale, v_scale, _err_ptr(dev_err, pool),
-        _stream_of(stream, pool))
+        _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev), _ptr(start, "start", (B,), I32, dev),
+        ta, M, page_size, pa, pages, k_scale, v_scale, _err_ptr(dev_err, dev),
+        _stream_of(stream, dev))
     _check("kda_kv4_gather", status)
     return k, v
 
@@ -791,62 +797,60 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
     defaults to D ** -0.5.  ``workspace``: ``make_kv4_workspace()``, kept by the caller
     (one for each stream); a call without one makes its own.  Returns (o, lse), o in
     q's dtype and lse fp32 [T, H_q]; a row that sees nothing has o = 0, lse = -inf."""
-    _first(q, "q", 3)
-    dtype, shape = q.dtype, q.shape
+    shape, dev = _first(q, "q", 3)
+    dtype = q.dtype
     dt = _kv_dt(dtype)
     T, H, D = shape
-    qa, qs = _rows(q, "q", dtype, shape, q)
-    pa, pages, H_kv, page_size = _pool(pool, D, q)
-    ta, B, M = _table(page_table, q)
+    qa, qs = _rows(q, "q", dtype, shape, dev)
+    pa, pages, H_kv, page_size = _pool(pool, D, dev)
+    ta, B, M = _table(page_table, dev)
     if o is None:
         o = torch.empty(T, H, D, dtype=dtype, device=q.device)
         oa = o.data_ptr()
     else:
-        oa = _ptr(o, "o", shape, dtype, q)
+        oa = _ptr(o, "o", shape, dtype, dev)
     if lse is None:
         lse = torch.empty(T, H, dtype=F32, device=q.device)
         la = lse.data_ptr()
     else:
-        la = _ptr(lse, "lse", (T, H), F32, q)
+        la = _ptr(lse, "lse", (T, H), F32, dev)
     if workspace is None:
         workspace = make_kv4_workspace(q.device)
-    _first(workspace, "workspace", 1)
-    wb = workspace.numel()
+    (wb,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_kv4_attention(
-        dt, B, T, max_q, H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, q),
-        _ptr(kv_lens, "kv_lens", (B,), I32, q), ta, M, page_size, pa, pages, window,
+        dt, B, T, max_q, H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size, pa, pages, window,
         D ** -0.5 if scale is None else scale, k_scale, v_scale, oa, la,
-        _ptr(workspace, "workspace", (wb,), _U8, q), wb,
-        _err_ptr(dev_err, q), _stream_of(stream, q))
+        _ptr(workspace, "workspace", (wb,), _U8, dev), wb,
+        _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_kv4_attention", status)
     return o, lse
 
 
 def _page_state(refs, page_table, lens):
     """refs int32 [num_pages], page_table int32 [B, max_pages], lens int32 [B].  Returns their
-    addresses and (B, max_pages, num_pages)."""
-    _first(refs, "refs", 1)
-    N = refs.numel()
-    ta, B, M = _table(page_table, refs)
-    return (_ptr(refs, "refs", (N,), I32, refs), ta,
-            None if lens is None else _ptr(lens, "lens", (B,), I32, refs), B, M, N)
+    addresses, (B, max_pages, num_pages) and the device's number."""
+    (N,), dev = _first(refs, "refs", 1)
+    ta, B, M = _table(page_table, dev)
+    return (_ptr(refs, "refs", (N,), I32, dev), ta,
+            None if lens is None else _ptr(lens, "lens", (B,), I32, dev), B, M, N, dev)
 
 
-def _page_pools(pools, num_pages, first):
-    """Layers' pools [num_pages, ...] with pages of one size.  Returns (the array of their
-    addresses, its address, bytes of a page); the array has to outlive the call."""
+def _page_pools(pools, num_pages, dev):
+    """Layers' pools [num_pages, ...] of one size.  Returns (the array of their addresses, its
+    address, bytes of a page); the array has to outlive the call."""
     if len(pools) == 0:
         raise ValueError("pools must be a non-empty list")
     try:
-        shapes, widths = [p.shape for p in pools], list(map(_width, pools))
-        one = (shapes.count(shapes[0]) == widths.count(widths[0]) == len(pools) and
-               len(shapes[0]) >= 2 and shapes[0][0] == num_pages and
-               set(map(_device_of, pools)) == {first.get_device()} and all(map(_dense, pools)))
+        shape, sizes, widths = pools[0].shape, list(map(_numel, pools)), list(map(_width, pools))
+        one = (sizes.count(sizes[0]) == widths.count(widths[0]) == len(pools) and
+               len(shape) >= 2 and shape[0] == num_pages and
+               set(map(_device_of, pools)) == {dev} and all(map(_dense, pools)))
     except (AttributeError, TypeError):
         one = False
     if not one:
         for n, q in enumerate(pools):
-            _need(q, "pools[%d]" % n, device=first.device)
+            _need(q, "pools[%d]" % n, device=torch.device("cuda", dev))
             if q.dim() < 2 or q.shape[0] != num_pages or q.shape != pools[0].shape or (
                     q.dtype != pools[0].dtype):
                 raise ValueError("pools[%d]: every pool is [%d, ...] of one shape and dtype" % (
@@ -860,9 +864,9 @@ def kda_page_alloc(refs, page_table, lens, grow, page_size: int, dev_err=None, s
     """Row b grows by grow[b] tokens (int32 [B]): the pages that takes are the lowest free
     ones, rows in order; a negative grow takes tokens back and lets go of their pages.  refs int32 [num_pages] (holders of each page, 0: free),
     page_table int32 [B, max_pages], lens int32 [B]; all three change in place."""
-    ra, ta, la, B, M, N = _page_state(refs, page_table, lens)
-    status = lib().kda_page_alloc(B, M, page_size, N, ra, ta, la, _ptr(grow, "grow", (B,), I32, refs),
-                                  _err_ptr(dev_err, refs), _stream_of(stream, refs))
+    ra, ta, la, B, M, N, dev = _page_state(refs, page_table, lens)
+    status = lib().kda_page_alloc(B, M, page_size, N, ra, ta, la, _ptr(grow, "grow", (B,), I32, dev),
+                                  _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_page_alloc", status)
 
 
@@ -871,28 +875,25 @@ def kda_page_fork(pools, refs, page_table, lens, src, dst, page_size: int, works
     """Copy-on-write: row dst[i] (empty) also holds row src[i]'s full pages, and gets a
     copy of its partial last page in every pool of the list.  ``workspace``: int32, at
     least 2 n; a call without one makes its own."""
-    ra, ta, la, B, M, N = _page_state(refs, page_table, lens)
-    keep, ptrs, page_bytes = _page_pools(pools, N, refs)
-    _first(src, "src", 1)
-    n = src.numel()
+    ra, ta, la, B, M, N, dev = _page_state(refs, page_table, lens)
+    keep, ptrs, page_bytes = _page_pools(pools, N, dev)
+    (n,), _ = _first(src, "src", 1)
     if workspace is None:
         workspace = torch.empty(2 * n, dtype=I32, device=refs.device)
-    _first(workspace, "workspace", 1)
-    wn = workspace.numel()
+    (wn,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_page_fork(
-        len(pools), ptrs, page_bytes, B, M, page_size, N, ra, ta, la, _ptr(src, "src", (n,), I32, refs),
-        _ptr(dst, "dst", (n,), I32, refs), n, _ptr(workspace, "workspace", (wn,), I32, refs), wn,
-        _err_ptr(dev_err, refs), _stream_of(stream, refs))
+        len(pools), ptrs, page_bytes, B, M, page_size, N, ra, ta, la, _ptr(src, "src", (n,), I32, dev),
+        _ptr(dst, "dst", (n,), I32, dev), n, _ptr(workspace, "workspace", (wn,), I32, dev), wn,
+        _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_page_fork", status)
 
 
 def kda_page_free(refs, page_table, lens, rows, page_size: int, dev_err=None, stream=None):
     """Rows (int32 [n], distinct) let go of their pages; those nobody holds are free."""
-    ra, ta, la, B, M, N = _page_state(refs, page_table, lens)
-    _first(rows, "rows", 1)
-    n = rows.numel()
-    status = lib().kda_page_free(B, M, page_size, N, ra, ta, la, _ptr(rows, "rows", (n,), I32, refs), n,
-                                 _err_ptr(dev_err, refs), _stream_of(stream, refs))
+    ra, ta, la, B, M, N, dev = _page_state(refs, page_table, lens)
+    (n,), _ = _first(rows, "rows", 1)
+    status = lib().kda_page_free(B, M, page_size, N, ra, ta, la, _ptr(rows, "rows", (n,), I32, dev), n,
+                                 _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_page_free", status)
 
 
@@ -900,18 +901,17 @@ def kda_page_compact(pools, refs, page_table, live=None, workspace=None, dev_err
     """Move the held pages above the number of held pages into the free ones below, in
     every pool; refs and page_table follow.  Returns live, int32 [1] on the device: the
     pages from there on are free.  ``workspace``: int32, at least 3 num_pages + 16."""
-    ra, ta, _, B, M, N = _page_state(refs, page_table, None)
-    keep, ptrs, page_bytes = _page_pools(pools, N, refs)
+    ra, ta, _, B, M, N, dev = _page_state(refs, page_table, None)
+    keep, ptrs, page_bytes = _page_pools(pools, N, dev)
     if live is None:
         live = torch.empty(1, dtype=I32, device=refs.device)
     if workspace is None:
         workspace = torch.empty(3 * N + 16, dtype=I32, device=refs.device)
-    _first(workspace, "workspace", 1)
-    wn = workspace.numel()
+    (wn,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_page_compact(
-        len(pools), ptrs, page_bytes, B, M, N, ra, ta, _ptr(live, "live", (1,), I32, refs),
-        _ptr(workspace, "workspace", (wn,), I32, refs), wn, _err_ptr(dev_err, refs),
-        _stream_of(stream, refs))
+        len(pools), ptrs, page_bytes, B, M, N, ra, ta, _ptr(live, "live", (1,), I32, dev),
+        _ptr(workspace, "workspace", (wn,), I32, dev), wn, _err_ptr(dev_err, dev),
+        _stream_of(stream, dev))
     _check("kda_page_compact", status)
     return live
 
@@ -920,15 +920,14 @@ def kda_page_copy(pools, src, dst, dev_err=None, stream=None):
     """Page dst[i] <- page src[i] in every pool of the list (int32 device index tensors)."""
     if len(pools) == 0:
         raise ValueError("pools must be a non-empty list")
-    _first(src, "src", 1)
-    n = src.numel()
+    (n,), dev = _first(src, "src", 1)
     if not isinstance(pools[0], torch.Tensor) or pools[0].dim() < 1:
         raise ValueError("pools[0] needs a page axis")
     N = pools[0].shape[0]
-    keep, ptrs, page_bytes = _page_pools(pools, N, src)
+    keep, ptrs, page_bytes = _page_pools(pools, N, dev)
     status = lib().kda_page_copy(
-        len(pools), ptrs, page_bytes, N, _ptr(src, "src", (n,), I32, src),
-        _ptr(dst, "dst", (n,), I32, src), n, _err_ptr(dev_err, src), _stream_of(stream, src))
+        len(pools), ptrs, page_bytes, N, _ptr(src, "src", (n,), I32, dev),
+        _ptr(dst, "dst", (n,), I32, dev), n, _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_page_copy", status)
 
 

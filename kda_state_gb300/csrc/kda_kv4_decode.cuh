@@ -29,6 +29,8 @@
 // before the last one's result leaves.
 #pragma once
 
+#include <atomic>
+
 #include "kda_async.cuh"
 #include "kda_internal.h"
 #include "kda_kv4.cuh"
@@ -777,12 +779,24 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     }
 }
 
+// Lets a kernel use `bytes` of dynamic shared memory on the current device: asked for once a device (a call costs as
+// much as a launch's arguments do), `done` has a bit for each of the first 64.
+inline cudaError_t allow_shared(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
+
 template <int D, int NT, typename T>
 cudaError_t launch_decode_attention(const KvAttentionArgs &a, cudaStream_t s) {
     using Sh = DecodeShape<D, NT>;
     static_assert((size_t)MAX_CTAS * (4 + 2 * Sh::PARTIAL * 4) <= KDA_KV4_WORKSPACE, "workspace");
-    const cudaError_t set = cudaFuncSetAttribute(decode_attention_kernel<D, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
-    if (set != cudaSuccess) return set;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(decode_attention_kernel<D, NT, T>), Sh::SMEM, done);
+    if (e != cudaSuccess) return e;
     decode_attention_kernel<D, NT, T><<<NT == 1 ? MAX_CTAS : MAX_CTAS / 2, THREADS, Sh::SMEM, s>>>(a);
     return cudaGetLastError();
 }

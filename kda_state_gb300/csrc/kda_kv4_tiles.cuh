@@ -1021,9 +1021,9 @@ cudaError_t launch_tile_attention(const KvAttentionArgs &a, cudaStream_t s) {
     constexpr int SMEM = Sh::META + sizeof(TileMeta);
     static_assert(SMEM <= 232448, "shared memory");
     static_assert((size_t)MAX_CTAS * 4 + MAX_SLOTS * (size_t)Sh::PARTIAL * 4 <= KDA_KV4_WORKSPACE, "workspace");
-    const cudaError_t set =
-        cudaFuncSetAttribute(tile_attention_kernel<D, QT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (set != cudaSuccess) return set;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(tile_attention_kernel<D, QT, T>), SMEM, done);
+    if (e != cudaSuccess) return e;
     tile_attention_kernel<D, QT, T><<<SMS, TILE_THREADS, SMEM, s>>>(a);
     return cudaGetLastError();
 }
