@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 const int e = min(max((int)(__float_as_uint(top) >> 23 & 255), 1), 253);
                 const float down = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), a.scale_k);
                 factor = fabsf(a.scale_k) * __uint_as_float((uint32_t)e << 23);
-                if (QT == 2 || g == 0) {
+                if (QT == 2 || (g == 0 && tiles > 0)) {        // (a piece without tiles hands over none)
                     if ((my_row & ~31) < p.rows)
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) {
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             // ============================ products =====================================================
             constexpr uint32_t ID_S = idesc_f16(128, TT), ID_O = idesc_f16(128, D);
             const uint32_t base = shared_addr(smem);
-            uint32_t done[2] = {0, 0}, kv = 0;
+            uint32_t done[2] = {0, 0}, kv = 0, queries = 0;
             for (uint32_t part = 0;; ++part) {
                 wait_or_dead(PART_FULL + 8 * (part & 3), part >> 2 & 1, dead);
                 const int tiles = __shfl_sync(~0u, meta.parts[part & 3].tiles, 0);
@@ -894,9 +894,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 };
                 auto k_wait = [&](int j) { wait_or_dead(K_FULL + 8 * ((kv + j) & 1), (kv + j) >> 1 & 1, dead); };
                 auto v_wait = [&](int j) { wait_or_dead(V_FULL + 8 * ((kv + j) & 1), (kv + j) >> 1 & 1, dead); };
-                wait_or_dead(Q_FULL, part & 1, dead);
+                if (QT == 2 || tiles > 0) wait_or_dead(Q_FULL, queries & 1, dead);
                 if (QT == 2) {
-                    wait_or_dead(Q_FULL + 8, part & 1, dead);
+                    wait_or_dead(Q_FULL + 8, queries & 1, dead);
                     k_wait(0);
                     scores(0, 0, false);
                     scores(1, 0, true);
@@ -927,6 +927,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     }
                 }
                 kv += tiles;
+                queries += QT == 2 || tiles > 0;
             }
             if (elect_one()) {
                 mma_done(FINISHED);

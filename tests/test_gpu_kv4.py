@@ -265,6 +265,20 @@ def test_no_lse_split_over_many_blocks_and_repeats(ws):
     assert torch.equal(o, o3) and torch.equal(lse, lse3)
 
 
+def test_pieces_without_tiles(ws):
+    """A narrow window under cut requests: half of the pieces have nothing to read."""
+    B, H, G, D, P, window = 30, 2, 4, 64, 16, 16
+    lens = [130 + 9 * b for b in range(B)]
+    news = [5 + b % 3 for b in range(B)]
+    pool, table = make_cache(lens, H, D, P, 60)
+    q = packed_q(news, H * G, D, BF, 61)
+    want = expected(q, news, lens, pool, table, P, window, D ** -0.5)
+    for _ in range(20):
+        o, lse, err = attend(pool, table, news, lens, q, H * G, ws, window=window)
+        assert err == 0
+        check(o, lse, want, BF)
+
+
 def test_offsets_past_32_bits(ws):
     """Pages that lie more than 2^32 bytes into the pool."""
     H, D, P = 8, 128, 256
