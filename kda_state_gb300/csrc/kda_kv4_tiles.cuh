@@ -61,6 +61,10 @@ struct TileShape {
     static constexpr int K_AT = QT * QBYTES, V_AT = K_AT + 2 * KBYTES, RAW_AT = V_AT + 2 * KBYTES;
     static constexpr int META = RAW_AT + RAW * RAW_BYTES;
     static constexpr int PARTIAL = 128 * (D + 2);        // floats
+    // With QT = 2 the products with V start when the first half of a tile's weights is there, in steps of 16 tokens
+    // (prompts of 2048 tokens: 815 -> 793 us; at 5 or 6 steps 794, 826).  With QT = 1 they wait for all, as they
+    // are not what its groups wait for (64 requests of 8 tokens: 136, with halves 140 us).
+    static constexpr int FIRST = QT == 2 ? TT / 32 : TT / 16;
     static constexpr uint32_t O_COL = 256;
 };
 
@@ -75,7 +79,7 @@ struct alignas(16) TileMeta {
     int2 raw_about[8];                 // by stage of codes: tokens before the end; a bit a run of 16 out of range
     uint32_t tmem;
     int last, dead, cut;
-    uint64_t bars[25 + 2 * 6];
+    uint64_t bars[27 + 2 * 6];
 };
 
 __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {   // K-major, 128-byte swizzle, 8-row groups 1 KB apart
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
     const uint32_t bar = shared_addr(meta.bars);
     const uint32_t PART_FULL = bar, PART_FREE = bar + 32, Q_FULL = bar + 64, S_FULL = bar + 80, P_FULL = bar + 96, PV_DONE = bar + 112,
                    K_FULL = bar + 128, K_FREE = bar + 144, V_FULL = bar + 160, V_FREE = bar + 176, FINISHED = bar + 192,
-                   RAW_FULL = bar + 200, RAW_FREE = RAW_FULL + 8 * S::RAW;
+                   P_HALF = bar + 200, RAW_FULL = bar + 216, RAW_FREE = RAW_FULL + 8 * S::RAW;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int G = a.Hq / a.Hkv;
 
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             barrier_init(Q_FULL + 8 * i, 4);
             barrier_init(S_FULL + 8 * i, 1);
             barrier_init(P_FULL + 8 * i, 4);
+            barrier_init(P_HALF + 8 * i, 4);
             barrier_init(PV_DONE + 8 * i, 1);
             barrier_init(K_FULL + 8 * i, 8);
             barrier_init(K_FREE + 8 * i, 1);
@@ -579,6 +584,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(u1));
                         pk[e / 2] = half_pair(p0, p1);
                         pk[e / 2 + 1] = half_pair(p2, p3);
+                    }
+                    if (c == S::FIRST) {
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        tmem_before_sync();
+                        __syncwarp();
+                        if (lane == 0) barrier_arrive(P_HALF + 8 * g);
                     }
                     tmem_st8(s_col + 8 * c, pk);
                 }
@@ -877,16 +888,30 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 };
                 auto values = [&](int g, int j, bool first, bool frees) {
                     const uint32_t n = kv + j;
-                    wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
-                    ++done[g];
+                    if (QT == 2) {
+                        wait_or_dead(P_HALF + 8 * g, done[g] & 1, dead);
+                    } else {
+                        wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
+                        ++done[g];
+                    }
                     const uint64_t dv = tile_desc(base + S::V_AT + (n & 1) * S::KBYTES);
                     tmem_after_sync();
-                    if (elect_one()) {
+                    auto steps = [&](int from, int to) {
 #pragma unroll
-                        for (int s = 0; s < TT / 16; ++s) {
+                        for (int s = from; s < to; ++s) {
                             const uint64_t at = (uint64_t)(((s >> 2) * D * 128 + (s & 3) * 32) >> 4);
                             mma_f16_ts(tmem + S::O_COL + g * D, tmem + g * 128 + 8 * s, dv + at, ID_O, s > 0 || !first);
                         }
+                    };
+                    if (QT == 2) {
+                        if (elect_one()) steps(0, S::FIRST);
+                        __syncwarp();
+                        wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
+                        ++done[g];
+                        tmem_after_sync();
+                    }
+                    if (elect_one()) {
+                        steps(QT == 2 ? S::FIRST : 0, TT / 16);
                         mma_done(PV_DONE + 8 * g);
                         if (frees) mma_done(V_FREE + 8 * (n & 1));
                     }
