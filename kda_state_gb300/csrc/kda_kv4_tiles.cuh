@@ -65,7 +65,11 @@ struct TileShape {
     // (prompts of 2048 tokens: 815 -> 793 us; at 5 or 6 steps 794, 826).  With QT = 1 they wait for all, as they
     // are not what its groups wait for (64 requests of 8 tokens: 136, with halves 140 us).
     static constexpr int FIRST = QT == 2 ? TT / 32 : TT / 16;
-    static constexpr uint32_t O_COL = 256;
+    // Columns of TMEM: S, O, and P, a column for two tokens' weights.  If there is room, P has columns of its own; else
+    // it lies over S, and the next S waits for the product that reads P (products of different accumulators are
+    // not ordered among themselves).
+    static constexpr bool OWN_P = D == 64;
+    static constexpr uint32_t O_COL = 256, P_COL = OWN_P ? O_COL + 2 * D : 0, P_STEP = OWN_P ? TT / 2 : TT;
 };
 
 // The small shared arrays behind the tiles.
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
         // ================================ softmax ======================================================
         const int g = w >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
-        const uint32_t s_col = lanes + g * 128, o_col = lanes + S::O_COL + g * D;
+        const uint32_t s_col = lanes + g * 128, o_col = lanes + S::O_COL + g * D, p_col = lanes + S::P_COL + g * S::P_STEP;
         uint8_t *const q_tile = smem + (QT == 2 ? g : 0) * S::QBYTES;
         const int my_row = (QT == 2 ? g * 128 : 0) + row;      // of the part
         uint32_t done = 0;             // this group's tiles so far
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         __syncwarp();
                         if (lane == 0) barrier_arrive(P_HALF + 8 * g);
                     }
-                    tmem_st8(s_col + 8 * c, pk);
+                    tmem_st8(p_col + 8 * c, pk);
                 }
                 l += (__uint_as_float((uint32_t)sum0) + __uint_as_float((uint32_t)(sum0 >> 32))) +
                      (__uint_as_float((uint32_t)sum1) + __uint_as_float((uint32_t)(sum1 >> 32)));
@@ -900,7 +904,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
 #pragma unroll
                         for (int s = from; s < to; ++s) {
                             const uint64_t at = (uint64_t)(((s >> 2) * D * 128 + (s & 3) * 32) >> 4);
-                            mma_f16_ts(tmem + S::O_COL + g * D, tmem + g * 128 + 8 * s, dv + at, ID_O, s > 0 || !first);
+                            mma_f16_ts(tmem + S::O_COL + g * D, tmem + S::P_COL + g * S::P_STEP + 8 * s, dv + at, ID_O, s > 0 || !first);
                         }
                     };
                     if (QT == 2) {
@@ -917,6 +921,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     }
                     __syncwarp();
                 };
+                // the weights of the group's last tile have been read
+                auto p_wait = [&](int g) {
+                    if (!S::OWN_P) wait_or_dead(PV_DONE + 8 * g, (done[g] - 1) & 1, dead);
+                };
                 auto k_wait = [&](int j) { wait_or_dead(K_FULL + 8 * ((kv + j) & 1), (kv + j) >> 1 & 1, dead); };
                 auto v_wait = [&](int j) { wait_or_dead(V_FULL + 8 * ((kv + j) & 1), (kv + j) >> 1 & 1, dead); };
                 if (QT == 2 || tiles > 0) wait_or_dead(Q_FULL, queries & 1, dead);
@@ -931,10 +939,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         values(0, j, j == 0, false);
                         if (j + 1 < tiles) {
                             k_wait(j + 1);
+                            p_wait(0);
                             scores(0, j + 1, false);
                         }
                         values(1, j, j == 0, true);
-                        if (j + 1 < tiles) scores(1, j + 1, true);
+                        if (j + 1 < tiles) {
+                            p_wait(1);
+                            scores(1, j + 1, true);
+                        }
                     }
                 } else {
                     for (int j = 0; j < min(tiles, 2); ++j) {
@@ -947,6 +959,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         values(j & 1, j, j < 2, true);
                         if (j + 2 < tiles) {
                             k_wait(j + 2);
+                            p_wait(j & 1);
                             scores(j & 1, j + 2, true);
                         }
                     }
