@@ -14,7 +14,7 @@
 //                         bytes in an order of its own, so that the eight rows of
 //                         each stored matrix lie in different banks
 //   product (warp 16)     S = Q K^T and O += P V on tcgen05 (fp16, fp32 sums): S, P
-//                         and O stay in TMEM, P over S's columns
+//                         and O stay in TMEM, with D = 128 P over S's columns
 //   softmax (warps 0-7)   two groups of four warps, a thread a row: the running
 //                         maximum (it moves only when a score passes it by 2^6, so O
 //                         is seldom rescaled), the weights as fp16 into TMEM, the sum
@@ -62,13 +62,16 @@ struct TileShape {
     static constexpr int META = RAW_AT + RAW * RAW_BYTES;
     static constexpr int PARTIAL = 128 * (D + 2);        // floats
     // With QT = 2 the products with V start when the first half of a tile's weights is there, in steps of 16 tokens
-    // (prompts of 2048 tokens: 815 -> 793 us; at 5 or 6 steps 794, 826).  With QT = 1 they wait for all, as they
+    // (prompts of 2048 tokens: 815 -> 793 us; at 5 or 6 steps 794, 826; now 852, for the wait below).  With QT = 1 they wait for all, as they
     // are not what its groups wait for (64 requests of 8 tokens: 136, with halves 140 us).
     static constexpr int FIRST = QT == 2 ? TT / 32 : TT / 16;
     // Columns of TMEM: S, O, and P, a column for two tokens' weights.  If there is room, P has columns of its own; else
-    // it lies over S, and the next S waits for the product that reads P (products of different accumulators are
-    // not ordered among themselves).
+    // it lies over S, and the next S waits for the product that reads P: products of different accumulators are
+    // not ordered among themselves.  The wait costs prompts of 2048 tokens 7% (791 -> 851 us).
     static constexpr bool OWN_P = D == 64;
+    // Then, with QT = 2, the next S is asked for as soon as the softmax has this one in registers (2 x 2048 tokens on
+    // up to 6 K, D = 64: 141 -> 132 us).
+    static constexpr bool EARLY = OWN_P && QT == 2;
     static constexpr uint32_t O_COL = 256, P_COL = OWN_P ? O_COL + 2 * D : 0, P_STEP = OWN_P ? TT / 2 : TT;
 };
 
@@ -83,7 +86,7 @@ struct alignas(16) TileMeta {
     int2 raw_about[8];                 // by stage of codes: tokens before the end; a bit a run of 16 out of range
     uint32_t tmem;
     int last, dead, cut;
-    uint64_t bars[27 + 2 * 6];
+    uint64_t bars[29 + 2 * 6];
 };
 
 __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {   // K-major, 128-byte swizzle, 8-row groups 1 KB apart
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
     const uint32_t bar = shared_addr(meta.bars);
     const uint32_t PART_FULL = bar, PART_FREE = bar + 32, Q_FULL = bar + 64, S_FULL = bar + 80, P_FULL = bar + 96, PV_DONE = bar + 112,
                    K_FULL = bar + 128, K_FREE = bar + 144, V_FULL = bar + 160, V_FREE = bar + 176, FINISHED = bar + 192,
-                   P_HALF = bar + 200, RAW_FULL = bar + 216, RAW_FREE = RAW_FULL + 8 * S::RAW;
+                   P_HALF = bar + 200, S_FREE = bar + 216, RAW_FULL = bar + 232, RAW_FREE = RAW_FULL + 8 * S::RAW;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int G = a.Hq / a.Hkv;
 
@@ -399,6 +402,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             barrier_init(S_FULL + 8 * i, 1);
             barrier_init(P_FULL + 8 * i, 4);
             barrier_init(P_HALF + 8 * i, 4);
+            barrier_init(S_FREE + 8 * i, 4);
             barrier_init(PV_DONE + 8 * i, 1);
             barrier_init(K_FULL + 8 * i, 8);
             barrier_init(K_FREE + 8 * i, 1);
@@ -527,6 +531,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 for (int c = 0; c < 4; ++c) tmem_ld32_async(s_col + 32 * c, x + 32 * c);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld_wait(x + 32 * c);
+                if constexpr (S::EARLY) {
+                    tmem_before_sync();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(S_FREE + 8 * g);
+                }
                 if (some) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -594,6 +603,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         tmem_before_sync();
                         __syncwarp();
                         if (lane == 0) barrier_arrive(P_HALF + 8 * g);
+                    }
+                    if (S::EARLY && c == 0 && mine > 0) {      // the last weights have been read
+                        wait_or_dead(PV_DONE + 8 * g, (done - 1) & 1, dead);
+                        tmem_after_sync();
                     }
                     tmem_st8(p_col + 8 * c, pk);
                 }
@@ -935,15 +948,29 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     scores(1, 0, true);
 #pragma unroll 1
                     for (int j = 0; j < tiles; ++j) {
+                        const bool more = j + 1 < tiles;
+                        if constexpr (S::EARLY) {
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                if (more) {
+                                    wait_or_dead(S_FREE + 8 * g, done[g] & 1, dead);
+                                    if (g == 0) k_wait(j + 1);
+                                    scores(g, j + 1, g == 1);
+                                }
+                                if (g == 0) v_wait(j);
+                                values(g, j, j == 0, g == 1);
+                            }
+                            continue;
+                        }
                         v_wait(j);
                         values(0, j, j == 0, false);
-                        if (j + 1 < tiles) {
+                        if (more) {
                             k_wait(j + 1);
                             p_wait(0);
                             scores(0, j + 1, false);
                         }
                         values(1, j, j == 0, true);
-                        if (j + 1 < tiles) {
+                        if (more) {
                             p_wait(1);
                             scores(1, j + 1, true);
                         }
