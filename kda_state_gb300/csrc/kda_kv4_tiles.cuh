@@ -62,12 +62,14 @@ struct TileShape {
     static constexpr int META = RAW_AT + RAW * RAW_BYTES;
     static constexpr int PARTIAL = 128 * (D + 2);        // floats
     // With QT = 2 the products with V start when the first half of a tile's weights is there, in steps of 16 tokens
-    // (prompts of 2048 tokens: 815 -> 793 us; at 5 or 6 steps 794, 826; now 852, for the wait below).  With QT = 1 they wait for all, as they
-    // are not what its groups wait for (64 requests of 8 tokens: 136, with halves 140 us).
+    // (2 x 2048 tokens on up to 14 K: 860 -> 856 us, D = 64 651 -> 646; at 3 or 6 steps 868, 869; in three parts
+    // 919).  With QT = 1 they wait for all (64 requests of 8 tokens: 136, with halves 140 us).
     static constexpr int FIRST = QT == 2 ? TT / 32 : TT / 16;
     // Columns of TMEM: S, O, and P, a column for two tokens' weights.  If there is room, P has columns of its own; else
     // it lies over S, and the next S waits for the product that reads P: products of different accumulators are
-    // not ordered among themselves.  The wait costs prompts of 2048 tokens 7% (791 -> 851 us).
+    // not ordered among themselves.  The wait costs prompts of 2048 tokens 7% (791 -> 851 us),
+    // drafts of 8 tokens 2% (136 -> 138).  A product warp for each group instead of one that alternates: 913; half
+    // tiles in turn, so that the next scores are always there: 1035.
     static constexpr bool OWN_P = D == 64;
     // Then, with QT = 2, the next S is asked for as soon as the softmax has this one in registers (2 x 2048 tokens on
     // up to 6 K, D = 64: 141 -> 132 us).
