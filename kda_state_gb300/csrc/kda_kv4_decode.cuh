@@ -296,12 +296,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     // when its chunk's turn comes, or one lane for all of a chunk that lies in one page.
     constexpr int WINDOW = 32 / TILES;     // chunks
     const bool one_copy = 1 << a.page_shift >= CHUNK;
-    int page_next = -2;                    // -2: past the end
+    int page_next = -2;                    // -2: past the end (a negative entry of the table counts as -1)
     const uint8_t *source = nullptr;
     uint32_t oks = 0, here = 0;            // tiles of the window whose page is good; of each stage, those loaded
     auto look = [&](int k) {
         const long long t = ((long long)(u.c0 + k) * TILES + lane) * KV_TILE;
-        return k + lane / TILES < u.count && t < u.len ? a.page_table[(size_t)u.b * a.max_pages + (t >> a.page_shift)] : -2;
+        return k + lane / TILES < u.count && t < u.len ? max(a.page_table[(size_t)u.b * a.max_pages + (t >> a.page_shift)], -1) : -2;
     };
     auto fetch = [&](int k) {              // the unit's k-th chunk
         const int j = k % WINDOW;

@@ -1024,9 +1024,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 const int32_t *const pages = a.page_table + (size_t)p.b * a.max_pages;
                 const int boxes = 2 * p.tiles, from = p.tile0 * TT;
                 // a lane looks up one run of 16 tokens of each 8 stages, and asks for it when its stage's turn comes
-                auto look = [&](int i) {               // the page of the part's i-th run; -2 past the end
+                // the page of the part's i-th run; -2 past the end (a negative entry of the table counts as -1)
+                auto look = [&](int i) {
                     const long long pos = (long long)from + (long long)i * KV_TILE;
-                    return i < boxes * 4 && pos < p.len ? pages[pos >> a.page_shift] : -2;
+                    return i < boxes * 4 && pos < p.len ? max(pages[pos >> a.page_shift], -1) : -2;
                 };
                 const bool one_copy = a.page_shift >= 6;       // a stage lies in one page
                 int then = look(lane);
