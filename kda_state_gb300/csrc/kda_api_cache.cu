@@ -129,7 +129,9 @@ KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, 
     kda::KvAttentionArgs a;
     memset(&a, 0, sizeof(a));
     a.dt = dt; a.B = B; a.T = total_tokens; a.max_q = max_q; a.Hq = H_q; a.Hkv = H_kv; a.D = D;
-    a.max_pages = max_pages; a.page_shift = shift; a.num_pages = num_pages; a.window = window;
+    a.max_pages = max_pages; a.page_shift = shift; a.num_pages = num_pages;
+    // a window that no cache of this table can fill is none: positions minus a window then stay in 32 bits
+    a.window = window < (max_pages << shift) ? window : 0;
     a.q = q; a.q_stride = q_stride; a.cu = cu_seqlens; a.kv_lens = kv_lens; a.page_table = page_table;
     a.pool = (const uint8_t *)pool;
     a.scale_k = (float)((double)scale * k_scale * 1.4426950408889634); a.v_scale = v_scale;

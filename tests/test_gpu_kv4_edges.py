@@ -99,3 +99,24 @@ def test_entries_that_name_no_page(ws, news, page):
             close(o[at:at + n], lse[at:at + n],
                   definition(q[at:at + n], *ref.load(pool, table[b], lens[b], P), there, window, D ** -0.5), BF)
             at += n
+
+
+# ---------------------------------------------------------------------------
+# windows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("news,lens,Hq,Hkv", [([8, 2], [2, 9], 1, 1), ([5, 4], [1, 60], 6, 2), ([40, 17], [20, 300], 8, 1),
+                                              ([700, 599], [30, 599], 64, 8)])
+def test_windows_longer_than_the_cache(ws, news, lens, Hq, Hkv):
+    """A window no row can fill is no window, also for requests with rows before their first token."""
+    D, P = 64, 16
+    pool, table = make_cache(lens, Hkv, D, P, 62)
+    q = packed_q(news, Hq, D, BF, 63)
+    want = attend(pool, table, news, lens, q, ws)
+    rows = lambda b, x: definition(x, *ref.load(pool, table[b], lens[b], P), np.ones(lens[b], bool), 0, D ** -0.5)
+    n, last = news[0], q[-min(3, news[1]):]
+    close(want[0][:n], want[1][:n], rows(0, q[:n]), BF)
+    close(want[0][-len(last):], want[1][-len(last):], rows(1, last), BF)
+    for window in (max(lens), table.shape[1] * P, table.shape[1] * P + 1, 2 ** 30, 2 ** 31 - 2, 2 ** 31 - 1):
+        o, lse, err = attend(pool, table, news, lens, q, ws, window)
+        assert err == 0 and torch.equal(lse, want[1]) and torch.equal(o, want[0])
