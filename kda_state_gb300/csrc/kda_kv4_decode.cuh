@@ -15,7 +15,11 @@
 // range.  Weights are rounded to fp16 (2^-11 of a weight, against 2^-9 and more
 // of bf16), and held 2^9 above the running maximum, which moves only when a
 // score passes it by 2^6: a weight is a normal fp16 number down to 2^-23 of the
-// largest, and most steps rescale nothing.
+// largest, and most steps rescale nothing.  The maximum m is held as a product
+// y = q . k before the row's factor f, and the exponent is (y - m) f + 9, two packed
+// operations for two scores: with y f - (m f - 9) the rounding of m f alone would pass
+// 2^6 from scores of 2^28 on (the weights then leave fp16, or are all 0).  128 requests:
+// 131 us with either.
 //
 // Work is the list of all (request, block of rows, kv head, 32 tokens), cut into
 // equal contiguous ranges, one a warp: a ragged batch and one long request are
@@ -43,7 +47,8 @@ constexpr int THREADS = WARPS * 32;
 constexpr int MAX_CTAS = 152 * 2;
 constexpr float HEADROOM = 9.f;        // log2 of a weight at the running maximum
 constexpr float MOVE = HEADROOM + 6.f; // a score this far above m makes the maximum move
-constexpr float NOTHING = -1e30f;      // the running maximum before any score
+constexpr float NOTHING = -1e30f;      // the running maximum before any product (they lie within 2^21)
+constexpr float LOWEST = -3.4028234e38f;   // the maximum of a partial result without weights, as a score
 
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -119,6 +124,21 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// What a row's products are scaled by to be scores, up a power of two.  Neither 0 nor infinite: a difference of 0 and a
+// masked -inf stay what they are.
+__device__ __forceinline__ float factor_of(float scale, float up) {
+    return fminf(fmaxf(fabsf(scale) * up, 1.1754944e-38f), -LOWEST);
+}
+// The score at which a weight is 1, of a row whose maximum is m and whose weights add up to sum: finite, so that
+// results can be joined.
+__device__ __forceinline__ float base_of(float m, float factor, float sum) {
+    return sum == 0.f ? LOWEST : fminf(fmaxf(fmaf(m, factor, -HEADROOM), LOWEST), -LOWEST);
+}
+__device__ __forceinline__ uint64_t pair_of_floats(float a, float b) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
 }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -374,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                 qf[t][i] = half_pair(f.x * down, f.y * down);
             }
             // scores come back by columns: this lane holds those of rows 2 c and 2 c + 1
-            const float f = fabsf(a.scale_k) * up;
+            const float f = factor_of(a.scale_k, up);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 factor[t][k] = __shfl_sync(~0u, f, (2 * c + k) * 4);
@@ -474,7 +494,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[i][t][e] = fmaf(y[i][t][e], factor[t][e & 1], -m[t][e & 1]);
+                        for (int e = 0; e < 4; e += 2) {
+                            uint64_t v = pair_of_floats(y[i][t][e], y[i][t][e + 1]);
+                            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(pair_of_floats(-m[t][0], -m[t][1])));
+                            asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(pair_of_floats(factor[t][0], factor[t][1])), "l"(pair_of_floats(HEADROOM, HEADROOM)));
+                            asm("mov.b64 {%0, %1}, %2;" : "=f"(x[i][t][e]), "=f"(x[i][t][e + 1]) : "l"(v));
+                        }
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < TILES; ++i)
@@ -503,11 +528,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                         for (int i = 0; i < TILES; ++i)
 #pragma unroll
                             for (int e = k2; e < 4; e += 2)
-                                if (seen >> ((i * NT + t) * 4 + e) & 1) top = fmaxf(top, y[i][t][e] * factor[t][k2]);
+                                if (seen >> ((i * NT + t) * 4 + e) & 1) top = fmaxf(top, y[i][t][e]);
                         top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
                         top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-                        const float to = fmaxf(m[t][k2], top - HEADROOM), keep = exp2_fast(m[t][k2] - to);
+                        const float to = fmaxf(m[t][k2], top), keep = exp2_fast((m[t][k2] - to) * factor[t][k2]);
                         m[t][k2] = to;
                         l[t][k2] *= keep;
 #pragma unroll
@@ -619,12 +644,13 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                 sum += __shfl_xor_sync(~0u, sum, 4);
                 sum += __shfl_xor_sync(~0u, sum, 8);
                 sum += __shfl_xor_sync(~0u, sum, 16);
+                const float base = base_of(m[t][k2], factor[t][k2], sum);
                 const int col = t * 8 + 2 * c + k2;
                 if (begun && ended) {
                     if (col >= x.rows || dead) continue;
                     const size_t row = row_of(x, col);
                     const float f = sum == 0.f ? 0.f : a.v_scale / sum;
-                    if (r == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (m[t][k2] + log2f(sum)) * LN2;
+                    if (r == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * LN2;
                     uint32_t y[KS];
 #pragma unroll
                     for (int j = 0; j < KS; ++j)
@@ -633,7 +659,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
 #pragma unroll
                     for (int j = 0; j < KS / 4; ++j) dst[j] = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
                 } else {
-                    if (r == 0) ml_s[((begun ? WARPS : 0) + w) * S::ROWS + col] = make_float2(m[t][k2], sum);
+                    if (r == 0) ml_s[((begun ? WARPS : 0) + w) * S::ROWS + col] = make_float2(base, sum);
                     float *dst = (begun ? reinterpret_cast<float *>(ring) : out_s + w * S::ROWS * S::OSTRIDE) + col * S::OSTRIDE + r * (D / 8);
 #pragma unroll
                     for (int j = 0; j < KS; j += 2)
@@ -671,7 +697,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     // four channels of a row over this CTA's pieces of the unit x that begins in warp w0's first or last piece
     auto gather = [&](const Piece &x, int w0, bool with_last, int col, int d, float &top, float &sum) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        top = NOTHING, sum = 0.f;
+        top = LOWEST, sum = 0.f;
         if (with_last)
             add(v, top, sum, *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w0 * S::STAGES * S::STAGE_BYTES) +
                                                                col * S::OSTRIDE + d),
@@ -740,7 +766,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         float4 v[N];
         float top[N], sum[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f), top[k] = NOTHING, sum[k] = 0.f;
+        for (int k = 0; k < N; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f), top[k] = LOWEST, sum[k] = 0.f;
 #pragma unroll 2
         for (int y = cta0 + (w & 3); y <= cta1; y += 4) {
             const float *src = partials + (size_t)(2 * y + (y == cta0)) * S::PARTIAL;
@@ -749,7 +775,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 const int i = 32 * k + lane, col = i / (D / 4);
-                z[k] = make_float4(0.f, 0.f, 0.f, 0.f), ml[k] = make_float2(NOTHING, 0.f);
+                z[k] = make_float4(0.f, 0.f, 0.f, 0.f), ml[k] = make_float2(LOWEST, 0.f);
                 if (col < x.rows) {
                     z[k] = __ldcg(reinterpret_cast<const float4 *>(src) + i);
                     ml[k] = __ldcg(reinterpret_cast<const float2 *>(src + S::ROWS * D) + col);
@@ -770,7 +796,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     for (int i = st; i < x.rows * (D / 4); i += 128) {
         const int col = i / (D / 4), d = i % (D / 4) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float top = NOTHING, sum = 0.f;
+        float top = LOWEST, sum = 0.f;
 #pragma unroll
         for (int y = 0; y < 4; ++y)
             add(v, top, sum, *reinterpret_cast<const float4 *>(out_s + ((4 * side + y) * S::ROWS + col) * S::OSTRIDE + d),

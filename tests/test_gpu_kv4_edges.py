@@ -120,3 +120,67 @@ def test_windows_longer_than_the_cache(ws, news, lens, Hq, Hkv):
     for window in (max(lens), table.shape[1] * P, table.shape[1] * P + 1, 2 ** 30, 2 ** 31 - 2, 2 ** 31 - 1):
         o, lse, err = attend(pool, table, news, lens, q, ws, window)
         assert err == 0 and torch.equal(lse, want[1]) and torch.equal(o, want[0])
+
+
+# ---------------------------------------------------------------------------
+# scores of every size
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("news,lens", [([1, 1, 1], [300, 40, 9000]), ([3, 4, 2], [300, 40, 9000]), ([90, 40, 64], [300, 40, 3000]),
+                                       ([700, 1, 599], [1500, 77, 2000])])
+def test_scores_of_every_size(ws, news, lens, D):
+    """Scores far apart, from 2^20 to 2^122 and below zero: the largest, tied ones, share the row.
+
+    Keys are one value in all channels, so that scores are exact; ties have equal weights, all else
+    none, and the sums are exact too.  What is left is the quotient (2^-20) and o's rounding; lse is
+    a product of four roundings (2^-22 of it)."""
+    P, H, Hq = 64, 8 if news[0] == 700 else 1, 64 if news[0] == 700 else 4
+    rng = np.random.default_rng(70)
+    pool, table = make_cache([0] * 3, H, D, P, 71)
+    need = [-(-n // P) for n in lens]
+    pool = np.full((sum(need), H, P // 16, 18 * D), 255, np.uint8)
+    table = np.full((3, max(need) + 1), -1, np.int32)
+    pages = rng.permutation(sum(need))
+    level, value = [], []
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = pages[sum(need[:b]):sum(need[:b + 1])]
+        level.append(rng.choice([1.0, 1.5, 2.0], n))
+        value.append(rng.choice([-6.0, -4, -3, -2, -1.5, -1, 0.5, 1, 1.5, 2, 3, 4, 6], (n, D)))
+        value[b][:, ::16] = 6.0            # a scale of 1 for each block
+        for pos in range(n):
+            ref.store(pool, table[b], pos, np.full((H, D), level[b][pos]), np.repeat(value[b][pos:pos + 1], H, 0), P)
+        k, v = ref.load(pool, table[b], n, P)                  # as they are stored
+        level[b], value[b] = k[:, 0, 0], v[:, 0]
+    for power in (20, 24, 27, 28, 31, 40, 64, 100, 114):
+        for sign in (1.0, -1.0):
+            q = torch.full((sum(news), Hq, D), 2.0 ** power).to(BF)
+            o, lse, err = attend(pool, table, news, lens, q, ws, scale=sign)
+            assert err == 0
+            at = 0
+            for b, n in enumerate(news):
+                for i in sorted({0, 1, n // 2, n - 2, n - 1} & set(range(n))):
+                    last = lens[b] - n + i
+                    x = level[b][:last + 1] * sign
+                    wo = value[b][:last + 1][x == x.max()].mean(0)
+                    wl = x.max() * D * 2.0 ** power + np.log((x == x.max()).sum())
+                    go, gl = o[at + i].double().cpu().numpy(), lse[at + i].double().cpu().numpy()
+                    assert (np.abs(go - wo) <= (2.0 ** -8 + 2.0 ** -20) * np.abs(wo) + 2.0 ** -20 * 6).all(), (power, sign, b, i)
+                    assert (np.abs(gl - wl) <= 2.0 ** -22 * np.abs(wl)).all(), (power, sign, b, i)
+                at += n
+
+
+@pytest.mark.parametrize("news,lens", [([1, 1], [300, 9000]), ([3, 5], [40, 9000]), ([90, 64], [300, 3000])])
+def test_scores_near_zero(ws, news, lens):
+    """Queries so small that all of a row's tokens weigh the same."""
+    D, P, H, Hq = 64, 64, 1, 4
+    pool, table = make_cache(lens, H, D, P, 74)
+    for power in (-126, -110, -104, -102, -101, -100, -99, -98, -97, -96, -90, -60):
+        q = packed_q(news, Hq, D, BF, 75) * 2.0 ** power
+        o, lse, err = attend(pool, table, news, lens, q, ws, scale=1.0)
+        assert err == 0
+        at = 0
+        for b, n in enumerate(news):
+            close(o[at:at + n], lse[at:at + n],
+                  definition(q[at:at + n], *ref.load(pool, table[b], lens[b], P), np.ones(lens[b], bool), 0, 1.0), BF)
+            at += n
