@@ -516,7 +516,8 @@ KDA_API size_t kda_kv4_workspace_bytes(void);
  *     o   = sum_j softmax_j(scale q . k_j) v_j
  *     lse = ln sum_j exp(scale q . k_j)
  * A row that sees nothing has o = 0 and lse = -inf.  What lies in the pages at
- * positions a row does not see has no influence, NaN included.
+ * positions a row does not see has no influence, NaN included.  A row that sees
+ * something from a query with an infinity or a NaN has NaN results.
  *
  *   max_q       no request has more new tokens (host; sizes the launch)
  *   q           device dtype [total_tokens][H_q][D], rows q_stride elements apart

@@ -130,6 +130,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ float factor_of(float scale, float up) {
     return fminf(fmaxf(fabsf(scale) * up, 1.1754944e-38f), -LOWEST);
 }
+// f, or NaN for a row whose largest query is infinite or NaN: all its products are then NaN, and so are the results of
+// what it sees (infinite scores of one sign would be taken for masked ones).
+__device__ __forceinline__ float finite_or_nan(float top, float f) {
+    return top <= -LOWEST ? f : __uint_as_float(0x7fc00000u);
+}
 // The score at which a weight is 1, of a row whose maximum is m and whose weights add up to sum: finite, so that
 // results can be joined.
 __device__ __forceinline__ float base_of(float m, float factor, float sum) {
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
             top = max_nan(top, __shfl_xor_sync(~0u, top, 1));
             top = max_nan(top, __shfl_xor_sync(~0u, top, 2));
             const int e = min(max((int)(__float_as_uint(top) >> 23 & 255), 1), 253);
-            const float down = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), a.scale_k), up = __uint_as_float((uint32_t)e << 23);
+            const float down = copysignf(finite_or_nan(top, __uint_as_float((uint32_t)(254 - e) << 23)), a.scale_k), up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
                 const float2 f = pair_of<T>(q_raw[t][i]);

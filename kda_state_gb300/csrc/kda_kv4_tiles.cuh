@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 const float2 tops = pair_of<T>(most);
                 const float top = max_nan(tops.x, tops.y);
                 const int e = min(max((int)(__float_as_uint(top) >> 23 & 255), 1), 253);
-                const float down = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), a.scale_k);
+                const float down = copysignf(finite_or_nan(top, __uint_as_float((uint32_t)(254 - e) << 23)), a.scale_k);
                 factor = factor_of(a.scale_k, __uint_as_float((uint32_t)e << 23));
                 if (QT == 2 || (g == 0 && tiles > 0)) {        // (a piece without tiles hands over none)
                     if ((my_row & ~31) < p.rows)

@@ -184,3 +184,26 @@ def test_scores_near_zero(ws, news, lens):
             close(o[at:at + n], lse[at:at + n],
                   definition(q[at:at + n], *ref.load(pool, table[b], lens[b], P), np.ones(lens[b], bool), 0, 1.0), BF)
             at += n
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [4, 5, 2], [90, 30, 64]])
+def test_infinite_queries(ws, news):
+    """A query with an infinity has NaN results, of one sign or both, unless its row sees nothing."""
+    D, P, H, Hq = 128, 16, 2, 4
+    lens = [300, max(news[1] - 2, 0), 200]                      # the second request's first rows see nothing
+    pool, table = make_cache(lens, H, D, P, 72)
+    for b, n in enumerate(lens):
+        for pos in range(n):
+            ref.store(pool, table[b], pos, np.full((H, D), -1.0 - pos % 3), np.ones((H, D)), P)
+    q = packed_q(news, Hq, D, BF, 73)
+    q[0, 1, 7] = float("inf")                                   # all of its scores are -inf
+    q[news[0], 0, 3] = float("inf")                             # a row that sees nothing
+    q[sum(news[:2]), 2, 9] = -float("inf")                      # all of its scores are +inf
+    q[-1, 3, 0] = float("nan")
+    for window in (0, 30):
+        o, lse, err = attend(pool, table, news, lens, q, ws, window)
+        assert err == 0
+        nan = torch.zeros(sum(news), Hq, dtype=torch.bool)
+        nan[0, 1] = nan[sum(news[:2]), 2] = nan[-1, 3] = True
+        assert torch.equal(lse.isnan().cpu(), nan) and torch.equal(o.isnan().cpu(), nan[..., None].expand(-1, -1, D))
+        assert not o[news[0], 0].any() and lse[news[0], 0] == -float("inf")
