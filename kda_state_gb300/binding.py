@@ -140,6 +140,28 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _make(stream, shape, dtype, device, zero=False, result=True):
+    """A result that the caller did not pass, or (``result`` false) a buffer for the call alone.
+
+    Made, zeroed and given back on the stream that the call runs on: on the current one nothing
+    would order the zeroing before the kernels, or a later owner of the memory after them.  A
+    result is used on the current stream next, so that one holds its memory too."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else
+                  torch.cuda.default_stream(device))
+    current = torch.cuda.current_stream(device)
+    if current.cuda_stream == stream.cuda_stream:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(current)
+    return t
+
+
 def _check(fn, status):
     if status != KDA_OK:
         raise KdaError(fn, status)
@@ -292,7 +314,7 @@ def kda_chunk_prefill(q, k, v, gk, beta, cu_seqlens, cu_seqlens_host, state_pool
     _need_prefill_common(cu_seqlens, N, state_pool, H, K, V, init_slot, out_slot, snap_slot,
                          dev_err, dev)
     if o is None:
-        o = torch.empty(T, H, V, dtype=q.dtype, device=q.device)
+        o = _make(stream, (T, H, V), q.dtype, q.device)
     _need(o, "o", (T, H, V), dt, dev)
     hp = host.numpy().ctypes.data_as(ctypes.c_void_p)
     _check("kda_chunk_prefill", lib().kda_chunk_prefill(
@@ -318,7 +340,7 @@ def kda_chunk_prefill_checkpoints(q, k, v, gk, beta, cu_seqlens, cu_seqlens_host
                          dev_err, dev)
     _need(ckpt_slots, "ckpt_slots", (N, None), I32, dev)
     if o is None:
-        o = torch.empty(T, H, V, dtype=q.dtype, device=q.device)
+        o = _make(stream, (T, H, V), q.dtype, q.device)
     _need(o, "o", (T, H, V), dt, dev)
     hp = host.numpy().ctypes.data_as(ctypes.c_void_p)
     _check("kda_chunk_prefill_checkpoints", lib().kda_chunk_prefill_checkpoints(
@@ -340,7 +362,7 @@ def kda_decode_step(q, k, v, gk, beta, slot_ids, state_pool, o=None, scale: floa
     _need(state_pool, "state_pool", (None, H, K, V), F32, dev)
     _need_err(dev_err, dev)
     if o is None:
-        o = torch.empty(B, H, V, dtype=q.dtype, device=q.device)
+        o = _make(stream, (B, H, V), q.dtype, q.device)
     _need(o, "o", (B, H, V), dt, dev)
     _check("kda_decode_step", lib().kda_decode_step(
         _dt(q), B, H, K, V, _p(q), _p(k), _p(v), _p(gk), _p(beta), _p(slot_ids), _p(state_pool),
@@ -361,7 +383,7 @@ def kda_verify_store_inputs(q, k, v, gk, beta, slot_ids, state_pool, ring: RingB
     _need(ring_base, "ring_base", (B,), I32, dev, optional=True)
     _need_err(dev_err, dev)
     if o is None:
-        o = torch.empty(B, G, H, V, dtype=q.dtype, device=q.device)
+        o = _make(stream, (B, G, H, V), q.dtype, q.device)
     _need(o, "o", (B, G, H, V), dt, dev)
     desc = ring.descriptor()
     _check("kda_verify_store_inputs", lib().kda_verify_store_inputs(
@@ -391,7 +413,7 @@ def kda_verify_store_inputs_ragged(q, k, v, gk, beta, cu_drafts, G_max: int, slo
     _need(ring_base, "ring_base", (B,), I32, dev, optional=True)
     _need_err(dev_err, dev)
     if o is None:
-        o = torch.zeros(T, H, V, dtype=q.dtype, device=q.device)
+        o = _make(stream, (T, H, V), q.dtype, q.device, zero=True)
     _need(o, "o", (T, H, V), dt, dev)
     desc = ring.descriptor()
     _check("kda_verify_store_inputs_ragged", lib().kda_verify_store_inputs_ragged(
@@ -445,7 +467,7 @@ def kda_verify_snapshot(q, k, v, gk, beta, slot_ids, state_pool, snaps, snap_ids
     _need(snap_ids, "snap_ids", (B,), I32, dev)
     _need_err(dev_err, dev)
     if o is None:
-        o = torch.empty(B, G, H, V, dtype=q.dtype, device=q.device)
+        o = _make(stream, (B, G, H, V), q.dtype, q.device)
     _need(o, "o", (B, G, H, V), dt, dev)
     _check("kda_verify_snapshot", lib().kda_verify_snapshot(
         _dt(q), B, G, H, K, V, _p(q), _p(k), _p(v), _p(gk), _p(beta), _p(slot_ids),
@@ -532,10 +554,8 @@ def kda_conv_prologue(q_raw, k_raw, v_raw, b_raw, conv_w, conv_state, init_slot,
     _need(cu_seqlens, "cu_seqlens", (N + 1,), I32, dev)
     _need_err(dev_err, dev)
     if out is None:
-        out = (torch.empty(T, H, K, dtype=q_raw.dtype, device=q_raw.device),
-               torch.empty(T, H, K, dtype=q_raw.dtype, device=q_raw.device),
-               torch.empty(T, H, K, dtype=q_raw.dtype, device=q_raw.device),
-               torch.empty(T, H, dtype=q_raw.dtype, device=q_raw.device))
+        out = tuple(_make(stream, shape, q_raw.dtype, q_raw.device)
+                    for shape in ((T, H, K), (T, H, K), (T, H, K), (T, H)))
     q, k, v, beta = out
     for name, t in (("out[0]", q), ("out[1]", k), ("out[2]", v)):
         _need(t, name, (T, H, K), dt, dev)
@@ -560,7 +580,7 @@ def kda_gated_rmsnorm(o, gate, w_norm, eps: float = EPS_NORM, out=None, stream=N
     _need(gate, "gate", (T, H, V), dt, dev)
     _need(w_norm, "w_norm", (V,), dt, dev)
     if out is None:
-        out = torch.empty(T, H, V, dtype=o.dtype, device=o.device)
+        out = _make(stream, (T, H, V), o.dtype, o.device)
     _need(out, "out", (T, H, V), dt, dev)
     _check("kda_gated_rmsnorm", lib().kda_gated_rmsnorm(
         _dt(o), T, H, V, _p(o), o.stride(0), o.stride(1), _p(gate), _p(w_norm), float(eps),
@@ -592,7 +612,7 @@ def kda_decode_fused(q_raw, k_raw, v_raw, gk, b_raw, conv_w, conv_state, gate, w
     _need(slot_ids, "slot_ids", (B,), I32, dev)
     _need_err(dev_err, dev)
     if out is None:
-        out = torch.empty(B, H, V, dtype=q_raw.dtype, device=q_raw.device)
+        out = _make(stream, (B, H, V), q_raw.dtype, q_raw.device)
     _need(out, "out", (B, H, V), dt, dev)
     _check("kda_decode_fused", lib().kda_decode_fused(
         _dt(q_raw), B, H, K, V, _p(q_raw), _p(k_raw), _p(v_raw), st, _p(gk), _p(b_raw),
@@ -769,12 +789,12 @@ def kda_kv4_gather(cu_seqlens, start, total_tokens: int, page_table, pool, dtype
     pa, pages, H, page_size = _pool(pool, D, dev)
     ta, B, M = _table(page_table, dev)
     if k is None:
-        k = torch.empty(T, H, D, dtype=dtype, device=pool.device)
+        k = _make(stream, (T, H, D), dtype, pool.device)
         ka = k.data_ptr()
     else:
         ka = _ptr(k, "k", (T, H, D), dtype, dev)
     if v is None:
-        v = torch.empty(T, H, D, dtype=dtype, device=pool.device)
+        v = _make(stream, (T, H, D), dtype, pool.device)
         va = v.data_ptr()
     else:
         va = _ptr(v, "v", (T, H, D), dtype, dev)
@@ -805,17 +825,17 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
     pa, pages, H_kv, page_size = _pool(pool, D, dev)
     ta, B, M = _table(page_table, dev)
     if o is None:
-        o = torch.empty(T, H, D, dtype=dtype, device=q.device)
+        o = _make(stream, shape, dtype, q.device)
         oa = o.data_ptr()
     else:
         oa = _ptr(o, "o", shape, dtype, dev)
     if lse is None:
-        lse = torch.empty(T, H, dtype=F32, device=q.device)
+        lse = _make(stream, (T, H), F32, q.device)
         la = lse.data_ptr()
     else:
         la = _ptr(lse, "lse", (T, H), F32, dev)
     if workspace is None:
-        workspace = make_kv4_workspace(q.device)
+        workspace = _make(stream, (kv4_workspace_bytes(),), _U8, q.device, zero=True, result=False)
     (wb,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_kv4_attention(
         dt, B, T, max_q, H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
@@ -879,7 +899,7 @@ def kda_page_fork(pools, refs, page_table, lens, src, dst, page_size: int, works
     keep, ptrs, page_bytes = _page_pools(pools, N, dev)
     (n,), _ = _first(src, "src", 1)
     if workspace is None:
-        workspace = torch.empty(2 * n, dtype=I32, device=refs.device)
+        workspace = _make(stream, (2 * n,), I32, refs.device, result=False)
     (wn,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_page_fork(
         len(pools), ptrs, page_bytes, B, M, page_size, N, ra, ta, la, _ptr(src, "src", (n,), I32, dev),
@@ -904,9 +924,9 @@ def kda_page_compact(pools, refs, page_table, live=None, workspace=None, dev_err
     ra, ta, _, B, M, N, dev = _page_state(refs, page_table, None)
     keep, ptrs, page_bytes = _page_pools(pools, N, dev)
     if live is None:
-        live = torch.empty(1, dtype=I32, device=refs.device)
+        live = _make(stream, (1,), I32, refs.device)
     if workspace is None:
-        workspace = torch.empty(3 * N + 16, dtype=I32, device=refs.device)
+        workspace = _make(stream, (3 * N + 16,), I32, refs.device, result=False)
     (wn,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_page_compact(
         len(pools), ptrs, page_bytes, B, M, N, ra, ta, _ptr(live, "live", (1,), I32, dev),
@@ -959,7 +979,7 @@ def kda_selftest_prefill_wait(q, k, v, gk, beta, cu_seqlens, cu_seqlens_host, st
     if dev_err is None:
         raise ValueError("dev_err is required")
     if o is None:
-        o = torch.empty(T, H, V, dtype=q.dtype, device=q.device)
+        o = _make(stream, (T, H, V), q.dtype, q.device)
     _need(o, "o", (T, H, V), dt, dev)
     hp = host.numpy().ctypes.data_as(ctypes.c_void_p)
     _check("kda_selftest_prefill_wait", lib().kda_selftest_prefill_wait(
