@@ -704,7 +704,10 @@ def _err_ptr(dev_err, dev):
 
 
 def _stream_of(stream, dev):
-    """The stream argument as a handle: by default the current one of the operands' device."""
+    """The stream argument as a handle, by default the current one.  The library launches on the current
+    device, which has to be the operands'."""
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError("the operands are on cuda:%d, the current device is cuda:%d" % (dev, torch._C._cuda_getDevice()))
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)

@@ -151,3 +151,12 @@ def test_the_workspace_is_zeroed_there(world):
     attention(SIDE)
     zeroed = [(s, t.numel()) for s, z, t in made if z]
     assert zeroed == [(SIDE, 1 << 10)]
+
+
+@pytest.mark.parametrize("call", [attention, gather, fork, compact])
+@pytest.mark.parametrize("stream", [None, SIDE])
+def test_operands_of_another_device_are_refused(world, monkeypatch, call, stream):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    with pytest.raises(ValueError, match="operands are on cuda:0, the current device is cuda:1"):
+        call(stream)
+    assert not world[0]
