@@ -561,8 +561,9 @@ KDA_API int kda_page_alloc(int B, int max_pages, int page_size, int num_pages, i
 /*
  * kda_page_fork -- copy-on-write: row dst[i] becomes a second holder of row
  * src[i]'s full pages, and gets a copy of its partial last page (in all pools).
- * Row dst[i] is empty before (else KDA_DEVERR_SEQLENS, skipped) and is no source
- * in the same call.  Where no page is left the fork is not made.
+ * Row dst[i] is empty before, is named once and is no source in the same call: a
+ * fork to a row that is not empty, or that an earlier fork goes to, is skipped
+ * (KDA_DEVERR_SEQLENS).  Where no page is left the fork is not made.
  *
  *   num_pools   P in [1, KDA_MAX_LAYERS]; pools host array [P] of device pools
  *   page_bytes  bytes of one page in one pool, a multiple of 16

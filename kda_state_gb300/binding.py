@@ -895,7 +895,7 @@ def kda_page_alloc(refs, page_table, lens, grow, page_size: int, dev_err=None, s
 
 def kda_page_fork(pools, refs, page_table, lens, src, dst, page_size: int, workspace=None,
                   dev_err=None, stream=None):
-    """Copy-on-write: row dst[i] (empty) also holds row src[i]'s full pages, and gets a
+    """Copy-on-write: row dst[i] (empty, named once) also holds row src[i]'s full pages, and gets a
     copy of its partial last page in every pool of the list.  ``workspace``: int32, at
     least 2 n; a call without one makes its own."""
     ra, ta, la, B, M, N, dev = _page_state(refs, page_table, lens)

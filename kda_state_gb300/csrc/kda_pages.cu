@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(SCAN) alloc_kernel(const PageArgs a, const int
 }
 
 // Forks: tables and counts here; the partial last pages to copy go to moves[2 i]
-// (from) and moves[2 i + 1] (to), -1 where there is none.
+// (from) and moves[2 i + 1] (to), -1 where there is none.  While a step's forks are
+// made the length of a row forked to holds a negative mark of the first fork to it.
 __global__ void __launch_bounds__(SCAN) fork_kernel(const PageArgs a, const int32_t *__restrict__ src,
                                                     const int32_t *__restrict__ dst, int n_forks, int32_t *moves) {
     __shared__ int upto[SCAN], fresh_s[SCAN];
@@ -222,11 +223,20 @@ __global__ void __launch_bounds__(SCAN) fork_kernel(const PageArgs a, const int3
                 if (len < 0 || (long long)len > ((long long)a.max_pages << a.page_shift) || a.lens[d] != 0) {
                     report(a.err, DEVERR_SEQLENS);   // the row forked to has to be empty
                     s = -1;
-                } else {
-                    full = len >> a.page_shift;
-                    need = (len & ((1 << a.page_shift) - 1)) != 0;
                 }
             }
+        }
+        __syncthreads();
+        if (s >= 0) atomicMin(&a.lens[d], (int)threadIdx.x - SCAN);
+        __syncthreads();
+        if (s >= 0 && __ldcg(&a.lens[d]) != (int)threadIdx.x - SCAN) {
+            report(a.err, DEVERR_SEQLENS);           // another fork to this row comes first
+            s = -1;
+        }
+        const bool mine = s >= 0;
+        if (mine) {
+            full = len >> a.page_shift;
+            need = (len & ((1 << a.page_shift) - 1)) != 0;
         }
         int total;
         const int before = cta_scan(need, total);
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(SCAN) fork_kernel(const PageArgs a, const int3
         if (got < total) out = true;
         __syncthreads();
         int from = -1, to = -1;
-        bool served = s >= 0;
+        bool served = mine;
         if (served && need) {
             served = before + need <= got;
             if (!served) report(a.err, DEVERR_PAGES);
@@ -275,8 +285,7 @@ __global__ void __launch_bounds__(SCAN) fork_kernel(const PageArgs a, const int3
                 }
             }
         }
-        __syncthreads();               // lens of this step's rows are read above
-        if (served) a.lens[d] = len;
+        if (mine) a.lens[d] = served ? len : 0;
         __syncthreads();
     }
 }
