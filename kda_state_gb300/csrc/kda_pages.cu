@@ -20,23 +20,25 @@ constexpr int SCAN = 1024;             // threads of a scanning CTA
 constexpr int PER = 16;                // refs a thread looks at in one step
 
 // Exclusive prefix sum over the CTA; total to every thread.
-__device__ __forceinline__ int cta_scan(int x, int &total) {
-    __shared__ int warp_sum[33];
+template <typename T>
+__device__ __forceinline__ T cta_scan(T x, T &total) {
+    __shared__ T warp_sum[33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int in = x;
+    T in = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(~0u, in, o);
+        const T y = __shfl_up_sync(~0u, in, o);
         if (lane >= o) in += y;
     }
     __syncthreads();                   // the last call's readers are done
     if (lane == 31) warp_sum[w] = in;
     __syncthreads();
     if (w == 0) {
-        int s = lane < (int)(blockDim.x >> 5) ? warp_sum[lane] : 0, t = s;
+        const T s = lane < (int)(blockDim.x >> 5) ? warp_sum[lane] : 0;
+        T t = s;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(~0u, t, o);
+            const T y = __shfl_up_sync(~0u, t, o);
             if (lane >= o) t += y;
         }
         warp_sum[lane] = t - s;
@@ -90,7 +92,8 @@ __device__ int hand_out(const int32_t *refs, int num_pages, int &cursor, int wan
 }
 
 // The first i in [0, n) with upto[i] > k.
-__device__ __forceinline__ int which(const int *upto, int n, int k) {
+template <typename T>
+__device__ __forceinline__ int which(const T *upto, int n, int k) {
     int lo = 0, hi = n;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -115,7 +118,8 @@ __device__ __forceinline__ void let_go(const PageArgs &a, int32_t *entry) {
 }
 
 __global__ void __launch_bounds__(SCAN) alloc_kernel(const PageArgs a, const int32_t *__restrict__ grow) {
-    __shared__ int upto[SCAN], have_s[SCAN], need_s[SCAN];
+    __shared__ long long upto[SCAN];   // (what 1024 rows ask for may pass 32 bits)
+    __shared__ int have_s[SCAN], need_s[SCAN];
     int cursor = 0;
     // Rows that shrink come first: all of them are looked at before any lets go of a page, so that what a row may do
     // does not depend on when another's count went down.  (65536 rows in one go: a bit each of a thread's 64.)
@@ -173,17 +177,17 @@ __global__ void __launch_bounds__(SCAN) alloc_kernel(const PageArgs a, const int
                 need = pages_of((int)to, a.page_shift) - have;
             }
         }
-        int total;
-        const int before = cta_scan(need, total);
+        long long total;
+        const long long before = cta_scan((long long)need, total);
         upto[threadIdx.x] = before + need;
         have_s[threadIdx.x] = have;
         need_s[threadIdx.x] = need;
         __syncthreads();
         int got = 0;
         if (!out)
-            got = hand_out(a.refs, a.num_pages, cursor, total, [&](int k, int page) {
+            got = hand_out(a.refs, a.num_pages, cursor, (int)min(total, 0x7fffffffLL), [&](int k, int page) {
                 const int i = which(upto, n, k);
-                a.page_table[(size_t)(b0 + i) * a.max_pages + have_s[i] + k - (upto[i] - need_s[i])] = page;
+                a.page_table[(size_t)(b0 + i) * a.max_pages + have_s[i] + k - (int)(upto[i] - need_s[i])] = page;
             });
         if (got < total) out = true;
         __syncthreads();

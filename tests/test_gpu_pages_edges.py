@@ -60,3 +60,15 @@ def test_a_first_fork_without_a_page():
     s.o.fork([1], [3], s.data)
     s.same(err=64 | 4)
     consistent(s)
+
+
+@pytest.mark.parametrize("rows", [34, 66])
+def test_growth_past_32_bits_of_pages(rows):
+    """Rows that together ask for 2^31 (2^32) pages and more: those after the first get none."""
+    M, P, N = 1 << 26, 16, 40
+    table = torch.full((rows, M), -1, dtype=torch.int32, device=DEV)
+    refs, lens, err = i32([0] * N), i32([0] * rows), i32([0])
+    kda().kda_page_alloc(refs, table, lens, i32([21] + [1 << 30] * (rows - 2) + [3]), P, dev_err=err)
+    assert int(err) == 64
+    assert refs.tolist() == [1, 1] + [0] * (N - 2) and lens.tolist() == [21] + [0] * (rows - 1)
+    assert table[0, :2].tolist() == [0, 1] and int((table != -1).sum()) == 2
