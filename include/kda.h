@@ -454,8 +454,8 @@ KDA_API int kda_slot_copy(int num_pools, float *const *pools, size_t slot_elems,
  * V scales [D/16][16].  Codes are e2m1, the even channel in the low nibble;
  * scales are e4m3, one for 16 channels of one token; a value is
  *     code x scale x k_scale (or v_scale).
- * k_scale and v_scale are powers of two, so that they round nothing.  D is 64
- * or 128.  16-byte aligned.
+ * k_scale and v_scale are powers of two, 2^-127 to 2^127, so that they round
+ * nothing.  D is 64 or 128.  16-byte aligned.
  *
  * Row b of page_table, device int32 [B][max_pages], names the pages of request
  * b's tokens in order; entries past its pages are not read (-1 by convention).

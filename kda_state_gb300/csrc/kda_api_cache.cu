@@ -16,9 +16,10 @@ int page_shift_of(int page_size) {
         if (page_size == 1 << s) return s;
     return -1;
 }
+// a power of two whose reciprocal is one too
 bool power_of_two(float x) {
     int e;
-    return x > 0.f && isfinite(x) && frexpf(x, &e) == 0.5f;
+    return x > 0.f && isfinite(x) && isfinite(1.f / x) && frexpf(x, &e) == 0.5f;
 }
 bool row_stride_ok(const void *p, long long stride, long long row) {
     return aligned16(p) && stride >= row && stride % 8 == 0;
