@@ -33,7 +33,7 @@ int fill_cache_args(kda::KvCacheArgs &a, int dt, int B, int total_tokens, int H,
     if (B < 0 || total_tokens < 0 || H < 1 || max_pages < 1 || num_pages < 1 || shift < 0 ||
         !power_of_two(k_scale) || !power_of_two(v_scale) || (B == 0 && total_tokens > 0))
         return KDA_ERR_INVALID_ARG;
-    if ((long long)total_tokens * H > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
+    if ((long long)total_tokens * H > 0x7fffffffLL || (long long)H * D > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
     if (total_tokens == 0) return KDA_OK;
     if (!cu || !start || !page_table || !pool || !aligned16(pool)) return KDA_ERR_INVALID_ARG;
     memset(&a, 0, sizeof(a));
@@ -120,7 +120,8 @@ KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, 
         num_pages < 1 || shift < 0 || window < 0 || !isfinite(scale) || !power_of_two(k_scale) ||
         !power_of_two(v_scale) || (B == 0 && total_tokens > 0))
         return KDA_ERR_INVALID_ARG;
-    if ((long long)total_tokens * H_q > 0x7fffffffLL || ((long long)max_pages << shift) > 0x40000000LL)
+    if ((long long)total_tokens * H_q > 0x7fffffffLL || (long long)H_q * D > 0x7fffffffLL ||
+        ((long long)max_pages << shift) > 0x40000000LL)
         return KDA_ERR_INVALID_ARG;
     if (total_tokens == 0 || max_q == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
     if (!q || !cu_seqlens || !kv_lens || !page_table || !pool || !o || !workspace) return KDA_ERR_INVALID_ARG;

@@ -12,3 +12,14 @@ def test_scales_without_a_reciprocal_are_refused(L, which, scale):  # noqa: F811
         assert call(*{**args, which: scale}.values()) == -1
         for fine in (2.0 ** -127, 2.0 ** -126, 2.0 ** 127):
             assert call(*{**args, which: fine, "T": 0}.values()) == 0
+
+
+@pytest.mark.parametrize("change", [dict(H=1 << 25, T=1), dict(H=(1 << 31) - 1, T=1)])
+def test_rows_past_32_bits_are_refused(L, change):  # noqa: F811
+    """Heads times channels of a token index in 32 bits."""
+    wide = 1 << 40
+    h = change["H"]
+    assert L.kda_kv4_append(*{**APP, **change, "kst": wide, "vst": wide}.values()) == -1
+    assert L.kda_kv4_gather(*{**GAT, **change}.values()) == -1
+    assert L.kda_kv4_attention(*{**ATT, "T": 1, "Hq": h, "Hkv": h, "qs": wide}.values()) == -1
+    assert L.kda_kv4_attention(*{**ATT, "T": 1, "Hq": h, "Hkv": 1, "qs": wide}.values()) == -1
