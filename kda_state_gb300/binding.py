@@ -860,7 +860,7 @@ def _page_state(refs, page_table, lens):
 
 
 def _page_pools(pools, num_pages, dev):
-    """Layers' pools [num_pages, ...] of one size.  Returns (the array of their addresses, its
+    """Layers' pools [num_pages, ...], dense, of one size and element width (their shapes do not matter).  Returns (the array of their addresses, its
     address, bytes of a page); the array has to outlive the call."""
     if len(pools) == 0:
         raise ValueError("pools must be a non-empty list")
@@ -874,9 +874,9 @@ def _page_pools(pools, num_pages, dev):
     if not one:
         for n, q in enumerate(pools):
             _need(q, "pools[%d]" % n, device=torch.device("cuda", dev))
-            if q.dim() < 2 or q.shape[0] != num_pages or q.shape != pools[0].shape or (
-                    q.dtype != pools[0].dtype):
-                raise ValueError("pools[%d]: every pool is [%d, ...] of one shape and dtype" % (
+            p = pools[0]
+            if p.dim() < 2 or p.shape[0] != num_pages or q.numel() != p.numel() or q.element_size() != p.element_size():
+                raise ValueError("pools[%d]: every pool is [%d, ...] of one size and element width" % (
                     n, num_pages))
     ptrs = array.array("Q", map(_address, pools))
     p = pools[0]

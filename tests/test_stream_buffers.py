@@ -160,3 +160,38 @@ def test_operands_of_another_device_are_refused(world, monkeypatch, call, stream
     with pytest.raises(ValueError, match="operands are on cuda:0, the current device is cuda:1"):
         call(stream)
     assert not world[0]
+
+
+U8 = torch.uint8
+ALIKE = [Card(8, 64, dtype=U8), Card(8, 8, 8, dtype=U8), Card(8, 64, dtype=torch.int8)]   # pages of 64 bytes
+
+
+@pytest.mark.parametrize("odd,message", [
+    (None, None), (Card(8, 32, dtype=U8), "pools.3.: every pool"), (Card(8, 64, dtype=BF), "pools.3.: every pool"),
+    (Card(8, 32, dtype=BF), "pools.3.: every pool"), (Card(8, 64, dtype=U8, device="cuda:1"), "pools.3. is on cuda:1"),
+    (torch.ones(8, 64, dtype=U8), "pools.3. must be a CUDA tensor"), (None, "pools.3. is required")])
+def test_a_list_of_pools_is_judged_one_way(world, odd, message):
+    """Pools are pages of bytes: of one size and element width, whatever their shapes, also where another is at fault."""
+    s, one = state(), Card(1, dtype=I32)
+    pools = ALIKE + ([odd] if message else [])
+    for call in (lambda: binding.kda_page_fork(pools, *s.values(), one, one, 16),
+                 lambda: binding.kda_page_compact(pools, s["refs"], s["page_table"]),
+                 lambda: binding.kda_page_copy(pools, one, one)):
+        world[0].clear()
+        if message:
+            with pytest.raises(ValueError, match=message):
+                call()
+            assert not world[0]
+        else:
+            call()
+            assert world[0][0][1][0] == 3 and 64 in world[0][0][1]
+
+
+@pytest.mark.parametrize("pools", [[Card(9, 64, dtype=U8)], [Card(8, dtype=U8)]])
+def test_pools_of_other_pages_are_refused(world, pools):
+    s, one = state(), Card(1, dtype=I32)
+    for call in (lambda: binding.kda_page_fork(pools, *s.values(), one, one, 16),
+                 lambda: binding.kda_page_compact(pools, s["refs"], s["page_table"])):
+        with pytest.raises(ValueError, match="every pool"):
+            call()
+    assert not world[0]
