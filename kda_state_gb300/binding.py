@@ -696,6 +696,11 @@ def _ptr(t, name, shape, dtype, dev):
     return t.data_ptr()
 
 
+def _int(x):
+    """A number as a C int, at its ends where it is past them (ctypes would take it modulo 2^32)."""
+    return x if -0x80000000 <= x <= 0x7fffffff else 0x7fffffff if x > 0 else -0x80000000
+
+
 def _err_ptr(dev_err, dev):
     if dev_err is None:
         return None
@@ -841,8 +846,8 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
         workspace = _make(stream, (kv4_workspace_bytes(),), _U8, q.device, zero=True, result=False)
     (wb,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_kv4_attention(
-        dt, B, T, max_q, H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
-        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size, pa, pages, window,
+        dt, B, T, _int(max_q), H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size, pa, pages, _int(window),
         D ** -0.5 if scale is None else scale, k_scale, v_scale, oa, la,
         _ptr(workspace, "workspace", (wb,), _U8, dev), wb,
         _err_ptr(dev_err, dev), _stream_of(stream, dev))
@@ -888,7 +893,7 @@ def kda_page_alloc(refs, page_table, lens, grow, page_size: int, dev_err=None, s
     ones, rows in order; a negative grow takes tokens back and lets go of their pages.  refs int32 [num_pages] (holders of each page, 0: free),
     page_table int32 [B, max_pages], lens int32 [B]; all three change in place."""
     ra, ta, la, B, M, N, dev = _page_state(refs, page_table, lens)
-    status = lib().kda_page_alloc(B, M, page_size, N, ra, ta, la, _ptr(grow, "grow", (B,), I32, dev),
+    status = lib().kda_page_alloc(B, M, _int(page_size), N, ra, ta, la, _ptr(grow, "grow", (B,), I32, dev),
                                   _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_page_alloc", status)
 
@@ -905,7 +910,7 @@ def kda_page_fork(pools, refs, page_table, lens, src, dst, page_size: int, works
         workspace = _make(stream, (2 * n,), I32, refs.device, result=False)
     (wn,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_page_fork(
-        len(pools), ptrs, page_bytes, B, M, page_size, N, ra, ta, la, _ptr(src, "src", (n,), I32, dev),
+        len(pools), ptrs, page_bytes, B, M, _int(page_size), N, ra, ta, la, _ptr(src, "src", (n,), I32, dev),
         _ptr(dst, "dst", (n,), I32, dev), n, _ptr(workspace, "workspace", (wn,), I32, dev), wn,
         _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_page_fork", status)
@@ -915,7 +920,7 @@ def kda_page_free(refs, page_table, lens, rows, page_size: int, dev_err=None, st
     """Rows (int32 [n], distinct) let go of their pages; those nobody holds are free."""
     ra, ta, la, B, M, N, dev = _page_state(refs, page_table, lens)
     (n,), _ = _first(rows, "rows", 1)
-    status = lib().kda_page_free(B, M, page_size, N, ra, ta, la, _ptr(rows, "rows", (n,), I32, dev), n,
+    status = lib().kda_page_free(B, M, _int(page_size), N, ra, ta, la, _ptr(rows, "rows", (n,), I32, dev), n,
                                  _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_page_free", status)
 

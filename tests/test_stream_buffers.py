@@ -195,3 +195,19 @@ def test_pools_of_other_pages_are_refused(world, pools):
         with pytest.raises(ValueError, match="every pool"):
             call()
     assert not world[0]
+
+
+@pytest.mark.parametrize("number,passed", [(2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1),
+                                           (2 ** 63 - 1, 2 ** 31 - 1), (-2 ** 32, -2 ** 31), (7, 7)])
+def test_numbers_past_32_bits_keep_their_meaning(world, number, passed):
+    """A C int would take them modulo 2^32: a window of 2^32 + 5 was one of 5."""
+    binding.kda_kv4_attention(Card(3, 8, 64, dtype=BF), Card(4, dtype=I32), number, Card(3, dtype=I32), Card(3, 4, dtype=I32),
+                              Card(8, 2, 1, 1152, dtype=U8), window=number, workspace=Card(1 << 10, dtype=U8))
+    (_, args), = world[0]
+    assert args[3] == passed and args[16] == passed
+    s, one = state(), Card(1, dtype=I32)
+    world[0].clear()
+    binding.kda_page_alloc(*s.values(), s["lens"], number)
+    binding.kda_page_free(*s.values(), one, number)
+    binding.kda_page_fork(ALIKE, *s.values(), one, one, number)
+    assert [args[i] for i, (_, args) in zip((2, 2, 5), world[0])] == [passed] * 3
