@@ -530,7 +530,9 @@ KDA_API size_t kda_kv4_workspace_bytes(void);
  * of [0, max_pages page_size] is skipped (KDA_DEVERR_SEQLENS, its rows are not
  * written); tokens of a page that is out of range are left out
  * (KDA_DEVERR_PAGE_RANGE).  After KDA_DEVERR_TIMEOUT the outputs of the call are
- * not valid, and the workspace has to be zeroed.
+ * not valid and the workspace has to be zeroed; a copy that has not landed may
+ * still do so in shared memory that a later launch uses, so the error is fatal for
+ * the context, as it is in the other calls.
  */
 KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv,
                               int D, const void *q, long long q_stride, const int32_t *cu_seqlens,
@@ -643,6 +645,27 @@ KDA_API int kda_selftest_prefill_wait(int num_seqs, int total_tokens, int H, con
                                       int num_slots, const int32_t *init_slot,
                                       const int32_t *out_slot, void *o, int32_t *dev_err,
                                       int wait_us, void *stream);
+
+/*
+ * kda_selftest_kv4_wait -- exercises the cache attention's own bounded waits.
+ *
+ * Runs the kernel that kda_kv4_attention launches for these arguments (window 0,
+ * scale 1), except that the barrier of every CTA's (with few rows: warp's) first
+ * codes expects 16 bytes that nobody copies.  Waits give up after wait_us
+ * microseconds: KDA_DEVERR_TIMEOUT is set in *dev_err, every copy lands, tensor
+ * memory is freed and the kernel returns.  o is not valid and the workspace has to
+ * be zeroed; the context stays usable.  Not part of the cache's path.
+ *
+ *   arguments as kda_kv4_attention; total_tokens >= 1; dev_err required; wait_us
+ *   1 .. 2,000,000
+ */
+KDA_API int kda_selftest_kv4_wait(kda_dtype dt, int B, int total_tokens, int max_q, int H_q,
+                                  int H_kv, int D, const void *q, long long q_stride,
+                                  const int32_t *cu_seqlens, const int32_t *kv_lens,
+                                  const int32_t *page_table, int max_pages, int page_size,
+                                  const void *pool, int num_pages, void *o, void *workspace,
+                                  size_t workspace_bytes, int32_t *dev_err, int wait_us,
+                                  void *stream);
 
 /* Human-readable name of a kda_status value. */
 KDA_API const char *kda_status_string(int status);

@@ -101,6 +101,8 @@ def lib() -> ctypes.CDLL:
         L.kda_kv4_workspace_bytes.restype = sz
         L.kda_kv4_attention.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, vp, i, i, f, f,
                                         f, vp, vp, vp, sz, ip, vp]
+        L.kda_selftest_kv4_wait.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, vp, i, vp, vp,
+                                            sz, ip, i, vp]
         L.kda_page_alloc.argtypes = [i, i, i, i, ip, ip, ip, ip, ip, vp]
         L.kda_page_fork.argtypes = [i, vp, sz, i, i, i, i, ip, ip, ip, ip, ip, i, vp, sz, ip, vp]
         L.kda_page_free.argtypes = [i, i, i, i, ip, ip, ip, ip, i, ip, vp]
@@ -116,7 +118,7 @@ def lib() -> ctypes.CDLL:
                    "kda_kv4_append", "kda_kv4_gather", "kda_kv4_attention", "kda_page_alloc",
                    "kda_page_fork", "kda_page_free", "kda_page_compact", "kda_page_copy",
                    "kda_replay_fold", "kda_slot_copy", "kda_selftest_bounded_wait",
-                   "kda_selftest_prefill_wait"):
+                   "kda_selftest_prefill_wait", "kda_selftest_kv4_wait"):
             getattr(L, fn).restype = ctypes.c_int
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
@@ -994,4 +996,28 @@ def kda_selftest_prefill_wait(q, k, v, gk, beta, cu_seqlens, cu_seqlens_host, st
         N, T, H, _p(q), _p(k), _p(v), _p(gk), _p(beta), _p(cu_seqlens), hp, _p(state_pool),
         state_pool.shape[0], _p(init_slot), _p(out_slot), _p(o), _p(dev_err), int(wait_us),
         _stream(stream)))
+    return o
+
+
+def kda_selftest_kv4_wait(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, workspace, dev_err, o=None,
+                          wait_us: int = 1000, stream=None):
+    """The cache attention with first codes that never arrive: its waits give up after wait_us and set
+    KDA_DEVERR_TIMEOUT in dev_err.  Arguments as ``kda_kv4_attention``; zero the workspace
+    afterwards.  Returns o (not valid)."""
+    shape, dev = _first(q, "q", 3)
+    dt = _kv_dt(q.dtype)
+    T, H, D = shape
+    qa, qs = _rows(q, "q", q.dtype, shape, dev)
+    pa, pages, H_kv, page_size = _pool(pool, D, dev)
+    ta, B, M = _table(page_table, dev)
+    if dev_err is None:
+        raise ValueError("dev_err is required")
+    if o is None:
+        o = _make(stream, shape, q.dtype, q.device)
+    (wb,), _ = _first(workspace, "workspace", 1)
+    _check("kda_selftest_kv4_wait", lib().kda_selftest_kv4_wait(
+        dt, B, T, _int(max_q), H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size, pa, pages, _ptr(o, "o", shape, q.dtype, dev),
+        _ptr(workspace, "workspace", (wb,), _U8, dev), wb, _err_ptr(dev_err, dev), int(wait_us),
+        _stream_of(stream, dev)))
     return o

@@ -70,6 +70,39 @@ int fill_copy_params(kda::PageCopyParams &p, int num_pools, void *const *pools, 
     return KDA_OK;
 }
 
+int attention(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv, int D, const void *q,
+              long long q_stride, const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
+              int max_pages, int page_size, const void *pool, int num_pages, int window, float scale, float k_scale,
+              float v_scale, void *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_err,
+              uint64_t wait_ns, int starve, void *stream) {
+    if (!dtype_ok(dt) || (D != 64 && D != 128)) return KDA_ERR_UNSUPPORTED;
+    const int shift = page_shift_of(page_size);
+    if (B < 0 || total_tokens < 0 || max_q < 0 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || max_pages < 1 ||
+        num_pages < 1 || shift < 0 || window < 0 || !isfinite(scale) || !power_of_two(k_scale) ||
+        !power_of_two(v_scale) || (B == 0 && total_tokens > 0))
+        return KDA_ERR_INVALID_ARG;
+    if ((long long)total_tokens * H_q > 0x7fffffffLL || (long long)H_q * D > 0x7fffffffLL ||
+        ((long long)max_pages << shift) > 0x40000000LL)
+        return KDA_ERR_INVALID_ARG;
+    if (total_tokens == 0 || max_q == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (!q || !cu_seqlens || !kv_lens || !page_table || !pool || !o || !workspace) return KDA_ERR_INVALID_ARG;
+    if (!row_stride_ok(q, q_stride, (long long)H_q * D) || !aligned16(pool) || !aligned16(o) ||
+        !aligned16(workspace) || workspace_bytes < kda_kv4_workspace_bytes())
+        return KDA_ERR_INVALID_ARG;
+    kda::KvAttentionArgs a;
+    memset(&a, 0, sizeof(a));
+    a.dt = dt; a.B = B; a.T = total_tokens; a.max_q = max_q; a.Hq = H_q; a.Hkv = H_kv; a.D = D;
+    a.max_pages = max_pages; a.page_shift = shift; a.num_pages = num_pages;
+    // a window that no cache of this table can fill is none: positions minus a window then stay in 32 bits
+    a.window = window < (max_pages << shift) ? window : 0;
+    a.q = q; a.q_stride = q_stride; a.cu = cu_seqlens; a.kv_lens = kv_lens; a.page_table = page_table;
+    a.pool = (const uint8_t *)pool;
+    a.scale_k = (float)((double)scale * k_scale * 1.4426950408889634); a.v_scale = v_scale;
+    a.o = o; a.lse = lse; a.ws = (uint8_t *)workspace; a.err = dev_err;
+    a.wait_ns = wait_ns; a.starve = starve;
+    return from_cuda(kda::launch_kv4_attention(a, (cudaStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -114,31 +147,22 @@ KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, 
                               float scale, float k_scale, float v_scale, void *o, float *lse,
                               void *workspace, size_t workspace_bytes, int32_t *dev_err,
                               void *stream) {
-    if (!dtype_ok(dt) || (D != 64 && D != 128)) return KDA_ERR_UNSUPPORTED;
-    const int shift = page_shift_of(page_size);
-    if (B < 0 || total_tokens < 0 || max_q < 0 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || max_pages < 1 ||
-        num_pages < 1 || shift < 0 || window < 0 || !isfinite(scale) || !power_of_two(k_scale) ||
-        !power_of_two(v_scale) || (B == 0 && total_tokens > 0))
-        return KDA_ERR_INVALID_ARG;
-    if ((long long)total_tokens * H_q > 0x7fffffffLL || (long long)H_q * D > 0x7fffffffLL ||
-        ((long long)max_pages << shift) > 0x40000000LL)
-        return KDA_ERR_INVALID_ARG;
-    if (total_tokens == 0 || max_q == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
-    if (!q || !cu_seqlens || !kv_lens || !page_table || !pool || !o || !workspace) return KDA_ERR_INVALID_ARG;
-    if (!row_stride_ok(q, q_stride, (long long)H_q * D) || !aligned16(pool) || !aligned16(o) ||
-        !aligned16(workspace) || workspace_bytes < kda_kv4_workspace_bytes())
-        return KDA_ERR_INVALID_ARG;
-    kda::KvAttentionArgs a;
-    memset(&a, 0, sizeof(a));
-    a.dt = dt; a.B = B; a.T = total_tokens; a.max_q = max_q; a.Hq = H_q; a.Hkv = H_kv; a.D = D;
-    a.max_pages = max_pages; a.page_shift = shift; a.num_pages = num_pages;
-    // a window that no cache of this table can fill is none: positions minus a window then stay in 32 bits
-    a.window = window < (max_pages << shift) ? window : 0;
-    a.q = q; a.q_stride = q_stride; a.cu = cu_seqlens; a.kv_lens = kv_lens; a.page_table = page_table;
-    a.pool = (const uint8_t *)pool;
-    a.scale_k = (float)((double)scale * k_scale * 1.4426950408889634); a.v_scale = v_scale;
-    a.o = o; a.lse = lse; a.ws = (uint8_t *)workspace; a.err = dev_err;
-    return from_cuda(kda::launch_kv4_attention(a, (cudaStream_t)stream));
+    return attention(dt, B, total_tokens, max_q, H_q, H_kv, D, q, q_stride, cu_seqlens, kv_lens, page_table, max_pages,
+                     page_size, pool, num_pages, window, scale, k_scale, v_scale, o, lse, workspace, workspace_bytes,
+                     dev_err, KDA_KV4_WAIT_NS, 0, stream);
+}
+
+KDA_API int kda_selftest_kv4_wait(kda_dtype dt, int B, int total_tokens, int max_q, int H_q,
+                                  int H_kv, int D, const void *q, long long q_stride,
+                                  const int32_t *cu_seqlens, const int32_t *kv_lens,
+                                  const int32_t *page_table, int max_pages, int page_size,
+                                  const void *pool, int num_pages, void *o, void *workspace,
+                                  size_t workspace_bytes, int32_t *dev_err, int wait_us,
+                                  void *stream) {
+    if (!dev_err || wait_us < 1 || wait_us > 2000000 || total_tokens < 1) return KDA_ERR_INVALID_ARG;
+    return attention(dt, B, total_tokens, max_q, H_q, H_kv, D, q, q_stride, cu_seqlens, kv_lens, page_table, max_pages,
+                     page_size, pool, num_pages, 0, 1.f, 1.f, 1.f, o, nullptr, workspace, workspace_bytes, dev_err,
+                     (uint64_t)wait_us * 1000ull, 1, stream);
 }
 
 KDA_API int kda_page_alloc(int B, int max_pages, int page_size, int num_pages, int32_t *refs,

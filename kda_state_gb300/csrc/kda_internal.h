@@ -10,6 +10,8 @@
 
 // Bytes of the cache attention's workspace: a counter and two partial results a CTA.
 #define KDA_KV4_WORKSPACE (16u << 20)
+// Limit of the cache attention's waits.
+#define KDA_KV4_WAIT_NS 2000000000ull
 
 namespace kda {
 
@@ -160,6 +162,8 @@ struct KvAttentionArgs {
     float *lse;
     uint8_t *ws;
     int32_t *err;
+    uint64_t wait_ns;              // limit of the kernels' waits
+    int starve;                    // self-test: the first codes never arrive
 };
 
 // The page table's state: refs [num_pages], page_table [B][max_pages], lens [B].

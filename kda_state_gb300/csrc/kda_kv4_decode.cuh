@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         if (lane == 0) {
 #pragma unroll
             for (int s = 0; s < S::STAGES; ++s) barrier_init(shared_addr(bars + (w * S::STAGES + s) * 8), 1);
+            if (a.starve) barrier_await(shared_addr(bars + w * S::STAGES * 8), 16);    // (a self-test: bytes that nobody copies)
         }
         __syncthreads();
         long long before = 0, total = 0;
@@ -421,8 +422,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         for (int k = 0; k < u.count && !dead; ++k) {
             const int s = taken & 1, t0 = (u.c0 + k) * CHUNK;
             const uint32_t parity = taken >> 1 & 1;
-            if (!__all_sync(~0u, barrier_test(bar0 + 8 * s, parity) || barrier_wait(bar0 + 8 * s, parity))) {
-                if (asked - taken > 1) barrier_wait(bar0 + 8 * (1 - s), (taken + 1) >> 1 & 1);
+            if (!__all_sync(~0u, barrier_test(bar0 + 8 * s, parity) || barrier_wait_for(bar0 + 8 * s, parity, a.wait_ns))) {
+                if (asked - taken > 1) barrier_wait_for(bar0 + 8 * (1 - s), (taken + 1) >> 1 & 1, a.wait_ns);
                 if (lane == 0) report(a.err, DEVERR_TIMEOUT);
                 dead = true;
                 break;

@@ -91,6 +91,7 @@ struct alignas(16) TileMeta {
     Part parts[4];
     int2 raw_about[8];                 // by stage of codes: tokens before the end; a bit a run of 16 out of range
     uint32_t tmem;
+    uint2 asked;                       // the stage of codes to be filled next, and how often that ring went round
     int last, dead, cut;
     uint64_t bars[29 + 2 * 6];
 };
@@ -203,13 +204,20 @@ __device__ __forceinline__ void group_sync(uint32_t id, uint32_t count) {
 }
 
 // A warp's bounded wait; once one has given up (*dead), none waits any longer and the CTA runs out on what it has.
-__device__ __forceinline__ void wait_or_dead(uint32_t bar, uint32_t parity, volatile int *dead) {
+__device__ __forceinline__ void wait_or_dead(uint32_t bar, uint32_t parity, volatile int *dead, uint64_t limit_ns = ASYNC_WAIT_NS) {
     if (!barrier_test(bar, parity)) {
         const uint64_t t0 = global_timer();
         while (!*dead && !barrier_test(bar, parity))
-            if (global_timer() - t0 > ASYNC_WAIT_NS) *dead = 1;
+            if (global_timer() - t0 > limit_ns) *dead = 1;
     }
     __syncwarp();
+}
+// The same for the loading warp, whether it may go on.  Once a wait has given up it leaves what others may still use as it
+// is: a part's description (its readers meet at barriers by it), and a stage whose copies may be under way (its barrier
+// takes no second arrival before they land).  A warp that gave up has said so before it handed anything back.
+__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int *dead) {
+    wait_or_dead(bar, parity, dead);
+    return !__any_sync(~0u, *dead);
 }
 // Whether any thread of the named barrier's says so.
 __device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool mine) {
@@ -428,6 +436,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             barrier_init(RAW_FREE + 8 * i, 8);
         }
         barrier_init(FINISHED, 1);
+        if (a.starve) barrier_await(RAW_FULL, 16);     // (a self-test: bytes that nobody copies)
         meta.dead = 0;
     }
     if (QT == 1 && w == 17) {
@@ -803,7 +812,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             bool end = false;
 #pragma unroll
             for (int box = 0; box < 2; ++box) {
-                wait_or_dead(RAW_FULL + 8 * raw, raw_parity, dead);
+                wait_or_dead(RAW_FULL + 8 * raw, raw_parity, dead, a.wait_ns);
                 const int2 about = meta.raw_about[raw];        // tokens before the end; runs of 16 out of range
                 end |= about.x < 0;
                 const uint8_t *t = codes + raw * S::RAW_BYTES;
@@ -1026,7 +1035,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 pi = __shfl_sync(~0u, pi, 0);
                 Part p;
                 const bool found = walk.find(a, pi, p) && !__any_sync(~0u, *dead);
-                if (part >= 4) wait_or_dead(PART_FREE + 8 * (part & 3), ((part >> 2) - 1) & 1, dead);
+                if (part >= 4 && !wait_or_stop(PART_FREE + 8 * (part & 3), ((part >> 2) - 1) & 1, dead)) break;
                 if (lane == 0) {
                     if (found) meta.parts[part & 3] = p;
                     else meta.parts[part & 3].tiles = -1;
@@ -1054,7 +1063,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     const uint8_t *const src = a.pool + ((((size_t)page * a.Hkv + p.h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
                     const int mine = lane & 3, left = p.len - from - i0 * BOX;
                     for (int i = 0; i < min(8, boxes - i0); ++i) {
-                        if (raw_round > 0) wait_or_dead(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead);
+                        if (raw_round > 0 && !wait_or_stop(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead)) goto gave_up;
                         const int runs = __popc(oks >> (4 * i) & 15u);
                         if (lane == 4 * i) {
                             meta.raw_about[raw] = make_int2(min(max(left - i * BOX, 0), BOX), gone >> (4 * i) & 15u);
@@ -1068,14 +1077,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     }
                 }
             }
-            // after a wait that gave up: the copies that were asked for may still be on their way
-            if (__any_sync(~0u, *dead)) {
-                for (uint32_t i = 0; i < S::RAW; ++i)
-                    if (i < raw || raw_round > 0) barrier_wait(RAW_FULL + 8 * i, (i < raw ? raw_round : raw_round - 1) & 1);
-            }
+        gave_up:
             // the end, for the unpacking warps; the last CTA leaves the counters as the next call needs them
             for (int i = 0; i < 2; ++i) {              // (they look at two stages at a time)
-                if (raw_round > 0) wait_or_dead(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead);
+                if (raw_round > 0 && !wait_or_stop(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead)) break;
                 if (lane == 0) {
                     meta.raw_about[raw] = make_int2(-1, 0);
                     barrier_arrive(RAW_FULL + 8 * raw);
@@ -1083,6 +1088,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 if (++raw == S::RAW) raw = 0, ++raw_round;
             }
             if (lane == 0) {
+                meta.asked = make_uint2(raw, raw_round);
                 if (atomicAdd(counters + CTAS_DONE, 1) == (int)gridDim.x - 1) {
                     counters[NEXT_PART] = 0;
                     counters[CTAS_DONE] = 0;
@@ -1093,7 +1099,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
 
     tmem_before_sync();
     __syncthreads();
-    if (tid == 0 && *dead) report(a.err, DEVERR_TIMEOUT);
+    if (w == 17 && *dead) {                            // the copies that were asked for may still be on their way
+        const uint2 upto = meta.asked;
+        for (uint32_t i = 0; i < S::RAW; ++i)
+            if (i < upto.x || upto.y > 0) barrier_wait_for(RAW_FULL + 8 * i, (i < upto.x ? upto.y : upto.y - 1) & 1, a.wait_ns);
+        if (lane == 0) report(a.err, DEVERR_TIMEOUT);
+    }
     if (w == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 

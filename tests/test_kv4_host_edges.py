@@ -23,3 +23,12 @@ def test_rows_past_32_bits_are_refused(L, change):  # noqa: F811
     assert L.kda_kv4_gather(*{**GAT, **change}.values()) == -1
     assert L.kda_kv4_attention(*{**ATT, "T": 1, "Hq": h, "Hkv": h, "qs": wide}.values()) == -1
     assert L.kda_kv4_attention(*{**ATT, "T": 1, "Hq": h, "Hkv": 1, "qs": wide}.values()) == -1
+
+
+def test_selftest_kv4_wait_refuses(L):  # noqa: F811
+    from test_kv4_host import FAKE
+    names = ("dt", "B", "T", "max_q", "Hq", "Hkv", "D", "q", "qs", "cu", "lens", "table", "M", "P", "pool", "pages", "o", "ws", "wsb")
+    call = lambda err=FAKE, us=1000, **kw: L.kda_selftest_kv4_wait(*({**ATT, **kw}[n] for n in names), err, us, None)
+    for kw in (dict(err=None), dict(us=0), dict(us=2000001), dict(T=0), dict(ws=None), dict(q=None), dict(wsb=1)):
+        assert call(**kw) == -1
+    assert call(D=96) == -2
