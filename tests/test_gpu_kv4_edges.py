@@ -47,18 +47,22 @@ def definition(q, k, v, there, window, scale):
     q, at = q.double().numpy(), np.arange(L)
     last = L - n + np.arange(n)[:, None]
     seen = (at <= last) & there & ((at > last - window) if window else True)
-    kk, vv = np.repeat(k, G, 1), np.repeat(v, G, 1)
+    # [Hkv, n G, D] queries, [Hkv, L, D] keys and values: batched products
+    q = q.reshape(n, -1, G, D).transpose(1, 0, 2, 3).reshape(-1, n * G, D)
+    k, v = k.transpose(1, 0, 2), v.transpose(1, 0, 2)
+    rows = lambda x: x.reshape(k.shape[0], n, G, -1).transpose(1, 0, 2, 3).reshape(n, Hq, -1)
     with np.errstate(invalid="ignore", divide="ignore"):
-        s = np.where(seen[:, None], np.einsum("nhd,thd->nht", q, kk) * scale, -np.inf)
-        big = np.where(seen[:, None], np.einsum("nhd,thd->nht", np.abs(q), np.abs(kk)) * abs(scale), 0).max(-1)
+        s = np.where(seen[:, None], rows(q @ k.transpose(0, 2, 1)) * scale, -np.inf)
+        big = np.where(seen[:, None], rows(np.abs(q) @ np.abs(k).transpose(0, 2, 1)) * abs(scale), 0).max(-1)
         m = np.max(s, -1, keepdims=True)
         p = np.exp(s - np.where(np.isneginf(m), 0, m))
         total = p.sum(-1)
         lse = m[..., 0] + np.log(total)
         # a NaN value reaches the rows that see it, whatever its weight
-        bad = np.einsum("nt,thd->nhd", seen.astype(float), np.isnan(vv).astype(float)) > 0
-        mean = lambda x: np.einsum("nht,thd->nhd", p, np.nan_to_num(x)) / np.where(total == 0, 1, total)[..., None]
-        o, a = np.where(bad, np.nan, mean(vv)), mean(np.abs(vv))
+        bad = np.repeat((seen.astype(float) @ np.isnan(v).astype(float)).transpose(1, 0, 2) > 0, G, 1)
+        weights = p.reshape(n, -1, G, L).transpose(1, 0, 2, 3).reshape(-1, n * G, L)
+        mean = lambda x: rows(weights @ np.nan_to_num(x)) / np.where(total == 0, 1, total)[..., None]
+        o, a = np.where(bad, np.nan, mean(v)), mean(np.abs(v))
     es = 2 * D * 2.0 ** -23 * big + 2.0 ** -20
     bo = a * (2.0 ** -11 + 4 * es[..., None]) + 2.0 ** -30 * max(1, L) * np.nanmax(np.abs(v), initial=0)
     return o, lse, bo, es + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))
@@ -207,3 +211,107 @@ def test_infinite_queries(ws, news):
         nan[0, 1] = nan[sum(news[:2]), 2] = nan[-1, 3] = True
         assert torch.equal(lse.isnan().cpu(), nan) and torch.equal(o.isnan().cpu(), nan[..., None].expand(-1, -1, D))
         assert not o[news[0], 0].any() and lse[news[0], 0] == -float("inf")
+
+
+# ---------------------------------------------------------------------------
+# pages that cannot be read, and NaN, in requests that are cut and in wide parts
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("news,lens,Hq,Hkv,D,dtype", [
+    ([1, 1], [2500, 1300], 8, 1, 128, BF),                    # few rows, joined over blocks
+    ([9, 3], [2500, 1300], 2, 2, 64, FP),
+    ([70, 40], [2500, 1300], 4, 2, 128, BF),                  # tiles of 128 rows, cut along the tokens and joined
+    ([90, 33], [1900, 1300], 2, 1, 64, FP),
+    ([700, 599], [1500, 700], 64, 8, 128, BF),                # tiles of 256 rows
+    ([700, 599], [1500, 700], 64, 8, 64, FP)])
+def test_missing_pages_and_nan_among_many(ws, news, lens, Hq, Hkv, D, dtype, window):
+    """Pages out of range in the middle of a request, and NaN keys and values in single heads, against the definition of
+    every row."""
+    P = 64
+    pool, table = make_cache(lens, Hkv, D, P, 76)
+    one, nan = np.full((Hkv, D), 0.5), np.full((Hkv, D), 0.5)
+    nan[0, 17] = np.nan
+    early, late = lens[0] - news[0] - 200 if news[0] < 400 else 300, lens[0] - max(2, news[0] // 2)
+    ref.store(pool, table[0], early, one, nan, P)             # a value that many rows see
+    ref.store(pool, table[0], late, one, nan, P)              # one that the last rows see
+    ref.store(pool, table[1], lens[1] - 2, nan, one, P)       # a key near the end
+    q = packed_q(news, Hq, D, dtype, 77)
+    t = table.copy()
+    gone = [[1, 2, lens[0] // P // 2, lens[0] // P - 1], [0, lens[1] // P - 3]]
+    for b, pages in enumerate(gone):
+        t[b, pages] = [-1, len(pool), -2, 2 ** 31 - 1][:len(pages)]
+    o, lse, err = attend(pool, t, news, lens, q, ws, window)
+    assert err == 32
+    o2, lse2, _ = attend(pool, t, news, lens, q, ws, window)
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse.view(torch.int32), lse2.view(torch.int32))
+    at = 0
+    for b, n in enumerate(news):
+        there = np.ones(lens[b], bool)
+        for page in gone[b]:
+            there[page * P:(page + 1) * P] = False
+        k, v = ref.load(pool, table[b], lens[b], P)
+        for i in range(0, n, 100):                            # (100 rows at a time: the definition holds all scores)
+            z = min(n, i + 100)
+            upto = lens[b] - n + z
+            close(o[at + i:at + z], lse[at + i:at + z], definition(q[at + i:at + z], k[:upto], v[:upto], there[:upto], window,
+                                                                   D ** -0.5), dtype)
+        at += n
+
+
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("D,dtype", [(128, BF), (64, FP)])
+def test_every_row_of_wide_parts(ws, D, dtype, window):
+    news, lens, Hq, Hkv, P = [700, 1, 599], [900, 77, 599], 64, 8, 32
+    pool, table = make_cache(lens, Hkv, D, P, 78)
+    q = packed_q(news, Hq, D, dtype, 79, 2.0)
+    o, lse, err = attend(pool, table, news, lens, q, ws, window)
+    assert err == 0
+    at = 0
+    for b, n in enumerate(news):
+        k, v = ref.load(pool, table[b], lens[b], P)
+        for i in range(0, n, 100):
+            z = min(n, i + 100)
+            upto = lens[b] - n + z
+            close(o[at + i:at + z], lse[at + i:at + z], definition(q[at + i:at + z], k[:upto], v[:upto], np.ones(upto, bool), window,
+                                                                   D ** -0.5), dtype)
+        at += n
+
+
+# ---------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D,P,H", [(64, 16, 3), (128, 64, 2)])
+def test_append_writes_its_bytes_and_no_others(dtype, D, P, H):
+    """Every byte of the pool is the oracle's, but for the codes of the blocks that hold a NaN (their scale says it)."""
+    news, starts = [3, 20, 1], [0, 30, P - 1]
+    lens = [a + n for a, n in zip(starts, news)]
+    rng = np.random.default_rng(80)
+    need = [-(-n // P) for n in lens]
+    pool = rng.integers(0, 256, (sum(need) + 3, H, P // 16, 18 * D), dtype=np.uint8)
+    table = np.full((3, max(need)), -1, np.int32)
+    order = rng.permutation(len(pool))
+    for b, n in enumerate(need):
+        table[b, :n] = order[sum(need[:b]):sum(need[:b]) + n]
+    x = (torch.randn(sum(news), 2, H, D, generator=torch.Generator().manual_seed(81)) * 3).to(dtype)
+    x[4, 0, 1, 20] = x[9, 1, 0, 3] = float("nan")
+    want, free = pool.copy(), np.zeros(pool.shape, bool)
+    t = 0
+    for b, n in enumerate(news):
+        for i in range(n):
+            k, v = x[t].double().numpy()
+            ref.store(want, table[b], starts[b] + i, k, v, P)
+            page, tile, tok = ref.place(table[b], starts[b] + i, P)
+            for y, base in ((k, 0), (v, 9 * D)):
+                for h, c in zip(*np.nonzero(np.isnan(y))):
+                    a = base + tok * (D // 2) + c // 16 * 8
+                    free[page, h, tile, a:a + 8] = True
+            t += 1
+    assert free.sum() == 16
+    d, err = dev(pool), torch.zeros(1, dtype=torch.int32, device=DEV)
+    kda().kda_kv4_append(x[:, 0].to(DEV), x[:, 1].to(DEV), cu_of(news).to(DEV), dev(starts, torch.int32), dev(table), d, dev_err=err)
+    assert int(err) == 0
+    got = d.cpu().numpy()
+    assert np.array_equal(got[~free], want[~free])
