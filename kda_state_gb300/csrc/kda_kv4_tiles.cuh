@@ -65,10 +65,6 @@ struct TileShape {
     static constexpr int K_AT = QT * QBYTES, V_AT = K_AT + 2 * KBYTES, RAW_AT = V_AT + 2 * KBYTES;
     static constexpr int META = RAW_AT + RAW * RAW_BYTES;
     static constexpr int PARTIAL = 128 * (D + 2);        // floats
-    // With QT = 2 the products with V start when the first half of a tile's weights is there, in steps of 16 tokens
-    // (2 x 2048 tokens on up to 14 K: 860 -> 856 us, D = 64 651 -> 646; at 3 or 6 steps 868, 869; in three parts
-    // 919).  With QT = 1 they wait for all (64 requests of 8 tokens: 136, with halves 140 us).
-    static constexpr int FIRST = QT == 2 ? TT / 32 : TT / 16;
     // Columns of TMEM: S, O, and P, a column for two tokens' weights.  If there is room, P has columns of its own; else
     // it lies over S, and the next S waits for the product that reads P: products of different accumulators are
     // not ordered among themselves.  The wait costs prompts of 2048 tokens 7% (791 -> 851 us),
@@ -93,7 +89,7 @@ struct alignas(16) TileMeta {
     uint32_t tmem;
     uint2 asked;                       // the stage of codes to be filled next, and how often that ring went round
     int last, dead, cut;
-    uint64_t bars[29 + 2 * 6];
+    uint64_t bars[27 + 2 * 6];
 };
 
 __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {   // K-major, 128-byte swizzle, 8-row groups 1 KB apart
@@ -406,7 +402,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
     const uint32_t bar = shared_addr(meta.bars);
     const uint32_t PART_FULL = bar, PART_FREE = bar + 32, Q_FULL = bar + 64, S_FULL = bar + 80, P_FULL = bar + 96, PV_DONE = bar + 112,
                    K_FULL = bar + 128, K_FREE = bar + 144, V_FULL = bar + 160, V_FREE = bar + 176, FINISHED = bar + 192,
-                   P_HALF = bar + 200, S_FREE = bar + 216, RAW_FULL = bar + 232, RAW_FREE = RAW_FULL + 8 * S::RAW;
+                   S_FREE = bar + 200, RAW_FULL = bar + 216, RAW_FREE = RAW_FULL + 8 * S::RAW;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int G = a.Hq / a.Hkv;
 
@@ -423,7 +419,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             barrier_init(Q_FULL + 8 * i, 4);
             barrier_init(S_FULL + 8 * i, 1);
             barrier_init(P_FULL + 8 * i, 4);
-            barrier_init(P_HALF + 8 * i, 4);
             barrier_init(S_FREE + 8 * i, 4);
             barrier_init(PV_DONE + 8 * i, 1);
             barrier_init(K_FULL + 8 * i, 8);
@@ -620,12 +615,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(u1));
                         pk[e / 2] = half_pair(p0, p1);
                         pk[e / 2 + 1] = half_pair(p2, p3);
-                    }
-                    if (c == S::FIRST) {
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                        tmem_before_sync();
-                        __syncwarp();
-                        if (lane == 0) barrier_arrive(P_HALF + 8 * g);
                     }
                     if (S::EARLY && c == 0 && mine > 0) {      // the last weights have been read
                         wait_or_dead(PV_DONE + 8 * g, (done - 1) & 1, dead);
@@ -929,30 +918,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 };
                 auto values = [&](int g, int j, bool first, bool frees) {
                     const uint32_t n = kv + j;
-                    if (QT == 2) {
-                        wait_or_dead(P_HALF + 8 * g, done[g] & 1, dead);
-                    } else {
-                        wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
-                        ++done[g];
-                    }
+                    wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
+                    ++done[g];
                     const uint64_t dv = tile_desc(base + S::V_AT + (n & 1) * S::KBYTES);
                     tmem_after_sync();
-                    auto steps = [&](int from, int to) {
+                    if (elect_one()) {
 #pragma unroll
-                        for (int s = from; s < to; ++s) {
+                        for (int s = 0; s < TT / 16; ++s) {
                             const uint64_t at = (uint64_t)(((s >> 2) * D * 128 + (s & 3) * 32) >> 4);
                             mma_f16_ts(tmem + S::O_COL + g * D, tmem + S::P_COL + g * S::P_STEP + 8 * s, dv + at, ID_O, s > 0 || !first);
                         }
-                    };
-                    if (QT == 2) {
-                        if (elect_one()) steps(0, S::FIRST);
-                        __syncwarp();
-                        wait_or_dead(P_FULL + 8 * g, done[g] & 1, dead);
-                        ++done[g];
-                        tmem_after_sync();
-                    }
-                    if (elect_one()) {
-                        steps(QT == 2 ? S::FIRST : 0, TT / 16);
                         mma_done(PV_DONE + 8 * g);
                         if (frees) mma_done(V_FREE + 8 * (n & 1));
                     }
