@@ -25,8 +25,8 @@
 // tile, joined at the end.  Queries are scaled by powers of two and weights held
 // 2^9 above the maximum as in the kernel for few rows.  The exponent of a weight is
 // one fused operation, y f - (m f - 9), while a warp's maxima are below 2^10 as
-// scores (m f is then rounded by 2^-14 or less), and (y - m) f + 9 beyond (prompts of 2048 tokens
-// 855 -> 866 us, 64 requests of 8 tokens 138 -> 142; with the second form everywhere 914, 141).
+// scores (m f is then rounded by 2^-14 or less), and (y - m) f + 9 beyond.  (With the second form
+// everywhere prompts of 2048 tokens take 870 us instead of 862, with 64 channels 662 instead of 643.)
 //
 // If there are fewer (request, rows, head) than SMs, each is cut along the tokens;
 // the last part to arrive joins the results in order, so they do not depend on
@@ -146,12 +146,6 @@ __device__ __forceinline__ void fma_pair(uint32_t &x0, uint32_t &x1, uint64_t f,
     asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(f), "l"(c));
     asm("mov.b64 {%0, %1}, %2;" : "=r"(x0), "=r"(x1) : "l"(v));
 }
-__device__ __forceinline__ void add_pair(uint32_t &x0, uint32_t &x1, uint64_t y) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(x0), "r"(x1));
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(y));
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(x0), "=r"(x1) : "l"(v));
-}
 // What is added to y f for the exponent of a weight, up to FAR; finite before any product, so that a masked -inf stays.
 __device__ __forceinline__ float offset_of(float m, float factor) {
     return fminf(fmaf(-m, factor, HEADROOM), -LOWEST);
@@ -200,20 +194,26 @@ __device__ __forceinline__ void group_sync(uint32_t id, uint32_t count) {
 }
 
 // A warp's bounded wait; once one has given up (*dead), none waits any longer and the CTA runs out on what it has.
-__device__ __forceinline__ void wait_or_dead(uint32_t bar, uint32_t parity, volatile int *dead, uint64_t limit_ns = ASYNC_WAIT_NS) {
+__device__ __forceinline__ void wait_or_dead(uint32_t bar, uint32_t parity, volatile int *dead) {
     if (!barrier_test(bar, parity)) {
         const uint64_t t0 = global_timer();
         while (!*dead && !barrier_test(bar, parity))
-            if (global_timer() - t0 > limit_ns) *dead = 1;
+            if (global_timer() - t0 > ASYNC_WAIT_NS) *dead = 1;
     }
     __syncwarp();
 }
-// The same for the loading warp, whether it may go on.  Once a wait has given up it leaves what others may still use as it
-// is: a part's description (its readers meet at barriers by it), and a stage whose copies may be under way (its barrier
-// takes no second arrival before they land).  A warp that gave up has said so before it handed anything back.
-__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int *dead) {
-    wait_or_dead(bar, parity, dead);
-    return !__any_sync(~0u, *dead);
+// The same, and whether the phase is complete: the loading and unpacking warps end where it is not.  They leave what others
+// may still use as it is, a part's description (its readers meet at barriers by it) and a stage whose copies may be under
+// way (its barrier takes no second arrival before they land).
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *dead, uint64_t limit_ns = ASYNC_WAIT_NS) {
+    bool ok = barrier_test(bar, parity);
+    if (__all_sync(~0u, ok)) return true;
+    const uint64_t t0 = global_timer();
+    while (!ok && !*dead) {
+        ok = barrier_test(bar, parity);
+        if (global_timer() - t0 > limit_ns) *dead = 1;
+    }
+    return __all_sync(~0u, ok);
 }
 // Whether any thread of the named barrier's says so.
 __device__ __forceinline__ bool group_any(uint32_t id, uint32_t count, bool mine) {
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 if (far) {
                     add = HEADROOM;
 #pragma unroll
-                    for (int e = 0; e < TT; e += 2) add_pair(x[e], x[e + 1], pair_of_floats(-m, -m));
+                    for (int e = 0; e < TT; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - m);
                 }
                 const uint64_t ff = pair_of_floats(factor, factor), aa = pair_of_floats(add, add);
                 uint64_t sum0 = 0, sum1 = 0;
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             bool end = false;
 #pragma unroll
             for (int box = 0; box < 2; ++box) {
-                wait_or_dead(RAW_FULL + 8 * raw, raw_parity, dead, a.wait_ns);
+                if (!wait_all(RAW_FULL + 8 * raw, raw_parity, dead, a.wait_ns)) goto unpacked;
                 const int2 about = meta.raw_about[raw];        // tokens before the end; runs of 16 out of range
                 end |= about.x < 0;
                 const uint8_t *t = codes + raw * S::RAW_BYTES;
@@ -889,6 +889,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             __syncwarp();
             if (lane == 0) barrier_arrive(V_FULL + 8 * stage);
         }
+    unpacked:;
     } else {
         give_registers<REGS_OTHER>();
         if (w == 16) {
@@ -1010,7 +1011,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 pi = __shfl_sync(~0u, pi, 0);
                 Part p;
                 const bool found = walk.find(a, pi, p) && !__any_sync(~0u, *dead);
-                if (part >= 4 && !wait_or_stop(PART_FREE + 8 * (part & 3), ((part >> 2) - 1) & 1, dead)) break;
+                if (part >= 4 && !wait_all(PART_FREE + 8 * (part & 3), ((part >> 2) - 1) & 1, dead)) break;
                 if (lane == 0) {
                     if (found) meta.parts[part & 3] = p;
                     else meta.parts[part & 3].tiles = -1;
@@ -1021,10 +1022,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 const int32_t *const pages = a.page_table + (size_t)p.b * a.max_pages;
                 const int boxes = 2 * p.tiles, from = p.tile0 * TT;
                 // a lane looks up one run of 16 tokens of each 8 stages, and asks for it when its stage's turn comes
-                // the page of the part's i-th run; -2 past the end (a negative entry of the table counts as -1)
-                auto look = [&](int i) {
-                    const long long pos = (long long)from + (long long)i * KV_TILE;
-                    return i < boxes * 4 && pos < p.len ? max(pages[pos >> a.page_shift], -1) : -2;
+                const int runs_in = min(boxes * 4, (max(p.len - from, 0) + KV_TILE - 1) / KV_TILE);    // that are to be read
+                auto look = [&](int i) {               // the page of the part's i-th run
+                    return i < runs_in ? pages[((long long)from + (long long)i * KV_TILE) >> a.page_shift] : -1;
                 };
                 const bool one_copy = a.page_shift >= 6;       // a stage lies in one page
                 int then = look(lane);
@@ -1032,13 +1032,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                     const int page = then;
                     then = look((i0 + 8) * 4 + lane);
                     const bool ok = page >= 0 && page < a.num_pages;
-                    const uint32_t oks = __ballot_sync(~0u, ok), gone = __ballot_sync(~0u, !ok && page != -2);
+                    const uint32_t oks = __ballot_sync(~0u, ok), gone = __ballot_sync(~0u, !ok && i0 * 4 + lane < runs_in);
                     if (gone && lane == 0) report(a.err, DEVERR_PAGE_RANGE);
                     const int in_page = (from + (i0 * 4 + lane) * KV_TILE) & ((1 << a.page_shift) - 1);
                     const uint8_t *const src = a.pool + ((((size_t)page * a.Hkv + p.h) << (a.page_shift - 4)) + (in_page >> 4)) * L::BYTES;
                     const int mine = lane & 3, left = p.len - from - i0 * BOX;
                     for (int i = 0; i < min(8, boxes - i0); ++i) {
-                        if (raw_round > 0 && !wait_or_stop(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead)) goto gave_up;
+                        if (raw_round > 0 && !wait_all(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead)) goto gave_up;
                         const int runs = __popc(oks >> (4 * i) & 15u);
                         if (lane == 4 * i) {
                             meta.raw_about[raw] = make_int2(min(max(left - i * BOX, 0), BOX), gone >> (4 * i) & 15u);
@@ -1055,7 +1055,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
         gave_up:
             // the end, for the unpacking warps; the last CTA leaves the counters as the next call needs them
             for (int i = 0; i < 2; ++i) {              // (they look at two stages at a time)
-                if (raw_round > 0 && !wait_or_stop(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead)) break;
+                if (raw_round > 0 && !wait_all(RAW_FREE + 8 * raw, (raw_round - 1) & 1, dead)) break;
                 if (lane == 0) {
                     meta.raw_about[raw] = make_int2(-1, 0);
                     barrier_arrive(RAW_FULL + 8 * raw);
