@@ -78,7 +78,8 @@ enum {
     KDA_DEVERR_SLOT_RANGE = 1,   /* a slot id outside [0, num_slots) */
     KDA_DEVERR_ACCEPT_RANGE = 2, /* an accept length outside [0, max_accept] */
     KDA_DEVERR_SEQLENS = 4,      /* cu_seqlens or cu_drafts not monotone or past total_tokens,
-                                    or a draft count above G_max */
+                                    a draft count above G_max, a length that its row of the page
+                                    table cannot have, or a fork to a row that is not empty */
     KDA_DEVERR_RANGE = 8,        /* reserved: no kernel sets it.  The chunked prefill runs any
                                     chunk whose products could leave fp32 range (strong decays,
                                     positive gk, large k, v or state) through an fp32 recurrence
@@ -442,10 +443,13 @@ KDA_API int kda_slot_copy(int num_pools, float *const *pools, size_t slot_elems,
 /*
  * The paged 4-bit key/value cache of a hybrid model's full-attention layers.
  * ---------------------------------------------------------------------------
- * Next to the recurrent state pools ("Unified memory" and "Hybrid KDA Memory
- * Management" of the same pages: one pool of memory behind slots and pages,
- * copy-on-write, checkpoints at boundaries) such a model keeps the keys and
- * values of its attention layers in pages.  One pool per layer:
+ * For hybrids whose attention layers have keys and values of 64 or 128 channels
+ * (multi-head or grouped-query).  Next to the recurrent state pools ("Unified
+ * memory" and "Hybrid KDA Memory Management" of the same pages: one pool of
+ * memory behind slots and pages, copy-on-write, checkpoints at boundaries) such a
+ * model keeps them in pages.  The model of those pages has MLA layers beside its
+ * KDA layers, one 576-wide latent a token: this format does not hold that, while
+ * the calls on pages (kda_page_*) take pages of any layout.  One pool per layer:
  *
  *     uint8 [num_pages][H_kv][page_size / 16][18 D]
  *
@@ -554,7 +558,8 @@ KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, 
  * KDA_DEVERR_PAGES); later rows that need a page then get none either.  A
  * negative grow takes tokens back (drafts that were not accepted) and lets go of
  * the pages behind the new end, before any are given out; into a page that
- * another row holds too a row cannot shrink (KDA_DEVERR_PAGES, it stays).
+ * another row holds too a row cannot shrink (KDA_DEVERR_PAGES, it stays); what is
+ * shared is looked at before any of 65536 rows lets go.
  */
 KDA_API int kda_page_alloc(int B, int max_pages, int page_size, int num_pages, int32_t *refs,
                            int32_t *page_table, int32_t *lens, const int32_t *grow,

@@ -15,14 +15,14 @@ template <int D, typename T>
 cudaError_t launch(const KvAttentionArgs &a, cudaStream_t s) {
     const long long rows = (long long)a.max_q * (a.Hq / a.Hkv);
     // Few rows: the kernel that reads the cache once, 8 or 16 rows at a time.  64 requests of 0.5 to 6 K tokens, D = 128,
-    // 8 kv heads: 16 rows 90 us against 128 us in tiles, 24 rows 148 against 129, 64 rows 279 against 134.
+    // 8 kv heads: 16 rows 89 us against 136 us in tiles, 24 rows 149 against 137, 64 rows 280 against 143.
     if (rows <= 8) return kv4::launch_decode_attention<D, 1, T>(a, s);
     if (rows <= 16) return kv4::launch_decode_attention<D, 2, T>(a, s);
-    // Tiles with 256 rows a part make half as many parts, which take 1.3 times as long (3470 cycles a tile against 2700)
-    // and are not cut.  One request: as the waves of parts come out (300 new tokens of 8 x 8 heads over 3259: 43 us with
-    // 128 rows, one wave; 340: 58 with 256 rows, 75 with 128 in two waves).  Several, of unknown lengths: 256 rows where
-    // the average request fills them and there are a quarter more parts than SMs (218 parts: 96 us against 111; 109
-    // parts: 73 against 69).
+    // Tiles with 256 rows a part make half as many parts, which take 1.4 times as long (3.7 K cycles a tile against 2.7 K)
+    // and are not cut.  One request: as the waves of parts come out, at 1.3 (300 new tokens of 8 x 8 heads over 3259: 44 us
+    // with 128 rows, one wave, 62 with 256; 340: 61 with 256 rows, 79 with 128 in two waves).  Several, of unknown lengths:
+    // 256 rows where the average request fills them and there are a quarter more parts than SMs (4 requests of 0.5 to 6 K,
+    // 218 parts: 99 us against 119; 109 parts: 76 against 73; between them, 163 parts: 80 against 92, which are left to 128).
     const long long all = (long long)a.T * (a.Hq / a.Hkv);
     bool wide;
     if (a.B == 1) {

@@ -67,9 +67,9 @@ struct TileShape {
     static constexpr int PARTIAL = 128 * (D + 2);        // floats
     // Columns of TMEM: S, O, and P, a column for two tokens' weights.  If there is room, P has columns of its own; else
     // it lies over S, and the next S waits for the product that reads P: products of different accumulators are
-    // not ordered among themselves.  The wait costs prompts of 2048 tokens 7% (791 -> 851 us),
-    // drafts of 8 tokens 2% (136 -> 138).  A product warp for each group instead of one that alternates: 913; half
-    // tiles in turn, so that the next scores are always there: 1035.
+    // not ordered among themselves.  When it came the wait cost prompts of 2048 tokens 7% (791 -> 851 us), drafts of 8
+    // tokens 2% (136 -> 138); a product warp for each group instead of one that alternates took 913, half tiles in turn,
+    // so that the next scores are always there, 1035, weights handed on by halves 869 (whole: 859).
     static constexpr bool OWN_P = D == 64;
     // Then, with QT = 2, the next S is asked for as soon as the softmax has this one in registers (2 x 2048 tokens on
     // up to 6 K, D = 64: 141 -> 132 us).
