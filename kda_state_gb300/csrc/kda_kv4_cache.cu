@@ -130,15 +130,17 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const KvCacheArgs a) {
     if (tile) {
         const uint2 code = *reinterpret_cast<const uint2 *>(tile + (side ? L::VC : L::KC) + tok * (D / 2) + blk * 8);
         const uint32_t sb = tile[side ? L::VS + blk * KV_TILE + tok : L::KS + tok * NB + blk];
-        const float s = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x * (side ? a.v_scale : a.k_scale);
-        uint32_t h0[4], h1[4];
-        e2m1x8_to_f16x2(code.x, h0);
-        e2m1x8_to_f16x2(code.y, h1);
+        // code times scale first, exact in fp16: scale times tensor scale alone may leave fp32's range
+        const uint32_t ss = e4m3x2_to_f16x2(sb | sb << 8);
+        const __half2 s = *reinterpret_cast<const __half2 *>(&ss);
+        const float by = side ? a.v_scale : a.k_scale;
+        uint32_t h[8];
+        e2m1x8_to_f16x2(code.x, *reinterpret_cast<uint32_t(*)[4]>(h));
+        e2m1x8_to_f16x2(code.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = f16x2_to_float2(h0[i]), g = f16x2_to_float2(h1[i]);
-            out[i] = pack2(f.x * s, f.y * s, T());
-            out[i + 4] = pack2(g.x * s, g.y * s, T());
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = __half22float2(__hmul2_rn(*reinterpret_cast<const __half2 *>(&h[i]), s));
+            out[i] = pack2(f.x * by, f.y * by, T());
         }
     }
     T *dst = (side ? (T *)a.v_out : (T *)a.k_out) + ((size_t)t * a.H + h) * D + blk * 16;

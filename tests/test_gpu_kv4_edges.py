@@ -315,3 +315,21 @@ def test_append_writes_its_bytes_and_no_others(dtype, D, P, H):
     assert int(err) == 0
     got = d.cpu().numpy()
     assert np.array_equal(got[~free], want[~free])
+
+
+@pytest.mark.parametrize("dtype,power", [(BF, 118), (BF, 120), (BF, 127), (BF, -120), (FP, 7), (FP, -14)])
+def test_gather_at_the_ends_of_the_type(dtype, power):
+    """A value in the type's range is read back exactly, also where its block's scale times the tensor's is not in fp32's."""
+    H, D, P, n = 2, 64, 16, 20
+    rng = np.random.default_rng(82)
+    pool, table = make_cache([0], H, D, P, 83, spare=2, max_pages=3)
+    table[0, :2] = [1, 0]
+    for pos in range(n):
+        x = rng.choice([0.0, 0.5, -1, 1.5, -2, 3, 4, -6], (2, H, D)) * 2.0 ** rng.integers(-8, 3)
+        x[..., ::16] = np.sign(rng.standard_normal((2, H, D // 16))) * 6 * rng.choice([448.0, 4.0, 2.0 ** -9], (2, H, D // 16))
+        ref.store(pool, table[0], pos, x[0], x[1], P)
+    k, v = kda().kda_kv4_gather(cu_of([n]).to(DEV), dev([0], torch.int32), n, dev(table), dev(pool), dtype=dtype,
+                                k_scale=2.0 ** power, v_scale=2.0 ** power)
+    wk, wv = ref.load(pool, table[0], n, P, 2.0 ** power, 2.0 ** power)
+    for got, want in ((k, wk), (v, wv)):
+        assert torch.equal(got.cpu(), torch.from_numpy(want).to(dtype))
