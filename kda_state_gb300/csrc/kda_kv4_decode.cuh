@@ -655,12 +655,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                 if (begun && ended) {
                     if (col >= x.rows || dead) continue;
                     const size_t row = row_of(x, col);
-                    const float f = sum == 0.f ? 0.f : a.v_scale / sum;
+                    const float f = sum == 0.f ? 0.f : 1.f / sum;      // (apart from v_scale: their quotient may underflow)
                     if (r == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * LN2;
                     uint32_t y[KS];
 #pragma unroll
                     for (int j = 0; j < KS; ++j)
-                        y[j] = sum == 0.f ? 0u : pack_of<T>(o[t][j][k2] * f, o[t][j][k2 + 2] * f);
+                        y[j] = sum == 0.f ? 0u : pack_of<T>(o[t][j][k2] * f * a.v_scale, o[t][j][k2 + 2] * f * a.v_scale);
                     uint4 *dst = reinterpret_cast<uint4 *>((T *)a.o + row * D + r * (D / 8));
 #pragma unroll
                     for (int j = 0; j < KS / 4; ++j) dst[j] = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
@@ -688,9 +688,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     auto finish = [&](const Piece &x, int col, int d, float4 v, float top, float sum) {
         const int row = x.row0 + col;
         const size_t at_row = (size_t)(x.q0 + row / G) * a.Hq + x.h * G + row % G;
-        const float f = sum == 0.f ? 0.f : a.v_scale / sum;
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
         *reinterpret_cast<uint2 *>((T *)a.o + at_row * D + d) =
-            sum == 0.f ? make_uint2(0, 0) : make_uint2(pack_of<T>(v.x * f, v.y * f), pack_of<T>(v.z * f, v.w * f));
+            sum == 0.f ? make_uint2(0, 0) : make_uint2(pack_of<T>(v.x * f * a.v_scale, v.y * f * a.v_scale), pack_of<T>(v.z * f * a.v_scale, v.w * f * a.v_scale));
         if (d == 0 && a.lse) a.lse[at_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * LN2;
     };
     auto add = [](float4 &v, float &top, float &sum, const float4 &z, const float2 &ml) {

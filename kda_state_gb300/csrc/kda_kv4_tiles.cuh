@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
             const int rr = p.row0 + my_row;
             const size_t at_row = (size_t)(p.q0 + rr / G) * a.Hq + p.h * G + rr % G;
             if (QT == 2) {
-                const float f = l == 0.f ? 0.f : a.v_scale / l;
+                const float f = l == 0.f ? 0.f : 1.f / l;              // (apart from v_scale: their quotient may underflow)
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t x[32];
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                             uint32_t y[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const float u = __uint_as_float(x[e + 2 * k]) * f, v = __uint_as_float(x[e + 2 * k + 1]) * f;
+                                const float u = __uint_as_float(x[e + 2 * k]) * f * a.v_scale, v = __uint_as_float(x[e + 2 * k + 1]) * f * a.v_scale;
                                 y[k] = bad ? 0x7fff7fffu : l == 0.f ? 0u : pack_of<T>(u, v);
                             }
                             *reinterpret_cast<uint4 *>((T *)a.o + at_row * D + 32 * c + e) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                 const float both = fmaxf(ml0.x, ml1.x);
                 const float k0 = exp2_fast(ml0.x - both), k1 = exp2_fast(ml1.x - both), sum = ml0.y * k0 + ml1.y * k1;
                 const bool split = p.pieces > 1;
-                const float f = split ? 1.f : sum == 0.f ? 0.f : a.v_scale / sum, f0 = k0 * f, f1 = k1 * f;
+                const float f = split ? 1.f : sum == 0.f ? 0.f : 1.f / sum, f0 = k0 * f, f1 = k1 * f;
                 float *const partials = reinterpret_cast<float *>(a.ws + MAX_CTAS * 4);
                 float *const my_part = partials + (size_t)(p.slot0 + p.piece) * S::PARTIAL;
 #pragma unroll 1
@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                         for (int e = 0; e < 32; e += 8) {
                             uint32_t y[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) y[k] = pack_of<T>(__uint_as_float(x0[e + 2 * k]), __uint_as_float(x0[e + 2 * k + 1]));
+                            for (int k = 0; k < 4; ++k) y[k] = pack_of<T>(__uint_as_float(x0[e + 2 * k]) * a.v_scale, __uint_as_float(x0[e + 2 * k + 1]) * a.v_scale);
                             *reinterpret_cast<uint4 *>((T *)a.o + at_row * D + 32 * c + e) = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     }
@@ -765,10 +765,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1) tile_attention_kernel(const K
                                 if (col >= p.rows) continue;
                                 const int orow = p.row0 + col;
                                 const size_t at = (size_t)(p.q0 + orow / G) * a.Hq + p.h * G + orow % G;
-                                const float fo = total[k] == 0.f ? 0.f : a.v_scale / total[k];
+                                const float fo = total[k] == 0.f ? 0.f : 1.f / total[k];
                                 *reinterpret_cast<uint2 *>((T *)a.o + at * D + d) =
                                     total[k] == 0.f ? make_uint2(0, 0)
-                                                    : make_uint2(pack_of<T>(v[k].x * fo, v[k].y * fo), pack_of<T>(v[k].z * fo, v[k].w * fo));
+                                                    : make_uint2(pack_of<T>(v[k].x * fo * a.v_scale, v[k].y * fo * a.v_scale), pack_of<T>(v[k].z * fo * a.v_scale, v[k].w * fo * a.v_scale));
                                 if (d == 0 && a.lse) a.lse[at] = total[k] == 0.f ? -INFINITY : (to[k] + log2f(total[k])) * LN2;
                             }
                         }

@@ -333,3 +333,23 @@ def test_gather_at_the_ends_of_the_type(dtype, power):
     wk, wv = ref.load(pool, table[0], n, P, 2.0 ** power, 2.0 ** power)
     for got, want in ((k, wk), (v, wv)):
         assert torch.equal(got.cpu(), torch.from_numpy(want).to(dtype))
+
+
+@pytest.mark.parametrize("news,lens", [([1, 1], [9000, 30]), ([3, 5], [9000, 30]), ([90, 40], [5000, 70]), ([600, 550], [3000, 700])])
+def test_value_scales_of_every_size(ws, news, lens):
+    """Outputs in the type's normal range are as exact with a tiny or a huge tensor scale as with 1."""
+    D, P, H, Hq = 64, 64, 8 if news[0] == 600 else 2, 64 if news[0] == 600 else 4
+    pool, table = make_cache(lens, H, D, P, 84)
+    q = packed_q(news, Hq, D, BF, 85)
+    for b, n in enumerate(lens):                              # values around 1000
+        for pos in range(0, n, 3):
+            ref.store(pool, table[b], pos, np.full((H, D), 0.5), np.full((H, D), 900.0 + pos % 200), P)
+    one, want_lse, _ = attend(pool, table, news, lens, q, ws)
+    for power in (-127, -118, -105, 100, 114):
+        o, lse, err = attend(pool, table, news, lens, q, ws, v_scale=2.0 ** power)
+        assert err == 0 and torch.equal(lse, want_lse)
+        o, want = o.double() * 2.0 ** -power, one.double()
+        # both are one rounding to bf16 of values that differ by fp32 arithmetic; below 2^-126 the type's steps are 2^-133
+        step = 2.0 ** -7 * want.abs() + 2.0 ** (-133 - power if power < -100 else -200)
+        assert ((o - want).abs() <= step * 1.01).all()
+        assert ((o == want) | (want.abs() * 2.0 ** power < 2.0 ** -126)).double().mean() > 0.99
