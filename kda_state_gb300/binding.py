@@ -799,12 +799,14 @@ def kda_kv4_gather(cu_seqlens, start, total_tokens: int, page_table, pool, dtype
     pa, pages, H, page_size = _pool(pool, D, dev)
     ta, B, M = _table(page_table, dev)
     if k is None:
-        k = _make(stream, (T, H, D), dtype, pool.device)
+        k = _make(stream, (T, H, D), dtype, pool.device) if stream is not None else torch.empty(
+            T, H, D, dtype=dtype, device=pool.device)
         ka = k.data_ptr()
     else:
         ka = _ptr(k, "k", (T, H, D), dtype, dev)
     if v is None:
-        v = _make(stream, (T, H, D), dtype, pool.device)
+        v = _make(stream, (T, H, D), dtype, pool.device) if stream is not None else torch.empty(
+            T, H, D, dtype=dtype, device=pool.device)
         va = v.data_ptr()
     else:
         va = _ptr(v, "v", (T, H, D), dtype, dev)
@@ -835,21 +837,25 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
     pa, pages, H_kv, page_size = _pool(pool, D, dev)
     ta, B, M = _table(page_table, dev)
     if o is None:
-        o = _make(stream, shape, dtype, q.device)
+        o = _make(stream, shape, dtype, q.device) if stream is not None else torch.empty(
+            shape, dtype=dtype, device=q.device)
         oa = o.data_ptr()
     else:
         oa = _ptr(o, "o", shape, dtype, dev)
     if lse is None:
-        lse = _make(stream, (T, H), F32, q.device)
+        lse = _make(stream, (T, H), F32, q.device) if stream is not None else torch.empty(
+            T, H, dtype=F32, device=q.device)
         la = lse.data_ptr()
     else:
         la = _ptr(lse, "lse", (T, H), F32, dev)
     if workspace is None:
         workspace = _make(stream, (kv4_workspace_bytes(),), _U8, q.device, zero=True, result=False)
     (wb,), _ = _first(workspace, "workspace", 1)
+    if (max_q | window) >> 31:
+        max_q, window = _int(max_q), _int(window)
     status = lib().kda_kv4_attention(
-        dt, B, T, _int(max_q), H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
-        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size, pa, pages, _int(window),
+        dt, B, T, max_q, H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size, pa, pages, window,
         D ** -0.5 if scale is None else scale, k_scale, v_scale, oa, la,
         _ptr(workspace, "workspace", (wb,), _U8, dev), wb,
         _err_ptr(dev_err, dev), _stream_of(stream, dev))
