@@ -69,8 +69,8 @@ typedef enum {
     KDA_ERR_CUDA = -3
 } kda_status;
 
-/* KDA_DTYPE_FP16: the kda_kv4_* calls only (bf16 or fp16 there; a cache of 4
- * bits has nothing for fp32 operands). */
+/* KDA_DTYPE_FP16: the kda_kv4_* calls (bf16 or fp16 there; a cache of 4 bits has
+ * nothing for fp32 operands) and kda_add_rmsnorm (all three). */
 typedef enum { KDA_DTYPE_BF16 = 0, KDA_DTYPE_FP32 = 1, KDA_DTYPE_FP16 = 2 } kda_dtype;
 
 /* Bits OR-ed into *dev_err by kernels. */
@@ -407,6 +407,37 @@ KDA_API int kda_gated_rmsnorm(kda_dtype dt, int tokens, int H, int V, const void
                               void *stream);
 
 /*
+ * kda_add_rmsnorm -- the norm that a layer begins with: residual addition, RMS
+ * norm, and the output for 16-bit or 8-bit projections.
+ *
+ *     h   = x + residual, rounded to the dtype (h = x without a residual)
+ *     y   = w_norm * h / sqrt(mean_c h^2 + eps)              in fp32
+ * KDA_NORM_TYPE        out = y in the dtype, [tokens][C]
+ * KDA_NORM_E4M3_ROW    scales[t] = max_c |y| / 448, out = e4m3(y / scale), to
+ *                      nearest; codes are 0 where the scale is
+ * KDA_NORM_E4M3_BLOCK  the same with a scale for 128 channels,
+ *                      scales [tokens][(C + 127) / 128]; the last may have fewer
+ * Sums of squares are fp32: a row whose mean square passes its range gives 0.
+ * A NaN or an infinity makes its row's (its block's) scale and codes NaN.
+ *
+ *   dt              bf16, fp16 or fp32, of x, residual, w_norm, sum and out
+ *   C               channels, a multiple of 8, 8 to 32768
+ *   x, residual, sum device dtype, rows x_stride, residual_stride and sum_stride
+ *                   elements apart (>= C, multiples of 16 bytes; 16-byte aligned)
+ *   residual        may be NULL
+ *   sum             h, or NULL (then h is not kept; NULL without a residual).  It
+ *                   may be residual or x: each row is read before it is written
+ *   scales          device float, or NULL with KDA_NORM_TYPE
+ *   out             overlaps none of the others
+ */
+typedef enum { KDA_NORM_TYPE = 0, KDA_NORM_E4M3_ROW = 1, KDA_NORM_E4M3_BLOCK = 2 } kda_norm_out;
+
+KDA_API int kda_add_rmsnorm(kda_dtype dt, int tokens, int C, const void *x, long long x_stride,
+                            const void *residual, long long residual_stride, const void *w_norm,
+                            float eps, kda_norm_out mode, void *sum, long long sum_stride,
+                            void *out, float *scales, void *stream);
+
+/*
  * kda_decode_fused -- conv + KDA + onorm: one token per request in one kernel.
  *
  * For request b (slot s = slot_ids[b]) and head h: conv of the new raw q, k, v
@@ -493,6 +524,36 @@ KDA_API int kda_kv4_append(kda_dtype dt, int B, int total_tokens, int H_kv, int 
                            void *stream);
 
 /*
+ * kda_kv4_append_rope -- the append with the position rotation on the way.
+ *
+ * The first R channels of every head of q and k turn by the angles of the token's
+ * position p = start[b] + i, in pairs (c, c + R / 2) or, with pairs, (2 c, 2 c + 1):
+ *     x1' = x1 cos - x2 sin,   x2' = x2 cos + x1 sin
+ * products and sums rounded to fp32, the result to the dtype.  q goes to q_out;
+ * k and v are stored as kda_kv4_append stores them: the bytes are those of a
+ * rotation followed by that call.
+ *
+ *   q           device dtype [total_tokens][H_q][D], rows q_stride elements apart
+ *   rope        device float [positions][R], 16-byte aligned: R / 2 cosines, then
+ *               R / 2 sines of each position.  R is 32, 64, 96 or 128, at most D
+ *   q_out       device dtype [total_tokens][H_q][D], rows q_out_stride elements
+ *               apart; may be q (with its stride).  Strides and alignment as k's
+ * A token past the table of angles or past max_pages, or whose page is missing or
+ * out of range, is not stored (KDA_DEVERR_SEQLENS, KDA_DEVERR_PAGE_RANGE); its
+ * q_out has the rotated queries, or zeros past the angles.  Tokens of no request
+ * set KDA_DEVERR_SEQLENS and nothing is written for them.
+ */
+KDA_API int kda_kv4_append_rope(kda_dtype dt, int B, int total_tokens, int H_q, int H_kv, int D,
+                                int R, int pairs, const void *q, long long q_stride,
+                                const void *k, long long k_stride, const void *v,
+                                long long v_stride, const float *rope, int positions,
+                                const int32_t *cu_seqlens, const int32_t *start,
+                                const int32_t *page_table, int max_pages, int page_size,
+                                void *pool, int num_pages, float k_scale, float v_scale,
+                                void *q_out, long long q_out_stride, int32_t *dev_err,
+                                void *stream);
+
+/*
  * kda_kv4_gather -- read tokens back as the values they stand for.
  *
  * The inverse of kda_kv4_append: positions start[b] + i into k, v
@@ -545,6 +606,90 @@ KDA_API int kda_kv4_attention(kda_dtype dt, int B, int total_tokens, int max_q, 
                               float scale, float k_scale, float v_scale, void *o, float *lse,
                               void *workspace, size_t workspace_bytes, int32_t *dev_err,
                               void *stream);
+
+/*
+ * Sparse attention: of a long cache a token reads the pages that a cheap score
+ * picks for it and a kv head.  kda_kv4_bounds keeps a record of each page's keys
+ * beside the pool, kda_kv4_pick picks by the records, kda_kv4_attention_picked
+ * reads what was picked.  A page is the unit of all three.
+ *
+ * kda_kv4_bounds -- bounds of the keys in the pages that new tokens lie in.
+ *
+ *   bounds      device int8 [num_pages][H_kv][2 D + 16], 16-byte aligned: hi [D],
+ *               lo [D], e, 15 zeros
+ * For every page with positions start[b] .. start[b] + n - 1 of request b (n =
+ * cu_seqlens[b + 1] - cu_seqlens[b]) and every head, over the page's tokens up to
+ * the last of those, with k = code x scale (without k_scale):
+ *     e the least whole number with max |k| <= 127 x 2^e (0 where all are 0),
+ *     hi_c = ceil(max k_c / 2^e),  lo_c = floor(min k_c / 2^e)
+ * A NaN among the scales makes e = 127 and the rest 0.  Called after the append
+ * with the same arguments it keeps the records up to date; with start = 0 it makes
+ * a request's records anew (after a fork, whose copied page has none yet, for that
+ * page; after a compaction, which moves pages but not records, for all).
+ */
+KDA_API int kda_kv4_bounds(int B, int total_tokens, int H_kv, int D, const int32_t *cu_seqlens,
+                           const int32_t *start, const int32_t *page_table, int max_pages,
+                           int page_size, const void *pool, int num_pages, int8_t *bounds,
+                           int32_t *dev_err, void *stream);
+
+/*
+ * Bytes of kda_kv4_pick's workspace.  0 for sizes that no call takes.
+ */
+KDA_API size_t kda_kv4_pick_workspace_bytes(int total_tokens, int H_kv, int max_pages);
+
+/*
+ * kda_kv4_pick -- the pages that each new token attends to, by kv head.
+ *
+ * A token at position p sees own + 1 pages, own = p / page_size.  Picked are all of
+ * them, or count: the first `first`, the last `recent` (the token's own among
+ * them), and of the others those with the highest scores, the lower page of equal
+ * ones.  The score of a page bounds the sum of its products with the kv head's
+ * queries from above (for a positive scale of the attention):
+ *     up_c = sum_h max(q_hc, 0),  down_c = sum_h max(-q_hc, 0)   over its queries,
+ *     u, d = up / 2^f, down / 2^f to the nearest whole number (ties to even), f the
+ *            least >= -100 with max(up, down) <= 127 x 2^f,
+ *     score = 2^e sum_c (u_c hi_c - d_c lo_c)
+ * a whole number times a power of two: exact.  A page with e = 127 is above all
+ * others; queries with an infinity or a NaN (or sums beyond fp32) score 0.
+ *
+ *   q           as kda_kv4_attention (rotated)
+ *   count       1 .. max_pages or more; 0 <= first, 1 <= recent, first + recent <=
+ *               count
+ *   picked      device int32 [total_tokens][H_kv][count]: page ordinals of the
+ *               request's row, ascending, then -1
+ *   workspace   device, kda_kv4_pick_workspace_bytes(total_tokens, H_kv, max_pages),
+ *               16-byte aligned, not kept between calls; calls that may run at the
+ *               same time need one each
+ * Requests with inconsistent numbers are skipped as in kda_kv4_attention, a token
+ * at a negative position sees none; pages out of range come after all others
+ * (KDA_DEVERR_PAGE_RANGE).
+ */
+KDA_API int kda_kv4_pick(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv, int D,
+                         const void *q, long long q_stride, const int32_t *cu_seqlens,
+                         const int32_t *kv_lens, const int32_t *page_table, int max_pages,
+                         int page_size, const int8_t *bounds, int num_pages, int count, int first,
+                         int recent, int32_t *picked, void *workspace, size_t workspace_bytes,
+                         int32_t *dev_err, void *stream);
+
+/*
+ * kda_kv4_attention_picked -- kda_kv4_attention over the picked pages alone.
+ *
+ * A token whose own page is own reads the first c = min(count, own + 1) entries of
+ * its and the kv head's row of `picked`: entry c - 1 is own, the others are pages
+ * below it, each once (one that is named twice counts twice), in any order; it sees
+ * their positions up to its own.  An entry of -1 has no tokens; any other sets
+ * KDA_DEVERR_PAGE_RANGE and is left out.
+ *   (other arguments as kda_kv4_attention, without a window)
+ * Every token reads its pages by itself: meant for single tokens and drafts.
+ */
+KDA_API int kda_kv4_attention_picked(kda_dtype dt, int B, int total_tokens, int max_q, int H_q,
+                                     int H_kv, int D, const void *q, long long q_stride,
+                                     const int32_t *cu_seqlens, const int32_t *kv_lens,
+                                     const int32_t *page_table, int max_pages, int page_size,
+                                     const int32_t *picked, int count, const void *pool,
+                                     int num_pages, float scale, float k_scale, float v_scale,
+                                     void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                     int32_t *dev_err, void *stream);
 
 /*
  * Pages: refs, device int32 [num_pages], counts the rows that hold each page (a

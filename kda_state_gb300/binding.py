@@ -39,6 +39,9 @@ KDA_DEVERR_RANGE = 8
 KDA_DEVERR_TIMEOUT = 16
 KDA_DEVERR_PAGE_RANGE = 32
 KDA_DEVERR_PAGES = 64
+KDA_NORM_TYPE = 0
+KDA_NORM_E4M3_ROW = 1
+KDA_NORM_E4M3_BLOCK = 2
 KDA_MAX_LAYERS = 256
 K_DIM = 128
 V_DIM = 128
@@ -103,6 +106,16 @@ def lib() -> ctypes.CDLL:
                                         f, vp, vp, vp, sz, ip, vp]
         L.kda_selftest_kv4_wait.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, vp, i, vp, vp,
                                             sz, ip, i, vp]
+        L.kda_kv4_append_rope.argtypes = [i, i, i, i, i, i, i, i, vp, ll, vp, ll, vp, ll, vp, i, ip, ip, ip,
+                                          i, i, vp, i, f, f, vp, ll, ip, vp]
+        L.kda_kv4_bounds.argtypes = [i, i, i, i, ip, ip, ip, i, i, vp, i, vp, ip, vp]
+        L.kda_kv4_pick_workspace_bytes.argtypes = [i, i, i]
+        L.kda_kv4_pick_workspace_bytes.restype = sz
+        L.kda_kv4_pick.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, vp, i, i, i, i, ip, vp, sz,
+                                   ip, vp]
+        L.kda_kv4_attention_picked.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, ip, i, vp, i, f,
+                                               f, f, vp, vp, vp, sz, ip, vp]
+        L.kda_add_rmsnorm.argtypes = [i, i, i, vp, ll, vp, ll, vp, f, i, vp, ll, vp, vp, vp]
         L.kda_page_alloc.argtypes = [i, i, i, i, ip, ip, ip, ip, ip, vp]
         L.kda_page_fork.argtypes = [i, vp, sz, i, i, i, i, ip, ip, ip, ip, ip, i, vp, sz, ip, vp]
         L.kda_page_free.argtypes = [i, i, i, i, ip, ip, ip, ip, i, ip, vp]
@@ -115,7 +128,8 @@ def lib() -> ctypes.CDLL:
                    "kda_verify_store_inputs_ragged", "kda_verify_snapshot",
                    "kda_snapshot_commit", "kda_conv_prologue", "kda_gated_rmsnorm",
                    "kda_decode_fused",
-                   "kda_kv4_append", "kda_kv4_gather", "kda_kv4_attention", "kda_page_alloc",
+                   "kda_add_rmsnorm", "kda_kv4_append_rope", "kda_kv4_bounds", "kda_kv4_pick",
+                   "kda_kv4_attention_picked", "kda_kv4_append", "kda_kv4_gather", "kda_kv4_attention", "kda_page_alloc",
                    "kda_page_fork", "kda_page_free", "kda_page_compact", "kda_page_copy",
                    "kda_replay_fold", "kda_slot_copy", "kda_selftest_bounded_wait",
                    "kda_selftest_prefill_wait", "kda_selftest_kv4_wait"):
@@ -590,6 +604,74 @@ def kda_gated_rmsnorm(o, gate, w_norm, eps: float = EPS_NORM, out=None, stream=N
     return out
 
 
+_NORM_DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_FP16, torch.float32: KDA_DTYPE_FP32}
+_NORM_OUT = {"none": KDA_NORM_TYPE, "row": KDA_NORM_E4M3_ROW, "block": KDA_NORM_E4M3_BLOCK}
+NORM_BLOCK = 128      # channels of a scale
+
+
+def _norm_rows(t, name, dtype, shape, dev):
+    """[tokens, C] whose channels are dense and whose rows may be strided.  Returns the address and the
+    stride between rows, in elements."""
+    try:
+        same = t.dtype is dtype and t.shape == shape and t.get_device() == dev
+    except AttributeError:
+        same = False
+    if not same:
+        _need(t, name, shape, dtype, torch.device("cuda", dev), dense=False)
+    T, C = shape
+    stride, one = t.stride()
+    if T <= 1:
+        stride = C
+    at = t.data_ptr()
+    if one != 1 or stride < C or stride * t.element_size() % 16 != 0 or at % 16 != 0:
+        raise ValueError("%s: channels must be dense, rows start on 16-byte boundaries and not overlap" % name)
+    return at, stride
+
+
+def kda_add_rmsnorm(x, residual, weight, eps: float = EPS_NORM, scales: str = "none", residual_out=None,
+                    out=None, scales_out=None, stream=None):
+    """The norm that a layer begins with: h = x + residual (x [T, C] and residual bf16, fp16 or fp32,
+    rows may be strided; h is rounded to their dtype; residual None: h = x) and
+    y = weight * h / sqrt(mean h^2 + eps).  ``scales``: "none" for y in the dtype, "row" or "block" for
+    e4m3 codes with fp32 scales of a row [T] or of 128 channels [T, ceil(C / 128)].  Returns (out,
+    scales or None, h); ``residual_out`` takes h and may be ``residual`` itself."""
+    shape, dev = _first(x, "x", 2)
+    dtype = x.dtype
+    if dtype not in _NORM_DT:
+        raise TypeError("unsupported dtype %s (bf16, fp16 or fp32)" % dtype)
+    if scales not in _NORM_OUT:
+        raise ValueError('scales is "none", "row" or "block", not %r' % (scales,))
+    T, C = shape
+    xa, xs = _norm_rows(x, "x", dtype, shape, dev)
+    wa = _ptr(weight, "weight", (C,), dtype, dev)
+    ra = rs = ha = hs = None
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        residual_out = x
+    else:
+        ra, rs = _norm_rows(residual, "residual", dtype, shape, dev)
+        if residual_out is None:
+            residual_out = _make(stream, shape, dtype, x.device)
+        ha, hs = _norm_rows(residual_out, "residual_out", dtype, shape, dev)
+    kind = dtype if scales == "none" else torch.float8_e4m3fn
+    if out is None:
+        out = _make(stream, shape, kind, x.device)
+    oa, sa = _ptr(out, "out", shape, kind, dev), None
+    if scales == "none":
+        if scales_out is not None:
+            raise ValueError('scales_out needs scales "row" or "block"')
+    else:
+        sshape = (T,) if scales == "row" else (T, (C + NORM_BLOCK - 1) // NORM_BLOCK)
+        if scales_out is None:
+            scales_out = _make(stream, sshape, F32, x.device)
+        sa = _ptr(scales_out, "scales_out", sshape, F32, dev)
+    status = lib().kda_add_rmsnorm(_NORM_DT[dtype], T, C, xa, xs, ra, rs or 0, wa, eps, _NORM_OUT[scales],
+                                   ha, hs or 0, oa, sa, _stream_of(stream, dev))
+    _check("kda_add_rmsnorm", status)
+    return out, scales_out, residual_out
+
+
 def kda_decode_fused(q_raw, k_raw, v_raw, gk, b_raw, conv_w, conv_state, gate, w_norm, slot_ids,
                      state_pool, out=None, scale: float = 1.0, eps_l2: float = EPS_L2,
                      eps_norm: float = EPS_NORM, dev_err=None, stream=None):
@@ -860,6 +942,137 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
         _ptr(workspace, "workspace", (wb,), _U8, dev), wb,
         _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_kv4_attention", status)
+    return o, lse
+
+
+def make_rope_table(positions: int, R: int, base: float = 10000.0, device="cuda"):
+    """The angles that ``kda_kv4_append_rope`` turns by: fp32 [positions, R], R / 2 cosines and R / 2 sines of
+    p base^(-2 i / R) each, computed in 64 bits."""
+    turns = float(base) ** (-torch.arange(0, R, 2, dtype=torch.float64, device=device) / R)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * turns
+    return torch.cat([angle.cos(), angle.sin()], -1).float()
+
+
+def kda_kv4_append_rope(q, k, v, rope, cu_seqlens, start, page_table, pool, pairs: bool = False,
+                        k_scale: float = 1.0, v_scale: float = 1.0, q_out=None, dev_err=None, stream=None):
+    """``kda_kv4_append`` of k, v [T, H_kv, D] with the position rotation on the way: the first R channels of
+    each head of q [T, H_q, D] and k turn by their token's row of ``rope`` (fp32 [positions, R]:
+    ``make_rope_table``), as pairs (c, c + R / 2) or, with ``pairs``, (2 c, 2 c + 1).  q, k and v may be views
+    of a fused projection's output.  Returns the rotated q; ``q_out`` takes it and may be q itself."""
+    shape, dev = _first(q, "q", 3)
+    dtype = q.dtype
+    dt = _kv_dt(dtype)
+    T, Hq, D = shape
+    kshape, _ = _first(k, "k", 3)
+    H = kshape[1]
+    qa, qs = _rows(q, "q", dtype, shape, dev)
+    ka, ks = _rows(k, "k", dtype, (T, H, D), dev)
+    va, vs = _rows(v, "v", dtype, (T, H, D), dev)
+    (positions, R), _ = _first(rope, "rope", 2)
+    pa, pages, Hp, page_size = _pool(pool, D, dev)
+    if Hp != H:
+        raise ValueError("pool has %d heads, k has %d" % (Hp, H))
+    ta, B, M = _table(page_table, dev)
+    if q_out is None:
+        q_out = _make(stream, shape, dtype, q.device)
+    oa, os_ = _rows(q_out, "q_out", dtype, shape, dev)
+    status = lib().kda_kv4_append_rope(
+        dt, B, T, Hq, H, D, R, 1 if pairs else 0, qa, qs, ka, ks, va, vs,
+        _ptr(rope, "rope", (positions, R), F32, dev), positions,
+        _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev), _ptr(start, "start", (B,), I32, dev), ta, M,
+        page_size, pa, pages, k_scale, v_scale, oa, os_, _err_ptr(dev_err, dev), _stream_of(stream, dev))
+    _check("kda_kv4_append_rope", status)
+    return q_out
+
+
+def kv4_bounds_bytes(D: int = K_DIM) -> int:
+    """Bytes of one page and head's record of bounds."""
+    return 2 * int(D) + 16
+
+
+def make_kv4_bounds(num_pages: int, H_kv: int, D: int = K_DIM, device="cuda"):
+    """One layer's records of its pages' keys, int8 [num_pages, H_kv, 2 D + 16]."""
+    return torch.zeros(num_pages, H_kv, kv4_bounds_bytes(D), dtype=torch.int8, device=device)
+
+
+def kda_kv4_bounds(cu_seqlens, start, total_tokens: int, page_table, pool, bounds, dev_err=None, stream=None):
+    """Bring the records of the pages up to date that hold positions start[b] .. of each request's new tokens
+    (cu_seqlens int32 [B + 1]), after those were appended.  ``bounds``: ``make_kv4_bounds()``, in place."""
+    shape, dev = _first(pool, "pool", 4)
+    D = shape[3] // 18
+    pa, pages, H, page_size = _pool(pool, D, dev)
+    ta, B, M = _table(page_table, dev)
+    status = lib().kda_kv4_bounds(
+        B, _int(int(total_tokens)), H, D, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(start, "start", (B,), I32, dev), ta, M, page_size, pa, pages,
+        _ptr(bounds, "bounds", (pages, H, 2 * D + 16), torch.int8, dev), _err_ptr(dev_err, dev),
+        _stream_of(stream, dev))
+    _check("kda_kv4_bounds", status)
+
+
+def kv4_pick_workspace_bytes(total_tokens: int, H_kv: int, max_pages: int) -> int:
+    return int(lib().kda_kv4_pick_workspace_bytes(_int(total_tokens), _int(H_kv), _int(max_pages)))
+
+
+def kda_kv4_pick(q, cu_seqlens, max_q: int, kv_lens, page_table, bounds, page_size: int, count: int,
+                 first: int = 1, recent: int = 1, picked=None, workspace=None, dev_err=None, stream=None):
+    """The pages that each new token attends to, by kv head: ``count`` of those up to its own, the ``first`` and
+    the ``recent`` ones (its own among them) and of the others those whose score is highest, or all of them where
+    they are no more.  q [T, H_q, D], as it is attended with; cu_seqlens, max_q and kv_lens as in
+    ``kda_kv4_attention``; ``bounds`` from ``kda_kv4_bounds``.  Returns int32 [T, H_kv, count]: numbers of pages in
+    the request's row, ascending, then -1.  ``workspace``: uint8, ``kv4_pick_workspace_bytes(T, H_kv, max_pages)`` at
+    least, kept by the caller (one for each stream); a call without one makes its own."""
+    shape, dev = _first(q, "q", 3)
+    dtype = q.dtype
+    dt = _kv_dt(dtype)
+    T, Hq, D = shape
+    qa, qs = _rows(q, "q", dtype, shape, dev)
+    (pages, H, width), _ = _first(bounds, "bounds", 3)
+    ba = _ptr(bounds, "bounds", (pages, H, 2 * D + 16), torch.int8, dev)
+    ta, B, M = _table(page_table, dev)
+    if picked is None:
+        picked = _make(stream, (T, H, count), I32, q.device)
+    if workspace is None:
+        workspace = _make(stream, (kv4_pick_workspace_bytes(T, H, M),), _U8, q.device, result=False)
+    (wb,), _ = _first(workspace, "workspace", 1)
+    status = lib().kda_kv4_pick(
+        dt, B, T, _int(max_q), Hq, H, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, _int(page_size), ba, pages, count, _int(first), _int(recent),
+        _ptr(picked, "picked", (T, H, count), I32, dev), _ptr(workspace, "workspace", (wb,), _U8, dev), wb,
+        _err_ptr(dev_err, dev), _stream_of(stream, dev))
+    _check("kda_kv4_pick", status)
+    return picked
+
+
+def kda_kv4_attention_picked(q, cu_seqlens, max_q: int, kv_lens, page_table, picked, pool, scale=None,
+                             k_scale: float = 1.0, v_scale: float = 1.0, o=None, lse=None, workspace=None,
+                             dev_err=None, stream=None):
+    """``kda_kv4_attention`` over the pages that ``picked`` (int32 [T, H_kv, count], of ``kda_kv4_pick``) names for
+    each token and kv head.  Returns (o, lse)."""
+    shape, dev = _first(q, "q", 3)
+    dtype = q.dtype
+    dt = _kv_dt(dtype)
+    T, H, D = shape
+    qa, qs = _rows(q, "q", dtype, shape, dev)
+    pa, pages, H_kv, page_size = _pool(pool, D, dev)
+    ta, B, M = _table(page_table, dev)
+    pshape, _ = _first(picked, "picked", 3)
+    count = pshape[2]
+    if o is None:
+        o = _make(stream, shape, dtype, q.device)
+    if lse is None:
+        lse = _make(stream, (T, H), F32, q.device)
+    if workspace is None:
+        workspace = _make(stream, (kv4_workspace_bytes(),), _U8, q.device, zero=True, result=False)
+    (wb,), _ = _first(workspace, "workspace", 1)
+    status = lib().kda_kv4_attention_picked(
+        dt, B, T, _int(max_q), H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size,
+        _ptr(picked, "picked", (T, H_kv, count), I32, dev), count, pa, pages,
+        D ** -0.5 if scale is None else scale, k_scale, v_scale, _ptr(o, "o", shape, dtype, dev),
+        _ptr(lse, "lse", (T, H), F32, dev), _ptr(workspace, "workspace", (wb,), _U8, dev), wb,
+        _err_ptr(dev_err, dev), _stream_of(stream, dev))
+    _check("kda_kv4_attention_picked", status)
     return o, lse
 
 

@@ -333,6 +333,27 @@ KDA_API int kda_gated_rmsnorm(kda_dtype dt, int tokens, int H, int V, const void
     return from_cuda(kda::launch_gated_rmsnorm(a, (cudaStream_t)stream));
 }
 
+KDA_API int kda_add_rmsnorm(kda_dtype dt, int tokens, int C, const void *x, long long x_stride,
+                            const void *residual, long long residual_stride, const void *w_norm,
+                            float eps, kda_norm_out mode, void *sum, long long sum_stride,
+                            void *out, float *scales, void *stream) {
+    if (!dtype_ok(dt) && dt != KDA_DTYPE_FP16) return KDA_ERR_UNSUPPORTED;
+    if (mode != KDA_NORM_TYPE && mode != KDA_NORM_E4M3_ROW && mode != KDA_NORM_E4M3_BLOCK) return KDA_ERR_UNSUPPORTED;
+    if (tokens < 0 || C < 8 || C % 8 != 0 || C > 32768 || !(eps >= 0.f) || !isfinite(eps)) return KDA_ERR_INVALID_ARG;
+    if (tokens == 0) return KDA_OK;
+    if (!x || !w_norm || !out || (mode != KDA_NORM_TYPE && !scales) || (sum && !residual)) return KDA_ERR_INVALID_ARG;
+    const long long vec = dt == KDA_DTYPE_FP32 ? 4 : 8;
+    auto rows_ok = [&](const void *p, long long stride) { return aligned16(p) && stride >= C && stride % vec == 0; };
+    if (!rows_ok(x, x_stride) || (residual && !rows_ok(residual, residual_stride)) || (sum && !rows_ok(sum, sum_stride)) ||
+        !aligned16(w_norm) || !aligned16(out))
+        return KDA_ERR_INVALID_ARG;
+    kda::AddNormArgs a;
+    a.dt = dt; a.tokens = tokens; a.C = C; a.mode = mode; a.x = x; a.residual = residual; a.w_norm = w_norm;
+    a.x_stride = x_stride; a.residual_stride = residual_stride; a.sum_stride = sum_stride; a.eps = eps;
+    a.sum = sum; a.out = out; a.scales = scales;
+    return from_cuda(kda::launch_add_rmsnorm(a, (cudaStream_t)stream));
+}
+
 KDA_API int kda_decode_fused(kda_dtype dt, int B, int H, int K, int V, const void *q_raw,
                              const void *k_raw, const void *v_raw, long long raw_stride,
                              const void *gk, const void *b_raw, const void *conv_w,

@@ -74,7 +74,7 @@ int attention(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_k
               long long q_stride, const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
               int max_pages, int page_size, const void *pool, int num_pages, int window, float scale, float k_scale,
               float v_scale, void *o, float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_err,
-              uint64_t wait_ns, int starve, void *stream) {
+              uint64_t wait_ns, int starve, void *stream, const int32_t *picked = nullptr, int count = 0) {
     if (!dtype_ok(dt) || (D != 64 && D != 128)) return KDA_ERR_UNSUPPORTED;
     const int shift = page_shift_of(page_size);
     if (B < 0 || total_tokens < 0 || max_q < 0 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || max_pages < 1 ||
@@ -100,6 +100,8 @@ int attention(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_k
     a.scale_k = (float)((double)scale * k_scale * 1.4426950408889634); a.v_scale = v_scale;
     a.o = o; a.lse = lse; a.ws = (uint8_t *)workspace; a.err = dev_err;
     a.wait_ns = wait_ns; a.starve = starve;
+    a.picked = picked; a.count = count;
+    if (picked) return from_cuda(kda::launch_kv4_attention_picked(a, (cudaStream_t)stream));
     return from_cuda(kda::launch_kv4_attention(a, (cudaStream_t)stream));
 }
 
@@ -122,6 +124,103 @@ KDA_API int kda_kv4_append(kda_dtype dt, int B, int total_tokens, int H_kv, int 
         return KDA_ERR_INVALID_ARG;
     a.k = k; a.v = v; a.k_stride = k_stride; a.v_stride = v_stride;
     return from_cuda(kda::launch_kv4_cache(a, true, (cudaStream_t)stream));
+}
+
+KDA_API int kda_kv4_append_rope(kda_dtype dt, int B, int total_tokens, int H_q, int H_kv, int D,
+                                int R, int pairs, const void *q, long long q_stride,
+                                const void *k, long long k_stride, const void *v,
+                                long long v_stride, const float *rope, int positions,
+                                const int32_t *cu_seqlens, const int32_t *start,
+                                const int32_t *page_table, int max_pages, int page_size,
+                                void *pool, int num_pages, float k_scale, float v_scale,
+                                void *q_out, long long q_out_stride, int32_t *dev_err,
+                                void *stream) {
+    kda::KvCacheArgs c;
+    const int st = fill_cache_args(c, dt, B, total_tokens, H_kv, D, cu_seqlens, start, page_table, max_pages,
+                                   page_size, pool, num_pages, k_scale, v_scale, dev_err);
+    if (st != KDA_OK) return st;
+    if (R < 32 || R > D || R % 32 != 0 || H_q < 1 || positions < 1) return KDA_ERR_INVALID_ARG;
+    const long long heads = (long long)H_q + 2LL * H_kv;
+    if (heads * D > 0x7fffffffLL || heads * total_tokens > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
+    if (total_tokens == 0) return KDA_OK;
+    if (!q || !k || !v || !rope || !q_out || !aligned16(rope) || !row_stride_ok(q, q_stride, (long long)H_q * D) ||
+        !row_stride_ok(k, k_stride, (long long)H_kv * D) || !row_stride_ok(v, v_stride, (long long)H_kv * D) ||
+        !row_stride_ok(q_out, q_out_stride, (long long)H_q * D) || (q == q_out && q_stride != q_out_stride))
+        return KDA_ERR_INVALID_ARG;
+    kda::KvRopeArgs a;
+    memset(&a, 0, sizeof(a));
+    a.dt = dt; a.B = B; a.T = total_tokens; a.Hq = H_q; a.Hkv = H_kv; a.D = D; a.max_pages = max_pages;
+    a.page_shift = c.page_shift; a.num_pages = num_pages; a.R = R; a.positions = positions; a.pairs = pairs != 0;
+    a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.qo_stride = q_out_stride; a.rope = rope; a.cu = cu_seqlens; a.start = start; a.page_table = page_table;
+    a.pool = c.pool; a.q_out = q_out; a.k_inv = c.k_inv; a.v_inv = c.v_inv; a.err = dev_err;
+    return from_cuda(kda::launch_kv4_rope(a, (cudaStream_t)stream));
+}
+
+KDA_API int kda_kv4_bounds(int B, int total_tokens, int H_kv, int D, const int32_t *cu_seqlens,
+                           const int32_t *start, const int32_t *page_table, int max_pages,
+                           int page_size, const void *pool, int num_pages, int8_t *bounds,
+                           int32_t *dev_err, void *stream) {
+    kda::KvCacheArgs c;
+    const int st = fill_cache_args(c, KDA_DTYPE_BF16, B, total_tokens, H_kv, D, cu_seqlens, start, page_table, max_pages,
+                                   page_size, pool, num_pages, 1.f, 1.f, dev_err);
+    if (st != KDA_OK || total_tokens == 0) return st;
+    if (!bounds || !aligned16(bounds)) return KDA_ERR_INVALID_ARG;
+    kda::KvBoundsArgs a;
+    memset(&a, 0, sizeof(a));
+    a.B = B; a.T = total_tokens; a.H = H_kv; a.D = D; a.max_pages = max_pages; a.page_shift = c.page_shift;
+    a.num_pages = num_pages; a.cu = cu_seqlens; a.start = start; a.page_table = page_table; a.pool = c.pool;
+    a.bounds = bounds; a.err = dev_err;
+    return from_cuda(kda::launch_kv4_bounds(a, (cudaStream_t)stream));
+}
+
+KDA_API size_t kda_kv4_pick_workspace_bytes(int total_tokens, int H_kv, int max_pages) {
+    if (total_tokens < 0 || H_kv < 1 || max_pages < 1 || (long long)total_tokens * H_kv > 0x7fffffffLL) return 0;
+    return 16 + ((size_t)total_tokens * H_kv * max_pages * 4 + 15) / 16 * 16;
+}
+
+KDA_API int kda_kv4_pick(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv, int D,
+                         const void *q, long long q_stride, const int32_t *cu_seqlens,
+                         const int32_t *kv_lens, const int32_t *page_table, int max_pages,
+                         int page_size, const int8_t *bounds, int num_pages, int count, int first,
+                         int recent, int32_t *picked, void *workspace, size_t workspace_bytes,
+                         int32_t *dev_err, void *stream) {
+    if (!dtype_ok(dt) || (D != 64 && D != 128)) return KDA_ERR_UNSUPPORTED;
+    const int shift = page_shift_of(page_size);
+    if (B < 0 || total_tokens < 0 || max_q < 0 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || max_pages < 1 ||
+        num_pages < 1 || shift < 0 || (B == 0 && total_tokens > 0) || count < 1 || first < 0 || recent < 1 ||
+        (long long)first + recent > count)
+        return KDA_ERR_INVALID_ARG;
+    if ((long long)total_tokens * H_q > 0x7fffffffLL || (long long)H_q * D > 0x7fffffffLL ||
+        ((long long)max_pages << shift) > 0x40000000LL)
+        return KDA_ERR_INVALID_ARG;
+    if (total_tokens == 0 || max_q == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (!q || !cu_seqlens || !kv_lens || !page_table || !bounds || !picked || !workspace) return KDA_ERR_INVALID_ARG;
+    if (!row_stride_ok(q, q_stride, (long long)H_q * D) || !aligned16(bounds) || !aligned16(workspace) ||
+        workspace_bytes < kda_kv4_pick_workspace_bytes(total_tokens, H_kv, max_pages))
+        return KDA_ERR_INVALID_ARG;
+    kda::KvPickArgs a;
+    memset(&a, 0, sizeof(a));
+    a.dt = dt; a.B = B; a.T = total_tokens; a.max_q = max_q < total_tokens ? max_q : total_tokens;
+    a.Hq = H_q; a.Hkv = H_kv; a.D = D; a.max_pages = max_pages; a.page_shift = shift; a.num_pages = num_pages; a.count = count; a.first = first;
+    a.recent = recent; a.q = q; a.q_stride = q_stride; a.cu = cu_seqlens; a.kv_lens = kv_lens;
+    a.page_table = page_table; a.bounds = bounds; a.picked = picked; a.keys = (uint32_t *)workspace;
+    a.key_stride = max_pages; a.err = dev_err;
+    return from_cuda(kda::launch_kv4_pick(a, (cudaStream_t)stream));
+}
+
+KDA_API int kda_kv4_attention_picked(kda_dtype dt, int B, int total_tokens, int max_q, int H_q,
+                                     int H_kv, int D, const void *q, long long q_stride,
+                                     const int32_t *cu_seqlens, const int32_t *kv_lens,
+                                     const int32_t *page_table, int max_pages, int page_size,
+                                     const int32_t *picked, int count, const void *pool,
+                                     int num_pages, float scale, float k_scale, float v_scale,
+                                     void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                     int32_t *dev_err, void *stream) {
+    if (count < 1 || (!picked && total_tokens > 0)) return KDA_ERR_INVALID_ARG;
+    return attention(dt, B, total_tokens, max_q, H_q, H_kv, D, q, q_stride, cu_seqlens, kv_lens, page_table, max_pages,
+                     page_size, pool, num_pages, 0, scale, k_scale, v_scale, o, lse, workspace, workspace_bytes,
+                     dev_err, KDA_KV4_WAIT_NS, 0, stream, picked, count);
 }
 
 KDA_API int kda_kv4_gather(kda_dtype dt, int B, int total_tokens, int H_kv, int D, void *k,

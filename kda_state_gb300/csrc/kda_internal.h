@@ -162,8 +162,58 @@ struct KvAttentionArgs {
     float *lse;
     uint8_t *ws;
     int32_t *err;
+    const int32_t *picked;         // [T][Hkv][count] of a row's pages, or NULL: all of them
+    int count;
     uint64_t wait_ns;              // limit of the kernels' waits
     int starve;                    // self-test: the first codes never arrive
+};
+
+// Append with rotation: KvCacheArgs' sizes, q beside k and v, and the angles' table.
+struct KvRopeArgs {
+    int dt, B, T, Hq, Hkv, D, max_pages, page_shift, num_pages, R, positions, pairs;
+    int groups;                    // of a token's heads, a thread each (set by the launch)
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride, qo_stride;
+    const float *rope;             // [positions][R]: R / 2 cosines, R / 2 sines
+    const int32_t *cu, *start, *page_table;
+    uint8_t *pool;
+    void *q_out;
+    float k_inv, v_inv;
+    int32_t *err;
+};
+
+// The bounds of the pages that new tokens lie in.
+struct KvBoundsArgs {
+    int B, T, H, D, max_pages, page_shift, num_pages;
+    int slice;                     // tokens a warp looks at (set by the launch)
+    const int32_t *cu, *start, *page_table;
+    const uint8_t *pool;
+    int8_t *bounds;
+    int32_t *err;
+};
+
+// The pages that each token attends to.
+struct KvPickArgs {
+    int dt, B, T, max_q, Hq, Hkv, D, max_pages, page_shift, num_pages, count, first, recent;
+    int blocks, chunks;            // of tokens a request, of pages (set by the launch)
+    const void *q;
+    long long q_stride;
+    const int32_t *cu, *kv_lens, *page_table;
+    const int8_t *bounds;
+    int32_t *picked;
+    uint32_t *keys;                // [T][Hkv][key_stride]
+    long long key_stride;
+    int32_t *err;
+};
+
+// out = (x + residual) normed, in dtype or in e4m3 with scales.
+struct AddNormArgs {
+    int dt, tokens, C, mode;
+    const void *x, *residual, *w_norm;
+    long long x_stride, residual_stride, sum_stride;
+    float eps;
+    void *sum, *out;
+    float *scales;
 };
 
 // The page table's state: refs [num_pages], page_table [B][max_pages], lens [B].
@@ -187,6 +237,12 @@ struct PageCopyParams {
 
 cudaError_t launch_kv4_cache(const KvCacheArgs &a, bool append, cudaStream_t s);
 cudaError_t launch_kv4_attention(const KvAttentionArgs &a, cudaStream_t s);
+// The same with the rows' picked pages alone.
+cudaError_t launch_kv4_attention_picked(const KvAttentionArgs &a, cudaStream_t s);
+cudaError_t launch_kv4_rope(const KvRopeArgs &a, cudaStream_t s);
+cudaError_t launch_kv4_bounds(KvBoundsArgs a, cudaStream_t s);
+cudaError_t launch_kv4_pick(const KvPickArgs &a, cudaStream_t s);
+cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t s);
 cudaError_t launch_page_alloc(const PageArgs &a, const int32_t *grow, cudaStream_t s);
 cudaError_t launch_page_fork(const PageArgs &a, const int32_t *src, const int32_t *dst, int n, PageCopyParams p,
                              int32_t *ws, cudaStream_t s);

@@ -34,7 +34,18 @@ cudaError_t launch(const KvAttentionArgs &a, cudaStream_t s) {
     return wide ? kv4::launch_tile_attention<D, 2, T>(a, s) : kv4::launch_tile_attention<D, 1, T>(a, s);
 }
 
+// A token's rows of one kv head, 8 or 16 at a time.
+template <int D, typename T>
+cudaError_t launch_picked(const KvAttentionArgs &a, cudaStream_t s) {
+    return a.Hq / a.Hkv <= 8 ? kv4::launch_decode_attention<D, 1, T, true>(a, s) : kv4::launch_decode_attention<D, 2, T, true>(a, s);
+}
+
 }  // namespace
+
+cudaError_t launch_kv4_attention_picked(const KvAttentionArgs &a, cudaStream_t s) {
+    if (a.dt == KDA_DTYPE_BF16) return a.D == 128 ? launch_picked<128, __nv_bfloat16>(a, s) : launch_picked<64, __nv_bfloat16>(a, s);
+    return a.D == 128 ? launch_picked<128, __half>(a, s) : launch_picked<64, __half>(a, s);
+}
 
 cudaError_t launch_kv4_attention(const KvAttentionArgs &a, cudaStream_t s) {
     if (a.dt == KDA_DTYPE_BF16) return a.D == 128 ? launch<128, __nv_bfloat16>(a, s) : launch<64, __nv_bfloat16>(a, s);

@@ -31,6 +31,11 @@
 // A warp's tokens come through a ring of its own, filled by bulk copies (one
 // contiguous block of 18 D bytes for 16 tokens); the next unit's are asked for
 // before the last one's result leaves.
+//
+// With PICKED each token is a request of its own, whose cache is the list of pages that was picked for it and a kv head:
+// position j of it is token j % P of the page in the list's place j / P.  The last place is the token's own page, so that
+// the list's length and what the token sees of it follow from its position alone, whatever the head; an entry of -1 is a
+// page without tokens.
 #pragma once
 
 #include <atomic>
@@ -172,7 +177,42 @@ __device__ __forceinline__ uint32_t pack_of<__half>(float a, float b) {
 // What one request asks for; chunks = 0 where it asks for nothing or is malformed.
 struct Request {
     int q0, n, len, first_chunk, chunks, row_blocks;
+    int row, own;                          // PICKED: the request that token q0 is of, and the page that it lies in
 };
+// The request that token t is of, or -1; a thread's work, which single tokens and drafts of one number make short.
+__device__ __forceinline__ int request_of_token(const KvAttentionArgs &a, int t) {
+    int b = (int)((long long)t * a.B / a.T);
+    if (a.cu[b] <= t && t < a.cu[b + 1]) return b;
+    int lo = 0, hi = a.B;                  // the first b with cu[b + 1] > t
+    while (lo < hi) {
+        b = lo + (hi - lo) / 2;
+        if (a.cu[b + 1] > t) hi = b;
+        else lo = b + 1;
+    }
+    return lo < a.B && a.cu[lo] <= t ? lo : -1;
+}
+// Token t and the pages picked for it, as a request.
+__device__ __forceinline__ Request request_of_picked(const KvAttentionArgs &a, int t, int rows, int chunk, bool tell) {
+    Request r;
+    r.q0 = t;
+    r.n = r.len = r.first_chunk = r.chunks = r.row_blocks = r.own = 0;
+    r.row = request_of_token(a, t);
+    if (r.row < 0) return r;
+    const int q0 = a.cu[r.row], n = a.cu[r.row + 1] - q0, len = a.kv_lens[r.row];
+    if (q0 < 0 || n > a.max_q || (long long)q0 + n > a.T || len < 0 || (long long)len > ((long long)a.max_pages << a.page_shift)) {
+        if (tell) report(a.err, DEVERR_SEQLENS);
+        return r;
+    }
+    const int pos = len - n + (t - q0);
+    r.n = 1;
+    if (pos >= 0) {
+        r.own = pos >> a.page_shift;
+        r.len = (min(a.count, r.own + 1) - 1 << a.page_shift) + (pos & ((1 << a.page_shift) - 1)) + 1;
+    }
+    r.chunks = max(1, (r.len + chunk - 1) / chunk);
+    r.row_blocks = (a.Hq / a.Hkv + rows - 1) / rows;
+    return r;
+}
 __device__ __forceinline__ Request request_of(const KvAttentionArgs &a, int b, int rows, int chunk, bool tell) {
     Request r;
     r.q0 = a.cu[b];
@@ -198,7 +238,7 @@ __device__ __forceinline__ long long divide(long long x, int y) {
     return x >> 32 == 0 ? (long long)((unsigned)x / (unsigned)y) : x / y;
 }
 
-template <int D, int NT, typename T>
+template <int D, int NT, typename T, bool PICKED>
 __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_kernel(const KvAttentionArgs a) {
     using L = KvTile<D>;
     using S = DecodeShape<D, NT>;
@@ -213,6 +253,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     WarpPieces *const pieces = reinterpret_cast<WarpPieces *>(bars + WARPS * S::STAGES * 8 + 16);
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int G = a.Hq / a.Hkv;
+    const int requests = PICKED ? a.T : a.B;
+    auto request = [&](int i, bool tell) {
+        if constexpr (PICKED) return request_of_picked(a, i, S::ROWS, CHUNK, tell);
+        else return request_of(a, i, S::ROWS, CHUNK, tell);
+    };
 
     // ---- the work's total and this CTA's range -------------------------------------------------
     long long begin, end, per, base;       // base: where request b's work begins
@@ -223,12 +268,12 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         __shared__ long long found_s;
         __shared__ int found_b;
         __shared__ Request found_rq;
-        const int share = (a.B + THREADS - 1) / THREADS;
+        const int share = (requests + THREADS - 1) / THREADS;
         long long mine = 0;
         for (int i = 0; i < share; ++i) {
             const int bb = tid * share + i;
-            if (bb >= a.B) break;
-            const Request q = request_of(a, bb, S::ROWS, CHUNK, blockIdx.x == 0);
+            if (bb >= requests) break;
+            const Request q = request(bb, blockIdx.x == 0);
             mine += (long long)q.chunks * q.row_blocks * a.Hkv;
         }
         long long in = mine;
@@ -258,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         if (begin >= before && begin < before + mine) {
             for (int i = 0; i < share; ++i) {
                 const int bb = tid * share + i;
-                const Request q = request_of(a, bb, S::ROWS, CHUNK, false);
+                const Request q = request(bb, false);
                 const long long here = (long long)q.chunks * q.row_blocks * a.Hkv;
                 if (begin < before + here) {
                     found_b = bb;
@@ -287,17 +332,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     // A unit: the rows of one (request, block of rows, kv head), and the chunks of it that are this warp's.
     struct Unit {
         long long begin, end;
-        int b, q0, n, len, h, row0, rows, c0, count;
+        int b, q0, n, len, h, row0, rows, c0, count, own;
     } u;
     auto plan = [&]() {                    // of the unit at `at`
         while (at >= base + (long long)rq.chunks * rq.row_blocks * a.Hkv) {
             base += (long long)rq.chunks * rq.row_blocks * a.Hkv;
-            rq = request_of(a, ++b, S::ROWS, CHUNK, false);
+            rq = request(++b, false);
         }
         const int index = (int)divide(at - base, rq.chunks);
         u.begin = base + (long long)index * rq.chunks;
         u.end = u.begin + rq.chunks;
-        u.b = b, u.q0 = rq.q0, u.n = rq.n, u.len = rq.len;
+        u.b = PICKED ? rq.row : b, u.q0 = rq.q0, u.n = rq.n, u.len = rq.len;
+        if constexpr (PICKED) u.own = rq.own;
         u.h = index % a.Hkv;
         u.row0 = index / a.Hkv * S::ROWS;
         u.rows = min(S::ROWS, rq.n * G - u.row0);
@@ -325,9 +371,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     int page_next = -2;                    // -2: past the end (a negative entry of the table counts as -1)
     const uint8_t *source = nullptr;
     uint32_t oks = 0, here = 0;            // tiles of the window whose page is good; of each stage, those loaded
-    auto look = [&](int k) {
+    auto look = [&](int k) -> int {
         const long long t = ((long long)(u.c0 + k) * TILES + lane) * KV_TILE;
-        return k + lane / TILES < u.count && t < u.len ? max(a.page_table[(size_t)u.b * a.max_pages + (t >> a.page_shift)], -1) : -2;
+        if constexpr (PICKED) {
+            if (k + lane / TILES >= u.count || t >= u.len) return -2;
+            const int place = (int)(t >> a.page_shift);
+            const int entry = a.picked[((size_t)u.q0 * a.Hkv + u.h) * a.count + place];
+            if (entry == -1) return -2;
+            const bool good = place == (u.len - 1) >> a.page_shift ? entry == u.own : entry >= 0 && entry < u.own;
+            return good ? max(a.page_table[(size_t)u.b * a.max_pages + entry], -1) : -1;
+        } else {
+            return k + lane / TILES < u.count && t < u.len ? max(a.page_table[(size_t)u.b * a.max_pages + (t >> a.page_shift)], -1) : -2;
+        }
     };
     auto fetch = [&](int k) {              // the unit's k-th chunk
         const int j = k % WINDOW;
@@ -822,14 +877,14 @@ inline cudaError_t allow_shared(const void *kernel, int bytes, std::atomic<uint6
     return e;
 }
 
-template <int D, int NT, typename T>
+template <int D, int NT, typename T, bool PICKED = false>
 cudaError_t launch_decode_attention(const KvAttentionArgs &a, cudaStream_t s) {
     using Sh = DecodeShape<D, NT>;
     static_assert((size_t)MAX_CTAS * (4 + 2 * Sh::PARTIAL * 4) <= KDA_KV4_WORKSPACE, "workspace");
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(decode_attention_kernel<D, NT, T>), Sh::SMEM, done);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void *>(decode_attention_kernel<D, NT, T, PICKED>), Sh::SMEM, done);
     if (e != cudaSuccess) return e;
-    decode_attention_kernel<D, NT, T><<<NT == 1 ? MAX_CTAS : MAX_CTAS / 2, THREADS, Sh::SMEM, s>>>(a);
+    decode_attention_kernel<D, NT, T, PICKED><<<NT == 1 ? MAX_CTAS : MAX_CTAS / 2, THREADS, Sh::SMEM, s>>>(a);
     return cudaGetLastError();
 }
 

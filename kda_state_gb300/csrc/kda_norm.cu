@@ -1,0 +1,183 @@
+// Residual addition and RMS norm in one pass, with the output in the type or in 8 bits.
+//
+//     h = x + residual, rounded to the type      (the new residual; h = x where there is none)
+//     y = h w / sqrt(mean h^2 + eps)
+// Output y, or e4m3 codes with scales of a row or of 128 channels: s = max|y| / 448, code = e4m3(y / s), 0 where s = 0.
+// With r = 1 / sqrt(..) the same for a row, max|y| = r max|h w| and y / s = h w (448 / max|h w|): the row's sum and its
+// maximum are taken together, with one exchange between threads, and codes do not wait for r.
+//
+// A row is one warp's or one CTA's, in registers from its one read on: bound by HBM (bf16: 4 bytes read, 3 or 4 written a
+// channel), and by the launch and two round trips for a row alone.
+#include "kda_internal.h"
+#include "kda_kv4_store.cuh"
+
+namespace kda {
+namespace {
+
+constexpr float TOP = 448.f;           // the largest e4m3
+
+template <typename T> struct Vec8;     // eight channels
+template <> struct Vec8<__nv_bfloat16> { uint4 w; };
+template <> struct Vec8<__half> { uint4 w; };
+template <> struct Vec8<float> { float4 a, b; };
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const Vec8<T> &v, float (&x)[8]) { unpack16(v.w, x, T()); }
+__device__ __forceinline__ void unpack8(const Vec8<float> &v, float (&x)[8]) {
+    x[0] = v.a.x, x[1] = v.a.y, x[2] = v.a.z, x[3] = v.a.w, x[4] = v.b.x, x[5] = v.b.y, x[6] = v.b.z, x[7] = v.b.w;
+}
+template <typename T>
+__device__ __forceinline__ void pack8(const float (&x)[8], Vec8<T> &v) {
+    v.w = make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
+}
+__device__ __forceinline__ void pack8(const float (&x)[8], Vec8<float> &v) {
+    v.a = make_float4(x[0], x[1], x[2], x[3]), v.b = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> load8(const T *p) { return *reinterpret_cast<const Vec8<T> *>(p); }
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const Vec8<T> &v) { *reinterpret_cast<Vec8<T> *>(p) = v; }
+
+// To e4m3, lo in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// What h w is multiplied by to be a code, of the scale s and the largest |h w|: 0 where the scale is 0, NaN where it is.
+__device__ __forceinline__ float per_code(float s, float top) { return s == 0.f ? 0.f : isnan(s) ? s : TOP / top; }
+
+// WARPS warps a row, N vectors of 8 channels a thread.
+template <typename T, int WARPS, int N>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) add_rmsnorm_kernel(const AddNormArgs a) {
+    constexpr int ROWS = WARPS == 1 ? 4 : 1, THREADS = 32 * WARPS;
+    const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int row = blockIdx.x * ROWS + (WARPS == 1 ? w : 0);
+    if (row >= a.tokens) return;
+    const int vectors = a.C / 8;
+    const T *const x_at = (const T *)a.x + row * a.x_stride, *const w_at = (const T *)a.w_norm;
+    const T *const r_at = (const T *)a.residual + row * a.residual_stride;
+    Vec8<T> xv[N], rv[N], wv[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = tid + i * THREADS;
+        if (c < vectors) {
+            xv[i] = load8(x_at + c * 8);
+            if (a.residual) rv[i] = load8(r_at + c * 8);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (tid + i * THREADS < vectors) wv[i] = load8(w_at + (tid + i * THREADS) * 8);
+    float sum = 0.f, top = 0.f, block_top[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = tid + i * THREADS;
+        block_top[i] = 0.f;
+        if (c < vectors) {
+            float h[8], g[8];
+            unpack8(xv[i], h);
+            if (a.residual) {
+                unpack8(rv[i], g);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) h[k] += g[k];
+                pack8(h, xv[i]);
+                if (a.sum) store8((T *)a.sum + row * a.sum_stride + c * 8, xv[i]);
+                unpack8(xv[i], h);
+            }
+            unpack8(wv[i], g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sum = fmaf(h[k], h[k], sum);
+                block_top[i] = max_nan(block_top[i], fabsf(h[k] * g[k]));
+            }
+        }
+        top = max_nan(top, block_top[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sum += __shfl_xor_sync(~0u, sum, o);
+        top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+    }
+    if constexpr (WARPS > 1) {
+        __shared__ float2 part[WARPS];
+        if (lane == 0) part[w] = make_float2(sum, top);
+        __syncthreads();
+        const float2 p = lane < WARPS ? part[lane] : make_float2(0.f, 0.f);
+        sum = p.x, top = p.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            sum += __shfl_xor_sync(~0u, sum, o);
+            top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+        }
+    }
+    const float r = rsqrtf(sum / (float)a.C + a.eps);
+    if (a.mode == KDA_NORM_TYPE) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = tid + i * THREADS;
+            if (c >= vectors) continue;
+            float h[8], g[8];
+            unpack8(xv[i], h);
+            unpack8(wv[i], g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = h[k] * r * g[k];
+            pack8(h, xv[i]);
+            store8((T *)a.out + (size_t)row * a.C + c * 8, xv[i]);
+        }
+        return;
+    }
+    float s = r * top / TOP, per = per_code(s, top);
+    if (a.mode == KDA_NORM_E4M3_ROW && tid == 0) a.scales[row] = s;
+    const int blocks = (a.C + 127) / 128;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = tid + i * THREADS;
+        if (a.mode == KDA_NORM_E4M3_BLOCK) {       // 16 neighbouring lanes hold a block
+            float t = block_top[i];
+#pragma unroll
+            for (int o = 8; o; o >>= 1) t = max_nan(t, __shfl_xor_sync(~0u, t, o));
+            s = r * t / TOP;
+            per = per_code(s, t);
+            if ((lane & 15) == 0 && c < vectors) a.scales[(size_t)row * blocks + c / 16] = s;
+        }
+        if (c >= vectors) continue;
+        float h[8], g[8];
+        unpack8(xv[i], h);
+        unpack8(wv[i], g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = h[k] * g[k] * per;
+        *reinterpret_cast<uint2 *>((uint8_t *)a.out + (size_t)row * a.C + c * 8) =
+            make_uint2(to_e4m3x2(h[0], h[1]) | to_e4m3x2(h[2], h[3]) << 16, to_e4m3x2(h[4], h[5]) | to_e4m3x2(h[6], h[7]) << 16);
+    }
+}
+
+template <typename T, int WARPS, int N>
+cudaError_t go(const AddNormArgs &a, cudaStream_t s) {
+    constexpr int ROWS = WARPS == 1 ? 4 : 1;
+    add_rmsnorm_kernel<T, WARPS, N><<<(a.tokens + ROWS - 1) / ROWS, WARPS == 1 ? 128 : 32 * WARPS, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch(const AddNormArgs &a, cudaStream_t s) {
+    const int v = a.C / 8;
+    if (v <= 32) return go<T, 1, 1>(a, s);
+    if (v <= 64) return go<T, 1, 2>(a, s);
+    if (v <= 128) return go<T, 1, 4>(a, s);
+    if (v <= 256) return go<T, 4, 2>(a, s);
+    if (v <= 512) return go<T, 4, 4>(a, s);
+    if (v <= 1024) return go<T, 8, 4>(a, s);
+    if (v <= 2048) return go<T, 16, 4>(a, s);
+    return go<T, 32, 4>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t s) {
+    if (a.dt == KDA_DTYPE_BF16) return launch<__nv_bfloat16>(a, s);
+    if (a.dt == KDA_DTYPE_FP16) return launch<__half>(a, s);
+    return launch<float>(a, s);
+}
+
+}  // namespace kda
