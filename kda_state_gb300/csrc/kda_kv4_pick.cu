@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(THREADS) score_kernel(const KvPickArgs a) {
     const int h0 = (int)(at % (unsigned)groups) * HEADS, heads = min(HEADS, a.Hkv - h0);
     at /= (unsigned)groups;
     const int b = (int)(at / (unsigned)a.blocks), i0 = (int)(at % (unsigned)a.blocks) * NT;
-    const Tokens r = tokens_of(a, b, chunk == 0 && h0 == 0 && i0 == 0);
+    const Tokens r = tokens_of(a, b, false);
     if (i0 >= r.n) return;
     const int nt = min(NT, r.n - i0), last = r.len - r.n + i0 + nt - 1;      // the last token's position
     const int pages = last < 0 ? 0 : (last >> a.page_shift) + 1;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const K
     const int t = (int)(row / (unsigned)a.Hkv);
     const int b = owner_of(a.cu, a.B, t);
     if (b < 0) return;
-    const Tokens r = tokens_of(a, b, false);
+    const Tokens r = tokens_of(a, b, true);
     if (r.n == 0) return;
     int32_t *const out = a.picked + (size_t)row * a.count;
     const int pos = r.len - r.n + (t - r.q0), pages = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
