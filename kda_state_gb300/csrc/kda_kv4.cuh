@@ -95,4 +95,22 @@ __device__ __forceinline__ int owner_of(const int32_t *cu, int B, int t) {
     return lo < B && cu[lo] <= t ? lo : -1;
 }
 
+// The owner of token t of T and what is known of it; a whole warp calls it, with its lanes' t ascending.  One request is
+// guessed, the right one where all have as many tokens (single tokens among them), and what is asked of it is asked for
+// beside the check: one round of loads, not the three or four of a search.
+struct Owner {
+    int b, q0, end, more;                  // request or -1, its first token and the one behind its last, per[b]
+};
+__device__ __forceinline__ Owner owner_with(const int32_t *cu, const int32_t *per, int B, int T, int t) {
+    Owner o;
+    o.b = min((int)((unsigned long long)(unsigned)t * (unsigned)B / (unsigned)T), B - 1);
+    o.q0 = cu[o.b], o.end = cu[o.b + 1], o.more = per[o.b];
+    if (!__all_sync(~0u, t >= T || (o.q0 <= t && t < o.end))) {
+        o.b = owner_of(cu, B, t);
+        if (o.b >= 0) o.q0 = cu[o.b], o.end = cu[o.b + 1], o.more = per[o.b];
+    }
+    if (t >= T) o.b = -1;
+    return o;
+}
+
 }  // namespace kda

@@ -66,7 +66,7 @@ __device__ __forceinline__ void bound_page(const uint8_t *tiles, int fill, int8_
     uint32_t hi[16], lo[16], nan = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) hi[i] = 0xfc00fc00u, lo[i] = 0x7c007c00u;
-#pragma unroll 2
+#pragma unroll 4
     for (int t = lane / CHUNKS; t < fill; t += ROWS) {
         const uint8_t *tile = tiles + (t >> 4) * L::BYTES;
         const uint4 w = *reinterpret_cast<const uint4 *>(tile + L::KC + (t & 15) * (D / 2) + c * 16);
@@ -129,24 +129,20 @@ __global__ void __launch_bounds__(THREADS) bounds_kernel(const KvBoundsArgs a) {
     const long long t0 = (long long)(unit / (unsigned)a.H) * a.slice;
     if (t0 >= a.T) return;
     const int t = (int)min(t0 + min(lane, a.slice - 1), (long long)a.T);
-    const int b = owner_of(a.cu, a.B, t);
+    const Owner own = owner_with(a.cu, a.start, a.B, a.T, t);
     int page = -1, fill = 0;
     if (lane < a.slice && t < a.T) {
-        if (b < 0) {
+        const int i = t - own.q0, P = 1 << a.page_shift;
+        const long long pos = (long long)own.more + i, end = (long long)own.more + (own.end - own.q0);
+        if (own.b < 0 || pos < 0 || (pos >> a.page_shift) >= a.max_pages) {
             report(a.err, DEVERR_SEQLENS);
-        } else {
-            const int i = t - a.cu[b], P = 1 << a.page_shift;
-            const long long pos = (long long)a.start[b] + i, end = (long long)a.start[b] + (a.cu[b + 1] - a.cu[b]);
-            if (pos < 0 || (pos >> a.page_shift) >= a.max_pages) {
-                report(a.err, DEVERR_SEQLENS);
-            } else if (i == 0 || (pos & (P - 1)) == 0) {
-                page = a.page_table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
-                if (page < 0 || page >= a.num_pages) {
-                    report(a.err, DEVERR_PAGE_RANGE);
-                    page = -1;
-                }
-                fill = (int)min((long long)P, end - (pos & ~(long long)(P - 1)));
+        } else if (i == 0 || (pos & (P - 1)) == 0) {
+            page = a.page_table[(size_t)own.b * a.max_pages + (pos >> a.page_shift)];
+            if (page < 0 || page >= a.num_pages) {
+                report(a.err, DEVERR_PAGE_RANGE);
+                page = -1;
             }
+            fill = (int)min((long long)P, end - (pos & ~(long long)(P - 1)));
         }
     }
     for (uint32_t todo = __ballot_sync(~0u, page >= 0); todo; todo &= todo - 1) {
@@ -161,6 +157,8 @@ __global__ void __launch_bounds__(THREADS) bounds_kernel(const KvBoundsArgs a) {
 // ---------------------------------------------------------------------------
 
 constexpr int HEADS = 8;       // kv heads that a CTA takes
+constexpr int TOKENS = 8;      // and tokens
+constexpr int MISSING = 1000;  // in place of a unit: a page out of range, whose key is 1 (below every score; 0 is no page)
 
 // The bits of a finite or infinite float as a number that orders as it does.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -172,17 +170,12 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 struct Tokens {
     int q0, n, len;
 };
-__device__ __forceinline__ Tokens tokens_of(const KvPickArgs &a, int b, bool tell) {
-    Tokens r;
-    r.q0 = a.cu[b];
-    r.n = a.cu[b + 1] - r.q0;
-    r.len = a.kv_lens[b];
+__device__ __forceinline__ void check(const KvPickArgs &a, Tokens &r, bool tell) {
     if (r.q0 < 0 || r.n < 0 || r.n > a.max_q || (long long)r.q0 + r.n > a.T || r.len < 0 ||
         (long long)r.len > ((long long)a.max_pages << a.page_shift)) {
         if (tell) report(a.err, DEVERR_SEQLENS);
         r.n = 0;
     }
-    return r;
 }
 
 template <typename T> __device__ __forceinline__ float2 halves(uint32_t w);
@@ -191,147 +184,279 @@ template <> __device__ __forceinline__ float2 halves<__nv_bfloat16>(uint32_t w) 
 }
 template <> __device__ __forceinline__ float2 halves<__half>(uint32_t w) { return f16x2_to_float2(w); }
 
-// u and -d of one token and kv head, as 2 D bytes laid out as a record is; a warp's work.
-template <int D, typename T>
-__device__ __forceinline__ void ask_of(const T *q, int G, int8_t *out) {
+// u and -d of a token and kv head; a warp's work, N of them at once so that their loads are in flight together.  q(n) is where
+// number n's queries lie; put(n, channel, x, y) gets D / 32 of each, from `channel` on.
+template <int D, int N, typename T, typename Q, typename Put>
+__device__ __forceinline__ void ask_of(const Q &q, int G, const Put &put) {
     constexpr int W = D / 64;              // words of the lane: 2 W channels
     const int lane = threadIdx.x & 31;
-    float up[2 * W], down[2 * W];
+    float up[N][2 * W], down[N][2 * W];
 #pragma unroll
-    for (int i = 0; i < 2 * W; ++i) up[i] = down[i] = 0.f;
-#pragma unroll 8
-    for (int g = 0; g < G; ++g) {
-        uint32_t w[W];
-        if constexpr (W == 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(q + g * D + lane * 4);
-            w[0] = x.x, w[W - 1] = x.y;
-        } else {
-            w[0] = *reinterpret_cast<const uint32_t *>(q + g * D + lane * 2);
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 2 * W; ++i) up[n][i] = down[n][i] = 0.f;
+    for (int g0 = 0; g0 < G; g0 += 8) {    // eight heads' loads at once
+        uint32_t w[N][8][W];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const T *const src = q(n);
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                if constexpr (W == 2) {
+                    const uint2 x = g0 + g < G ? __ldg(reinterpret_cast<const uint2 *>(src + (g0 + g) * D + lane * 4)) : make_uint2(0, 0);
+                    w[n][g][0] = x.x, w[n][g][W - 1] = x.y;
+                } else {
+                    w[n][g][0] = g0 + g < G ? __ldg(reinterpret_cast<const uint32_t *>(src + (g0 + g) * D + lane * 2)) : 0u;
+                }
+            }
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const float2 f = halves<T>(w[i]);
-            up[2 * i] = __fadd_rn(up[2 * i], max_nan(f.x, 0.f)), down[2 * i] = __fadd_rn(down[2 * i], max_nan(-f.x, 0.f));
-            up[2 * i + 1] = __fadd_rn(up[2 * i + 1], max_nan(f.y, 0.f)), down[2 * i + 1] = __fadd_rn(down[2 * i + 1], max_nan(-f.y, 0.f));
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const float2 f = halves<T>(w[n][g][i]);
+                    up[n][2 * i] = __fadd_rn(up[n][2 * i], max_nan(f.x, 0.f)), down[n][2 * i] = __fadd_rn(down[n][2 * i], max_nan(-f.x, 0.f));
+                    up[n][2 * i + 1] = __fadd_rn(up[n][2 * i + 1], max_nan(f.y, 0.f)), down[n][2 * i + 1] = __fadd_rn(down[n][2 * i + 1], max_nan(-f.y, 0.f));
+                }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * W; ++i) top = max_nan(top, max_nan(up[n][i], down[n][i]));
+        const uint32_t bits = __reduce_max_sync(~0u, __float_as_uint(top) & 0x7fffffffu);       // (a NaN is above all)
+        // nothing to go by: all pages score 0
+        const float per = bits >= 0x7f800000u || bits < 0x00800000u ? 0.f : power_of(-max(unit_of(__uint_as_float(bits)), -100));
+        int u[2 * W], d[2 * W];
+#pragma unroll
+        for (int i = 0; i < 2 * W; ++i) {
+            u[i] = per == 0.f ? 0 : __float2int_rn(up[n][i] * per);
+            d[i] = per == 0.f ? 0 : -__float2int_rn(down[n][i] * per);
         }
-    }
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2 * W; ++i) top = max_nan(top, max_nan(up[i], down[i]));
-    const uint32_t bits = __reduce_max_sync(~0u, __float_as_uint(top) & 0x7fffffffu);       // (a NaN is above all)
-    // nothing to go by: all pages score 0
-    const float per = bits >= 0x7f800000u || bits < 0x00800000u ? 0.f : power_of(-max(unit_of(__uint_as_float(bits)), -100));
-    uint32_t u = 0, d = 0;
-#pragma unroll
-    for (int i = 0; i < 2 * W; ++i) {
-        const int x = per == 0.f ? 0 : __float2int_rn(up[i] * per), y = per == 0.f ? 0 : -__float2int_rn(down[i] * per);
-        u |= ((uint32_t)x & 255u) << (8 * i), d |= ((uint32_t)y & 255u) << (8 * i);
-    }
-    if constexpr (W == 2) {
-        *reinterpret_cast<uint32_t *>(out + lane * 4) = u;
-        *reinterpret_cast<uint32_t *>(out + D + lane * 4) = d;
-    } else {
-        *reinterpret_cast<uint16_t *>(out + lane * 2) = (uint16_t)u;
-        *reinterpret_cast<uint16_t *>(out + D + lane * 2) = (uint16_t)d;
+        put(n, lane * 2 * W, u, d);
     }
 }
 
-// Scores of up to NT tokens of one request with a run of its pages, for up to HEADS kv heads.  A record is held by eight
-// lanes, 16 or 32 bytes each, so that its loads are whole lines; four pages a warp at a time.
-template <int D, int NT, typename T>
-__global__ void __launch_bounds__(THREADS) score_kernel(const KvPickArgs a) {
-    constexpr int RECORD = 2 * D + 16, LOADS = D / 64;
-    __shared__ __align__(16) int8_t ask[NT * HEADS * 2 * D];
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 7, four = lane >> 3;
-    const int groups = (a.Hkv + HEADS - 1) / HEADS, G = a.Hq / a.Hkv;
+// What a CTA scores: up to `tokens` tokens of one request, with a run of its pages, for up to HEADS kv heads.
+struct Share {
+    int b, q0, nt, h0, heads, p0, p1;      // p0 >= p1: nothing
+};
+__device__ __forceinline__ Share share_of(const KvPickArgs &a, int tokens) {
+    Share s;
+    const int groups = (a.Hkv + HEADS - 1) / HEADS;
     unsigned at = blockIdx.x;
     const int chunk = (int)(at % (unsigned)a.chunks);
     at /= (unsigned)a.chunks;
-    const int h0 = (int)(at % (unsigned)groups) * HEADS, heads = min(HEADS, a.Hkv - h0);
+    s.h0 = (int)(at % (unsigned)groups) * HEADS, s.heads = min(HEADS, a.Hkv - s.h0);
     at /= (unsigned)groups;
-    const int b = (int)(at / (unsigned)a.blocks), i0 = (int)(at % (unsigned)a.blocks) * NT;
-    const Tokens r = tokens_of(a, b, false);
-    if (i0 >= r.n) return;
-    const int nt = min(NT, r.n - i0), last = r.len - r.n + i0 + nt - 1;      // the last token's position
+    s.b = (int)(at / (unsigned)a.blocks);
+    const int i0 = (int)(at % (unsigned)a.blocks) * tokens;
+    Tokens rq{a.cu[s.b], 0, a.kv_lens[s.b]};
+    rq.n = a.cu[s.b + 1] - rq.q0;
+    check(a, rq, false);                   // (told by pick_kernel)
+    s.p0 = s.p1 = 0;
+    if (i0 >= rq.n) return s;
+    s.q0 = rq.q0 + i0, s.nt = min(tokens, rq.n - i0);
+    const int last = rq.len - rq.n + i0 + s.nt - 1;        // the last token's position
     const int pages = last < 0 ? 0 : (last >> a.page_shift) + 1;
-    if (pages <= a.count) return;          // all of them are taken
-    const int per = ((pages + a.chunks - 1) / a.chunks + 31) & ~31, p0 = chunk * per, p1 = min(pages, p0 + per);
-    if (p0 >= p1) return;
-    for (int x = w; x < nt * heads; x += THREADS / 32) {
-        const int k = x / heads, h = x % heads;
-        ask_of<D, T>((const T *)a.q + (long long)(r.q0 + i0 + k) * a.q_stride + (h0 + h) * G * D, G, ask + (k * HEADS + h) * 2 * D);
+    if (pages <= a.count) return s;        // all of them are taken
+    const int per = a.chunks * 32 >= a.max_pages ? 32 : ((pages + a.chunks - 1) / a.chunks + 31) & ~31;
+    s.p0 = chunk * per, s.p1 = min(pages, s.p0 + per);
+    return s;
+}
+// Where every chunk is 32 pages: this lane's entry of the table, asked for before it is known that the CTA has work.
+__device__ __forceinline__ int early_page(const KvPickArgs &a) {
+    const int groups = (a.Hkv + HEADS - 1) / HEADS, p = (int)(blockIdx.x % (unsigned)a.chunks) * 32 + (int)(threadIdx.x & 31);
+    const unsigned b = blockIdx.x / (unsigned)a.chunks / (unsigned)groups / (unsigned)a.blocks;
+    return a.chunks * 32 >= a.max_pages && p < a.max_pages ? a.page_table[(size_t)b * a.max_pages + p] : 0;
+}
+__device__ __forceinline__ uint32_t key_of(float sum, int unit) {
+    return unit == MISSING ? 1u : unit == UNBOUNDED ? 0xff800000u : ordered(sum * power_of(unit));
+}
+// pg, or 0 with `bad` set where it is out of range
+__device__ __forceinline__ int page_or_0(const KvPickArgs &a, int pg, bool &bad) {
+    bad = pg < 0 || pg >= a.num_pages;
+    if (bad) report(a.err, DEVERR_PAGE_RANGE);
+    return bad ? 0 : pg;
+}
+
+// Single tokens.  A record is held by eight lanes, whose loads are whole lines, and multiplied on the integer units; a warp
+// has 32 pages of a head in flight.  (An 8-bit MMA of 16 pages and 32 channels takes 64 cycles a scheduler here; the same
+// products of one token take 4 of these instructions, 8 cycles.)
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS, 2) score_one_kernel(const KvPickArgs a) {
+    constexpr int RECORD = 2 * D + 16, LOADS = D / 64;
+    __shared__ __align__(16) int8_t ask[HEADS * 2 * D];
+    asm volatile("griddepcontrol.launch_dependents;");     // (pick_kernel may come in, and waits for the end of this one)
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 7;
+    const int guess = early_page(a);
+    const Share z = share_of(a, 1);
+    if (z.p0 >= z.p1) return;
+    // the warps are dealt over the heads, and those of a head over the runs of 32 pages
+    const int parts = (THREADS / 32) / z.heads, h = w % z.heads, part = w / z.heads, stride = 32 * parts;
+    uint4 x[8][LOADS];                     // of page p + (lane & 24) + i: this lane's eighth of each 128 bytes
+    int page = 0, unit = 0, next = 0;      // page p + lane, and its unit
+    auto look = [&](int p) { return p + lane < z.p1 ? a.page_table[(size_t)z.b * a.max_pages + p + lane] : 0; };
+    auto record = [&](int pg) { return a.bounds + ((size_t)pg * a.Hkv + z.h0 + h) * RECORD; };
+    auto load = [&](int i) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(record(__shfl_sync(~0u, page, (lane & 24) + i))) + j;
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) x[i][k] = __ldg(src + 8 * k);
+    };
+    auto begin = [&](int pg) {
+        bool bad;
+        page = page_or_0(a, pg, bad);
+        unit = bad ? MISSING : __ldg(record(page) + 2 * D);
+    };
+    int p = z.p0 + 32 * part;
+    const bool works = part < parts && p < z.p1;
+    if (works) {
+        begin(a.chunks * 32 >= a.max_pages ? (p + lane < z.p1 ? guess : 0) : look(p));
+        next = look(p + stride);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(i);
+    }
+    const int G = a.Hq / a.Hkv;
+    for (int i = w; i < z.heads; i += THREADS / 32)
+        ask_of<D, 1, T>([&](int) { return (const T *)a.q + (long long)z.q0 * a.q_stride + (z.h0 + i) * G * D; }, G, [&](int, int ch, const int *u, const int *d) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) ask[i * 2 * D + ch + k] = (int8_t)u[k], ask[i * 2 * D + D + ch + k] = (int8_t)d[k];
+        });
+    __syncthreads();
+    if (!works) return;
+    uint4 y[LOADS];
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) y[k] = *(reinterpret_cast<const uint4 *>(ask + h * 2 * D) + j + 8 * k);
+    uint32_t *const keys = a.keys + ((size_t)z.q0 * a.Hkv + z.h0 + h) * a.key_stride;
+    for (; p < z.p1; p += stride) {
+        const int now = unit, later = look(p + 2 * stride);
+        const bool on = p + stride < z.p1;
+        if (on) begin(next);
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int s = 0;
+#pragma unroll
+            for (int k = 0; k < LOADS; ++k) {
+                s = __dp4a((int)x[i][k].x, (int)y[k].x, s);
+                s = __dp4a((int)x[i][k].y, (int)y[k].y, s);
+                s = __dp4a((int)x[i][k].z, (int)y[k].z, s);
+                s = __dp4a((int)x[i][k].w, (int)y[k].w, s);
+            }
+            if (on) load(i);
+            s += __shfl_xor_sync(~0u, s, 1);
+            s += __shfl_xor_sync(~0u, s, 2);
+            s += __shfl_xor_sync(~0u, s, 4);
+            if (j == i) mine = s;          // of page p + lane
+        }
+        if (p + lane < z.p1) keys[p + lane] = key_of((float)mine, now);
+        next = later;
+    }
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four signed bytes as fp16: 1024 + 128 + byte has them in its low bits.
+__device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t v = w ^ 0x80808080u, bias = 0x64806480u;
+    uint32_t l = __byte_perm(v, 0x64646464u, 0x4140), h = __byte_perm(v, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&l), *reinterpret_cast<const __half2 *>(&bias));
+    const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&h), *reinterpret_cast<const __half2 *>(&bias));
+    lo = *reinterpret_cast<const uint32_t *>(&x), hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+// Up to 8 tokens of a request.  Pages stand on the 16 rows of an fp16 MMA and tokens on its 8 columns: whole numbers up to
+// 127 are exact, and so are their sums below 2^23.  The contraction may be permuted if both operands agree, so that a
+// lane's share of a record is whole 16-byte words, four lanes beside each other.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS, 2) score_kernel(const KvPickArgs a) {
+    constexpr int RECORD = 2 * D + 16, PARTS = D / 32;     // runs of 64 bytes of a record
+    constexpr int ROW = 4 * D + 64;        // bytes of one token's asked numbers: rows that follow each other meet no bank twice
+    __shared__ __align__(16) uint8_t ask[HEADS * TOKENS * ROW];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int guess = early_page(a);
+    const Share z = share_of(a, TOKENS);
+    if (z.p0 >= z.p1) return;
+    const int parts = (THREADS / 32) / z.heads, h = w % z.heads, part = w / z.heads, stride = 32 * parts;
+    uint4 x[2][2][PARTS];                  // of pages p + 16 s + 8 k + r: this lane's quarter of each 64 bytes
+    int unit[2];                           // of page p + 16 s + (lane & 15)
+    auto look = [&](int p) { return p + lane < z.p1 ? a.page_table[(size_t)z.b * a.max_pages + p + lane] : 0; };
+    auto record = [&](int pg) { return a.bounds + ((size_t)pg * a.Hkv + z.h0 + h) * RECORD; };
+    auto load = [&](int s, int pages) {    // half of a run, of 32 looked up
+        bool bad;
+        const int pg = page_or_0(a, __shfl_sync(~0u, pages, 16 * s + (lane & 15)), bad);
+        unit[s] = bad ? MISSING : __ldg(record(pg) + 2 * D);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(record(__shfl_sync(~0u, pg, 8 * k + r))) + c;
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) x[s][k][i] = __ldg(src + 4 * i);
+        }
+    };
+    int p = z.p0 + 32 * part, pages = 0, next = 0;
+    const bool works = part < parts && p < z.p1;
+    if (works) {
+        pages = a.chunks * 32 >= a.max_pages ? (p + lane < z.p1 ? guess : 0) : look(p);
+        next = look(p + stride);
+        if constexpr (D == 64) load(0, pages), load(1, pages);
+    }
+    const int G = a.Hq / a.Hkv;
+    // the CTA's rows (head, token), two at a time; rows of no token stay what they are: no column of theirs is looked at
+    for (int i = 2 * w; i < TOKENS * z.heads; i += 2 * (THREADS / 32)) {
+        const int hh = i / TOKENS, k0 = i % TOKENS;
+        if (k0 >= z.nt) continue;
+        ask_of<D, 2, T>([&](int n) { return (const T *)a.q + (long long)(z.q0 + min(k0 + n, z.nt - 1)) * a.q_stride + (z.h0 + hh) * G * D; }, G,
+                        [&](int n, int ch, const int *u, const int *d) {
+                            uint8_t *const row = ask + (i + n) * ROW;
+                            // channel ch of a record: 64-byte run ch / 64, lane's quarter ch / 16 % 4, half of it ch / 8 % 2
+                            auto place = [&](int c) { return reinterpret_cast<__half2 *>(row + (((c >> 6) * 2 + (c >> 3 & 1)) * 4 + (c >> 4 & 3)) * 16 + (c & 7) * 2); };
+#pragma unroll
+                            for (int m = 0; m < D / 32; m += 2) {
+                                *place(ch + m) = __floats2half2_rn((float)u[m], (float)u[m + 1]);
+                                *place(D + ch + m) = __floats2half2_rn((float)d[m], (float)d[m + 1]);
+                            }
+                        });
     }
     __syncthreads();
-    // the warps are dealt over the heads, and those of a head over the runs of 32 pages
-    const int parts = (THREADS / 32) / heads, h = w % heads, part = w / heads;
-    if (part >= parts) return;
-    for (int p = p0 + 32 * part; p < p1; p += 32 * parts) {
-        int page = p + lane < p1 ? a.page_table[(size_t)b * a.max_pages + p + lane] : 0;
-        if (page < 0 || page >= a.num_pages) {
-            report(a.err, DEVERR_PAGE_RANGE);
-            page = -1;
-        }
-        uint32_t mine = 0;                 // NT == 1: the key of page p + lane
-#pragma unroll 2
-        for (int step = 0; step < 8; ++step) {
-            // pages 8 four + step: the lane that has the step's number keeps the result
-            const int local = 8 * four + step, pg = __shfl_sync(~0u, page, local);
-            const bool good = p + local < p1 && pg >= 0;
-            const int8_t *rec = a.bounds + ((size_t)max(pg, 0) * a.Hkv + h0 + h) * RECORD;
-            uint4 x[LOADS];
-            int e = 0;
+    if (!works) return;
+    if constexpr (D == 128) load(0, pages), load(1, pages);        // (registers are short before)
+    const uint4 *const y = reinterpret_cast<const uint4 *>(ask + (h * TOKENS + r) * ROW) + c;
+    for (; p < z.p1; p += stride) {
+        const int later = look(p + 2 * stride);
 #pragma unroll
-            for (int k = 0; k < LOADS; ++k) x[k] = good ? __ldg(reinterpret_cast<const uint4 *>(rec) + j + 8 * k) : make_uint4(0, 0, 0, 0);
-            if (good) e = __ldg(rec + 2 * D);
-            int sum[NT];
+        for (int s = 0; s < 2; ++s) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < NT; ++k) {
-                sum[k] = 0;
-                if (k < nt) {
-                    const uint4 *y = reinterpret_cast<const uint4 *>(ask + (k * HEADS + h) * 2 * D);
+            for (int i = 0; i < PARTS; ++i) {
+                const uint4 y0 = y[8 * i], y1 = y[8 * i + 4];
+                const uint32_t xa[4] = {x[s][0][i].x, x[s][0][i].y, x[s][0][i].z, x[s][0][i].w}, xb[4] = {x[s][1][i].x, x[s][1][i].y, x[s][1][i].z, x[s][1][i].w};
+                const uint32_t b[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
-                    for (int z = 0; z < LOADS; ++z) {
-                        const uint4 v = y[j + 8 * z];
-                        sum[k] = __dp4a((int)x[z].x, (int)v.x, sum[k]);
-                        sum[k] = __dp4a((int)x[z].y, (int)v.y, sum[k]);
-                        sum[k] = __dp4a((int)x[z].z, (int)v.z, sum[k]);
-                        sum[k] = __dp4a((int)x[z].w, (int)v.w, sum[k]);
-                    }
+                for (int n = 0; n < 4; ++n) {
+                    uint32_t a0, a1, a2, a3;
+                    s8x4_to_f16(xa[n], a0, a2);
+                    s8x4_to_f16(xb[n], a1, a3);
+                    mma_f16(d, a0, a1, a2, a3, b[2 * n], b[2 * n + 1]);
                 }
             }
-            auto key_of = [&](int s) {     // 1: below every score (a page that is not there); 0 is no page
-                return !good ? 1u : e == UNBOUNDED ? 0xff800000u : ordered((float)s * power_of(e));
-            };
-            if constexpr (NT == 1) {
-                int s = sum[0];
-                s += __shfl_xor_sync(~0u, s, 1);
-                s += __shfl_xor_sync(~0u, s, 2);
-                s += __shfl_xor_sync(~0u, s, 4);
-                if (j == step) mine = key_of(s);
-            } else {
-                // lane j is left with token j's sum
-                static_assert(NT == 8, "one token a lane");
+            const int e = unit[s];
+            if (p + stride < z.p1) load(s, next);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bool u = j & 4;
-                    const int give = u ? sum[k] : sum[k + 4], keep = u ? sum[k + 4] : sum[k];
-                    sum[k] = keep + __shfl_xor_sync(~0u, give, 4);
-                }
+            for (int k = 0; k < 2; ++k) {
+                const int of = p + 16 * s + 8 * k + r, pe = __shfl_sync(~0u, e, 8 * k + r);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const bool u = j & 2;
-                    const int give = u ? sum[k] : sum[k + 2], keep = u ? sum[k + 2] : sum[k];
-                    sum[k] = keep + __shfl_xor_sync(~0u, give, 2);
-                }
-                const bool u = j & 1;
-                const int give = u ? sum[0] : sum[1], keep = u ? sum[1] : sum[0];
-                const int s = keep + __shfl_xor_sync(~0u, give, 1);
-                if (j < nt && p + local < p1)
-                    a.keys[((size_t)(r.q0 + i0 + j) * a.Hkv + h0 + h) * a.key_stride + p + local] = key_of(s);
+                for (int n = 0; n < 2; ++n)
+                    if (2 * c + n < z.nt && of < z.p1)
+                        a.keys[((size_t)(z.q0 + 2 * c + n) * a.Hkv + z.h0 + h) * a.key_stride + of] = key_of(d[2 * k + n], pe);
             }
         }
-        if constexpr (NT == 1)
-            if (p + lane < p1) a.keys[((size_t)(r.q0 + i0) * a.Hkv + h0 + h) * a.key_stride + p + lane] = mine;
+        next = later;
     }
 }
 
@@ -339,20 +464,22 @@ __global__ void __launch_bounds__(THREADS) score_kernel(const KvPickArgs a) {
 // the best of a row's scores
 // ---------------------------------------------------------------------------
 
-// One row (token, kv head) is W warps' work, each thread's K neighbouring pages in registers (K = 0: read again at every
-// step).  The count-th best key is found by halving an interval of keys: lo has at least as many pages at or above it as
-// are wanted, hi fewer; it ends early once there are exactly as many.
+// One row (token, kv head) is W warps' work, each with 32 K neighbouring pages in its lanes' registers (K = 0: read again at
+// every step).  The count-th best key is found by narrowing an interval of keys: lo has at least as many pages at or above
+// it as are wanted, hi fewer; it ends early once there are exactly as many.  Launched beside the scores' end: what comes
+// before the wait reads nothing of theirs.
 template <int W, int K>
 __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const KvPickArgs a) {
     constexpr int ROWS = W == 1 ? THREADS / 32 : 1;
     __shared__ uint32_t box[2][32];
     const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const unsigned row = blockIdx.x * (unsigned)ROWS + (W == 1 ? w : 0);
-    if (row >= (unsigned)a.T * (unsigned)a.Hkv) return;
-    const int t = (int)(row / (unsigned)a.Hkv);
-    const int b = owner_of(a.cu, a.B, t);
-    if (b < 0) return;
-    const Tokens r = tokens_of(a, b, true);
+    const int t = (int)min(row / (unsigned)a.Hkv, (unsigned)a.T);
+    const Owner own = owner_with(a.cu, a.kv_lens, a.B, a.T, t);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (own.b < 0) return;
+    Tokens r{own.q0, own.end - own.q0, own.more};
+    check(a, r, true);
     if (r.n == 0) return;
     int32_t *const out = a.picked + (size_t)row * a.count;
     const int pos = r.len - r.n + (t - r.q0), pages = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
@@ -365,6 +492,25 @@ __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const K
     for (int i = tid; i < a.recent; i += 32 * W) out[a.count - a.recent + i] = to + i;
     if (want == 0) return;
     const uint32_t *const keys = a.keys + (size_t)row * a.key_stride;
+    const int span = K ? K : (a.max_pages + 32 * W - 1) / (32 * W);          // pages a lane, 32 apart
+    const int p0 = (W == 1 ? 0 : w * 32 * span) + lane;
+    uint32_t key[K ? K : 1];
+    auto at = [&](int i) -> uint32_t {     // 0: no candidate
+        const int p = p0 + 32 * i;
+        return p >= from && p < to ? __ldcg(keys + p) : 0u;
+    };
+    if constexpr (K > 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) key[i] = at(i);
+    }
+    auto each = [&](const auto &f) {       // f(number, key)
+        if constexpr (K > 0) {
+#pragma unroll
+            for (int i = 0; i < K; ++i) f(i, key[i]);
+        } else {
+            for (int i = 0; i < span; ++i) f(i, at(i));
+        }
+    };
     int step = 0;
     // all threads' x, added up, or the largest
     auto total = [&](uint32_t x, bool largest) -> uint32_t {
@@ -378,115 +524,73 @@ __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const K
         }
         return x;
     };
-    const int span = K ? K : (a.max_pages + 32 * W - 1) / (32 * W);          // pages a thread
-    const int i0 = tid * span;
-    uint32_t key[K ? K : 1];
-    auto at = [&](int i) -> uint32_t {     // 0: no candidate
-        const int p = i0 + i;
-        return p >= from && p < to ? __ldcg(keys + p) : 0u;
-    };
-    if constexpr (K > 0) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) key[i] = at(i);
-    }
-    auto get = [&](int i) -> uint32_t {
-        if constexpr (K > 0) return key[i];
-        else return at(i);
-    };
-    auto above = [&](uint32_t x) -> uint32_t {       // candidates with a key of x or more
-        uint32_t n = 0;
-        if constexpr (K > 0) {
-#pragma unroll
-            for (int i = 0; i < K; ++i) n += key[i] >= x;
-        } else {
-            for (int i = 0; i < span; ++i) n += at(i) >= x;
-        }
-        return total(n, false);
-    };
     uint32_t high = 0, low = 0;            // low: of the keys' complements
-    if constexpr (K > 0) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) high = max(high, key[i]), low = max(low, key[i] ? ~key[i] : 0u);
-    } else {
-        for (int i = 0; i < span; ++i) {
-            const uint32_t k = at(i);
-            high = max(high, k), low = max(low, k ? ~k : 0u);
-        }
-    }
-    uint32_t lo = ~total(low, true), hi = total(high, true) + 1, have = (uint32_t)(to - from);
-    while (hi - lo > 1 && have != (uint32_t)want) {
-        const uint32_t mid = lo + (hi - lo) / 2, n = above(mid);
+    each([&](int, uint32_t k) { high = max(high, k), low = max(low, k ? ~k : 0u); });
+    uint32_t lo = ~total(low, true), hi = total(high, true) + 1, have = (uint32_t)(to - from), fewer = 0;
+    for (bool even = true; hi - lo > 1 && have != (uint32_t)want; even = !even) {
+        // in turn where the counts at both ends would have it, and in the middle, so that it ends soon on any keys
+        const float part = even ? (float)(have - want) / (float)(have - fewer) : 0.5f;
+        const uint32_t mid = lo + min(max((uint32_t)((float)(hi - lo) * part), 1u), hi - lo - 1);
+        uint32_t n = 0;
+        each([&](int, uint32_t k) { n += k >= mid; });
+        n = total(n, false);
         if (n >= (uint32_t)want) lo = mid, have = n;
-        else hi = mid;
+        else hi = mid, fewer = n;
     }
-    // those above lo, and of those at lo the first that are still wanted
-    const uint32_t extra = have == (uint32_t)want ? 0u : (uint32_t)want - above(hi);
-    const bool exact = have == (uint32_t)want;
-    uint32_t sure = 0, ties = 0;
-    if constexpr (K > 0) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) sure += exact ? key[i] >= lo : key[i] > lo, ties += !exact && key[i] == lo;
-    } else {
-        for (int i = 0; i < span; ++i) {
-            const uint32_t k = at(i);
-            sure += exact ? k >= lo : k > lo, ties += !exact && k == lo;
-        }
-    }
-    // what the threads before have
-    auto before = [&](uint32_t x) -> uint32_t {
-        uint32_t in = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(~0u, in, o);
-            if (lane >= o) in += y;
-        }
-        uint32_t base = 0;
-        if constexpr (W > 1) {
-            if (lane == 31) box[step & 1][w] = in;
+    // those above lo, and of those at lo the first `extra`
+    const uint32_t extra = have == (uint32_t)want ? have : (uint32_t)want - fewer;
+    uint32_t put = a.first, tied = 0;      // in the warps before
+    if constexpr (W > 1) {
+        uint32_t sure = 0, ties = 0;
+        each([&](int, uint32_t k) { sure += k > lo, ties += k == lo; });
+        auto before = [&](uint32_t x) -> uint32_t {
+            x = __reduce_add_sync(~0u, x);
+            if (lane == 0) box[step & 1][w] = x;
             __syncthreads();
-            const uint32_t y = lane < w ? box[step & 1][lane] : 0u;
-            base = __reduce_add_sync(~0u, y);
+            x = __reduce_add_sync(~0u, lane < w ? box[step & 1][lane] : 0u);
             ++step;
-        }
-        return base + in - x;
-    };
-    uint32_t tied = before(ties);
-    const uint32_t taken = min(extra, tied + ties) - min(extra, tied);
-    uint32_t put = before(sure + taken) + a.first;
-    if constexpr (K > 0) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const uint32_t k = key[i];
-            const bool tie = !exact && k == lo;
-            if ((exact ? k >= lo : k > lo) || (tie && tied < extra)) out[put++] = i0 + i;
-            tied += tie;
-        }
-    } else {
-        for (int i = 0; i < span; ++i) {
-            const uint32_t k = get(i);
-            const bool tie = !exact && k == lo;
-            if ((exact ? k >= lo : k > lo) || (tie && tied < extra)) out[put++] = i0 + i;
-            tied += tie;
-        }
+            return x;
+        };
+        sure = before(sure), ties = before(ties);
+        tied = ties;
+        put += sure + min(extra, ties);
     }
+    const uint32_t below = (1u << lane) - 1;
+    each([&](int i, uint32_t k) {
+        const uint32_t at_lo = __ballot_sync(~0u, k == lo);
+        const bool take = k > lo || (k == lo && tied + __popc(at_lo & below) < extra);
+        const uint32_t taken = __ballot_sync(~0u, take);
+        if (take) out[put + __popc(taken & below)] = p0 + 32 * i;
+        put += __popc(taken), tied += __popc(at_lo);
+    });
 }
 
 template <int W, int K>
 cudaError_t pick_rows(const KvPickArgs &a, cudaStream_t s) {
     const long long rows = (long long)a.T * a.Hkv, per = W == 1 ? THREADS / 32 : 1;
-    pick_kernel<W, K><<<(unsigned)((rows + per - 1) / per), W == 1 ? THREADS : 32 * W, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)((rows + per - 1) / per));
+    c.blockDim = dim3(W == 1 ? THREADS : 32 * W);
+    c.stream = s;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &early;
+    c.numAttrs = a.max_pages > a.count ? 1 : 0;      // (without scores there is nothing of this call's to run beside)
+    return cudaLaunchKernelEx(&c, pick_kernel<W, K>, a);
 }
 
 template <int D, typename T>
 cudaError_t score(KvPickArgs a, cudaStream_t s) {
-    const int nt = a.max_q == 1 ? 1 : 8, groups = (a.Hkv + HEADS - 1) / HEADS;
-    a.blocks = (a.max_q + nt - 1) / nt;
+    const int groups = (a.Hkv + HEADS - 1) / HEADS;
+    const int tokens = a.max_q == 1 ? 1 : TOKENS;
+    a.blocks = (a.max_q + tokens - 1) / tokens;
     const long long units = (long long)a.B * a.blocks * groups;
-    a.chunks = (int)max(1LL, min((SMS * 4LL + units - 1) / units, (a.max_pages + 31LL) / 32));
+    // 32 pages a CTA, unless that were more than some dozens an SM (with tables far wider than their rows most have nothing)
+    a.chunks = (int)max(1LL, min(SMS * (tokens == 1 ? 32LL : 4LL) / units, (a.max_pages + 31LL) / 32));
     if (units * a.chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (nt == 1) score_kernel<D, 1, T><<<(unsigned)(units * a.chunks), THREADS, 0, s>>>(a);
-    else score_kernel<D, 8, T><<<(unsigned)(units * a.chunks), THREADS, 0, s>>>(a);
+    if (tokens == 1) score_one_kernel<D, T><<<(unsigned)(units * a.chunks), THREADS, 0, s>>>(a);
+    else score_kernel<D, T><<<(unsigned)(units * a.chunks), THREADS, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -509,10 +613,14 @@ cudaError_t launch_kv4_pick(const KvPickArgs &a, cudaStream_t s) {
         else e = a.D == 128 ? score<128, __half>(a, s) : score<64, __half>(a, s);
         if (e != cudaSuccess) return e;
     }
+    // A warp a row where its lanes hold the row and rows are many, else a CTA with 8 pages a lane.
+    const bool many = (long long)a.T * a.Hkv >= SMS * 4;
     if (a.max_pages <= 256) return pick_rows<1, 8>(a, s);
-    if (a.max_pages <= 1024) return pick_rows<1, 32>(a, s);
-    if (a.max_pages <= 2048) return pick_rows<8, 8>(a, s);
-    if (a.max_pages <= 8192) return pick_rows<8, 32>(a, s);
+    if (many && a.max_pages <= 512) return pick_rows<1, 16>(a, s);
+    if (many && a.max_pages <= 1024) return pick_rows<1, 32>(a, s);
+    if (a.max_pages <= 1024) return pick_rows<4, 8>(a, s);
+    if (a.max_pages <= 4096) return pick_rows<16, 8>(a, s);
+    if (a.max_pages <= 8192) return pick_rows<32, 8>(a, s);
     if (a.max_pages <= 32768) return pick_rows<32, 32>(a, s);
     return pick_rows<32, 0>(a, s);
 }

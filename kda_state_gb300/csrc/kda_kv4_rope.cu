@@ -24,17 +24,26 @@ __global__ void __launch_bounds__(THREADS) append_rope_kernel(const KvRopeArgs a
     // (token, group of heads) slots; heads * T has 31 bits
     const unsigned slot = blockIdx.x * (unsigned)SLOTS + threadIdx.x / NB;
     const int t = (int)(slot / (unsigned)a.groups), g = (int)(slot - (unsigned)t * a.groups);
-    const int b = owner_of(a.cu, a.B, t);
-    const bool mine = t < a.T && b >= 0;
+    uint4 next[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    auto ask = [&](int h) {                // (what is read here is written by this thread's warp after it, or by none)
+        if (t >= a.T || h >= heads) return;
+        const T *src = h < a.Hq ? (const T *)a.q + t * a.q_stride + h * D
+                                : h < a.Hq + a.Hkv ? (const T *)a.k + t * a.k_stride + (h - a.Hq) * D : (const T *)a.v + t * a.v_stride + (h - a.Hq - a.Hkv) * D;
+        next[0] = reinterpret_cast<const uint4 *>(src + blk * 16)[0];
+        next[1] = reinterpret_cast<const uint4 *>(src + blk * 16)[1];
+    };
+    ask(g);
+    const Owner own = owner_with(a.cu, a.start, a.B, a.T, t);
+    const bool mine = own.b >= 0;
     long long pos = -1;
     uint8_t *page_at = nullptr;            // the token's tile of head 0
     int tok = 0;
     if (mine) {
-        pos = (long long)a.start[b] + (t - a.cu[b]);
+        pos = (long long)own.more + (t - own.q0);
         if (pos < 0 || pos >= a.positions || (pos >> a.page_shift) >= a.max_pages) {
             report(a.err, DEVERR_SEQLENS);
         } else {
-            const int page = a.page_table[(size_t)b * a.max_pages + (pos >> a.page_shift)];
+            const int page = a.page_table[(size_t)own.b * a.max_pages + (pos >> a.page_shift)];
             const int in_page = (int)pos & ((1 << a.page_shift) - 1);
             tok = in_page & (KV_TILE - 1);
             if (page < 0 || page >= a.num_pages) report(a.err, DEVERR_PAGE_RANGE);
@@ -66,13 +75,8 @@ __global__ void __launch_bounds__(THREADS) append_rope_kernel(const KvRopeArgs a
         const int h = g + i * a.groups;
         const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
         const bool have = mine && h < heads;
-        uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (have) {
-            const T *src = is_q ? (const T *)a.q + t * a.q_stride + h * D
-                                : is_k ? (const T *)a.k + t * a.k_stride + (h - a.Hq) * D : (const T *)a.v + t * a.v_stride + (h - a.Hq - a.Hkv) * D;
-            w[0] = reinterpret_cast<const uint4 *>(src + blk * 16)[0];
-            w[1] = reinterpret_cast<const uint4 *>(src + blk * 16)[1];
-        }
+        const uint4 w[2] = {next[0], next[1]};
+        ask(h + a.groups);
         float x[16];
         if constexpr (PAIRS) {
             unpack16(w[0], x, T());
@@ -133,8 +137,10 @@ template <int D, typename T>
 cudaError_t launch(KvRopeArgs a, cudaStream_t s) {
     constexpr int SLOTS = THREADS / (D / 16);
     const int heads = a.Hq + 2 * a.Hkv;
-    // One head a thread while that does not fill the GPU, then several, whose cos and sin are read once.
-    a.groups = heads;
+    // One head a thread while that does not fill the GPU, then up to eight, whose cos and sin are read once.
+    const long long fill = (long long)a.T * heads / (SLOTS * 152 * 8);
+    const int each = (int)(fill < 1 ? 1 : fill > 8 ? 8 : fill);
+    a.groups = (heads + each - 1) / each;
     const long long grid = ((long long)a.T * a.groups + SLOTS - 1) / SLOTS;
     if (a.pairs) append_rope_kernel<D, T, true><<<(unsigned)grid, THREADS, 0, s>>>(a);
     else append_rope_kernel<D, T, false><<<(unsigned)grid, THREADS, 0, s>>>(a);
