@@ -650,7 +650,8 @@ KDA_API size_t kda_kv4_pick_workspace_bytes(int total_tokens, int H_kv, int max_
  *            least >= -100 with max(up, down) <= 127 x 2^f,
  *     score = 2^e sum_c (u_c hi_c - d_c lo_c)
  * a whole number times a power of two: exact.  A page with e = 127 is above all
- * others; queries with an infinity or a NaN (or sums beyond fp32) score 0.
+ * others; queries with an infinity or a NaN, or whose magnitudes add up beyond
+ * fp32, score 0.
  *
  *   q           as kda_kv4_attention (rotated)
  *   count       1 .. max_pages or more; 0 <= first, 1 <= recent, first + recent <=

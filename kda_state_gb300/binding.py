@@ -605,6 +605,7 @@ def kda_gated_rmsnorm(o, gate, w_norm, eps: float = EPS_NORM, out=None, stream=N
 
 
 _NORM_DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float16: KDA_DTYPE_FP16, torch.float32: KDA_DTYPE_FP32}
+_NORM_BYTES = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4}
 _NORM_OUT = {"none": KDA_NORM_TYPE, "row": KDA_NORM_E4M3_ROW, "block": KDA_NORM_E4M3_BLOCK}
 NORM_BLOCK = 128      # channels of a scale
 
@@ -618,12 +619,11 @@ def _norm_rows(t, name, dtype, shape, dev):
         same = False
     if not same:
         _need(t, name, shape, dtype, torch.device("cuda", dev), dense=False)
-    T, C = shape
     stride, one = t.stride()
-    if T <= 1:
-        stride = C
+    if shape[0] <= 1:
+        stride = shape[1]
     at = t.data_ptr()
-    if one != 1 or stride < C or stride * t.element_size() % 16 != 0 or at % 16 != 0:
+    if one != 1 or stride < shape[1] or stride * _NORM_BYTES[dtype] % 16 != 0 or at % 16 != 0:
         raise ValueError("%s: channels must be dense, rows start on 16-byte boundaries and not overlap" % name)
     return at, stride
 
@@ -644,7 +644,9 @@ def kda_add_rmsnorm(x, residual, weight, eps: float = EPS_NORM, scales: str = "n
     T, C = shape
     xa, xs = _norm_rows(x, "x", dtype, shape, dev)
     wa = _ptr(weight, "weight", (C,), dtype, dev)
-    ra = rs = ha = hs = None
+    at, kind = x.device, dtype if scales == "none" else torch.float8_e4m3fn
+    ra = ha = sa = None
+    rs = hs = 0
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
@@ -652,23 +654,29 @@ def kda_add_rmsnorm(x, residual, weight, eps: float = EPS_NORM, scales: str = "n
     else:
         ra, rs = _norm_rows(residual, "residual", dtype, shape, dev)
         if residual_out is None:
-            residual_out = _make(stream, shape, dtype, x.device)
-        ha, hs = _norm_rows(residual_out, "residual_out", dtype, shape, dev)
-    kind = dtype if scales == "none" else torch.float8_e4m3fn
+            residual_out = torch.empty(shape, dtype=dtype, device=at) if stream is None else _make(stream, shape, dtype, at)
+            ha, hs = residual_out.data_ptr(), C
+        else:
+            ha, hs = _norm_rows(residual_out, "residual_out", dtype, shape, dev)
     if out is None:
-        out = _make(stream, shape, kind, x.device)
-    oa, sa = _ptr(out, "out", shape, kind, dev), None
+        out = torch.empty(shape, dtype=kind, device=at) if stream is None else _make(stream, shape, kind, at)
+        oa = out.data_ptr()
+    else:
+        oa = _ptr(out, "out", shape, kind, dev)
     if scales == "none":
         if scales_out is not None:
             raise ValueError('scales_out needs scales "row" or "block"')
     else:
         sshape = (T,) if scales == "row" else (T, (C + NORM_BLOCK - 1) // NORM_BLOCK)
         if scales_out is None:
-            scales_out = _make(stream, sshape, F32, x.device)
-        sa = _ptr(scales_out, "scales_out", sshape, F32, dev)
-    status = lib().kda_add_rmsnorm(_NORM_DT[dtype], T, C, xa, xs, ra, rs or 0, wa, eps, _NORM_OUT[scales],
-                                   ha, hs or 0, oa, sa, _stream_of(stream, dev))
-    _check("kda_add_rmsnorm", status)
+            scales_out = torch.empty(sshape, dtype=F32, device=at) if stream is None else _make(stream, sshape, F32, at)
+            sa = scales_out.data_ptr()
+        else:
+            sa = _ptr(scales_out, "scales_out", sshape, F32, dev)
+    status = lib().kda_add_rmsnorm(_NORM_DT[dtype], T, C, xa, xs, ra, rs, wa, eps, _NORM_OUT[scales],
+                                   ha, hs, oa, sa, _stream_of(stream, dev))
+    if status:
+        _check("kda_add_rmsnorm", status)
     return out, scales_out, residual_out
 
 
@@ -963,22 +971,22 @@ def kda_kv4_append_rope(q, k, v, rope, cu_seqlens, start, page_table, pool, pair
     dtype = q.dtype
     dt = _kv_dt(dtype)
     T, Hq, D = shape
-    kshape, _ = _first(k, "k", 3)
-    H = kshape[1]
+    pa, pages, H, page_size = _pool(pool, D, dev)
+    kshape = (T, H, D)
     qa, qs = _rows(q, "q", dtype, shape, dev)
-    ka, ks = _rows(k, "k", dtype, (T, H, D), dev)
-    va, vs = _rows(v, "v", dtype, (T, H, D), dev)
-    (positions, R), _ = _first(rope, "rope", 2)
-    pa, pages, Hp, page_size = _pool(pool, D, dev)
-    if Hp != H:
-        raise ValueError("pool has %d heads, k has %d" % (Hp, H))
+    ka, ks = _rows(k, "k", dtype, kshape, dev)
+    va, vs = _rows(v, "v", dtype, kshape, dev)
+    rshape, _ = _first(rope, "rope", 2)
     ta, B, M = _table(page_table, dev)
     if q_out is None:
-        q_out = _make(stream, shape, dtype, q.device)
-    oa, os_ = _rows(q_out, "q_out", dtype, shape, dev)
+        q_out = torch.empty(shape, dtype=dtype, device=q.device) if stream is None else _make(
+            stream, shape, dtype, q.device)
+        oa, os_ = q_out.data_ptr(), Hq * D
+    else:
+        oa, os_ = _rows(q_out, "q_out", dtype, shape, dev)
     status = lib().kda_kv4_append_rope(
-        dt, B, T, Hq, H, D, R, 1 if pairs else 0, qa, qs, ka, ks, va, vs,
-        _ptr(rope, "rope", (positions, R), F32, dev), positions,
+        dt, B, T, Hq, H, D, rshape[1], 1 if pairs else 0, qa, qs, ka, ks, va, vs,
+        _ptr(rope, "rope", rshape, F32, dev), rshape[0],
         _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev), _ptr(start, "start", (B,), I32, dev), ta, M,
         page_size, pa, pages, k_scale, v_scale, oa, os_, _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_kv4_append_rope", status)
@@ -1027,19 +1035,24 @@ def kda_kv4_pick(q, cu_seqlens, max_q: int, kv_lens, page_table, bounds, page_si
     dt = _kv_dt(dtype)
     T, Hq, D = shape
     qa, qs = _rows(q, "q", dtype, shape, dev)
-    (pages, H, width), _ = _first(bounds, "bounds", 3)
+    (pages, H, _), _ = _first(bounds, "bounds", 3)
     ba = _ptr(bounds, "bounds", (pages, H, 2 * D + 16), torch.int8, dev)
     ta, B, M = _table(page_table, dev)
+    if (max_q | page_size | count | first | recent) >> 31:
+        max_q, page_size, count, first, recent = map(_int, (max_q, page_size, count, first, recent))
     if picked is None:
-        picked = _make(stream, (T, H, count), I32, q.device)
+        picked = torch.empty((T, H, count), dtype=I32, device=q.device) if stream is None else _make(
+            stream, (T, H, count), I32, q.device)
+        oa = picked.data_ptr()
+    else:
+        oa = _ptr(picked, "picked", (T, H, count), I32, dev)
     if workspace is None:
         workspace = _make(stream, (kv4_pick_workspace_bytes(T, H, M),), _U8, q.device, result=False)
     (wb,), _ = _first(workspace, "workspace", 1)
     status = lib().kda_kv4_pick(
-        dt, B, T, _int(max_q), Hq, H, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
-        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, _int(page_size), ba, pages, count, _int(first), _int(recent),
-        _ptr(picked, "picked", (T, H, count), I32, dev), _ptr(workspace, "workspace", (wb,), _U8, dev), wb,
-        _err_ptr(dev_err, dev), _stream_of(stream, dev))
+        dt, B, T, max_q, Hq, H, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size, ba, pages, count, first, recent, oa,
+        _ptr(workspace, "workspace", (wb,), _U8, dev), wb, _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_kv4_pick", status)
     return picked
 
@@ -1059,9 +1072,15 @@ def kda_kv4_attention_picked(q, cu_seqlens, max_q: int, kv_lens, page_table, pic
     pshape, _ = _first(picked, "picked", 3)
     count = pshape[2]
     if o is None:
-        o = _make(stream, shape, dtype, q.device)
+        o = torch.empty(shape, dtype=dtype, device=q.device) if stream is None else _make(stream, shape, dtype, q.device)
+        oa = o.data_ptr()
+    else:
+        oa = _ptr(o, "o", shape, dtype, dev)
     if lse is None:
-        lse = _make(stream, (T, H), F32, q.device)
+        lse = torch.empty((T, H), dtype=F32, device=q.device) if stream is None else _make(stream, (T, H), F32, q.device)
+        la = lse.data_ptr()
+    else:
+        la = _ptr(lse, "lse", (T, H), F32, dev)
     if workspace is None:
         workspace = _make(stream, (kv4_workspace_bytes(),), _U8, q.device, zero=True, result=False)
     (wb,), _ = _first(workspace, "workspace", 1)
@@ -1069,9 +1088,8 @@ def kda_kv4_attention_picked(q, cu_seqlens, max_q: int, kv_lens, page_table, pic
         dt, B, T, _int(max_q), H, H_kv, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
         _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, page_size,
         _ptr(picked, "picked", (T, H_kv, count), I32, dev), count, pa, pages,
-        D ** -0.5 if scale is None else scale, k_scale, v_scale, _ptr(o, "o", shape, dtype, dev),
-        _ptr(lse, "lse", (T, H), F32, dev), _ptr(workspace, "workspace", (wb,), _U8, dev), wb,
-        _err_ptr(dev_err, dev), _stream_of(stream, dev))
+        D ** -0.5 if scale is None else scale, k_scale, v_scale, oa, la,
+        _ptr(workspace, "workspace", (wb,), _U8, dev), wb, _err_ptr(dev_err, dev), _stream_of(stream, dev))
     _check("kda_kv4_attention_picked", status)
     return o, lse
 

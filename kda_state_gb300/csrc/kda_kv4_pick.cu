@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(THREADS) bounds_kernel(const KvBoundsArgs a) {
 // scores
 // ---------------------------------------------------------------------------
 
-constexpr int HEADS = 8;       // kv heads that a CTA takes
-constexpr int TOKENS = 8;      // and tokens
-constexpr int MISSING = 1000;  // in place of a unit: a page out of range, whose key is 1 (below every score; 0 is no page)
+constexpr int HEADS_1 = 8, HEADS = 4;      // kv heads that a CTA takes with single tokens, and with several
+constexpr int TOKENS = 8;                  // several
+constexpr int MISSING = 1000;              // in place of a unit: a page out of range, whose key is 1 (below every score; 0 is no page)
 
 // The bits of a finite or infinite float as a number that orders as it does.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -190,11 +190,13 @@ template <int D, int N, typename T, typename Q, typename Put>
 __device__ __forceinline__ void ask_of(const Q &q, int G, const Put &put) {
     constexpr int W = D / 64;              // words of the lane: 2 W channels
     const int lane = threadIdx.x & 31;
-    float up[N][2 * W], down[N][2 * W];
+    // up = (sum |f| + sum f) / 2 and down = (sum |f| - sum f) / 2, an addition less a value than from their parts; halves
+    // are exact, and an infinity or a NaN stays one
+    float all[N][2 * W], net[N][2 * W];
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < 2 * W; ++i) up[n][i] = down[n][i] = 0.f;
+        for (int i = 0; i < 2 * W; ++i) all[n][i] = net[n][i] = 0.f;
     for (int g0 = 0; g0 < G; g0 += 8) {    // eight heads' loads at once
         uint32_t w[N][8][W];
 #pragma unroll
@@ -217,42 +219,41 @@ __device__ __forceinline__ void ask_of(const Q &q, int G, const Put &put) {
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     const float2 f = halves<T>(w[n][g][i]);
-                    up[n][2 * i] = __fadd_rn(up[n][2 * i], max_nan(f.x, 0.f)), down[n][2 * i] = __fadd_rn(down[n][2 * i], max_nan(-f.x, 0.f));
-                    up[n][2 * i + 1] = __fadd_rn(up[n][2 * i + 1], max_nan(f.y, 0.f)), down[n][2 * i + 1] = __fadd_rn(down[n][2 * i + 1], max_nan(-f.y, 0.f));
+                    all[n][2 * i] += fabsf(f.x), net[n][2 * i] += f.x;
+                    all[n][2 * i + 1] += fabsf(f.y), net[n][2 * i + 1] += f.y;
                 }
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2 * W; ++i) top = max_nan(top, max_nan(up[n][i], down[n][i]));
+        for (int i = 0; i < 2 * W; ++i) {
+            all[n][i] *= 0.5f, net[n][i] *= 0.5f;
+            top = max_nan(top, all[n][i] + fabsf(net[n][i]));
+        }
         const uint32_t bits = __reduce_max_sync(~0u, __float_as_uint(top) & 0x7fffffffu);       // (a NaN is above all)
         // nothing to go by: all pages score 0
         const float per = bits >= 0x7f800000u || bits < 0x00800000u ? 0.f : power_of(-max(unit_of(__uint_as_float(bits)), -100));
         int u[2 * W], d[2 * W];
 #pragma unroll
         for (int i = 0; i < 2 * W; ++i) {
-            u[i] = per == 0.f ? 0 : __float2int_rn(up[n][i] * per);
-            d[i] = per == 0.f ? 0 : -__float2int_rn(down[n][i] * per);
+            u[i] = per == 0.f ? 0 : __float2int_rn((all[n][i] + net[n][i]) * per);
+            d[i] = per == 0.f ? 0 : __float2int_rn((net[n][i] - all[n][i]) * per);
         }
         put(n, lane * 2 * W, u, d);
     }
 }
 
-// What a CTA scores: up to `tokens` tokens of one request, with a run of its pages, for up to HEADS kv heads.
+// What a CTA scores: up to `tokens` tokens of one request, with a run of its pages, for up to `heads` kv heads.
 struct Share {
     int b, q0, nt, h0, heads, p0, p1;      // p0 >= p1: nothing
 };
-__device__ __forceinline__ Share share_of(const KvPickArgs &a, int tokens) {
+__device__ __forceinline__ Share share_of(const KvPickArgs &a, int tokens, int heads) {
     Share s;
-    const int groups = (a.Hkv + HEADS - 1) / HEADS;
-    unsigned at = blockIdx.x;
-    const int chunk = (int)(at % (unsigned)a.chunks);
-    at /= (unsigned)a.chunks;
-    s.h0 = (int)(at % (unsigned)groups) * HEADS, s.heads = min(HEADS, a.Hkv - s.h0);
-    at /= (unsigned)groups;
-    s.b = (int)(at / (unsigned)a.blocks);
-    const int i0 = (int)(at % (unsigned)a.blocks) * tokens;
+    const int chunk = blockIdx.y;
+    s.h0 = blockIdx.z * heads, s.heads = min(heads, a.Hkv - s.h0);
+    s.b = tokens == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)a.blocks);
+    const int i0 = tokens == 1 ? 0 : (int)(blockIdx.x % (unsigned)a.blocks) * tokens;
     Tokens rq{a.cu[s.b], 0, a.kv_lens[s.b]};
     rq.n = a.cu[s.b + 1] - rq.q0;
     check(a, rq, false);                   // (told by pick_kernel)
@@ -267,9 +268,9 @@ __device__ __forceinline__ Share share_of(const KvPickArgs &a, int tokens) {
     return s;
 }
 // Where every chunk is 32 pages: this lane's entry of the table, asked for before it is known that the CTA has work.
-__device__ __forceinline__ int early_page(const KvPickArgs &a) {
-    const int groups = (a.Hkv + HEADS - 1) / HEADS, p = (int)(blockIdx.x % (unsigned)a.chunks) * 32 + (int)(threadIdx.x & 31);
-    const unsigned b = blockIdx.x / (unsigned)a.chunks / (unsigned)groups / (unsigned)a.blocks;
+__device__ __forceinline__ int early_page(const KvPickArgs &a, int tokens) {
+    const int p = (int)blockIdx.y * 32 + (int)(threadIdx.x & 31);
+    const unsigned b = tokens == 1 ? blockIdx.x : blockIdx.x / (unsigned)a.blocks;
     return a.chunks * 32 >= a.max_pages && p < a.max_pages ? a.page_table[(size_t)b * a.max_pages + p] : 0;
 }
 __device__ __forceinline__ uint32_t key_of(float sum, int unit) {
@@ -286,24 +287,25 @@ __device__ __forceinline__ int page_or_0(const KvPickArgs &a, int pg, bool &bad)
 // has 32 pages of a head in flight.  (An 8-bit MMA of 16 pages and 32 channels takes 64 cycles a scheduler here; the same
 // products of one token take 4 of these instructions, 8 cycles.)
 template <int D, typename T>
-__global__ void __launch_bounds__(THREADS, 2) score_one_kernel(const KvPickArgs a) {
+__global__ void __launch_bounds__(THREADS, 3) score_one_kernel(const KvPickArgs a) {
     constexpr int RECORD = 2 * D + 16, LOADS = D / 64;
-    __shared__ __align__(16) int8_t ask[HEADS * 2 * D];
+    __shared__ __align__(16) int8_t ask[HEADS_1 * 2 * D];
     asm volatile("griddepcontrol.launch_dependents;");     // (pick_kernel may come in, and waits for the end of this one)
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 7;
-    const int guess = early_page(a);
-    const Share z = share_of(a, 1);
+    const int guess = early_page(a, 1);
+    const Share z = share_of(a, 1, HEADS_1);
     if (z.p0 >= z.p1) return;
     // the warps are dealt over the heads, and those of a head over the runs of 32 pages
-    const int parts = (THREADS / 32) / z.heads, h = w % z.heads, part = w / z.heads, stride = 32 * parts;
-    uint4 x[8][LOADS];                     // of page p + (lane & 24) + i: this lane's eighth of each 128 bytes
+    const int parts = (THREADS / 32) / z.heads, part = w / z.heads, h = w - part * z.heads, stride = 32 * parts;
+    constexpr int FLIGHT = 4;              // steps of four pages that are asked for ahead (of 8: 128 registers, an SM holds 2 CTAs)
+    uint4 x[FLIGHT][LOADS];                // of page p + (lane & 24) + i: this lane's eighth of each 128 bytes
     int page = 0, unit = 0, next = 0;      // page p + lane, and its unit
     auto look = [&](int p) { return p + lane < z.p1 ? a.page_table[(size_t)z.b * a.max_pages + p + lane] : 0; };
     auto record = [&](int pg) { return a.bounds + ((size_t)pg * a.Hkv + z.h0 + h) * RECORD; };
     auto load = [&](int i) {
         const uint4 *src = reinterpret_cast<const uint4 *>(record(__shfl_sync(~0u, page, (lane & 24) + i))) + j;
 #pragma unroll
-        for (int k = 0; k < LOADS; ++k) x[i][k] = __ldg(src + 8 * k);
+        for (int k = 0; k < LOADS; ++k) x[i % FLIGHT][k] = __ldg(src + 8 * k);
     };
     auto begin = [&](int pg) {
         bool bad;
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 2) score_one_kernel(const KvPickArgs 
         begin(a.chunks * 32 >= a.max_pages ? (p + lane < z.p1 ? guess : 0) : look(p));
         next = look(p + stride);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load(i);
+        for (int i = 0; i < FLIGHT; ++i) load(i);
     }
     const int G = a.Hq / a.Hkv;
     for (int i = w; i < z.heads; i += THREADS / 32)
@@ -333,19 +335,19 @@ __global__ void __launch_bounds__(THREADS, 2) score_one_kernel(const KvPickArgs 
     for (; p < z.p1; p += stride) {
         const int now = unit, later = look(p + 2 * stride);
         const bool on = p + stride < z.p1;
-        if (on) begin(next);
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             int s = 0;
 #pragma unroll
             for (int k = 0; k < LOADS; ++k) {
-                s = __dp4a((int)x[i][k].x, (int)y[k].x, s);
-                s = __dp4a((int)x[i][k].y, (int)y[k].y, s);
-                s = __dp4a((int)x[i][k].z, (int)y[k].z, s);
-                s = __dp4a((int)x[i][k].w, (int)y[k].w, s);
+                s = __dp4a((int)x[i % FLIGHT][k].x, (int)y[k].x, s);
+                s = __dp4a((int)x[i % FLIGHT][k].y, (int)y[k].y, s);
+                s = __dp4a((int)x[i % FLIGHT][k].z, (int)y[k].z, s);
+                s = __dp4a((int)x[i % FLIGHT][k].w, (int)y[k].w, s);
             }
-            if (on) load(i);
+            if (i == 8 - FLIGHT && on) begin(next);
+            if (i < 8 - FLIGHT || on) load((i + FLIGHT) % 8);
             s += __shfl_xor_sync(~0u, s, 1);
             s += __shfl_xor_sync(~0u, s, 2);
             s += __shfl_xor_sync(~0u, s, 4);
@@ -380,10 +382,10 @@ __global__ void __launch_bounds__(THREADS, 2) score_kernel(const KvPickArgs a) {
     __shared__ __align__(16) uint8_t ask[HEADS * TOKENS * ROW];
     asm volatile("griddepcontrol.launch_dependents;");
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int guess = early_page(a);
-    const Share z = share_of(a, TOKENS);
+    const int guess = early_page(a, TOKENS);
+    const Share z = share_of(a, TOKENS, HEADS);
     if (z.p0 >= z.p1) return;
-    const int parts = (THREADS / 32) / z.heads, h = w % z.heads, part = w / z.heads, stride = 32 * parts;
+    const int parts = (THREADS / 32) / z.heads, part = w / z.heads, h = w - part * z.heads, stride = 32 * parts;
     uint4 x[2][2][PARTS];                  // of pages p + 16 s + 8 k + r: this lane's quarter of each 64 bytes
     int unit[2];                           // of page p + 16 s + (lane & 15)
     auto look = [&](int p) { return p + lane < z.p1 ? a.page_table[(size_t)z.b * a.max_pages + p + lane] : 0; };
@@ -582,15 +584,15 @@ cudaError_t pick_rows(const KvPickArgs &a, cudaStream_t s) {
 
 template <int D, typename T>
 cudaError_t score(KvPickArgs a, cudaStream_t s) {
-    const int groups = (a.Hkv + HEADS - 1) / HEADS;
-    const int tokens = a.max_q == 1 ? 1 : TOKENS;
+    const int tokens = a.max_q == 1 ? 1 : TOKENS, heads = tokens == 1 ? HEADS_1 : HEADS, groups = (a.Hkv + heads - 1) / heads;
     a.blocks = (a.max_q + tokens - 1) / tokens;
     const long long units = (long long)a.B * a.blocks * groups;
     // 32 pages a CTA, unless that were more than some dozens an SM (with tables far wider than their rows most have nothing)
     a.chunks = (int)max(1LL, min(SMS * (tokens == 1 ? 32LL : 4LL) / units, (a.max_pages + 31LL) / 32));
-    if (units * a.chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (tokens == 1) score_one_kernel<D, T><<<(unsigned)(units * a.chunks), THREADS, 0, s>>>(a);
-    else score_kernel<D, T><<<(unsigned)(units * a.chunks), THREADS, 0, s>>>(a);
+    if ((long long)a.B * a.blocks > 0x7fffffffLL || a.chunks > 65535 || groups > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(a.B * a.blocks), (unsigned)a.chunks, (unsigned)groups);
+    if (tokens == 1) score_one_kernel<D, T><<<grid, THREADS, 0, s>>>(a);
+    else score_kernel<D, T><<<grid, THREADS, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -613,15 +615,16 @@ cudaError_t launch_kv4_pick(const KvPickArgs &a, cudaStream_t s) {
         else e = a.D == 128 ? score<128, __half>(a, s) : score<64, __half>(a, s);
         if (e != cudaSuccess) return e;
     }
-    // A warp a row where its lanes hold the row and rows are many, else a CTA with 8 pages a lane.
-    const bool many = (long long)a.T * a.Hkv >= SMS * 4;
-    if (a.max_pages <= 256) return pick_rows<1, 8>(a, s);
-    if (many && a.max_pages <= 512) return pick_rows<1, 16>(a, s);
-    if (many && a.max_pages <= 1024) return pick_rows<1, 32>(a, s);
-    if (a.max_pages <= 1024) return pick_rows<4, 8>(a, s);
-    if (a.max_pages <= 4096) return pick_rows<16, 8>(a, s);
-    if (a.max_pages <= 8192) return pick_rows<32, 8>(a, s);
-    if (a.max_pages <= 32768) return pick_rows<32, 32>(a, s);
+    // A warp a row where its lanes hold the candidates (pages before the last `recent`) and rows fill the GPU, else a CTA.
+    const bool many = (long long)a.T * a.Hkv >= SMS * 24;
+    const int width = a.max_pages - a.recent;
+    if (many && width <= 256) return pick_rows<1, 8>(a, s);
+    if (many && width <= 512) return pick_rows<1, 16>(a, s);
+    if (many && width <= 1024) return pick_rows<1, 32>(a, s);
+    if (width <= 512) return pick_rows<4, 4>(a, s);
+    if (width <= 2048) return pick_rows<8, 8>(a, s);
+    if (width <= 8192) return pick_rows<32, 8>(a, s);
+    if (width <= 32768) return pick_rows<32, 32>(a, s);
     return pick_rows<32, 0>(a, s);
 }
 

@@ -65,7 +65,7 @@ def asked(q):
     """(u, d) whole numbers [D] of one kv head's queries q [G, D]."""
     up, down = np.maximum(q, 0).sum(0), np.maximum(-q, 0).sum(0)
     top = max(up.max(), down.max())
-    if not top <= np.finfo(np.float32).max or top == 0:
+    if not np.abs(q).sum(0).max() <= np.finfo(np.float32).max or top == 0:
         return np.zeros(q.shape[1], int), np.zeros(q.shape[1], int)
     f = max(unit(top), -100)
     return np.rint(up / 2.0 ** f).astype(int), np.rint(down / 2.0 ** f).astype(int)
