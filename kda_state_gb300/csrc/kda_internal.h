@@ -171,7 +171,9 @@ struct KvAttentionArgs {
 // Append with rotation: KvCacheArgs' sizes, q beside k and v, and the angles' table.
 struct KvRopeArgs {
     int dt, B, T, Hq, Hkv, D, max_pages, page_shift, num_pages, R, positions, pairs;
-    int groups;                    // of a token's heads, a thread each (set by the launch)
+    int q_groups, kv_groups;       // of a token's heads, a thread each, and the CTAs of q's (set by the launch)
+    unsigned q_blocks;
+    float minus_zero;
     const void *q, *k, *v;
     long long q_stride, k_stride, v_stride, qo_stride;
     const float *rope;             // [positions][R]: R / 2 cosines, R / 2 sines

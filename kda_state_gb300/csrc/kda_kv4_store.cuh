@@ -43,27 +43,37 @@ __device__ __forceinline__ float to_18_bits(float x) {
     return __uint_as_float((__float_as_uint(x) + 0x20u) & ~0x3fu);
 }
 
+// The scale (its byte) of a block whose largest magnitude is top, and what its values are multiplied by to be codes.
+__device__ __forceinline__ uint32_t scale_of(float top, float &one_over) {
+    const uint32_t sb = to_e4m3(isnan(top) ? top : to_18_bits(top * (1.f / 6.f)));
+    one_over = sb != 0 ? __frcp_rn(f16x2_to_float2(e4m3x2_to_f16x2(sb)).x) : 0.f;
+    return sb;
+}
+// Eight values as codes; sb is their scale's byte.
+__device__ __forceinline__ uint32_t codes_of(const float *x, uint32_t sb, float one_over) {
+    uint32_t code = 0;
+    if (sb != 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            code |= to_e2m1x2(to_18_bits(x[2 * i] * one_over), to_18_bits(x[2 * i + 1] * one_over)) << (8 * i);
+    }
+    return code;
+}
+
 // Channels 16 blk .. 16 blk + 15 of token tok of a tile, as V (side 1) or K; x is what was given, of 8 or 11 bits, and
 // inv the reciprocal of the tensor scale, a power of two.
 template <int D>
 __device__ __forceinline__ void store_block(uint8_t *tile, int tok, int blk, int side, float (&x)[16], float inv) {
     using L = KvTile<D>;
-    float top = 0.f;
+    float top = 0.f, one_over;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         x[i] *= inv;
         top = max_nan(top, fabsf(x[i]));
     }
-    const uint32_t sb = to_e4m3(isnan(top) ? top : to_18_bits(top * (1.f / 6.f)));
-    const float s = f16x2_to_float2(e4m3x2_to_f16x2(sb)).x;
-    uint32_t code[2] = {0, 0};
-    if (sb != 0) {
-        const float one_over = __frcp_rn(s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            code[i >> 2] |= to_e2m1x2(to_18_bits(x[2 * i] * one_over), to_18_bits(x[2 * i + 1] * one_over)) << (8 * (i & 3));
-    }
-    *reinterpret_cast<uint2 *>(tile + (side ? L::VC : L::KC) + tok * (D / 2) + blk * 8) = make_uint2(code[0], code[1]);
+    const uint32_t sb = scale_of(top, one_over);
+    *reinterpret_cast<uint2 *>(tile + (side ? L::VC : L::KC) + tok * (D / 2) + blk * 8) =
+        make_uint2(codes_of(x, sb, one_over), codes_of(x + 8, sb, one_over));
     tile[side ? L::VS + blk * KV_TILE + tok : L::KS + tok * L::BLOCKS + blk] = (uint8_t)sb;
 }
 
