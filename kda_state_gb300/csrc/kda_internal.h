@@ -171,8 +171,8 @@ struct KvAttentionArgs {
 // Append with rotation: KvCacheArgs' sizes, q beside k and v, and the angles' table.
 struct KvRopeArgs {
     int dt, B, T, Hq, Hkv, D, max_pages, page_shift, num_pages, R, positions, pairs;
-    int q_groups, kv_groups;       // of a token's heads, a thread each, and the CTAs of q's (set by the launch)
-    unsigned q_blocks;
+    int q_groups, kv_groups, q_each, kv_each;      // groups of a token's heads, a thread each, and heads a group (set by the launch)
+    unsigned q_blocks, kv_blocks;  // CTAs
     float minus_zero;
     const void *q, *k, *v;
     long long q_stride, k_stride, v_stride, qo_stride;

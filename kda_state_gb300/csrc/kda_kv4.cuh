@@ -103,7 +103,7 @@ struct Owner {
 };
 __device__ __forceinline__ Owner owner_with(const int32_t *cu, const int32_t *per, int B, int T, int t) {
     Owner o;
-    o.b = min((int)((unsigned long long)(unsigned)t * (unsigned)B / (unsigned)T), B - 1);
+    o.b = min((int)(((float)t + 0.5f) * ((float)B / (float)T)), B - 1);        // (0 <= t; off by one at worst, which is looked for)
     o.q0 = cu[o.b], o.end = cu[o.b + 1], o.more = per[o.b];
     if (!__all_sync(~0u, t >= T || (o.q0 <= t && t < o.end))) {
         o.b = owner_of(cu, B, t);
