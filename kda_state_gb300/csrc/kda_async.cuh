@@ -70,6 +70,12 @@ __device__ __forceinline__ void prefetch_l2(const void *src_global, uint32_t byt
                  "r"(bytes)
                  : "memory");
 }
+// Ends when the kernels ahead in the stream have ended and what they wrote is there; at once where this one was not
+// launched early.  Every CTA of a kernel that is launched early calls it, so that the kernel does not end before them.
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A kernel behind in the stream that is launched early may take what room is left once all CTAs have called this.  Called
+// after the wait, so that the kernels ahead of this one have ended when that one begins.
+__device__ __forceinline__ void let_later_kernels_in() { asm volatile("griddepcontrol.launch_dependents;"); }
 // Order this thread's earlier generic-proxy accesses of shared memory before
 // later async-proxy (bulk copy) writes to it.
 __device__ __forceinline__ void fence_async_shared() {

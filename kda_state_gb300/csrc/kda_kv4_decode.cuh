@@ -38,10 +38,9 @@
 // page without tokens.
 #pragma once
 
-#include <atomic>
-
 #include "kda_async.cuh"
 #include "kda_internal.h"
+#include "kda_launch.h"
 #include "kda_kv4.cuh"
 
 namespace kda {
@@ -246,6 +245,10 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     constexpr int TILES = S::TILES, CHUNK = S::CHUNK;
     constexpr int LW = D / 32;             // 32-bit words of a lane's share of a K row
     extern __shared__ __align__(128) uint8_t smem[];
+    if constexpr (PICKED) {
+        wait_for_earlier_kernels();
+        let_later_kernels_in();
+    }
     float *const out_s = reinterpret_cast<float *>(smem + S::RING);                  // [WARPS][ROWS][OSTRIDE]
     float2 *const ml_s = reinterpret_cast<float2 *>(smem + S::RING + S::OUT);        // [2][WARPS][ROWS]
     uint8_t *const bars = smem + S::RING + S::OUT + S::ML;
@@ -866,17 +869,6 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
     }
 }
 
-// Lets a kernel use `bytes` of dynamic shared memory on the current device: asked for once a device (a call costs as
-// much as a launch's arguments do), `done` has a bit for each of the first 64.
-inline cudaError_t allow_shared(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
-    return e;
-}
-
 template <int D, int NT, typename T, bool PICKED = false>
 cudaError_t launch_decode_attention(const KvAttentionArgs &a, cudaStream_t s) {
     using Sh = DecodeShape<D, NT>;
@@ -884,6 +876,7 @@ cudaError_t launch_decode_attention(const KvAttentionArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_shared(reinterpret_cast<const void *>(decode_attention_kernel<D, NT, T, PICKED>), Sh::SMEM, done);
     if (e != cudaSuccess) return e;
+    if (PICKED) return launch_early(decode_attention_kernel<D, NT, T, PICKED>, dim3(NT == 1 ? MAX_CTAS : MAX_CTAS / 2), dim3(THREADS), Sh::SMEM, s, a);
     decode_attention_kernel<D, NT, T, PICKED><<<NT == 1 ? MAX_CTAS : MAX_CTAS / 2, THREADS, Sh::SMEM, s>>>(a);
     return cudaGetLastError();
 }

@@ -9,8 +9,10 @@
 // picked do not depend on the order of a sum, and equal scores are equal: the lower page is taken.
 //
 // Records are int8 [num_pages][Hkv][2 D + 16]: hi, lo, e, zeros.  e = 127 marks a page with a NaN (its score is infinite).
+#include "kda_async.cuh"
 #include "kda_internal.h"
 #include "kda_kv4.cuh"
+#include "kda_launch.h"
 
 namespace kda {
 namespace {
@@ -123,6 +125,8 @@ __device__ __forceinline__ void bound_page(const uint8_t *tiles, int fill, int8_
 // A warp takes one head of `slice` tokens (1 to 32), and of those the ones that are their request's first in a page.
 template <int D>
 __global__ void __launch_bounds__(THREADS) bounds_kernel(const KvBoundsArgs a) {
+    wait_for_earlier_kernels();
+    let_later_kernels_in();
     const int lane = threadIdx.x & 31;
     const unsigned unit = blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
     const int h = (int)(unit % (unsigned)a.H);
@@ -263,15 +267,10 @@ __device__ __forceinline__ Share share_of(const KvPickArgs &a, int tokens, int h
     const int last = rq.len - rq.n + i0 + s.nt - 1;        // the last token's position
     const int pages = last < 0 ? 0 : (last >> a.page_shift) + 1;
     if (pages <= a.count) return s;        // all of them are taken
-    const int per = a.chunks * 32 >= a.max_pages ? 32 : ((pages + a.chunks - 1) / a.chunks + 31) & ~31;
-    s.p0 = chunk * per, s.p1 = min(pages, s.p0 + per);
+    const int run = 32 * ((THREADS / 32) / s.heads);       // what the CTA's warps take at a time
+    const int per = a.chunks * run >= a.max_pages ? run : ((pages + a.chunks - 1) / a.chunks + run - 1) / run * run;
+    s.p0 = (int)min((long long)chunk * per, (long long)pages), s.p1 = min(pages, s.p0 + per);
     return s;
-}
-// Where every chunk is 32 pages: this lane's entry of the table, asked for before it is known that the CTA has work.
-__device__ __forceinline__ int early_page(const KvPickArgs &a, int tokens) {
-    const int p = (int)blockIdx.y * 32 + (int)(threadIdx.x & 31);
-    const unsigned b = tokens == 1 ? blockIdx.x : blockIdx.x / (unsigned)a.blocks;
-    return a.chunks * 32 >= a.max_pages && p < a.max_pages ? a.page_table[(size_t)b * a.max_pages + p] : 0;
 }
 __device__ __forceinline__ uint32_t key_of(float sum, int unit) {
     return unit == MISSING ? 1u : unit == UNBOUNDED ? 0xff800000u : ordered(sum * power_of(unit));
@@ -283,43 +282,53 @@ __device__ __forceinline__ int page_or_0(const KvPickArgs &a, int pg, bool &bad)
     return bad ? 0 : pg;
 }
 
-// Single tokens.  A record is held by eight lanes, whose loads are whole lines, and multiplied on the integer units; a warp
-// has 32 pages of a head in flight.  (An 8-bit MMA of 16 pages and 32 channels takes 64 cycles a scheduler here; the same
-// products of one token take 4 of these instructions, 8 cycles.)
+template <int D>
+struct OneShape {
+    // a page's records lie 16 bytes further than they are long, so that neighbouring lanes' 16-byte words meet no bank twice
+    static constexpr int RECORD = 2 * D + 16, STAGE = 32 * (HEADS_1 * RECORD + 8 * 16), SMEM = STAGE + HEADS_1 * 2 * D + 16;
+};
+
+// Single tokens.  A run of pages' records, each one block of all the CTA's heads, comes by bulk copies while the queries are
+// added up; then a lane multiplies one page's on the integer units.  (An 8-bit MMA of 16 pages and 32 channels takes 64
+// cycles a scheduler here; the same products of one token take 4 of these instructions, 8 cycles.)
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, 3) score_one_kernel(const KvPickArgs a) {
-    constexpr int RECORD = 2 * D + 16, LOADS = D / 64;
-    __shared__ __align__(16) int8_t ask[HEADS_1 * 2 * D];
-    asm volatile("griddepcontrol.launch_dependents;");     // (pick_kernel may come in, and waits for the end of this one)
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 7;
-    const int guess = early_page(a, 1);
+    using S = OneShape<D>;
+    constexpr int RECORD = S::RECORD;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int8_t *const ask = reinterpret_cast<int8_t *>(smem + S::STAGE);
+    const uint32_t bar = shared_addr(smem + S::STAGE + HEADS_1 * 2 * D);
+    wait_for_earlier_kernels();
+    let_later_kernels_in();
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // where a chunk is one run, this lane's page is asked for beside the request's numbers
+    const int heads0 = min(HEADS_1, a.Hkv - (int)blockIdx.z * HEADS_1), run0 = 32 * ((THREADS / 32) / heads0);
+    const bool one_run = a.chunks * run0 >= a.max_pages;
+    const int early_at = (int)min((long long)blockIdx.y * run0 + 32 * (w / heads0) + lane, 0x7fffffffLL);
+    const int early = one_run && early_at < a.max_pages ? a.page_table[(size_t)blockIdx.x * a.max_pages + early_at] : 0;
     const Share z = share_of(a, 1, HEADS_1);
     if (z.p0 >= z.p1) return;
     // the warps are dealt over the heads, and those of a head over the runs of 32 pages
     const int parts = (THREADS / 32) / z.heads, part = w / z.heads, h = w - part * z.heads, stride = 32 * parts;
-    constexpr int FLIGHT = 4;              // steps of four pages that are asked for ahead (of 8: 128 registers, an SM holds 2 CTAs)
-    uint4 x[FLIGHT][LOADS];                // of page p + (lane & 24) + i: this lane's eighth of each 128 bytes
-    int page = 0, unit = 0, next = 0;      // page p + lane, and its unit
-    auto look = [&](int p) { return p + lane < z.p1 ? a.page_table[(size_t)z.b * a.max_pages + p + lane] : 0; };
-    auto record = [&](int pg) { return a.bounds + ((size_t)pg * a.Hkv + z.h0 + h) * RECORD; };
-    auto load = [&](int i) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(record(__shfl_sync(~0u, page, (lane & 24) + i))) + j;
-#pragma unroll
-        for (int k = 0; k < LOADS; ++k) x[i % FLIGHT][k] = __ldg(src + 8 * k);
-    };
-    auto begin = [&](int pg) {
-        bool bad;
-        page = page_or_0(a, pg, bad);
-        unit = bad ? MISSING : __ldg(record(page) + 2 * D);
+    const bool works = part < parts;
+    const int page_bytes = z.heads * RECORD, apart = page_bytes + 16;       // an odd number of 16 bytes for 8, 4, 2 heads
+    uint8_t *const stage = smem + 32 * part * apart;
+    if (threadIdx.x == 0) barrier_init(bar, parts);
+    __syncthreads();
+    bool good = false;                     // page p + lane
+    auto fetch = [&](int p) {
+        if (!works) return;
+        const int page = p + lane >= z.p1 ? -2 : one_run ? early : a.page_table[(size_t)z.b * a.max_pages + p + lane];
+        good = page >= 0 && page < a.num_pages;
+        if (!good && page != -2) report(a.err, DEVERR_PAGE_RANGE);
+        if (h != 0) return;
+        const uint32_t there = __ballot_sync(~0u, good);
+        if (lane == 0) barrier_expect(bar, __popc(there) * page_bytes);
+        __syncwarp();
+        if (good) bulk_copy(stage + lane * apart, a.bounds + ((size_t)page * a.Hkv + z.h0) * RECORD, page_bytes, bar);
     };
     int p = z.p0 + 32 * part;
-    const bool works = part < parts && p < z.p1;
-    if (works) {
-        begin(a.chunks * 32 >= a.max_pages ? (p + lane < z.p1 ? guess : 0) : look(p));
-        next = look(p + stride);
-#pragma unroll
-        for (int i = 0; i < FLIGHT; ++i) load(i);
-    }
+    fetch(p);
     const int G = a.Hq / a.Hkv;
     for (int i = w; i < z.heads; i += THREADS / 32)
         ask_of<D, 1, T>([&](int) { return (const T *)a.q + (long long)z.q0 * a.q_stride + (z.h0 + i) * G * D; }, G, [&](int, int ch, const int *u, const int *d) {
@@ -327,34 +336,30 @@ __global__ void __launch_bounds__(THREADS, 3) score_one_kernel(const KvPickArgs 
             for (int k = 0; k < D / 32; ++k) ask[i * 2 * D + ch + k] = (int8_t)u[k], ask[i * 2 * D + D + ch + k] = (int8_t)d[k];
         });
     __syncthreads();
-    if (!works) return;
-    uint4 y[LOADS];
-#pragma unroll
-    for (int k = 0; k < LOADS; ++k) y[k] = *(reinterpret_cast<const uint4 *>(ask + h * 2 * D) + j + 8 * k);
     uint32_t *const keys = a.keys + ((size_t)z.q0 * a.Hkv + z.h0 + h) * a.key_stride;
-    for (; p < z.p1; p += stride) {
-        const int now = unit, later = look(p + 2 * stride);
-        const bool on = p + stride < z.p1;
-        int mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            int s = 0;
-#pragma unroll
-            for (int k = 0; k < LOADS; ++k) {
-                s = __dp4a((int)x[i % FLIGHT][k].x, (int)y[k].x, s);
-                s = __dp4a((int)x[i % FLIGHT][k].y, (int)y[k].y, s);
-                s = __dp4a((int)x[i % FLIGHT][k].z, (int)y[k].z, s);
-                s = __dp4a((int)x[i % FLIGHT][k].w, (int)y[k].w, s);
-            }
-            if (i == 8 - FLIGHT && on) begin(next);
-            if (i < 8 - FLIGHT || on) load((i + FLIGHT) % 8);
-            s += __shfl_xor_sync(~0u, s, 1);
-            s += __shfl_xor_sync(~0u, s, 2);
-            s += __shfl_xor_sync(~0u, s, 4);
-            if (j == i) mine = s;          // of page p + lane
+    for (int turn = 0, q0 = z.p0;; ++turn) {       // (q0: of the CTA)
+        if (!barrier_wait_for(bar, turn & 1, KDA_KV4_WAIT_NS)) {
+            if (lane == 0) report(a.err, DEVERR_TIMEOUT);
+            return;
         }
-        if (p + lane < z.p1) keys[p + lane] = key_of((float)mine, now);
-        next = later;
+        if (works) {
+            const uint4 *x = reinterpret_cast<const uint4 *>(stage + lane * apart + h * RECORD), *y = reinterpret_cast<const uint4 *>(ask + h * 2 * D);
+            int s[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 u = x[i], v = y[i];
+                s[i & 1] = __dp4a((int)u.x, (int)v.x, s[i & 1]);
+                s[i & 1] = __dp4a((int)u.y, (int)v.y, s[i & 1]);
+                s[i & 1] = __dp4a((int)u.z, (int)v.z, s[i & 1]);
+                s[i & 1] = __dp4a((int)u.w, (int)v.w, s[i & 1]);
+            }
+            if (p + lane < z.p1) keys[p + lane] = key_of((float)(s[0] + s[1]), good ? (int)*reinterpret_cast<const int8_t *>(x + D / 8) : MISSING);
+        }
+        q0 += stride, p += stride;
+        if (q0 >= z.p1) break;
+        __syncthreads();                   // all have read the stage
+        fence_async_shared();
+        fetch(p);
     }
 }
 
@@ -380,9 +385,9 @@ __global__ void __launch_bounds__(THREADS, 2) score_kernel(const KvPickArgs a) {
     constexpr int RECORD = 2 * D + 16, PARTS = D / 32;     // runs of 64 bytes of a record
     constexpr int ROW = 4 * D + 64;        // bytes of one token's asked numbers: rows that follow each other meet no bank twice
     __shared__ __align__(16) uint8_t ask[HEADS * TOKENS * ROW];
-    asm volatile("griddepcontrol.launch_dependents;");
+    wait_for_earlier_kernels();
+    let_later_kernels_in();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int guess = early_page(a, TOKENS);
     const Share z = share_of(a, TOKENS, HEADS);
     if (z.p0 >= z.p1) return;
     const int parts = (THREADS / 32) / z.heads, part = w / z.heads, h = w - part * z.heads, stride = 32 * parts;
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 2) score_kernel(const KvPickArgs a) {
     int p = z.p0 + 32 * part, pages = 0, next = 0;
     const bool works = part < parts && p < z.p1;
     if (works) {
-        pages = a.chunks * 32 >= a.max_pages ? (p + lane < z.p1 ? guess : 0) : look(p);
+        pages = look(p);
         next = look(p + stride);
         if constexpr (D == 64) load(0, pages), load(1, pages);
     }
@@ -468,8 +473,8 @@ __global__ void __launch_bounds__(THREADS, 2) score_kernel(const KvPickArgs a) {
 
 // One row (token, kv head) is W warps' work, each with 32 K neighbouring pages in its lanes' registers (K = 0: read again at
 // every step).  The count-th best key is found by narrowing an interval of keys: lo has at least as many pages at or above
-// it as are wanted, hi fewer; it ends early once there are exactly as many.  Launched beside the scores' end: what comes
-// before the wait reads nothing of theirs.
+// it as are wanted, hi fewer; it ends early once there are exactly as many.  What comes before the wait reads nothing that
+// the scores' kernel writes, and that kernel begins after all others.
 template <int W, int K>
 __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const KvPickArgs a) {
     constexpr int ROWS = W == 1 ? THREADS / 32 : 1;
@@ -478,7 +483,8 @@ __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const K
     const unsigned row = blockIdx.x * (unsigned)ROWS + (W == 1 ? w : 0);
     const int t = (int)min(row / (unsigned)a.Hkv, (unsigned)a.T);
     const Owner own = owner_with(a.cu, a.kv_lens, a.B, a.T, t);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_earlier_kernels();
+    let_later_kernels_in();
     if (own.b < 0) return;
     Tokens r{own.q0, own.end - own.q0, own.more};
     check(a, r, true);
@@ -570,16 +576,10 @@ __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const K
 template <int W, int K>
 cudaError_t pick_rows(const KvPickArgs &a, cudaStream_t s) {
     const long long rows = (long long)a.T * a.Hkv, per = W == 1 ? THREADS / 32 : 1;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)((rows + per - 1) / per));
-    c.blockDim = dim3(W == 1 ? THREADS : 32 * W);
-    c.stream = s;
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &early;
-    c.numAttrs = a.max_pages > a.count ? 1 : 0;      // (without scores there is nothing of this call's to run beside)
-    return cudaLaunchKernelEx(&c, pick_kernel<W, K>, a);
+    const dim3 grid((unsigned)((rows + per - 1) / per)), block(W == 1 ? THREADS : 32 * W);
+    if (a.max_pages > a.count) return launch_early(pick_kernel<W, K>, grid, block, 0, s, a);
+    pick_kernel<W, K><<<grid, block, 0, s>>>(a);     // (no scores: what is ahead is not known to have begun after all others)
+    return cudaGetLastError();
 }
 
 template <int D, typename T>
@@ -587,13 +587,19 @@ cudaError_t score(KvPickArgs a, cudaStream_t s) {
     const int tokens = a.max_q == 1 ? 1 : TOKENS, heads = tokens == 1 ? HEADS_1 : HEADS, groups = (a.Hkv + heads - 1) / heads;
     a.blocks = (a.max_q + tokens - 1) / tokens;
     const long long units = (long long)a.B * a.blocks * groups;
-    // 32 pages a CTA, unless that were more than some dozens an SM (with tables far wider than their rows most have nothing)
-    a.chunks = (int)max(1LL, min(SMS * (tokens == 1 ? 32LL : 4LL) / units, (a.max_pages + 31LL) / 32));
+    // one run of pages a CTA, unless that were more than some dozens an SM (with tables far wider than their rows most have
+    // nothing); several tokens: a few CTAs an SM, as each adds up its queries
+    const int run = 32 * ((THREADS / 32) / min(heads, a.Hkv));
+    a.chunks = (int)max(1LL, min(SMS * (tokens == 1 ? 32LL : 4LL) / units, ((long long)a.max_pages + run - 1) / run));
     if ((long long)a.B * a.blocks > 0x7fffffffLL || a.chunks > 65535 || groups > 65535) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)(a.B * a.blocks), (unsigned)a.chunks, (unsigned)groups);
-    if (tokens == 1) score_one_kernel<D, T><<<grid, THREADS, 0, s>>>(a);
-    else score_kernel<D, T><<<grid, THREADS, 0, s>>>(a);
-    return cudaGetLastError();
+    if (tokens == 1) {
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_shared(reinterpret_cast<const void *>(score_one_kernel<D, T>), OneShape<D>::SMEM, done);
+        if (e != cudaSuccess) return e;
+        return launch_early(score_one_kernel<D, T>, grid, dim3(THREADS), OneShape<D>::SMEM, s, a);
+    }
+    return launch_early(score_kernel<D, T>, grid, dim3(THREADS), 0, s, a);
 }
 
 }  // namespace
@@ -603,9 +609,7 @@ cudaError_t launch_kv4_bounds(KvBoundsArgs a, cudaStream_t s) {
     a.slice = a.T >= 16LL * a.B ? 16 : 1;
     const long long units = ((long long)a.T + a.slice - 1) / a.slice * a.H;
     const unsigned grid = (unsigned)((units + THREADS / 32 - 1) / (THREADS / 32));
-    if (a.D == 128) bounds_kernel<128><<<grid, THREADS, 0, s>>>(a);
-    else bounds_kernel<64><<<grid, THREADS, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(a.D == 128 ? bounds_kernel<128> : bounds_kernel<64>, dim3(grid), dim3(THREADS), 0, s, a);
 }
 
 cudaError_t launch_kv4_pick(const KvPickArgs &a, cudaStream_t s) {

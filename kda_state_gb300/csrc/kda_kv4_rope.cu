@@ -11,8 +11,10 @@
 // sin stay in registers while the thread walks over several heads of its token, with the next ones' loads in flight.
 // Products and sums run on channel pairs, each half rounded as the scalar instruction does.  A CTA has queries, keys or
 // values.  Bound by HBM for prompts, by the launch for single tokens.
+#include "kda_async.cuh"
 #include "kda_internal.h"
 #include "kda_kv4_store.cuh"
+#include "kda_launch.h"
 
 namespace kda {
 namespace {
@@ -157,6 +159,8 @@ __device__ __forceinline__ void run(const KvRopeArgs &a, unsigned block) {
 
 template <int D, typename T, bool PAIRS, int AT_ONCE>
 __global__ void __launch_bounds__(THREADS) append_rope_kernel(const KvRopeArgs a) {
+    wait_for_earlier_kernels();
+    let_later_kernels_in();
     const unsigned b = blockIdx.x;
     if (b < a.q_blocks) run<D, T, PAIRS, QUERIES, AT_ONCE>(a, b);
     else if (b - a.q_blocks < a.kv_blocks) run<D, T, PAIRS, KEYS, AT_ONCE>(a, b - a.q_blocks);
@@ -180,14 +184,10 @@ cudaError_t launch(KvRopeArgs a, cudaStream_t s) {
     a.q_blocks = (unsigned)(((long long)a.T * a.q_groups + SLOTS - 1) / SLOTS);
     a.kv_blocks = (unsigned)(((long long)a.T * a.kv_groups + SLOTS - 1) / SLOTS);
     const unsigned grid = a.q_blocks + 2 * a.kv_blocks;
-    if (eq == 1 && ekv == 1) {
-        if (a.pairs) append_rope_kernel<D, T, true, 1><<<grid, THREADS, 0, s>>>(a);
-        else append_rope_kernel<D, T, false, 1><<<grid, THREADS, 0, s>>>(a);
-    } else {
-        if (a.pairs) append_rope_kernel<D, T, true, 2><<<grid, THREADS, 0, s>>>(a);
-        else append_rope_kernel<D, T, false, 2><<<grid, THREADS, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    const bool one = eq == 1 && ekv == 1;
+    const auto kernel = a.pairs ? (one ? append_rope_kernel<D, T, true, 1> : append_rope_kernel<D, T, true, 2>)
+                                : (one ? append_rope_kernel<D, T, false, 1> : append_rope_kernel<D, T, false, 2>);
+    return launch_early(kernel, dim3(grid), dim3(THREADS), 0, s, a);
 }
 
 }  // namespace

@@ -8,8 +8,10 @@
 //
 // A row is one warp's or one CTA's, in registers from its one read on: bound by HBM (bf16: 4 bytes read, 3 or 4 written a
 // channel), and by the launch and two round trips for a row alone.
+#include "kda_async.cuh"
 #include "kda_internal.h"
 #include "kda_kv4_store.cuh"
+#include "kda_launch.h"
 
 namespace kda {
 namespace {
@@ -53,6 +55,8 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) add_rmsnorm_ker
     constexpr int ROWS = WARPS == 1 ? 4 : 1, THREADS = 32 * WARPS;
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int row = blockIdx.x * ROWS + (WARPS == 1 ? w : 0);
+    wait_for_earlier_kernels();
+    let_later_kernels_in();
     if (row >= a.tokens) return;
     const int vectors = a.C / 8;
     const T *const x_at = (const T *)a.x + row * a.x_stride, *const w_at = (const T *)a.w_norm;
@@ -155,8 +159,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) add_rmsnorm_ker
 template <typename T, int WARPS, int N>
 cudaError_t go(const AddNormArgs &a, cudaStream_t s) {
     constexpr int ROWS = WARPS == 1 ? 4 : 1;
-    add_rmsnorm_kernel<T, WARPS, N><<<(a.tokens + ROWS - 1) / ROWS, WARPS == 1 ? 128 : 32 * WARPS, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(add_rmsnorm_kernel<T, WARPS, N>, dim3((a.tokens + ROWS - 1) / ROWS), dim3(WARPS == 1 ? 128 : 32 * WARPS), 0, s, a);
 }
 
 template <typename T>
