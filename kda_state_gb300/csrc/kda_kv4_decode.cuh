@@ -178,26 +178,25 @@ struct Request {
     int q0, n, len, first_chunk, chunks, row_blocks;
     int row, own;                          // PICKED: the request that token q0 is of, and the page that it lies in
 };
-// The request that token t is of, or -1; a thread's work, which single tokens and drafts of one number make short.
-__device__ __forceinline__ int request_of_token(const KvAttentionArgs &a, int t) {
-    int b = (int)((long long)t * a.B / a.T);
-    if (a.cu[b] <= t && t < a.cu[b + 1]) return b;
-    int lo = 0, hi = a.B;                  // the first b with cu[b + 1] > t
-    while (lo < hi) {
-        b = lo + (hi - lo) / 2;
-        if (a.cu[b + 1] > t) hi = b;
-        else lo = b + 1;
-    }
-    return lo < a.B && a.cu[lo] <= t ? lo : -1;
-}
-// Token t and the pages picked for it, as a request.
+// Token t and the pages picked for it, as a request; a thread's work.  One request is guessed, the right one where all
+// have as many tokens, and all of its numbers are asked for at once.
 __device__ __forceinline__ Request request_of_picked(const KvAttentionArgs &a, int t, int rows, int chunk, bool tell) {
     Request r;
     r.q0 = t;
     r.n = r.len = r.first_chunk = r.chunks = r.row_blocks = r.own = 0;
-    r.row = request_of_token(a, t);
-    if (r.row < 0) return r;
-    const int q0 = a.cu[r.row], n = a.cu[r.row + 1] - q0, len = a.kv_lens[r.row];
+    r.row = min((int)(((float)t + 0.5f) * ((float)a.B / (float)a.T)), a.B - 1);
+    int q0 = a.cu[r.row], n = a.cu[r.row + 1] - q0, len = a.kv_lens[r.row];
+    if (q0 > t || t - q0 >= n) {
+        int lo = 0, hi = a.B;              // the first request with cu[b + 1] > t
+        while (lo < hi) {
+            const int b = lo + (hi - lo) / 2;
+            if (a.cu[b + 1] > t) hi = b;
+            else lo = b + 1;
+        }
+        if (lo >= a.B || a.cu[lo] > t) return r;
+        r.row = lo;
+        q0 = a.cu[lo], n = a.cu[lo + 1] - q0, len = a.kv_lens[lo];
+    }
     if (q0 < 0 || n > a.max_q || (long long)q0 + n > a.T || len < 0 || (long long)len > ((long long)a.max_pages << a.page_shift)) {
         if (tell) report(a.err, DEVERR_SEQLENS);
         return r;
