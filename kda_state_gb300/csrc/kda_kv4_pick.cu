@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(THREADS) bounds_kernel(const KvBoundsArgs a) {
 // scores
 // ---------------------------------------------------------------------------
 
-constexpr int HEADS_1 = 8, HEADS = 4;      // kv heads that a CTA takes with single tokens, and with several
+constexpr int HEADS_1 = 8, HEADS = 2;      // kv heads that a CTA takes with single tokens, and with several
 constexpr int TOKENS = 8;                  // several
 constexpr int MISSING = 1000;              // in place of a unit: a page out of range, whose key is 1 (below every score; 0 is no page)
 
@@ -381,7 +381,7 @@ __device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &
 // 127 are exact, and so are their sums below 2^23.  The contraction may be permuted if both operands agree, so that a
 // lane's share of a record is whole 16-byte words, four lanes beside each other.
 template <int D, typename T>
-__global__ void __launch_bounds__(THREADS, 2) score_kernel(const KvPickArgs a) {
+__global__ void __launch_bounds__(THREADS, D == 64 ? 3 : 2) score_kernel(const KvPickArgs a) {
     constexpr int RECORD = 2 * D + 16, PARTS = D / 32;     // runs of 64 bytes of a record
     constexpr int ROW = 4 * D + 64;        // bytes of one token's asked numbers: rows that follow each other meet no bank twice
     __shared__ __align__(16) uint8_t ask[HEADS * TOKENS * ROW];
@@ -434,6 +434,9 @@ __global__ void __launch_bounds__(THREADS, 2) score_kernel(const KvPickArgs a) {
     if (!works) return;
     if constexpr (D == 128) load(0, pages), load(1, pages);        // (registers are short before)
     const uint4 *const y = reinterpret_cast<const uint4 *>(ask + (h * TOKENS + r) * ROW) + c;
+    uint32_t *const keys = a.keys + ((size_t)(z.q0 + 2 * c) * a.Hkv + z.h0 + h) * a.key_stride;      // of tokens 2 c and 2 c + 1
+    const size_t row = (size_t)a.Hkv * a.key_stride;
+    const bool has[2] = {2 * c < z.nt, 2 * c + 1 < z.nt};
     for (; p < z.p1; p += stride) {
         const int later = look(p + 2 * stride);
 #pragma unroll
@@ -457,10 +460,12 @@ __global__ void __launch_bounds__(THREADS, 2) score_kernel(const KvPickArgs a) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int of = p + 16 * s + 8 * k + r, pe = __shfl_sync(~0u, e, 8 * k + r);
+                const float per = power_of(pe);
+                const bool plain = pe < UNBOUNDED, there = of < z.p1;
+                const uint32_t other = key_of(0.f, pe);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
-                    if (2 * c + n < z.nt && of < z.p1)
-                        a.keys[((size_t)(z.q0 + 2 * c + n) * a.Hkv + z.h0 + h) * a.key_stride + of] = key_of(d[2 * k + n], pe);
+                    if (has[n] && there) keys[n * row + of] = plain ? ordered(d[2 * k + n] * per) : other;
             }
         }
         next = later;
@@ -511,10 +516,15 @@ __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const K
 #pragma unroll
         for (int i = 0; i < K; ++i) key[i] = at(i);
     }
+    const int ours = to - (p0 - lane);     // pages of the warp's that there are
     auto each = [&](const auto &f) {       // f(number, key)
         if constexpr (K > 0) {
 #pragma unroll
-            for (int i = 0; i < K; ++i) f(i, key[i]);
+            for (int b = 0; b < K; b += 4) {
+                if (32 * b >= ours) break;
+#pragma unroll
+                for (int i = b; i < b + 4; ++i) f(i, key[i]);
+            }
         } else {
             for (int i = 0; i < span; ++i) f(i, at(i));
         }
