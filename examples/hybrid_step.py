@@ -1,12 +1,15 @@
 """Serving steps of a small hybrid model: a KDA layer's recurrent state beside an attention
 layer's paged 4-bit cache, for one batch of requests.
 
-    python examples/hybrid_step.py [--requests 6] [--steps 4] [--seed 0]
+    python examples/hybrid_step.py [--requests 6] [--steps 4] [--seed 0] [--pick COUNT]
 
 Per step every request decodes one token through both layers.  Around the steps: prompts in
 pieces, a fork (copy-on-write of pages and of the state slot), a verify of draft tokens of which
 a part is accepted, requests that end, and a compaction that hands the pool's upper pages back.
 Projections are random numbers: the example shows the calls and their order.
+
+With --pick the attention layer begins with the residual's addition and norm, rotates its queries
+and keys on their way into the cache, and reads COUNT pages of each row that a score picks.
 """
 import argparse
 import os
@@ -98,14 +101,62 @@ class Hybrid:
         return kda.kda_page_compact([self.pool], self.refs, self.table, dev_err=self.err)
 
 
+class SparseHybrid(Hybrid):
+    """The same with an attention layer that adds and norms the residual stream, rotates, and reads `count` pages."""
+
+    def __init__(self, rows, count, seed=0):
+        super().__init__(rows, seed)
+        self.count = count
+        self.bounds = kda.make_kv4_bounds(PAGES, HKV, D, DEV)
+        self.rope = kda.make_rope_table(MAX_PAGES * PAGE, D, device=DEV)
+        self.norm = 1 + 0.1 * self.rand(HQ * D)
+        self.proj = self.rand(HQ * D, (HQ + 2 * HKV) * D) / (HQ * D) ** 0.5
+        self.residual = None
+
+    def attend(self, rows, new):
+        cu = i32([0] + torch.tensor(new).cumsum(0).tolist())
+        grow = torch.zeros_like(self.lens)
+        grow[rows.long()] = i32(new)
+        kda.kda_page_alloc(self.refs, self.table, self.lens, grow, PAGE, dev_err=self.err)
+        table, lens, T = self.table[rows.long()], self.lens[rows.long()], sum(new)
+        start = lens - i32(new)
+        self.residual = self.rand(T, HQ * D)
+        y, scales, _ = kda.kda_add_rmsnorm(self.rand(T, HQ * D), self.residual, self.norm, scales="block", residual_out=self.residual)
+        y = (y.float().view(T, -1, 128) * scales[..., None]).view(T, -1).to(torch.bfloat16)      # an 8-bit product's operands
+        qkv = (y @ self.proj).view(T, HQ + 2 * HKV, D)
+        q, k, v = qkv[:, :HQ], qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:]
+        q = kda.kda_kv4_append_rope(q, k, v, self.rope, cu, start, table, self.pool, q_out=q, dev_err=self.err)
+        kda.kda_kv4_bounds(cu, start, T, table, self.pool, self.bounds, dev_err=self.err)
+        self.picked = kda.kda_kv4_pick(q, cu, max(new), lens, table, self.bounds, PAGE, self.count, dev_err=self.err)
+        o, lse = kda.kda_kv4_attention_picked(q, cu, max(new), lens, table, self.picked, self.pool, workspace=self.workspace,
+                                              dev_err=self.err)
+        return q, k, v, o, lse
+
+    def rebound(self, rows):
+        """The records of all pages that rows hold, anew: a fork's copied page has none, and a compaction moves pages alone."""
+        lens = self.lens[rows.long()]
+        cu = i32([0] + lens.cumsum(0).tolist())
+        kda.kda_kv4_bounds(cu, torch.zeros_like(lens), int(cu[-1]), self.table[rows.long()], self.pool, self.bounds, dev_err=self.err)
+
+    def fork(self, src, dst):
+        super().fork(src, dst)
+        self.rebound(dst)
+
+    def compact(self):
+        live = super().compact()
+        self.rebound(torch.arange(self.lens.numel(), dtype=torch.int32, device=DEV))
+        return live
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--requests", type=int, default=6)
     ap.add_argument("--steps", type=int, default=4)
     ap.add_argument("--seed", type=int, default=0)
+    ap.add_argument("--pick", type=int, default=0, help="pages that a token's attention reads (0: all)")
     a = ap.parse_args(argv)
     n = a.requests
-    m = Hybrid(n + 2, a.seed)
+    m = SparseHybrid(n + 2, a.pick, a.seed) if a.pick else Hybrid(n + 2, a.seed)
     rows = i32(list(range(n)))
     m.prompt(rows, [37 + 61 * i for i in range(n)])
     for _ in range(a.steps):

@@ -309,6 +309,18 @@ def test_picks_in_tables_wider_than_every_kernel():
     assert np.array_equal(got[0, 0], np.sort(np.lexsort((np.arange(33000), -s))[:100]))
 
 
+@pytest.mark.parametrize("H,news", [(8, [1] * 80), (2, [2] * 80)])
+def test_picks_of_many_requests_in_a_wide_table(H, news):
+    """More chunks of pages than CTAs are launched: a CTA takes several runs of a long row."""
+    rng = np.random.default_rng(13)
+    lens = [int(x) for x in rng.integers(2, 400, 80)]
+    lens[3], lens[40], lens[79] = 2099 * 16, 700 * 16 - 3, 1000 * 16 + 1
+    rec, table = random_bounds(lens, H, 64, 16, 14)
+    q = packed_q(news, 2 * H, 64, BF, 15)
+    got, err = pick(q, news, lens, rec, table, 16, 9, 1, 2)
+    assert err == 0 and np.array_equal(got, picks_of(q, news, lens, rec, table, 16, 9, 1, 2))
+
+
 def test_picks_of_queries_that_are_not_numbers():
     lens = [640, 640, 640, 640]
     rec, table = random_bounds(lens, 1, 64, 16, 9)
