@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const K
     uint32_t lo = ~total(low, true), hi = total(high, true) + 1, have = (uint32_t)(to - from), fewer = 0;
     for (bool even = true; hi - lo > 1 && have != (uint32_t)want; even = !even) {
         // in turn where the counts at both ends would have it, and in the middle, so that it ends soon on any keys
-        const float part = even ? (float)(have - want) / (float)(have - fewer) : 0.5f;
+        const float part = even ? __fdividef((float)(have - want), (float)(have - fewer)) : 0.5f;
         const uint32_t mid = lo + min(max((uint32_t)((float)(hi - lo) * part), 1u), hi - lo - 1);
         uint32_t n = 0;
         each([&](int, uint32_t k) { n += k >= mid; });
