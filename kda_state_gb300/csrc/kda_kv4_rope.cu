@@ -106,7 +106,10 @@ __device__ __forceinline__ void run(const KvRopeArgs &a, unsigned block) {
     }
     const int partner = PAIRS || !turns ? (int)(threadIdx.x & 31) : (int)(threadIdx.x & 31) + (lower ? turn : -turn);
     const float inv = ROLE == KEYS ? a.k_inv : a.v_inv;
-    int n = t < a.T ? (heads - g + groups - 1) / groups : 0;              // heads of this thread that are still to be written
+    int n = out ? (heads - g + groups - 1) / groups : 0;                  // heads of this thread that are still to be written
+    if (ROLE == QUERIES && !angles) {      // (out: the token is a request's)
+        for (; n > 0; --n, out += out_step) *reinterpret_cast<uint4 *>(out) = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll 1
     for (int done = 0; done < turns_of_loop; done += AT_ONCE) {
         uint4 now[AT_ONCE];
@@ -138,7 +141,7 @@ __device__ __forceinline__ void run(const KvRopeArgs &a, unsigned block) {
                 }
             }
             if constexpr (ROLE == QUERIES) {
-                if (out && n > 0) *reinterpret_cast<uint4 *>(out) = angles ? w : make_uint4(0, 0, 0, 0);
+                if (n > 0) *reinterpret_cast<uint4 *>(out) = w;
             } else {
                 float x[8], top = 0.f, one_over;
                 unpack16(w, x, T());
@@ -146,12 +149,12 @@ __device__ __forceinline__ void run(const KvRopeArgs &a, unsigned block) {
                 for (int k = 0; k < 8; ++k) x[k] *= inv, top = max_nan(top, fabsf(x[k]));
                 top = max_nan(top, __shfl_xor_sync(~0u, top, 1));
                 const uint32_t sb = scale_of(top, one_over), code = codes_of(x, sb, one_over);
-                if (out && n > 0) {
+                if (n > 0) {
                     *reinterpret_cast<uint32_t *>(out + (ROLE == VALUES ? L::VC : L::KC) + tok * (D / 2) + j * 4) = code;
                     if ((j & 1) == 0) out[ROLE == VALUES ? L::VS + (j >> 1) * KV_TILE + tok : L::KS + tok * L::BLOCKS + (j >> 1)] = (uint8_t)sb;
                 }
             }
-            if (out) out += out_step;
+            out += out_step;
             --n;
         }
     }
