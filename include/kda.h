@@ -663,7 +663,8 @@ KDA_API size_t kda_kv4_pick_workspace_bytes(int total_tokens, int H_kv, int max_
  *               same time need one each
  * Requests with inconsistent numbers are skipped as in kda_kv4_attention, a token
  * at a negative position sees none; pages out of range come after all others
- * (KDA_DEVERR_PAGE_RANGE).
+ * (KDA_DEVERR_PAGE_RANGE).  After KDA_DEVERR_TIMEOUT the picks are not valid, and the
+ * error is fatal for the context as in the other calls.
  */
 KDA_API int kda_kv4_pick(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv, int D,
                          const void *q, long long q_stride, const int32_t *cu_seqlens,

