@@ -1,5 +1,6 @@
 """Build libkda.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, linked
-with the static CUDA runtime (the library then loads on hosts without a driver)."""
+with the static CUDA runtime (the library then loads on hosts without a driver); and
+_quick.so, the plain calls' way from Python to it (csrc/kda_quick.cpp), beside it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -7,11 +8,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkda.so")
+QUICK = os.path.join(HERE, "_quick.so")
+QUICK_SOURCE = os.path.join(CSRC, "kda_quick.cpp")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -31,15 +35,32 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+    return _sources() + [QUICK_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
         os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "kda.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(QUICK):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(QUICK))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _compile_quick():
+    """_quick.so against this interpreter's and this torch's headers and libraries."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = QUICK + ".%d.tmp" % os.getpid()
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + ["-isystem" + d for d in dirs] +
+           [QUICK_SOURCE, "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (QUICK_SOURCE, " ".join(cmd), r.stderr))
+    return tmp, r.stderr
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -58,7 +79,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        quick = ex.submit(_compile_quick)
         results = list(ex.map(compile_one, _sources()))
+        quick_tmp, _ = quick.result()
     if verbose or ptxas_info:
         for obj, log in results:
             if log.strip():
@@ -69,6 +92,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, LIB)
+    os.replace(quick_tmp, QUICK)
     return LIB
 
 

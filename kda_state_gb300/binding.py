@@ -17,6 +17,8 @@ from __future__ import annotations
 
 import array
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -24,6 +26,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
+QUICK_PATH = os.path.join(_HERE, "_quick.so")
 
 KDA_OK = 0
 KDA_ERR_INVALID_ARG = -1
@@ -49,6 +52,20 @@ V_DIM = 128
 _DT = {torch.bfloat16: KDA_DTYPE_BF16, torch.float32: KDA_DTYPE_FP32}
 
 _lib = None
+# The plain calls' way to the library (csrc/kda_quick.cpp), once that is loaded: it does what the functions here do for
+# exact torch tensors on the current device and stream, and returns None for whatever it does not take.
+_quick = None
+
+
+def _load_quick(L):
+    if not os.path.exists(QUICK_PATH):
+        raise RuntimeError("_quick.so is not built (%s); run __graft_entry__.build()" % QUICK_PATH)
+    loader = importlib.machinery.ExtensionFileLoader("_quick", QUICK_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_quick", QUICK_PATH, loader=loader))
+    loader.exec_module(module)
+    module.bind(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+        L.kda_add_rmsnorm, L.kda_kv4_append_rope, L.kda_kv4_bounds, L.kda_kv4_pick, L.kda_kv4_attention_picked)])
+    return module
 
 
 class KdaError(RuntimeError):
@@ -65,7 +82,7 @@ class kda_ring(ctypes.Structure):
 
 def lib() -> ctypes.CDLL:
     """Load libkda.so (built by ``kda_state_gb300._build.build()``)."""
-    global _lib
+    global _lib, _quick
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError("libkda.so is not built (%s); run __graft_entry__.build()" % LIB_PATH)
@@ -136,6 +153,7 @@ def lib() -> ctypes.CDLL:
             getattr(L, fn).restype = ctypes.c_int
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
+        _quick = _load_quick(L)
         _lib = L
     return _lib
 
@@ -635,6 +653,10 @@ def kda_add_rmsnorm(x, residual, weight, eps: float = EPS_NORM, scales: str = "n
     y = weight * h / sqrt(mean h^2 + eps).  ``scales``: "none" for y in the dtype, "row" or "block" for
     e4m3 codes with fp32 scales of a row [T] or of 128 channels [T, ceil(C / 128)].  Returns (out,
     scales or None, h); ``residual_out`` takes h and may be ``residual`` itself."""
+    if _quick is not None and stream is None and out is None and scales_out is None and scales in _NORM_OUT:
+        done = _quick.add_rmsnorm(x, residual, weight, eps, _NORM_OUT[scales], residual_out)
+        if done is not None:
+            return done
     shape, dev = _first(x, "x", 2)
     dtype = x.dtype
     if dtype not in _NORM_DT:
@@ -967,6 +989,10 @@ def kda_kv4_append_rope(q, k, v, rope, cu_seqlens, start, page_table, pool, pair
     each head of q [T, H_q, D] and k turn by their token's row of ``rope`` (fp32 [positions, R]:
     ``make_rope_table``), as pairs (c, c + R / 2) or, with ``pairs``, (2 c, 2 c + 1).  q, k and v may be views
     of a fused projection's output.  Returns the rotated q; ``q_out`` takes it and may be q itself."""
+    if _quick is not None and stream is None:
+        done = _quick.append_rope(q, k, v, rope, cu_seqlens, start, page_table, pool, pairs, k_scale, v_scale, q_out, dev_err)
+        if done is not None:
+            return done
     shape, dev = _first(q, "q", 3)
     dtype = q.dtype
     dt = _kv_dt(dtype)
@@ -1006,6 +1032,8 @@ def make_kv4_bounds(num_pages: int, H_kv: int, D: int = K_DIM, device="cuda"):
 def kda_kv4_bounds(cu_seqlens, start, total_tokens: int, page_table, pool, bounds, dev_err=None, stream=None):
     """Bring the records of the pages up to date that hold positions start[b] .. of each request's new tokens
     (cu_seqlens int32 [B + 1]), after those were appended.  ``bounds``: ``make_kv4_bounds()``, in place."""
+    if _quick is not None and stream is None and _quick.bounds(cu_seqlens, start, total_tokens, page_table, pool, bounds, dev_err):
+        return
     shape, dev = _first(pool, "pool", 4)
     D = shape[3] // 18
     pa, pages, H, page_size = _pool(pool, D, dev)
@@ -1030,6 +1058,10 @@ def kda_kv4_pick(q, cu_seqlens, max_q: int, kv_lens, page_table, bounds, page_si
     ``kda_kv4_attention``; ``bounds`` from ``kda_kv4_bounds``.  Returns int32 [T, H_kv, count]: numbers of pages in
     the request's row, ascending, then -1.  ``workspace``: uint8, ``kv4_pick_workspace_bytes(T, H_kv, max_pages)`` at
     least, kept by the caller (one for each stream); a call without one makes its own."""
+    if _quick is not None and stream is None and picked is None and workspace is not None:
+        done = _quick.pick(q, cu_seqlens, max_q, kv_lens, page_table, bounds, page_size, count, first, recent, workspace, dev_err)
+        if done is not None:
+            return done
     shape, dev = _first(q, "q", 3)
     dtype = q.dtype
     dt = _kv_dt(dtype)
@@ -1062,6 +1094,11 @@ def kda_kv4_attention_picked(q, cu_seqlens, max_q: int, kv_lens, page_table, pic
                              dev_err=None, stream=None):
     """``kda_kv4_attention`` over the pages that ``picked`` (int32 [T, H_kv, count], of ``kda_kv4_pick``) names for
     each token and kv head.  Returns (o, lse)."""
+    if _quick is not None and stream is None and o is None and lse is None and workspace is not None:
+        done = _quick.attention_picked(q, cu_seqlens, max_q, kv_lens, page_table, picked, pool, scale, k_scale, v_scale, workspace,
+                                       dev_err)
+        if done is not None:
+            return done
     shape, dev = _first(q, "q", 3)
     dtype = q.dtype
     dt = _kv_dt(dtype)
