@@ -64,7 +64,8 @@ def _load_quick(L):
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_quick", QUICK_PATH, loader=loader))
     loader.exec_module(module)
     module.bind(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in (
-        L.kda_add_rmsnorm, L.kda_kv4_append_rope, L.kda_kv4_bounds, L.kda_kv4_pick, L.kda_kv4_attention_picked)])
+        L.kda_add_rmsnorm, L.kda_kv4_append_rope, L.kda_kv4_bounds, L.kda_kv4_pick, L.kda_kv4_attention_picked,
+        L.kda_kv4_append, L.kda_kv4_gather, L.kda_kv4_attention)])
     return module
 
 
@@ -883,6 +884,8 @@ def kda_kv4_append(k, v, cu_seqlens, start, page_table, pool, k_scale: float = 1
     strided) as 4-bit codes: token i of request b at position start[b] + i of the
     pages that row b of page_table (int32 [B, max_pages]) names.  cu_seqlens int32
     [B + 1], start int32 [B]; the scales are powers of two.  Writes the pool in place."""
+    if _quick is not None and stream is None and _quick.append(k, v, cu_seqlens, start, page_table, pool, k_scale, v_scale, dev_err):
+        return
     shape, dev = _first(k, "k", 3)
     dtype = k.dtype
     dt = _kv_dt(dtype)
@@ -905,6 +908,10 @@ def kda_kv4_gather(cu_seqlens, start, total_tokens: int, page_table, pool, dtype
                    stream=None):
     """Read tokens back as the values they stand for: positions start[b] + i of request b
     into packed k, v [total_tokens, H_kv, D].  Returns (k, v)."""
+    if _quick is not None and stream is None and k is None and v is None:
+        done = _quick.gather(cu_seqlens, start, total_tokens, page_table, pool, dtype, k_scale, v_scale, dev_err)
+        if done is not None:
+            return done
     dt = _kv_dt(dtype)
     shape, dev = _first(pool, "pool", 4)
     D, T = shape[3] // 18, int(total_tokens)
@@ -941,6 +948,10 @@ def kda_kv4_attention(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, scal
     defaults to D ** -0.5.  ``workspace``: ``make_kv4_workspace()``, kept by the caller
     (one for each stream); a call without one makes its own.  Returns (o, lse), o in
     q's dtype and lse fp32 [T, H_q]; a row that sees nothing has o = 0, lse = -inf."""
+    if _quick is not None and stream is None and o is None and lse is None and workspace is not None:
+        done = _quick.attention(q, cu_seqlens, max_q, kv_lens, page_table, pool, scale, window, k_scale, v_scale, workspace, dev_err)
+        if done is not None:
+            return done
     shape, dev = _first(q, "q", 3)
     dtype = q.dtype
     dt = _kv_dt(dtype)

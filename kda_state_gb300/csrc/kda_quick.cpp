@@ -1,4 +1,4 @@
-// The plain calls of the operators around the cache's attention, from Python to the C entry points.
+// The plain calls of the cache and of the operators around its attention, from Python to the C entry points.
 //
 // A single token's kernels are done in a few microseconds, and a call's checks and buffers, step by step in Python, take
 // three times as long.  What is here does them for the usual call: exact torch tensors on the current device, of the
@@ -10,6 +10,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/kda.h"
@@ -21,6 +22,9 @@ decltype(&kda_kv4_append_rope) append_rope_fn;
 decltype(&kda_kv4_bounds) bounds_fn;
 decltype(&kda_kv4_pick) pick_fn;
 decltype(&kda_kv4_attention_picked) attention_picked_fn;
+decltype(&kda_kv4_append) append_fn;
+decltype(&kda_kv4_gather) gather_fn;
+decltype(&kda_kv4_attention) attention_fn;
 
 // What the arguments of one call were found to be; `good` goes false at the first that is not plain.
 struct Call {
@@ -290,14 +294,94 @@ PyObject *attention_picked(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of the five entry points, in this order)
+// (k, v, cu_seqlens, start, page_table, pool, k_scale, v_scale, dev_err or None); True where it was done
+PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 9) return none();
+    return plain([&]() -> PyObject * {
+        Call c;
+        const at::Tensor *k = c.first(a[0], 3);
+        if (!k) return none();
+        const auto type = k->scalar_type();
+        const int64_t T = k->size(0), H = k->size(1), D = k->size(2);
+        const Pool pool = pool_of(c, a[5], D);
+        const Table table = table_of(c, a[4]);
+        if (!c.good || kv_type(type) < 0 || pool.heads != H || T > INT_MAX) return none();
+        long long ks, vs;
+        void *kp = c.rows(k, ks), *vp = c.rows(c.like(a[1], type, {T, H, D}), vs);
+        void *cp = c.at(a[2], at::kInt, {table.B + 1}), *sp = c.at(a[3], at::kInt, {table.B});
+        const double k_scale = c.number(a[6]), v_scale = c.number(a[7]);
+        int32_t *err = c.error(a[8]);
+        if (!c.good || append_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, (int)H, (int)D, kp, ks, vp, vs, (const int32_t *)cp,
+                                 (const int32_t *)sp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, (float)k_scale,
+                                 (float)v_scale, err, c.stream()) != KDA_OK)
+            return none();
+        Py_RETURN_TRUE;
+    });
+}
+
+// (cu_seqlens, start, total_tokens, page_table, pool, dtype, k_scale, v_scale, dev_err or None)
+PyObject *gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 9) return none();
+    return plain([&]() -> PyObject * {
+        Call c;
+        const at::Tensor *p = c.first(a[4], 4);
+        if (!p || !THPDtype_Check(a[5])) return none();
+        const auto type = ((THPDtype *)a[5])->scalar_type;
+        const int64_t D = p->size(3) / 18;
+        const Pool pool = pool_of(c, a[4], D);
+        const Table table = table_of(c, a[3]);
+        const int T = c.integer(a[2]);
+        void *cp = c.at(a[0], at::kInt, {table.B + 1}), *sp = c.at(a[1], at::kInt, {table.B});
+        const double k_scale = c.number(a[6]), v_scale = c.number(a[7]);
+        int32_t *err = c.error(a[8]);
+        if (!c.good || kv_type(type) < 0 || T < 0) return none();
+        at::Tensor k = c.make({T, pool.heads, D}, type), v = c.make({T, pool.heads, D}, type);
+        if (gather_fn((kda_dtype)kv_type(type), (int)table.B, T, pool.heads, (int)D, k.data_ptr(), v.data_ptr(), (const int32_t *)cp,
+                      (const int32_t *)sp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, (float)k_scale, (float)v_scale, err,
+                      c.stream()) != KDA_OK)
+            return none();
+        return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
+    });
+}
+
+// (q, cu_seqlens, max_q, kv_lens, page_table, pool, scale or None, window, k_scale, v_scale, workspace, dev_err or None)
+PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 12) return none();
+    return plain([&]() -> PyObject * {
+        Call c;
+        const at::Tensor *q = c.first(a[0], 3);
+        if (!q) return none();
+        const auto type = q->scalar_type();
+        const int64_t T = q->size(0), Hq = q->size(1), D = q->size(2);
+        const Pool pool = pool_of(c, a[5], D);
+        const Table table = table_of(c, a[4]);
+        const at::Tensor *w = c.exact(a[10]);
+        if (!c.good || kv_type(type) < 0 || w->dim() != 1) return none();
+        const int64_t wb = w->size(0);
+        long long qs;
+        void *qp = c.rows(q, qs), *wp = c.at(a[10], at::kByte, {wb});
+        void *cp = c.at(a[1], at::kInt, {table.B + 1}), *lp = c.at(a[3], at::kInt, {table.B});
+        const int max_q = c.integer(a[2]), window = c.integer(a[7]);
+        const double scale = a[6] == Py_None ? 1.0 / std::sqrt((double)D) : c.number(a[6]), k_scale = c.number(a[8]), v_scale = c.number(a[9]);
+        int32_t *err = c.error(a[11]);
+        if (!c.good || T > INT_MAX) return none();
+        at::Tensor o = c.make({T, Hq, D}, type), lse = c.make({T, Hq}, at::kFloat);
+        if (attention_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, max_q, (int)Hq, pool.heads, (int)D, qp, qs, (const int32_t *)cp,
+                         (const int32_t *)lp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, window, (float)scale, (float)k_scale,
+                         (float)v_scale, o.data_ptr(), lse.data_ptr<float>(), wp, (size_t)wb, err, c.stream()) != KDA_OK)
+            return none();
+        return Py_BuildValue("NN", THPVariable_Wrap(o), THPVariable_Wrap(lse));
+    });
+}
+
+// bind(addresses of the eight entry points, in this order)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "five addresses");
+    if (n != 8) {
+        PyErr_SetString(PyExc_TypeError, "eight addresses");
         return nullptr;
     }
-    void *p[5];
-    for (int i = 0; i < 5; ++i) {
+    void *p[8];
+    for (int i = 0; i < 8; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no address");
@@ -309,11 +393,15 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     bounds_fn = (decltype(bounds_fn))p[2];
     pick_fn = (decltype(pick_fn))p[3];
     attention_picked_fn = (decltype(attention_picked_fn))p[4];
+    append_fn = (decltype(append_fn))p[5];
+    gather_fn = (decltype(gather_fn))p[6];
+    attention_fn = (decltype(attention_fn))p[7];
     Py_RETURN_NONE;
 }
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(add_rmsnorm), FAST(append_rope), FAST(bounds), FAST(pick), FAST(attention_picked), FAST(bind),
+PyMethodDef methods[] = {FAST(add_rmsnorm), FAST(append_rope), FAST(bounds), FAST(pick), FAST(attention_picked), FAST(append),
+                         FAST(gather), FAST(attention), FAST(bind),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_quick", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
