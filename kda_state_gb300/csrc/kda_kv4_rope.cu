@@ -162,36 +162,39 @@ __device__ __forceinline__ void run(const KvRopeArgs &a, unsigned block) {
     }
 }
 
-template <int D, typename T, bool PAIRS, int AT_ONCE>
+template <int D, typename T, bool PAIRS, int Q_AT_ONCE, int KV_AT_ONCE>
 __global__ void __launch_bounds__(THREADS) append_rope_kernel(const KvRopeArgs a) {
     wait_for_earlier_kernels();
     let_later_kernels_in();
     const unsigned b = blockIdx.x;
-    if (b < a.q_blocks) run<D, T, PAIRS, QUERIES, AT_ONCE>(a, b);
-    else if (b - a.q_blocks < a.kv_blocks) run<D, T, PAIRS, KEYS, AT_ONCE>(a, b - a.q_blocks);
-    else run<D, T, PAIRS, VALUES, AT_ONCE>(a, b - a.q_blocks - a.kv_blocks);
+    if (b < a.q_blocks) run<D, T, PAIRS, QUERIES, Q_AT_ONCE>(a, b);
+    else if (b - a.q_blocks < a.kv_blocks) run<D, T, PAIRS, KEYS, KV_AT_ONCE>(a, b - a.q_blocks);
+    else run<D, T, PAIRS, VALUES, KV_AT_ONCE>(a, b - a.q_blocks - a.kv_blocks);
 }
 
 template <int D, typename T>
 cudaError_t launch(KvRopeArgs a, cudaStream_t s) {
     constexpr int SLOTS = THREADS / (D / 8);
-    // One head a thread while that does not fill the GPU, then up to 16 of q and 4 of k and v, two at once, whose cos and sin
-    // are read once (prompts of 9.6 K tokens, 64 / 8 heads: 73 us with 16, 76 with 8, 83 with 4, 86 one at once; 384 single
-    // tokens: 7.6 us one a thread, 8.7 two at once).
+    // Heads a thread: as many as leave a CTA an SM, up to 8, and as leave two beyond, up to 32; its cos and sin are read once,
+    // and one start's chain of loads serves them all.  64 / 8 heads of 128, single tokens of 128 requests 3.4 us, one head a
+    // thread 4.8; of 384 4.5 (8 a thread), 7.6 (1); 1.3 K tokens 9.6 (16 a thread), 13.7 (32: a CTA an SM), 13.6 (8 of q, 1 of
+    // k and v); 9.6 K tokens 62 (32), 64 (16), 76 (8 and 4).
     auto each = [&](int heads, int most) {
-        const long long fill = (long long)a.T * heads / (SLOTS * 152 * 8);
+        const long long all = (long long)a.T * heads / (SLOTS * 152), fill = all < 8 ? all : all / 2 < 8 ? 8 : all / 2;
         return (int)(fill < 1 ? 1 : fill > most ? most : fill);
     };
     a.minus_zero = -0.f;
-    const int eq = each(a.Hq, 16), ekv = each(a.Hkv, 4);
+    const int eq = each(a.Hq, 32), ekv = each(a.Hkv, 8);
     a.q_groups = (a.Hq + eq - 1) / eq, a.kv_groups = (a.Hkv + ekv - 1) / ekv;
     a.q_each = (a.Hq + a.q_groups - 1) / a.q_groups, a.kv_each = (a.Hkv + a.kv_groups - 1) / a.kv_groups;
     a.q_blocks = (unsigned)(((long long)a.T * a.q_groups + SLOTS - 1) / SLOTS);
     a.kv_blocks = (unsigned)(((long long)a.T * a.kv_groups + SLOTS - 1) / SLOTS);
     const unsigned grid = a.q_blocks + 2 * a.kv_blocks;
-    const bool one = eq == 1 && ekv == 1;
-    const auto kernel = a.pairs ? (one ? append_rope_kernel<D, T, true, 1> : append_rope_kernel<D, T, true, 2>)
-                                : (one ? append_rope_kernel<D, T, false, 1> : append_rope_kernel<D, T, false, 2>);
+    const bool q1 = a.q_each == 1, kv1 = a.kv_each == 1;
+    const auto kernel = a.pairs ? (q1 ? (kv1 ? append_rope_kernel<D, T, true, 1, 1> : append_rope_kernel<D, T, true, 1, 2>)
+                                      : (kv1 ? append_rope_kernel<D, T, true, 2, 1> : append_rope_kernel<D, T, true, 2, 2>))
+                                : (q1 ? (kv1 ? append_rope_kernel<D, T, false, 1, 1> : append_rope_kernel<D, T, false, 1, 2>)
+                                      : (kv1 ? append_rope_kernel<D, T, false, 2, 1> : append_rope_kernel<D, T, false, 2, 2>));
     return launch_early(kernel, dim3(grid), dim3(THREADS), 0, s, a);
 }
 
