@@ -10,9 +10,9 @@
 // largest of a block of 16 from the lane beside, so that each value is read once and q may be turned in place.  cos and
 // sin stay in registers while the thread walks over several heads of its token, with the next ones' loads in flight.
 // Products and sums run on channel pairs, each half rounded as the scalar instruction does.  A CTA has queries, keys or
-// values.  Prompts of 9.6 K tokens, 64 / 8 heads: 73 us, of which queries alone 53 (6.0 TB/s, 0.88 of the copy bandwidth
-// measured) and keys and values 20, bound by the arithmetic of their codes; mixing the CTAs of both changes nothing.  384
-// single tokens: 7.6 us, the launch and three rounds of loads.
+// values.  Prompts of 9.6 K tokens, 64 / 8 heads: 62 us, 5.8 TB/s (0.86 of the copy bandwidth measured), the queries' bytes
+// alone 46; the rest is the arithmetic of keys' and values' codes.  384 single tokens: 4.5 us, the launch and three rounds
+// of loads.
 #include "kda_async.cuh"
 #include "kda_internal.h"
 #include "kda_kv4_store.cuh"
