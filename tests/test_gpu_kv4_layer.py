@@ -598,6 +598,52 @@ def test_a_step_in_graphs_that_take_turns():
             m.check(*out)
 
 
+def test_graphs_that_share_workspaces_run_one_after_the_other():
+    a, b = Layer([500, 77], [1, 1], 16, 5, 6), Layer([90, 400, 33], [2, 3, 1], 32, 3, 7)
+    b.ws, b.pick_ws = a.ws, torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    a.pick_ws = b.pick_ws
+    graphs = []
+    for m in (a, b):
+        m.step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = m.step()
+        graphs.append((g, out))
+    for turn in range(3):
+        for m in (a, b):
+            m.x.normal_()
+        for g, _ in graphs[::-1] if turn % 2 else graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for m, (_, out) in zip((a, b), graphs):
+            m.check(*out)
+
+
+def test_pages_past_4_gigabytes(ws):
+    """The same step with its pages at the far end of a pool of 6 GB."""
+    k, H, D, P, pages = kda(), 8, 128, 256, 20000
+    far = torch.zeros(pages, H, P // 16, 18 * D, dtype=torch.uint8, device=DEV)
+    near = far[:12].clone()
+    g = torch.Generator(device=DEV).manual_seed(8)
+    T = 12 * P
+    qkv = torch.randn(T, 24, D, generator=g, device=DEV).to(BF)
+    rope, cu, start, lens = k.make_rope_table(T, D), i32([0, T]), i32([0]), i32([T])
+    outs = []
+    for pool, table in ((far, torch.arange(pages - 12, pages, dtype=torch.int32, device=DEV)[None]), (near, torch.arange(12, dtype=torch.int32, device=DEV)[None])):
+        err = new_err()
+        bounds = k.make_kv4_bounds(len(pool), H, D)
+        q = k.kda_kv4_append_rope(qkv[:, :8], qkv[:, 8:16], qkv[:, 16:], rope, cu, start, table, pool, dev_err=err)
+        k.kda_kv4_bounds(cu, start, T, table, pool, bounds, dev_err=err)
+        picked = k.kda_kv4_pick(q[-3:], i32([0, 3]), 3, lens, table, bounds, P, 5, dev_err=err)
+        o, lse = k.kda_kv4_attention_picked(q[-3:], i32([0, 3]), 3, lens, table, picked, pool, workspace=ws, dev_err=err)
+        assert int(err) == 0
+        outs.append((q, pool[table[0].long()], bounds[table[0].long()], picked, o, lse))
+    assert not far[:pages - 12].any()
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
 def test_a_step_on_another_stream_is_the_same():
     a, b = Layer([500, 77], [1, 1], 16, 5, 3), Layer([500, 77], [1, 1], 16, 5, 3)
     want = a.step()
