@@ -74,7 +74,7 @@ __device__ __forceinline__ void bound_page(const uint8_t *tiles, int fill, int8_
     uint32_t hi[16], lo[16], nan = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) hi[i] = 0xfc00fc00u, lo[i] = 0x7c007c00u;
-#pragma unroll 4
+#pragma unroll 2
     for (int t = lane / CHUNKS; t < fill; t += ROWS) {
         const uint8_t *tile = tiles + (t >> 4) * L::BYTES;
         const uint4 w = *reinterpret_cast<const uint4 *>(tile + L::KC + (t & 15) * (D / 2) + c * 16);
