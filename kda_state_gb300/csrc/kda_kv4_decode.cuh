@@ -770,16 +770,6 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
                 add(v, top, sum, *reinterpret_cast<const float4 *>(out_s + (y * S::ROWS + col) * S::OSTRIDE + d), ml_s[y * S::ROWS + col]);
         return v;
     };
-    // units that begin and end in this CTA: a warp each
-    if (pieces[w].last.rows && pieces[w].last.end <= end) {
-        const Piece x = pieces[w].last;
-        for (int i = lane; i < x.rows * (D / 4); i += 32) {
-            const int col = i / (D / 4), d = i % (D / 4) * 4;
-            float top, sum;
-            const float4 v = gather(x, w, true, col, d, top, sum);
-            finish(x, col, d, v, top, sum);
-        }
-    }
     // the two that other CTAs share: four warps each, one for the unit that began before, one for that which goes on
     const int side = w >> 2, st = tid & 127;
     int w0 = -1;
@@ -821,7 +811,23 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) decode_attention_ker
         }
         shared[side] = arrived;
     }
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + side) : "memory");
+    // units that begin and end in this CTA, four channels a thread of all of them side by side
+    uint32_t inside = 0;                   // the warps where they begin, four bits each
+    int units = 0, most = 0;
+    for (int y = 0; y < WARPS; ++y)
+        if (pieces[y].last.rows && pieces[y].last.end <= end) {
+            inside |= (uint32_t)y << (4 * units++);
+            most = max(most, pieces[y].last.rows);
+        }
+    for (int i = tid; i < units * most * (D / 4); i += THREADS) {
+        const int unit = i / (most * (D / 4)), y = inside >> (4 * unit) & 15, col = i / (D / 4) - unit * most, d = i % (D / 4) * 4;
+        const Piece x = pieces[y].last;
+        if (col >= x.rows) continue;
+        float top, sum;
+        const float4 v = gather(x, y, true, col, d, top, sum);
+        finish(x, col, d, v, top, sum);
+    }
+    __syncthreads();
     if (!shared[side]) return;
     // each warp takes every fourth result, a lane QUADS / 32 times four channels of it
     {
