@@ -36,8 +36,8 @@ cudaError_t launch(const KvAttentionArgs &a, cudaStream_t s) {
 
 // A token's rows of one kv head, 8 or 16 at a time.  Its pages are read for it alone: of drafts that share three quarters of
 // theirs, two tokens' rows together (16, in the kernel that has room for one CTA an SM) would read 0.63 of the pages at 1.7
-// times the cost each.  96 requests, 64 pages of 32, 64 / 8 heads of 128: 59 us at 3.8 TB/s; 32 requests of 6 drafts, 32
-// pages of 64: 96 us, 32 tokens and kv heads a ns as with dense caches.
+// times the cost each.  96 requests, 64 pages of 32, 64 / 8 heads of 128: 55 us at 4.1 TB/s; 32 requests of 6 drafts, 32
+// pages of 64: 94 us, 33 tokens and kv heads a ns as with dense caches.
 template <int D, typename T>
 cudaError_t launch_picked(const KvAttentionArgs &a, cudaStream_t s) {
     return a.Hq / a.Hkv <= 8 ? kv4::launch_decode_attention<D, 1, T, true>(a, s) : kv4::launch_decode_attention<D, 2, T, true>(a, s);

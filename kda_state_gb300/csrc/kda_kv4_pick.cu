@@ -11,7 +11,7 @@
 // Records are int8 [num_pages][Hkv][2 D + 16]: hi, lo, e, zeros.  e = 127 marks a page with a NaN (its score is infinite).
 //
 // Single tokens are bound by the records' bytes and, as these are few, by a chain of dependent loads in each of three
-// kernels: 96 requests of 900 to 16 K tokens in pages of 32 take 29 us with the bounds before them (5 to 7 us bounds, 15
+// kernels: 96 requests of 900 to 16 K tokens in pages of 32 take 28 us with the bounds before them (5 to 7 us bounds, 15
 // scores at 3.7 TB/s, 3 behind them for the rows' picks; floor 9), one of 131 K tokens in pages of 64 takes 13.  Prompts are
 // bound by issue: 1536 tokens, 8 kv heads, up to 384 pages 35 us (5, 17, 11 behind them).
 #include "kda_async.cuh"
