@@ -4,7 +4,8 @@
 //     y = h w / sqrt(mean h^2 + eps)
 // Output y, or e4m3 codes with scales of a row or of 128 channels: s = max|y| / 448, code = e4m3(y / s), 0 where s = 0.
 // With r = 1 / sqrt(..) the same for a row, max|y| = r max|h w| and y / s = h w (448 / max|h w|): the row's sum and its
-// maximum are taken together, with one exchange between threads, and codes do not wait for r.
+// maximum are taken together, with one exchange between threads, and codes do not wait for r.  That holds while the products
+// and the scale are normal numbers; a row or block where they are not (faint or zero, NaN, products past fp32) goes by y.
 //
 // A row is one warp's or one CTA's, in registers from its one read on: bound by HBM (bf16: 4 bytes read, 3 or 4 written a
 // channel), and by the launch and two round trips for a row alone.  16384 rows of 8192 channels with a scale for 128: 148 us,
@@ -47,12 +48,82 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// What h w is multiplied by to be a code, of the scale s and the largest |h w|: 0 where the scale is 0, NaN where it is.
-__device__ __forceinline__ float per_code(float s, float top) { return s == 0.f ? 0.f : isnan(s) ? s : TOP / top; }
+// Whether codes are h w (448 / top), top the largest |h w|, y = r top: within [2^-100, 2^125] no product that counts has lost
+// bits and the factor is finite, within [2^-117, FLT_MAX] the scale y / 448 has all of its bits.  False for NaN.
+__device__ __forceinline__ bool by_products(float top, float y) {
+    return __float_as_uint(top) - 0x0d800000u <= 0x7e000000u - 0x0d800000u && __float_as_uint(y) - 0x05000000u < 0x7f800000u - 0x05000000u;
+}
+// The scale of a largest |y|; NaN for an infinity, which no scale brings into range.
+__device__ __forceinline__ float scale_of_y(float top) { return isinf(top) ? __uint_as_float(0x7fffffffu) : top / TOP; }
+
+// The 8-bit output of a row, or with scales of 128 channels of a warp's part of it, by y itself.  h is read again (a thread
+// its own channels), as this is rare: faint or zero rows and blocks, NaN, products past fp32.
+template <typename T, int WARPS, int N>
+__device__ __noinline__ void codes_of_y(const AddNormArgs &a, int row, float r) {
+    constexpr int THREADS = 32 * WARPS;
+    const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, vectors = a.C / 8;
+    auto y_of = [&](int i, float (&y)[8]) {
+        const int c = tid + i * THREADS;
+        float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, top = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = 0.f;
+        if (c < vectors) {
+            Vec8<T> v = load8(a.sum ? (const T *)a.sum + row * a.sum_stride + c * 8 : (const T *)a.x + row * a.x_stride + c * 8);
+            unpack8(v, y);
+            if (a.residual && !a.sum) {
+                unpack8(load8((const T *)a.residual + row * a.residual_stride + c * 8), g);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] += g[k];
+                pack8(y, v);
+                unpack8(v, y);
+            }
+            unpack8(load8((const T *)a.w_norm + c * 8), g);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = y[k] * r * g[k], top = max_nan(top, fabsf(y[k]));
+        return c < vectors ? top : 0.f;    // (0 r is NaN where r is infinite)
+    };
+    const bool by_block = a.mode == KDA_NORM_E4M3_BLOCK;
+    float y[8], s = 0.f;
+    if (!by_block) {
+        float t = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) t = max_nan(t, y_of(i, y));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t = max_nan(t, __shfl_xor_sync(~0u, t, o));
+        if constexpr (WARPS > 1) {
+            __shared__ float part[WARPS];
+            if (lane == 0) part[threadIdx.x >> 5] = t;
+            __syncthreads();
+            t = lane < WARPS ? part[lane] : 0.f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) t = max_nan(t, __shfl_xor_sync(~0u, t, o));
+        }
+        s = scale_of_y(t);
+        if (tid == 0) a.scales[row] = s;
+    }
+    const int blocks = (a.C + 127) / 128;
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+        const int c = tid + i * THREADS;
+        float t = y_of(i, y);
+        if (by_block) {
+#pragma unroll
+            for (int o = 8; o; o >>= 1) t = max_nan(t, __shfl_xor_sync(~0u, t, o));
+            s = scale_of_y(t);
+            if ((lane & 15) == 0 && c < vectors) a.scales[(size_t)row * blocks + c / 16] = s;
+        }
+        if (c >= vectors) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = s == 0.f ? 0.f : y[k] / s;
+        *reinterpret_cast<uint2 *>((uint8_t *)a.out + (size_t)row * a.C + c * 8) =
+            make_uint2(to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16, to_e4m3x2(y[4], y[5]) | to_e4m3x2(y[6], y[7]) << 16);
+    }
+}
 
 // WARPS warps a row, N vectors of 8 channels a thread.
 template <typename T, int WARPS, int N>
-__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) add_rmsnorm_kernel(const AddNormArgs a) {
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) add_rmsnorm_kernel(const __grid_constant__ AddNormArgs a) {
     constexpr int ROWS = WARPS == 1 ? 4 : 1, THREADS = 32 * WARPS;
     const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int row = blockIdx.x * ROWS + (WARPS == 1 ? w : 0);
@@ -132,21 +203,30 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) add_rmsnorm_ker
         }
         return;
     }
-    float s = r * top / TOP, per = per_code(s, top);
-    if (a.mode == KDA_NORM_E4M3_ROW && tid == 0) a.scales[row] = s;
+    const bool by_block = a.mode == KDA_NORM_E4M3_BLOCK;
+    bool plain = by_products(top, r * top);            // (the same for all of the row's threads)
+    if (by_block) {
+        plain = true;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {      // 16 neighbouring lanes hold a block
+#pragma unroll
+            for (int o = 8; o; o >>= 1) block_top[i] = max_nan(block_top[i], __shfl_xor_sync(~0u, block_top[i], o));
+            plain = plain && (tid + i * THREADS >= vectors || by_products(block_top[i], r * block_top[i]));
+        }
+        plain = __all_sync(~0u, plain);
+    }
+    if (!plain) return codes_of_y<T, WARPS, N>(a, row, r);
+    float s = r * top / TOP, per = TOP / top;
+    if (!by_block && tid == 0) a.scales[row] = s;
     const int blocks = (a.C + 127) / 128;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int c = tid + i * THREADS;
-        if (a.mode == KDA_NORM_E4M3_BLOCK) {       // 16 neighbouring lanes hold a block
-            float t = block_top[i];
-#pragma unroll
-            for (int o = 8; o; o >>= 1) t = max_nan(t, __shfl_xor_sync(~0u, t, o));
-            s = r * t / TOP;
-            per = per_code(s, t);
-            if ((lane & 15) == 0 && c < vectors) a.scales[(size_t)row * blocks + c / 16] = s;
-        }
         if (c >= vectors) continue;
+        if (by_block) {
+            s = r * block_top[i] / TOP, per = TOP / block_top[i];
+            if ((lane & 15) == 0) a.scales[(size_t)row * blocks + c / 16] = s;
+        }
         float h[8], g[8];
         unpack8(xv[i], h);
         unpack8(wv[i], g);
