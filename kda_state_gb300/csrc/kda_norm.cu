@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) add_rmsnorm_ker
 template <typename T, int WARPS, int N>
 cudaError_t go(const AddNormArgs &a, cudaStream_t s) {
     constexpr int ROWS = WARPS == 1 ? 4 : 1;
-    return launch_early(add_rmsnorm_kernel<T, WARPS, N>, dim3((a.tokens + ROWS - 1) / ROWS), dim3(WARPS == 1 ? 128 : 32 * WARPS), 0, s, a);
+    return launch_early(add_rmsnorm_kernel<T, WARPS, N>, dim3(((unsigned)a.tokens + ROWS - 1) / ROWS), dim3(WARPS == 1 ? 128 : 32 * WARPS), 0, s, a);
 }
 
 template <typename T>
