@@ -194,8 +194,121 @@ template <> __device__ __forceinline__ float2 halves<__nv_bfloat16>(uint32_t w) 
 }
 template <> __device__ __forceinline__ float2 halves<__half>(uint32_t w) { return f16x2_to_float2(w); }
 
+// A value of T, without its sign, as m 2^(place - 133) (finite).
+__device__ __forceinline__ uint32_t whole_of(uint32_t bits, __nv_bfloat16, int &place) {
+    const int e = bits >> 7 & 255;
+    place = max(e, 1) - 1;
+    return (bits & 127) | (e ? 128 : 0);
+}
+__device__ __forceinline__ uint32_t whole_of(uint32_t bits, __half, int &place) {
+    const int e = bits >> 10 & 31;
+    place = max(e, 1) + 108;
+    return (bits & 1023) | (e ? 1024 : 0);
+}
+
+// The sign of sum_h x_h - m 2^e, exact; x_h is max(v, 0), max(-v, 0) or |v| (side 1, -1, 0) of a head's value v, the first of
+// them at `at`.  m < 2^24, -101 <= e <= 122.
+template <int D, typename T>
+__device__ __forceinline__ int against(const uint16_t *at, int G, int side, uint32_t m, int e) {
+    float sum = 0.f;                       // off by less than G 2^-23 of itself
+    for (int g = 0; g < G; ++g) {
+        const float v = halves<T>(at[(size_t)g * D]).x;
+        sum += side == 0 ? fabsf(v) : fmaxf((float)side * v, 0.f);
+    }
+    const float mark = (float)m * power_of(e), off = sum * ((float)G * 0x1p-23f);
+    if (G < 1 << 20 && sum - mark > off) return 1;
+    if (G < 1 << 20 && mark - sum > off) return -1;
+    long long s = 0;                       // 16 bits at a time, from the lowest on
+    bool some = false;
+    for (int i = 0; i < 18; ++i) {
+        for (int g = 0; g < G; ++g) {
+            const uint32_t v = at[(size_t)g * D];
+            int place;
+            const uint32_t w = whole_of(v, T(), place);
+            if (place >> 4 == i && (side == 0 || (side < 0) == (v >> 15 != 0))) s += (long long)w << (place & 15);
+        }
+        if ((e + 133) >> 4 == i) s -= (long long)m << ((e + 133) & 15);
+        some |= (s & 0xffff) != 0;
+        s >>= 16;
+    }
+    return s < 0 ? -1 : s > 0 || some;
+}
+
+// The whole number that sum_h x_h / 2^f rounds to (x_h as above, side 1 or -1), known to be k or k + 1: up to 41 bits below
+// the border between them, and what the rest may add.
+template <int D, typename T>
+__device__ __noinline__ int settled(const uint16_t *at, int G, int side, int k, int f) {
+    long long s = -((long long)(2 * k + 1) << 40);
+    int parts = 0;                         // values that have bits below, less than 1 each
+    for (int g = 0; g < G; ++g) {
+        const uint32_t v = at[(size_t)g * D];
+        if ((side < 0) != (v >> 15 != 0)) continue;
+        int place;
+        const uint32_t w = whole_of(v, T(), place);
+        const int by = place - (f + 92);
+        if (by >= 0) {
+            s += (long long)w << by;
+        } else {
+            s += w >> min(-by, 31);
+            parts += (w & ((1u << min(-by, 31)) - 1)) != 0;
+        }
+    }
+    const int x = s >= 0 ? s > 0 || parts : s + parts <= 0 ? -1 : against<D, T>(at, G, side, 2 * k + 1, f - 1);
+    return k + (x > 0 || (x == 0 && (k & 1)));
+}
+
+// u and d of the lane's D / 32 channels, a byte each, from exact sums; a warp's work, where fp32 sums do not tell the unit.  f:
+// about the unit.
+template <int D, typename T>
+__device__ __noinline__ uint2 asked_exactly(const T *q, int G, int f) {
+    constexpr int N = D / 32;
+    const uint16_t *const at = reinterpret_cast<const uint16_t *>(q) + (threadIdx.x & 31) * N;
+    bool good = true;                      // finite, and |q| adds up to a finite fp32
+    for (int i = 0; i < N; ++i)
+        for (int g = 0; g < G; ++g) good = good && isfinite(halves<T>(at[(size_t)g * D + i]).x);
+    for (int i = 0; i < N; ++i) good = good && against<D, T>(at + i, G, 0, 0xffffffu, 104) <= 0;
+    if (!__all_sync(~0u, good)) return make_uint2(0, 0);
+    auto past = [&](int e) {
+        bool any = false;
+        for (int i = 0; i < N; ++i)
+            for (int side = -1; side <= 1; side += 2) any = any || against<D, T>(at + i, G, side, 127, e) > 0;
+        return __any_sync(~0u, any);
+    };
+    f = max(f - 1, -100);
+    while (f > -100 && !past(f - 1)) --f;
+    while (past(f)) ++f;
+    uint32_t r[2] = {0, 0};
+    for (int i = 0; i < 2 * N; ++i) {
+        const uint16_t *const c = at + (i >> 1);
+        const int side = i & 1 ? -1 : 1;
+        float sum = 0.f;
+        for (int g = 0; g < G; ++g) sum += fmaxf((float)side * halves<T>(c[(size_t)g * D]).x, 0.f);
+        auto above = [&](int k) {          // the nearest whole number is k + 1 or more
+            const int x = against<D, T>(c, G, side, 2 * k + 1, f - 1);
+            return x > 0 || (x == 0 && (k & 1));
+        };
+        int k = min(__float2int_rn(sum * power_of(-f)), 127);
+        while (k < 127 && above(k)) ++k;
+        while (k > 0 && !above(k - 1)) --k;
+        r[i & 1] |= (uint32_t)k << (8 * (i >> 1));
+    }
+    return make_uint2(r[0], r[1]);
+}
+
+// Half the sum of a channel's magnitudes up to which its fp32 sums are exact: 2^23 times the lowest bit that its values can
+// have, by the least of them that is not 0 (bits - 1 of it, or 0x7fff; 0 of a subnormal, which is not looked into).
+__device__ __forceinline__ float exact_to(uint32_t least, __nv_bfloat16) { return __uint_as_float((least + 1 & 0x7f80u) << 16) * 0x1p16f; }
+__device__ __forceinline__ float exact_to(uint32_t least, __half) {
+    const uint32_t e = least + 1 & 0x7c00u;
+    return e ? __uint_as_float((e << 13) + (112u << 23)) * 0x1p13f : 0.f;
+}
+
 // u and -d of a token and kv head; a warp's work, N of them at once so that their loads are in flight together.  q(n) is where
 // number n's queries lie; put(n, channel, x, y) gets D / 32 of each, from `channel` on.
+//
+// They are the exact sums' whole numbers.  fp32 sums are exact where a channel's values do not lie further apart than its 24
+// bits, and settle what is not near a tie or the border of a unit; the few channels where neither holds (a row in a thousand
+// of 8 heads in bf16 has one) are looked at exactly.
 template <int D, int N, typename T, typename Q, typename Put>
 __device__ __forceinline__ void ask_of(const Q &q, int G, const Put &put) {
     constexpr int W = D / 64;              // words of the lane: 2 W channels
@@ -203,10 +316,14 @@ __device__ __forceinline__ void ask_of(const Q &q, int G, const Put &put) {
     // up = (sum |f| + sum f) / 2 and down = (sum |f| - sum f) / 2, an addition less a value than from their parts; halves
     // are exact, and an infinity or a NaN stays one
     float all[N][2 * W], net[N][2 * W];
+    uint32_t least[N][W];                  // of each two channels the least |f| but 0: bits - 1 with the sign set, compared as signed
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int n = 0; n < N; ++n) {
 #pragma unroll
         for (int i = 0; i < 2 * W; ++i) all[n][i] = net[n][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) least[n][i] = 0x7fff7fffu;
+    }
     for (int g0 = 0; g0 < G; g0 += 8) {    // eight heads' loads at once
         uint32_t w[N][8][W];
 #pragma unroll
@@ -231,24 +348,46 @@ __device__ __forceinline__ void ask_of(const Q &q, int G, const Put &put) {
                     const float2 f = halves<T>(w[n][g][i]);
                     all[n][2 * i] += fabsf(f.x), net[n][2 * i] += f.x;
                     all[n][2 * i + 1] += fabsf(f.y), net[n][2 * i + 1] += f.y;
+                    least[n][i] = __vmins2(least[n][i], (w[n][g][i] | 0x80008000u) - 0x00010001u);
                 }
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         float top = 0.f;
+        uint32_t open = 0;                 // channels whose sums may have lost bits
 #pragma unroll
         for (int i = 0; i < 2 * W; ++i) {
             all[n][i] *= 0.5f, net[n][i] *= 0.5f;
             top = max_nan(top, all[n][i] + fabsf(net[n][i]));
+            if (!(all[n][i] <= exact_to(least[n][i / 2] >> (16 * (i & 1)), T()))) open |= 1u << i;
         }
         const uint32_t bits = __reduce_max_sync(~0u, __float_as_uint(top) & 0x7fffffffu);       // (a NaN is above all)
         // nothing to go by: all pages score 0
-        const float per = bits >= 0x7f800000u || bits < 0x00800000u ? 0.f : power_of(-max(unit_of(__uint_as_float(bits)), -100));
+        const int f = max(unit_of(__uint_as_float(bits)), -100);
+        const float per = bits >= 0x7f800000u || bits < 0x00800000u ? 0.f : power_of(-f);
         int u[2 * W], d[2 * W];
 #pragma unroll
         for (int i = 0; i < 2 * W; ++i) {
             u[i] = per == 0.f ? 0 : __float2int_rn((all[n][i] + net[n][i]) * per);
             d[i] = per == 0.f ? 0 : __float2int_rn((net[n][i] - all[n][i]) * per);
+        }
+        bool unit_open = bits >= 0x7e800000u;          // (2^126: |q| may add up to more than fp32 has)
+        if (open) {
+            unit_open = unit_open || G > 4096 || abs((int)(bits & 0x7fffffu) - 0x7e0000) <= 8 * (G + 2);
+            const float half = 0.5f - (float)(G + 2) * 0x1p-15f;       // (sums are off by G + 1 times 254 2^-24 of a unit)
+            const uint16_t *const at = reinterpret_cast<const uint16_t *>(q(n)) + lane * 2 * W;
+#pragma unroll
+            for (int i = 0; i < 2 * W; ++i) {
+                const float x = (all[n][i] + net[n][i]) * per, y = (all[n][i] - net[n][i]) * per;
+                if (!(open >> i & 1)) continue;
+                if (fabsf(x - rintf(x)) >= half) u[i] = settled<D, T>(at + i, G, 1, (int)x, f);
+                if (fabsf(y - rintf(y)) >= half) d[i] = -settled<D, T>(at + i, G, -1, (int)y, f);
+            }
+        }
+        if (__any_sync(~0u, unit_open)) {
+            const uint2 x = asked_exactly<D, T>(q(n), G, f);
+#pragma unroll
+            for (int i = 0; i < 2 * W; ++i) u[i] = x.x >> (8 * i) & 255, d[i] = -(int)(x.y >> (8 * i) & 255);
         }
         put(n, lane * 2 * W, u, d);
     }

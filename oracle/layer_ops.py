@@ -3,6 +3,8 @@ path): the residual norm with 8-bit outputs, the position rotation, the bounds o
 that a score picks, and attention over them."""
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
 
 from . import kv4
@@ -61,14 +63,37 @@ def page_bounds(k):
     return hi, lo, es
 
 
+def _adds_exactly(x):
+    """Whether the rows of x >= 0 add up without a rounding in fp64."""
+    total, lost = np.zeros(x.shape[1]), np.zeros(x.shape[1])
+    for row in x:
+        t = total + row
+        back = t - total
+        lost += np.abs((total - (t - back)) + (row - back))
+        total = t
+    return not lost.any()
+
+
 def asked(q):
-    """(u, d) whole numbers [D] of one kv head's queries q [G, D]."""
-    up, down = np.maximum(q, 0).sum(0), np.maximum(-q, 0).sum(0)
+    """(u, d) whole numbers [D] of one kv head's queries q [G, D]: of the exact sums."""
+    q = np.asarray(q, np.float64)
+    none = np.zeros(q.shape[1], int), np.zeros(q.shape[1], int)
+    if not np.isfinite(q).all():
+        return none
+    if _adds_exactly(np.abs(q)):
+        up, down = np.maximum(q, 0).sum(0), np.maximum(-q, 0).sum(0)
+        power = lambda f: 2.0 ** f
+    else:
+        exact = [[Fraction(float(x)) for x in row] for row in q.T]
+        up, down = (np.array([sum((s * x for x in row if s * x > 0), Fraction(0)) for row in exact], object) for s in (1, -1))
+        power = lambda f: Fraction(2) ** f
     top = max(up.max(), down.max())
-    if not np.abs(q).sum(0).max() <= np.finfo(np.float32).max or top == 0:
-        return np.zeros(q.shape[1], int), np.zeros(q.shape[1], int)
-    f = max(unit(top), -100)
-    return np.rint(up / 2.0 ** f).astype(int), np.rint(down / 2.0 ** f).astype(int)
+    if (up + down).max() > float(np.finfo(np.float32).max) or top == 0:
+        return none
+    f = max(unit(float(top)) - 1, -100)
+    while top > 127 * power(f):
+        f += 1
+    return tuple(np.array([round(x / power(f)) for x in side.tolist()], int) for side in (up, down))
 
 
 def pick(q, pos, records, page_size, count, first, recent):
