@@ -463,9 +463,10 @@ __global__ void __launch_bounds__(THREADS, 3) score_one_kernel(const KvPickArgs 
     bool good = false;                     // page p + lane
     auto fetch = [&](int p) {
         if (!works) return;
-        const int page = p + lane >= z.p1 ? -2 : one_run ? early : a.page_table[(size_t)z.b * a.max_pages + p + lane];
-        good = page >= 0 && page < a.num_pages;
-        if (!good && page != -2) report(a.err, DEVERR_PAGE_RANGE);
+        const bool asked = p + lane < z.p1;
+        const int page = !asked || one_run ? early : a.page_table[(size_t)z.b * a.max_pages + p + lane];
+        good = asked && page >= 0 && page < a.num_pages;
+        if (asked && !good) report(a.err, DEVERR_PAGE_RANGE);
         if (h != 0) return;
         const uint32_t there = __ballot_sync(~0u, good);
         if (lane == 0) barrier_expect(bar, __popc(there) * page_bytes);

@@ -72,3 +72,14 @@ def test_many_heads_of_every_size(news, G, D, dtype):
     q = q.to(dtype)
     got, err = pick(q, news, lens, rec, table, 16, 60, 1, 2)
     assert err == 0 and np.array_equal(got, picks_of(q, news, lens, rec, table, 16, 60, 1, 2))
+
+
+@pytest.mark.parametrize("news", [[1, 1], [2, 3]])
+@pytest.mark.parametrize("page", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1])
+def test_every_page_out_of_range_is_told(news, page):
+    lens = [640, 640]
+    rec, table = random_bounds(lens, 2, 64, 16, 35)
+    table[0, 7] = page
+    q = torch.randn(sum(news), 4, 64, generator=torch.Generator().manual_seed(36)).to(BF)
+    got, err = pick(q, news, lens, rec, table, 16, 8, 1, 1)
+    assert err == 32 and np.array_equal(got, picks_of(q, news, lens, rec, table, 16, 8, 1, 1))
