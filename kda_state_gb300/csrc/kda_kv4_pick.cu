@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const K
     int32_t *const out = a.picked + (size_t)row * a.count;
     const int pos = r.len - r.n + (t - r.q0), pages = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
     if (pages <= a.count) {
-        for (int i = tid; i < a.count; i += 32 * W) out[i] = i < pages ? i : -1;
+        for (unsigned i = tid; i < (unsigned)a.count; i += 32 * W) out[i] = i < (unsigned)pages ? (int)i : -1;     // (count may be 2^31 - 1)
         return;
     }
     const int want = a.count - a.first - a.recent, from = a.first, to = pages - a.recent;    // candidates from .. to - 1, more than want

@@ -83,3 +83,15 @@ def test_every_page_out_of_range_is_told(news, page):
     q = torch.randn(sum(news), 4, 64, generator=torch.Generator().manual_seed(36)).to(BF)
     got, err = pick(q, news, lens, rec, table, 16, 8, 1, 1)
     assert err == 32 and np.array_equal(got, picks_of(q, news, lens, rec, table, 16, 8, 1, 1))
+
+
+@pytest.mark.parametrize("count", [2 ** 31 - 1, 2 ** 31 - 100])
+def test_as_many_places_as_an_int_counts(count):
+    """A row of 8.6 GB whose token takes all of its pages: places in it are counted past 2^31 - 1 by no thread."""
+    rec, table = random_bounds([500], 1, 64, 16, 37)
+    picked = torch.full((1, 1, count), 5, dtype=torch.int32, device=DEV)
+    got = kda().kda_kv4_pick(torch.ones(1, 1, 64, dtype=BF, device=DEV), i32([0, 1]), 1, i32([500]), dev(table), dev(rec), 16, count, picked=picked)
+    assert got is picked and picked[0, 0, :32].tolist() == list(range(32)) and int(picked[0, 0, 32:].max()) == -1
+    assert int(picked[0, 0, 32:].min()) == -1
+    del picked, got
+    torch.cuda.empty_cache()
