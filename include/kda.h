@@ -819,6 +819,25 @@ KDA_API int kda_selftest_kv4_wait(kda_dtype dt, int B, int total_tokens, int max
                                   size_t workspace_bytes, int32_t *dev_err, int wait_us,
                                   void *stream);
 
+/*
+ * kda_selftest_kv4_pick_wait -- exercises the picks' own bounded wait.
+ *
+ * Runs the kernels that kda_kv4_pick launches for single tokens, except that the
+ * barrier of every CTA's first records expects 16 bytes that nobody copies.  Waits
+ * give up after wait_us microseconds: KDA_DEVERR_TIMEOUT is set in *dev_err, every
+ * copy lands and the kernels return.  picked is not valid; the context stays
+ * usable.  Not part of the cache's path.
+ *
+ *   arguments as kda_kv4_pick, with max_q 1 and count below max_pages (else nothing
+ *   is scored); total_tokens >= 1; dev_err required; wait_us 1 .. 2,000,000
+ */
+KDA_API int kda_selftest_kv4_pick_wait(kda_dtype dt, int B, int total_tokens, int max_q, int H_q,
+                                       int H_kv, int D, const void *q, long long q_stride, const int32_t *cu_seqlens,
+                                       const int32_t *kv_lens, const int32_t *page_table, int max_pages,
+                                       int page_size, const int8_t *bounds, int num_pages, int count, int first,
+                                       int recent, int32_t *picked, void *workspace, size_t workspace_bytes,
+                                       int32_t *dev_err, int wait_us, void *stream);
+
 /* Human-readable name of a kda_status value. */
 KDA_API const char *kda_status_string(int status);
 

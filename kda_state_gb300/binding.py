@@ -131,6 +131,8 @@ def lib() -> ctypes.CDLL:
         L.kda_kv4_pick_workspace_bytes.restype = sz
         L.kda_kv4_pick.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, vp, i, i, i, i, ip, vp, sz,
                                    ip, vp]
+        L.kda_selftest_kv4_pick_wait.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, vp, i, i, i, i, ip, vp, sz,
+                                                 ip, i, vp]
         L.kda_kv4_attention_picked.argtypes = [i, i, i, i, i, i, i, vp, ll, ip, ip, ip, i, i, ip, i, vp, i, f,
                                                f, f, vp, vp, vp, sz, ip, vp]
         L.kda_add_rmsnorm.argtypes = [i, i, i, vp, ll, vp, ll, vp, f, i, vp, ll, vp, vp, vp]
@@ -150,7 +152,7 @@ def lib() -> ctypes.CDLL:
                    "kda_kv4_attention_picked", "kda_kv4_append", "kda_kv4_gather", "kda_kv4_attention", "kda_page_alloc",
                    "kda_page_fork", "kda_page_free", "kda_page_compact", "kda_page_copy",
                    "kda_replay_fold", "kda_slot_copy", "kda_selftest_bounded_wait",
-                   "kda_selftest_prefill_wait", "kda_selftest_kv4_wait"):
+                   "kda_selftest_prefill_wait", "kda_selftest_kv4_wait", "kda_selftest_kv4_pick_wait"):
             getattr(L, fn).restype = ctypes.c_int
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
@@ -1306,3 +1308,25 @@ def kda_selftest_kv4_wait(q, cu_seqlens, max_q: int, kv_lens, page_table, pool, 
         _ptr(workspace, "workspace", (wb,), _U8, dev), wb, _err_ptr(dev_err, dev), int(wait_us),
         _stream_of(stream, dev)))
     return o
+
+
+def kda_selftest_kv4_pick_wait(q, cu_seqlens, kv_lens, page_table, bounds, page_size: int, count: int, workspace, dev_err,
+                               wait_us: int = 1000, stream=None):
+    """The picks of single tokens with first records that never all arrive: the scores' waits give up after wait_us
+    and set KDA_DEVERR_TIMEOUT in dev_err.  Arguments as ``kda_kv4_pick``.  Returns the picks (not valid)."""
+    shape, dev = _first(q, "q", 3)
+    dt = _kv_dt(q.dtype)
+    T, Hq, D = shape
+    qa, qs = _rows(q, "q", q.dtype, shape, dev)
+    (pages, H, _), _ = _first(bounds, "bounds", 3)
+    ta, B, M = _table(page_table, dev)
+    if dev_err is None:
+        raise ValueError("dev_err is required")
+    picked = _make(stream, (T, H, count), I32, q.device)
+    (wb,), _ = _first(workspace, "workspace", 1)
+    _check("kda_selftest_kv4_pick_wait", lib().kda_selftest_kv4_pick_wait(
+        dt, B, T, 1, Hq, H, D, qa, qs, _ptr(cu_seqlens, "cu_seqlens", (B + 1,), I32, dev),
+        _ptr(kv_lens, "kv_lens", (B,), I32, dev), ta, M, _int(page_size),
+        _ptr(bounds, "bounds", (pages, H, 2 * D + 16), torch.int8, dev), pages, _int(count), 1, 1, picked.data_ptr(),
+        _ptr(workspace, "workspace", (wb,), _U8, dev), wb, _err_ptr(dev_err, dev), int(wait_us), _stream_of(stream, dev)))
+    return picked

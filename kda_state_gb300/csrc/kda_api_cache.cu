@@ -105,6 +105,34 @@ int attention(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_k
     return from_cuda(kda::launch_kv4_attention(a, (cudaStream_t)stream));
 }
 
+int pick(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv, int D, const void *q, long long q_stride,
+         const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table, int max_pages, int page_size,
+         const int8_t *bounds, int num_pages, int count, int first, int recent, int32_t *picked, void *workspace,
+         size_t workspace_bytes, int32_t *dev_err, uint64_t wait_ns, int starve, void *stream) {
+    if (!dtype_ok(dt) || (D != 64 && D != 128)) return KDA_ERR_UNSUPPORTED;
+    const int shift = page_shift_of(page_size);
+    if (B < 0 || total_tokens < 0 || max_q < 0 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || max_pages < 1 ||
+        num_pages < 1 || shift < 0 || (B == 0 && total_tokens > 0) || count < 1 || first < 0 || recent < 1 ||
+        (long long)first + recent > count)
+        return KDA_ERR_INVALID_ARG;
+    if ((long long)total_tokens * H_q > 0x7fffffffLL || (long long)H_q * D > 0x7fffffffLL ||
+        ((long long)max_pages << shift) > 0x40000000LL)
+        return KDA_ERR_INVALID_ARG;
+    if (total_tokens == 0 || max_q == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (!q || !cu_seqlens || !kv_lens || !page_table || !bounds || !picked || !workspace) return KDA_ERR_INVALID_ARG;
+    if (!row_stride_ok(q, q_stride, (long long)H_q * D) || !aligned16(bounds) || !aligned16(workspace) ||
+        workspace_bytes < kda_kv4_pick_workspace_bytes(total_tokens, H_kv, max_pages))
+        return KDA_ERR_INVALID_ARG;
+    kda::KvPickArgs a;
+    memset(&a, 0, sizeof(a));
+    a.dt = dt; a.B = B; a.T = total_tokens; a.max_q = max_q < total_tokens ? max_q : total_tokens;
+    a.Hq = H_q; a.Hkv = H_kv; a.D = D; a.max_pages = max_pages; a.page_shift = shift; a.num_pages = num_pages; a.count = count; a.first = first;
+    a.recent = recent; a.q = q; a.q_stride = q_stride; a.cu = cu_seqlens; a.kv_lens = kv_lens;
+    a.page_table = page_table; a.bounds = bounds; a.picked = picked; a.keys = (uint32_t *)workspace;
+    a.key_stride = max_pages; a.err = dev_err; a.wait_ns = wait_ns; a.starve = starve;
+    return from_cuda(kda::launch_kv4_pick(a, (cudaStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -185,28 +213,19 @@ KDA_API int kda_kv4_pick(kda_dtype dt, int B, int total_tokens, int max_q, int H
                          int page_size, const int8_t *bounds, int num_pages, int count, int first,
                          int recent, int32_t *picked, void *workspace, size_t workspace_bytes,
                          int32_t *dev_err, void *stream) {
-    if (!dtype_ok(dt) || (D != 64 && D != 128)) return KDA_ERR_UNSUPPORTED;
-    const int shift = page_shift_of(page_size);
-    if (B < 0 || total_tokens < 0 || max_q < 0 || H_kv < 1 || H_q < H_kv || H_q % H_kv != 0 || max_pages < 1 ||
-        num_pages < 1 || shift < 0 || (B == 0 && total_tokens > 0) || count < 1 || first < 0 || recent < 1 ||
-        (long long)first + recent > count)
-        return KDA_ERR_INVALID_ARG;
-    if ((long long)total_tokens * H_q > 0x7fffffffLL || (long long)H_q * D > 0x7fffffffLL ||
-        ((long long)max_pages << shift) > 0x40000000LL)
-        return KDA_ERR_INVALID_ARG;
-    if (total_tokens == 0 || max_q == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
-    if (!q || !cu_seqlens || !kv_lens || !page_table || !bounds || !picked || !workspace) return KDA_ERR_INVALID_ARG;
-    if (!row_stride_ok(q, q_stride, (long long)H_q * D) || !aligned16(bounds) || !aligned16(workspace) ||
-        workspace_bytes < kda_kv4_pick_workspace_bytes(total_tokens, H_kv, max_pages))
-        return KDA_ERR_INVALID_ARG;
-    kda::KvPickArgs a;
-    memset(&a, 0, sizeof(a));
-    a.dt = dt; a.B = B; a.T = total_tokens; a.max_q = max_q < total_tokens ? max_q : total_tokens;
-    a.Hq = H_q; a.Hkv = H_kv; a.D = D; a.max_pages = max_pages; a.page_shift = shift; a.num_pages = num_pages; a.count = count; a.first = first;
-    a.recent = recent; a.q = q; a.q_stride = q_stride; a.cu = cu_seqlens; a.kv_lens = kv_lens;
-    a.page_table = page_table; a.bounds = bounds; a.picked = picked; a.keys = (uint32_t *)workspace;
-    a.key_stride = max_pages; a.err = dev_err;
-    return from_cuda(kda::launch_kv4_pick(a, (cudaStream_t)stream));
+    return pick(dt, B, total_tokens, max_q, H_q, H_kv, D, q, q_stride, cu_seqlens, kv_lens, page_table, max_pages, page_size,
+                bounds, num_pages, count, first, recent, picked, workspace, workspace_bytes, dev_err, KDA_KV4_WAIT_NS, 0, stream);
+}
+
+KDA_API int kda_selftest_kv4_pick_wait(kda_dtype dt, int B, int total_tokens, int max_q, int H_q,
+                                       int H_kv, int D, const void *q, long long q_stride, const int32_t *cu_seqlens,
+                                       const int32_t *kv_lens, const int32_t *page_table, int max_pages,
+                                       int page_size, const int8_t *bounds, int num_pages, int count, int first,
+                                       int recent, int32_t *picked, void *workspace, size_t workspace_bytes,
+                                       int32_t *dev_err, int wait_us, void *stream) {
+    if (!dev_err || wait_us < 1 || wait_us > 2000000 || total_tokens < 1 || max_q != 1 || count >= max_pages) return KDA_ERR_INVALID_ARG;
+    return pick(dt, B, total_tokens, max_q, H_q, H_kv, D, q, q_stride, cu_seqlens, kv_lens, page_table, max_pages, page_size,
+                bounds, num_pages, count, first, recent, picked, workspace, workspace_bytes, dev_err, (uint64_t)wait_us * 1000ull, 1, stream);
 }
 
 KDA_API int kda_kv4_attention_picked(kda_dtype dt, int B, int total_tokens, int max_q, int H_q,

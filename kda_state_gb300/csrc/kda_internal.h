@@ -206,6 +206,8 @@ struct KvPickArgs {
     uint32_t *keys;                // [T][Hkv][key_stride]
     long long key_stride;
     int32_t *err;
+    uint64_t wait_ns;              // limit of the scores' waits
+    int starve;                    // self-test: the first records never all arrive
 };
 
 // out = (x + residual) normed, in dtype or in e4m3 with scales.

@@ -458,7 +458,10 @@ __global__ void __launch_bounds__(THREADS, 3) score_one_kernel(const KvPickArgs 
     const bool works = part < parts;
     const int page_bytes = z.heads * RECORD, apart = page_bytes + 16;       // an odd number of 16 bytes for 8, 4, 2 heads
     uint8_t *const stage = smem + 32 * part * apart;
-    if (threadIdx.x == 0) barrier_init(bar, parts);
+    if (threadIdx.x == 0) {
+        barrier_init(bar, parts);
+        if (a.starve) barrier_await(bar, 16);      // (a self-test: bytes that nobody copies)
+    }
     __syncthreads();
     bool good = false;                     // page p + lane
     auto fetch = [&](int p) {
@@ -484,12 +487,12 @@ __global__ void __launch_bounds__(THREADS, 3) score_one_kernel(const KvPickArgs 
     __syncthreads();
     uint32_t *const keys = a.keys + ((size_t)z.q0 * a.Hkv + z.h0 + h) * a.key_stride;
     for (int turn = 0, q0 = z.p0;; ++turn) {       // (q0: of the CTA)
-        if (!barrier_wait_for(bar, turn & 1, KDA_KV4_WAIT_NS)) {
+        const bool landed = __all_sync(~0u, barrier_wait_for(bar, turn & 1, a.wait_ns));       // (each lane looks at its own clock)
+        if (!landed) {
             if (lane == 0) report(a.err, DEVERR_TIMEOUT);
-            barrier_wait_for(bar, turn & 1, KDA_KV4_WAIT_NS);      // (copies that are under way land in this CTA's memory)
-            return;
+            barrier_wait_for(bar, turn & 1, a.wait_ns);            // (copies that are under way land in this CTA's memory)
         }
-        if (works) {
+        if (works && landed) {
             const uint4 *x = reinterpret_cast<const uint4 *>(stage + lane * apart + h * RECORD), *y = reinterpret_cast<const uint4 *>(ask + h * 2 * D);
             int s[2] = {0, 0};
 #pragma unroll
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 3) score_one_kernel(const KvPickArgs 
         }
         q0 += stride, p += stride;
         if (q0 >= z.p1) break;
-        __syncthreads();                   // all have read the stage
+        if (!__syncthreads_and(landed)) return;                    // all have read the stage
         fence_async_shared();
         fetch(p);
     }
