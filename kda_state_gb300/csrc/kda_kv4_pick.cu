@@ -628,18 +628,17 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 3 : 2) score_kernel(const K
 
 // One row (token, kv head) is W warps' work, each with 32 K neighbouring pages in its lanes' registers (K = 0: read again at
 // every step).  The count-th best key is found by narrowing an interval of keys: lo has at least as many pages at or above
-// it as are wanted, hi fewer; it ends early once there are exactly as many.  What comes before the wait reads nothing that
-// the scores' kernel writes, and that kernel begins after all others.
+// it as are wanted, hi fewer; it ends early once there are exactly as many.
 template <int W, int K>
 __global__ void __launch_bounds__(W == 1 ? THREADS : 32 * W) pick_kernel(const KvPickArgs a) {
     constexpr int ROWS = W == 1 ? THREADS / 32 : 1;
     __shared__ uint32_t box[2][32];
+    wait_for_earlier_kernels();
+    let_later_kernels_in();
     const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const unsigned row = blockIdx.x * (unsigned)ROWS + (W == 1 ? w : 0);
     const int t = (int)min(row / (unsigned)a.Hkv, (unsigned)a.T);
     const Owner own = owner_with(a.cu, a.kv_lens, a.B, a.T, t);
-    wait_for_earlier_kernels();
-    let_later_kernels_in();
     if (own.b < 0) return;
     Tokens r{own.q0, own.end - own.q0, own.more};
     check(a, r, true);
@@ -737,9 +736,7 @@ template <int W, int K>
 cudaError_t pick_rows(const KvPickArgs &a, cudaStream_t s) {
     const long long rows = (long long)a.T * a.Hkv, per = W == 1 ? THREADS / 32 : 1;
     const dim3 grid((unsigned)((rows + per - 1) / per)), block(W == 1 ? THREADS : 32 * W);
-    if (a.max_pages > a.count) return launch_early(pick_kernel<W, K>, grid, block, 0, s, a);
-    pick_kernel<W, K><<<grid, block, 0, s>>>(a);     // (no scores: what is ahead is not known to have begun after all others)
-    return cudaGetLastError();
+    return launch_early(pick_kernel<W, K>, grid, block, 0, s, a);
 }
 
 template <int D, typename T>
