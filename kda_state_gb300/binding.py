@@ -20,9 +20,12 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 from dataclasses import dataclass
 
 import torch
+
+from . import _build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
@@ -58,11 +61,17 @@ _quick = None
 
 
 def _load_quick(L):
-    if not os.path.exists(QUICK_PATH):
-        raise RuntimeError("_quick.so is not built (%s); run __graft_entry__.build()" % QUICK_PATH)
-    loader = importlib.machinery.ExtensionFileLoader("_quick", QUICK_PATH)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_quick", QUICK_PATH, loader=loader))
-    loader.exec_module(module)
+    """The module, or None with a warning: it is a faster way, and only into the interpreter and torch it was built for."""
+    try:
+        had, key = _build.quick_built_for(), _build.quick_key()
+        if had != key or not os.path.exists(QUICK_PATH):
+            raise ImportError("it is built for %s, this is %s" % (had or "nothing", key) if had != key else "it is not there")
+        loader = importlib.machinery.ExtensionFileLoader("_quick", QUICK_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_quick", QUICK_PATH, loader=loader))
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn("calls take longer without %s (%s); run __graft_entry__.build()" % (QUICK_PATH, e), RuntimeWarning)
+        return None
     module.bind(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in (
         L.kda_add_rmsnorm, L.kda_kv4_append_rope, L.kda_kv4_bounds, L.kda_kv4_pick, L.kda_kv4_attention_picked,
         L.kda_kv4_append, L.kda_kv4_gather, L.kda_kv4_attention)])
