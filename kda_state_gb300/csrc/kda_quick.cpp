@@ -133,6 +133,12 @@ Table table_of(Call &c, PyObject *o) {
 }
 
 PyObject *none() { Py_RETURN_NONE; }
+// Results are made and the library is called without the interpreter's lock, as a launch may wait for room in its stream's
+// queue, and what makes room may wait for the lock.  No Python object is touched meanwhile.
+struct Unlocked {
+    PyThreadState *const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 // None instead of an exception: the functions of binding.py take over
 template <typename F>
 PyObject *plain(const F &f) {
@@ -162,14 +168,18 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor *given = nullptr;
         if (a[5] != Py_None) given = c.like(a[5], type, {T, C}), hp = c.rows(given, hs);
         if (!c.good || (given && !adds)) return none();
-        at::Tensor h = given ? *given : adds ? c.make({T, C}, type) : *x, scales;
-        if (adds && !given) hp = h.data_ptr(), hs = C;
-        at::Tensor out = c.make({T, C}, mode == KDA_NORM_TYPE ? type : at::kFloat8_e4m3fn);
-        if (mode == KDA_NORM_E4M3_ROW) scales = c.make({T}, at::kFloat);
-        if (mode == KDA_NORM_E4M3_BLOCK) scales = c.make({T, (C + 127) / 128}, at::kFloat);
-        if (add_rmsnorm_fn((kda_dtype)dt, (int)T, (int)C, xp, xs, rp, rs, wp, (float)eps, (kda_norm_out)mode, hp, hs, out.data_ptr(),
-                           scales.defined() ? scales.data_ptr<float>() : nullptr, c.stream()) != KDA_OK)
-            return none();
+        at::Tensor h, out, scales;
+        int status;
+        {
+            const Unlocked u;
+            if (adds && !given) h = c.make({T, C}, type), hp = h.data_ptr(), hs = C;
+            out = c.make({T, C}, mode == KDA_NORM_TYPE ? type : at::kFloat8_e4m3fn);
+            if (mode == KDA_NORM_E4M3_ROW) scales = c.make({T}, at::kFloat);
+            if (mode == KDA_NORM_E4M3_BLOCK) scales = c.make({T, (C + 127) / 128}, at::kFloat);
+            status = add_rmsnorm_fn((kda_dtype)dt, (int)T, (int)C, xp, xs, rp, rs, wp, (float)eps, (kda_norm_out)mode, hp, hs, out.data_ptr(),
+                                    scales.defined() ? scales.data_ptr<float>() : nullptr, c.stream());
+        }
+        if (status != KDA_OK) return none();
         PyObject *s = scales.defined() ? THPVariable_Wrap(scales) : Py_NewRef(Py_None);
         PyObject *kept = given ? Py_NewRef(a[5]) : adds ? THPVariable_Wrap(h) : Py_NewRef(a[0]);
         return Py_BuildValue("NNN", THPVariable_Wrap(out), s, kept);
@@ -203,12 +213,16 @@ PyObject *append_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
             PyErr_Clear();
             return none();
         }
-        at::Tensor out = given ? *given : c.make({T, Hq, D}, type);
-        if (!given) op = out.data_ptr();
-        if (append_rope_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, (int)Hq, (int)H, (int)D, (int)R, pairs, qp, qs, kp, ks, vp, vs,
-                           (const float *)rp, (int)positions, (const int32_t *)cp, (const int32_t *)sp, table.p, (int)table.M, pool.page_size,
-                           pool.p, pool.pages, (float)k_scale, (float)v_scale, op, os, err, c.stream()) != KDA_OK)
-            return none();
+        at::Tensor out;
+        int status;
+        {
+            const Unlocked u;
+            if (!given) out = c.make({T, Hq, D}, type), op = out.data_ptr();
+            status = append_rope_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, (int)Hq, (int)H, (int)D, (int)R, pairs, qp, qs, kp, ks, vp,
+                                    vs, (const float *)rp, (int)positions, (const int32_t *)cp, (const int32_t *)sp, table.p, (int)table.M,
+                                    pool.page_size, pool.p, pool.pages, (float)k_scale, (float)v_scale, op, os, err, c.stream());
+        }
+        if (status != KDA_OK) return none();
         return given ? Py_NewRef(a[11]) : THPVariable_Wrap(out);
     });
 }
@@ -228,9 +242,14 @@ PyObject *bounds(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *bp = c.at(a[5], at::kChar, {pool.pages, pool.heads, 2 * D + 16}), *cp = c.at(a[0], at::kInt, {table.B + 1});
         void *sp = c.at(a[1], at::kInt, {table.B});
         int32_t *err = c.error(a[6]);
-        if (!c.good || bounds_fn((int)table.B, T, pool.heads, (int)D, (const int32_t *)cp, (const int32_t *)sp, table.p, (int)table.M,
-                                 pool.page_size, pool.p, pool.pages, (int8_t *)bp, err, c.stream()) != KDA_OK)
-            return none();
+        if (!c.good) return none();
+        int status;
+        {
+            const Unlocked u;
+            status = bounds_fn((int)table.B, T, pool.heads, (int)D, (const int32_t *)cp, (const int32_t *)sp, table.p, (int)table.M,
+                               pool.page_size, pool.p, pool.pages, (int8_t *)bp, err, c.stream());
+        }
+        if (status != KDA_OK) return none();
         Py_RETURN_TRUE;
     });
 }
@@ -254,11 +273,16 @@ PyObject *pick(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int max_q = c.integer(a[2]), page = c.integer(a[6]), count = c.integer(a[7]), first = c.integer(a[8]), recent = c.integer(a[9]);
         int32_t *err = c.error(a[11]);
         if (!c.good || count < 1 || T > INT_MAX) return none();
-        at::Tensor out = c.make({T, H, count}, at::kInt);
-        if (pick_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, max_q, (int)Hq, (int)H, (int)D, qp, qs, (const int32_t *)cp,
-                    (const int32_t *)lp, table.p, (int)table.M, page, (const int8_t *)bp, (int)pages, count, first, recent,
-                    out.data_ptr<int32_t>(), wp, (size_t)wb, err, c.stream()) != KDA_OK)
-            return none();
+        at::Tensor out;
+        int status;
+        {
+            const Unlocked u;
+            out = c.make({T, H, count}, at::kInt);
+            status = pick_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, max_q, (int)Hq, (int)H, (int)D, qp, qs, (const int32_t *)cp,
+                             (const int32_t *)lp, table.p, (int)table.M, page, (const int8_t *)bp, (int)pages, count, first, recent,
+                             out.data_ptr<int32_t>(), wp, (size_t)wb, err, c.stream());
+        }
+        if (status != KDA_OK) return none();
         return THPVariable_Wrap(out);
     });
 }
@@ -284,12 +308,17 @@ PyObject *attention_picked(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const double scale = a[7] == Py_None ? 1.0 / std::sqrt((double)D) : c.number(a[7]), k_scale = c.number(a[8]), v_scale = c.number(a[9]);
         int32_t *err = c.error(a[11]);
         if (!c.good || T > INT_MAX || count > INT_MAX) return none();
-        at::Tensor o = c.make({T, Hq, D}, type), lse = c.make({T, Hq}, at::kFloat);
-        if (attention_picked_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, max_q, (int)Hq, pool.heads, (int)D, qp, qs, (const int32_t *)cp,
-                                (const int32_t *)lp, table.p, (int)table.M, pool.page_size, (const int32_t *)pp, (int)count, pool.p, pool.pages,
-                                (float)scale, (float)k_scale, (float)v_scale, o.data_ptr(), lse.data_ptr<float>(), wp, (size_t)wb, err,
-                                c.stream()) != KDA_OK)
-            return none();
+        at::Tensor o, lse;
+        int status;
+        {
+            const Unlocked u;
+            o = c.make({T, Hq, D}, type), lse = c.make({T, Hq}, at::kFloat);
+            status = attention_picked_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, max_q, (int)Hq, pool.heads, (int)D, qp, qs,
+                                         (const int32_t *)cp, (const int32_t *)lp, table.p, (int)table.M, pool.page_size, (const int32_t *)pp,
+                                         (int)count, pool.p, pool.pages, (float)scale, (float)k_scale, (float)v_scale, o.data_ptr(),
+                                         lse.data_ptr<float>(), wp, (size_t)wb, err, c.stream());
+        }
+        if (status != KDA_OK) return none();
         return Py_BuildValue("NN", THPVariable_Wrap(o), THPVariable_Wrap(lse));
     });
 }
@@ -311,10 +340,15 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *cp = c.at(a[2], at::kInt, {table.B + 1}), *sp = c.at(a[3], at::kInt, {table.B});
         const double k_scale = c.number(a[6]), v_scale = c.number(a[7]);
         int32_t *err = c.error(a[8]);
-        if (!c.good || append_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, (int)H, (int)D, kp, ks, vp, vs, (const int32_t *)cp,
-                                 (const int32_t *)sp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, (float)k_scale,
-                                 (float)v_scale, err, c.stream()) != KDA_OK)
-            return none();
+        if (!c.good) return none();
+        int status;
+        {
+            const Unlocked u;
+            status = append_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, (int)H, (int)D, kp, ks, vp, vs, (const int32_t *)cp,
+                               (const int32_t *)sp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, (float)k_scale, (float)v_scale,
+                               err, c.stream());
+        }
+        if (status != KDA_OK) return none();
         Py_RETURN_TRUE;
     });
 }
@@ -335,11 +369,16 @@ PyObject *gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const double k_scale = c.number(a[6]), v_scale = c.number(a[7]);
         int32_t *err = c.error(a[8]);
         if (!c.good || kv_type(type) < 0 || T < 0) return none();
-        at::Tensor k = c.make({T, pool.heads, D}, type), v = c.make({T, pool.heads, D}, type);
-        if (gather_fn((kda_dtype)kv_type(type), (int)table.B, T, pool.heads, (int)D, k.data_ptr(), v.data_ptr(), (const int32_t *)cp,
-                      (const int32_t *)sp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, (float)k_scale, (float)v_scale, err,
-                      c.stream()) != KDA_OK)
-            return none();
+        at::Tensor k, v;
+        int status;
+        {
+            const Unlocked u;
+            k = c.make({T, pool.heads, D}, type), v = c.make({T, pool.heads, D}, type);
+            status = gather_fn((kda_dtype)kv_type(type), (int)table.B, T, pool.heads, (int)D, k.data_ptr(), v.data_ptr(), (const int32_t *)cp,
+                               (const int32_t *)sp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, (float)k_scale, (float)v_scale,
+                               err, c.stream());
+        }
+        if (status != KDA_OK) return none();
         return Py_BuildValue("NN", THPVariable_Wrap(k), THPVariable_Wrap(v));
     });
 }
@@ -365,11 +404,17 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const double scale = a[6] == Py_None ? 1.0 / std::sqrt((double)D) : c.number(a[6]), k_scale = c.number(a[8]), v_scale = c.number(a[9]);
         int32_t *err = c.error(a[11]);
         if (!c.good || T > INT_MAX) return none();
-        at::Tensor o = c.make({T, Hq, D}, type), lse = c.make({T, Hq}, at::kFloat);
-        if (attention_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, max_q, (int)Hq, pool.heads, (int)D, qp, qs, (const int32_t *)cp,
-                         (const int32_t *)lp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, window, (float)scale, (float)k_scale,
-                         (float)v_scale, o.data_ptr(), lse.data_ptr<float>(), wp, (size_t)wb, err, c.stream()) != KDA_OK)
-            return none();
+        at::Tensor o, lse;
+        int status;
+        {
+            const Unlocked u;
+            o = c.make({T, Hq, D}, type), lse = c.make({T, Hq}, at::kFloat);
+            status = attention_fn((kda_dtype)kv_type(type), (int)table.B, (int)T, max_q, (int)Hq, pool.heads, (int)D, qp, qs,
+                                  (const int32_t *)cp, (const int32_t *)lp, table.p, (int)table.M, pool.page_size, pool.p, pool.pages, window,
+                                  (float)scale, (float)k_scale, (float)v_scale, o.data_ptr(), lse.data_ptr<float>(), wp, (size_t)wb, err,
+                                  c.stream());
+        }
+        if (status != KDA_OK) return none();
         return Py_BuildValue("NN", THPVariable_Wrap(o), THPVariable_Wrap(lse));
     });
 }
