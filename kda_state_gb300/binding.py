@@ -676,6 +676,7 @@ def kda_add_rmsnorm(x, residual, weight, eps: float = EPS_NORM, scales: str = "n
     if scales not in _NORM_OUT:
         raise ValueError('scales is "none", "row" or "block", not %r' % (scales,))
     T, C = shape
+    _sizes("x", T, C)
     xa, xs = _norm_rows(x, "x", dtype, shape, dev)
     wa = _ptr(weight, "weight", (C,), dtype, dev)
     at, kind = x.device, dtype if scales == "none" else torch.float8_e4m3fn
@@ -827,6 +828,12 @@ def _int(x):
     return x if -0x80000000 <= x <= 0x7fffffff else 0x7fffffff if x > 0 else -0x80000000
 
 
+def _sizes(name, *sizes):
+    """A tensor's sizes that the library takes as C ints."""
+    if any(n >> 31 for n in sizes):
+        raise ValueError("%s: a size is past 2^31 - 1 (%s)" % (name, ", ".join(map(str, sizes))))
+
+
 def _err_ptr(dev_err, dev):
     if dev_err is None:
         return None
@@ -886,7 +893,9 @@ def _table(page_table, dev):
     shape = page_table.shape if isinstance(page_table, torch.Tensor) else ()
     if len(shape) != 2:
         shape = (None, None)
-    return (_ptr(page_table, "page_table", shape, I32, dev),) + tuple(shape)
+    at = _ptr(page_table, "page_table", shape, I32, dev)
+    _sizes("page_table", *shape)
+    return (at,) + tuple(shape)
 
 
 def kda_kv4_append(k, v, cu_seqlens, start, page_table, pool, k_scale: float = 1.0,
@@ -1025,6 +1034,7 @@ def kda_kv4_append_rope(q, k, v, rope, cu_seqlens, start, page_table, pool, pair
     ka, ks = _rows(k, "k", dtype, kshape, dev)
     va, vs = _rows(v, "v", dtype, kshape, dev)
     rshape, _ = _first(rope, "rope", 2)
+    _sizes("rope", *rshape)
     ta, B, M = _table(page_table, dev)
     if q_out is None:
         q_out = torch.empty(shape, dtype=dtype, device=q.device) if stream is None else _make(
@@ -1130,6 +1140,7 @@ def kda_kv4_attention_picked(q, cu_seqlens, max_q: int, kv_lens, page_table, pic
     ta, B, M = _table(page_table, dev)
     pshape, _ = _first(picked, "picked", 3)
     count = pshape[2]
+    _sizes("picked", count)
     if o is None:
         o = torch.empty(shape, dtype=dtype, device=q.device) if stream is None else _make(stream, shape, dtype, q.device)
         oa = o.data_ptr()

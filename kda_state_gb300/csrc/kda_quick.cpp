@@ -127,7 +127,8 @@ Table table_of(Call &c, PyObject *o) {
     Table r;
     const at::Tensor *t = c.exact(o);
     if (!t) return r;
-    c.good = t->is_cuda() && t->get_device() == c.dev && t->scalar_type() == at::kInt && t->dim() == 2 && t->is_contiguous();
+    c.good = t->is_cuda() && t->get_device() == c.dev && t->scalar_type() == at::kInt && t->dim() == 2 && t->is_contiguous() &&
+             t->size(0) <= INT_MAX && t->size(1) <= INT_MAX;
     if (c.good) r.p = t->data_ptr<int32_t>(), r.B = t->size(0), r.M = t->size(1);
     return r;
 }

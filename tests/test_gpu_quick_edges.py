@@ -4,12 +4,14 @@ import threading
 import time
 
 import pytest
+import torch
 
 import kda_state_gb300 as kda
 import kda_state_gb300.binding as binding
 from test_gpu_quick_calls import Calls, _lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+DEV = "cuda"
 
 
 def addresses():
@@ -44,3 +46,21 @@ def test_other_threads_run_while_a_call_is_in_the_library():
         stop.set()
         worker.join()
     assert t1 - t0 > 1.5 and sum(t0 + 0.2 < t < t1 - 0.2 for t in seen) > 10
+
+
+def test_a_table_wider_than_32_bits_count_is_refused():
+    """[1, 2^32 + 1] (17 GB): not taken for a table of one page."""
+    c = Calls()
+    k, v, pool = c.qkv[:1, 8:10], c.qkv[:1, 10:], c.new_pool()
+    table = torch.zeros(1, 2 ** 32 + 1, dtype=torch.int32, device=DEV)
+    cu, zero = torch.tensor([0, 1], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    before = pool.clone()
+    assert binding._quick.append(k, v, cu, zero, table, pool, 1.0, 1.0, None) is None
+    for call in (lambda: kda.kda_kv4_attention(c.qkv[:1, :8], cu, 1, zero + 1, table, pool, workspace=c.ws),
+                 lambda: kda.kda_kv4_pick(c.qkv[:1, :8], cu, 1, zero + 1, table, c.bounds, 16, 3, workspace=c.pick_ws)):
+        with pytest.raises((ValueError, RuntimeError, ctypes.ArgumentError)):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(pool, before)
+    del table
+    torch.cuda.empty_cache()
