@@ -99,3 +99,27 @@ def test_an_infinite_weight_is_its_blocks_alone():
     assert s.isnan().tolist() == [[False, True, False, False]] * 2 and out.float().isnan().sum(-1).tolist() == [128, 128]
     out, s, _ = kda().kda_add_rmsnorm(x, None, w, scales="row")
     assert s.isnan().all() and out.float().isnan().all()
+
+
+@pytest.mark.parametrize("mode", ["row", "block"])
+@pytest.mark.parametrize("C", [96, 1000, 4096, 9000])
+def test_the_residuals_forms_are_one(C, mode):
+    """With the sum kept, kept in place (of either operand) or not at all, in faint rows and blocks and in usual ones."""
+    x, r, w = faint(4, C, BF, 13, 1.0), faint(4, C, BF, 14, 1.0), weights(C, BF, 15)
+    for t in (x, r):
+        t[0] *= 1e-37
+        t[1, 128:256] *= 1e-37
+        t[2] = 0
+    h = x + r
+    want = kda().kda_add_rmsnorm(h, None, w, scales=mode)
+    same = lambda out, s: torch.equal(out.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(s, want[1])
+    out, s, kept = kda().kda_add_rmsnorm(x, r, w, scales=mode)
+    assert same(out, s) and torch.equal(kept, h)
+    for into in (0, 1):
+        pair = [x.clone(), r.clone()]
+        out, s, kept = kda().kda_add_rmsnorm(*pair, w, scales=mode, residual_out=pair[into])
+        assert same(out, s) and kept is pair[into] and torch.equal(kept, h)
+    out, s = torch.empty_like(want[0]), torch.empty_like(want[1])
+    status = kda().lib().kda_add_rmsnorm(0, 4, C, x.data_ptr(), C, r.data_ptr(), C, w.data_ptr(), 1e-5, 1 if mode == "row" else 2, None, 0,
+                                         out.data_ptr(), s.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert status == 0 and same(out, s)
