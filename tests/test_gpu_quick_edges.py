@@ -64,3 +64,27 @@ def test_a_table_wider_than_32_bits_count_is_refused():
     assert torch.equal(pool, before)
     del table
     torch.cuda.empty_cache()
+
+
+def test_calls_of_several_threads():
+    """Each thread on a stream of its own, with operands and workspaces of its own."""
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                c = Calls()
+                want = c.norm(scales="block"), c.rope_append(), c.pick(), c.attention(), c.attention_picked()
+                for _ in range(100):
+                    got = c.norm(scales="block"), c.rope_append(), c.pick(), c.attention(), c.attention_picked()
+                    for x, y in zip(sum(map(tuple, got), ()), sum(map(tuple, want), ())):
+                        if not torch.equal(x.view(torch.uint8), y.view(torch.uint8)):
+                            wrong.append(i)
+        except Exception as e:             # noqa: BLE001
+            wrong.append(repr(e))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
