@@ -418,7 +418,8 @@ KDA_API int kda_gated_rmsnorm(kda_dtype dt, int tokens, int H, int V, const void
  * KDA_NORM_E4M3_BLOCK  the same with a scale for 128 channels,
  *                      scales [tokens][(C + 127) / 128]; the last may have fewer
  * Sums of squares are fp32: a row whose mean square passes its range gives 0.
- * A NaN or an infinity makes its row's (its block's) scale and codes NaN.
+ * A NaN or an infinity among y makes its row's (its block's) scale and codes NaN;
+ * all else has codes, however faint (a scale of few bits is what it is).
  *
  *   dt              bf16, fp16 or fp32, of x, residual, w_norm, sum and out
  *   C               channels, a multiple of 8, 8 to 32768
@@ -644,8 +645,9 @@ KDA_API size_t kda_kv4_pick_workspace_bytes(int total_tokens, int H_kv, int max_
  * them, or count: the first `first`, the last `recent` (the token's own among
  * them), and of the others those with the highest scores, the lower page of equal
  * ones.  The score of a page bounds the sum of its products with the kv head's
- * queries from above (for a positive scale of the attention):
- *     up_c = sum_h max(q_hc, 0),  down_c = sum_h max(-q_hc, 0)   over its queries,
+ * queries from above (for a positive scale of the attention, and up to the
+ * rounding of u and d):
+ *     up_c = sum_h max(q_hc, 0),  down_c = sum_h max(-q_hc, 0)   exact sums,
  *     u, d = up / 2^f, down / 2^f to the nearest whole number (ties to even), f the
  *            least >= -100 with max(up, down) <= 127 x 2^f,
  *     score = 2^e sum_c (u_c hi_c - d_c lo_c)
@@ -664,7 +666,8 @@ KDA_API size_t kda_kv4_pick_workspace_bytes(int total_tokens, int H_kv, int max_
  * Requests with inconsistent numbers are skipped as in kda_kv4_attention, a token
  * at a negative position sees none; pages out of range come after all others
  * (KDA_DEVERR_PAGE_RANGE).  After KDA_DEVERR_TIMEOUT the picks are not valid, and the
- * error is fatal for the context as in the other calls.
+ * error is fatal for the context as in the other calls.  Launches go with B times
+ * max_q: single tokens and long pieces are faster in calls of their own.
  */
 KDA_API int kda_kv4_pick(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv, int D,
                          const void *q, long long q_stride, const int32_t *cu_seqlens,
@@ -682,7 +685,8 @@ KDA_API int kda_kv4_pick(kda_dtype dt, int B, int total_tokens, int max_q, int H
  * their positions up to its own.  An entry of -1 has no tokens; any other sets
  * KDA_DEVERR_PAGE_RANGE and is left out.
  *   (other arguments as kda_kv4_attention, without a window)
- * Every token reads its pages by itself: meant for single tokens and drafts.
+ * Every token reads its pages by itself: meant for single tokens and drafts.  For
+ * pieces of prompts kda_kv4_attention over the whole cache may take less time.
  */
 KDA_API int kda_kv4_attention_picked(kda_dtype dt, int B, int total_tokens, int max_q, int H_q,
                                      int H_kv, int D, const void *q, long long q_stride,

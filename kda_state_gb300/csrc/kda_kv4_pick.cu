@@ -11,9 +11,9 @@
 // Records are int8 [num_pages][Hkv][2 D + 16]: hi, lo, e, zeros.  e = 127 marks a page with a NaN (its score is infinite).
 //
 // Single tokens are bound by the records' bytes and, as these are few, by a chain of dependent loads in each of three
-// kernels: 96 requests of 900 to 16 K tokens in pages of 32 take 28 us with the bounds before them (5 to 7 us bounds, 15
-// scores at 3.7 TB/s, 3 behind them for the rows' picks; floor 9), one of 131 K tokens in pages of 64 takes 13.  Prompts are
-// bound by issue: 1536 tokens, 8 kv heads, up to 384 pages 35 us (5, 17, 11 behind them).
+// kernels: 96 requests of 900 to 16 K tokens in pages of 32 take 29 us with the bounds before them (5 to 7 us bounds, 16
+// scores at 3.5 TB/s, 3 to 4 behind them for the rows' picks; floor 9), one of 131 K tokens in pages of 64 takes 13.  Prompts are
+// bound by issue: 1552 tokens, 8 kv heads, up to 384 pages 35 us (5, 18, 11 behind them).
 #include "kda_async.cuh"
 #include "kda_internal.h"
 #include "kda_kv4.cuh"
@@ -307,8 +307,8 @@ __device__ __forceinline__ float exact_to(uint32_t least, __half) {
 // number n's queries lie; put(n, channel, x, y) gets D / 32 of each, from `channel` on.
 //
 // They are the exact sums' whole numbers.  fp32 sums are exact where a channel's values do not lie further apart than its 24
-// bits, and settle what is not near a tie or the border of a unit; the few channels where neither holds (a row in a thousand
-// of 8 heads in bf16 has one) are looked at exactly.
+// bits, and settle what is not near a tie or the border of a unit; the few channels where neither holds (of normal queries one
+// row of 8 heads in 600 has one) are looked at exactly.
 template <int D, int N, typename T, typename Q, typename Put>
 __device__ __forceinline__ void ask_of(const Q &q, int G, const Put &put) {
     constexpr int W = D / 64;              // words of the lane: 2 W channels
@@ -744,8 +744,11 @@ cudaError_t score(KvPickArgs a, cudaStream_t s) {
     const int tokens = a.max_q == 1 ? 1 : TOKENS, heads = tokens == 1 ? HEADS_1 : HEADS, groups = (a.Hkv + heads - 1) / heads;
     a.blocks = (a.max_q + tokens - 1) / tokens;
     const long long units = (long long)a.B * a.blocks * groups;
-    // one run of pages a CTA, unless that were more than some dozens an SM (with tables far wider than their rows most have
-    // nothing); several tokens: a few CTAs an SM, as each adds up its queries
+    // One run of pages a CTA, unless that were more than some dozens an SM (with tables far wider than their rows most have
+    // nothing); several tokens: a few CTAs an SM, as each adds up its queries.  Picks by CTAs an SM, us: 384 single tokens on 1000
+    // pages 114 (4), 105 (16), 111 (32), 130 (128), on 200 pages 31, 34, 36, 36; 64 x 16 tokens on 1000 98 (1 to 4), 109 (16);
+    // 2 x 800 on 384 70 (1 to 8), 84 (16).  CTAs of tokens that a request does not have find out and leave: 255 single tokens
+    // and a piece of 2048 in one call take 422 us, 26 and 95 in two.
     const int run = 32 * ((THREADS / 32) / min(heads, a.Hkv));
     a.chunks = (int)max(1LL, min(SMS * (tokens == 1 ? 32LL : 4LL) / units, ((long long)a.max_pages + run - 1) / run));
     if ((long long)a.B * a.blocks > 0x7fffffffLL || a.chunks > 65535 || groups > 65535) return cudaErrorInvalidConfiguration;
@@ -776,7 +779,11 @@ cudaError_t launch_kv4_pick(const KvPickArgs &a, cudaStream_t s) {
         else e = a.D == 128 ? score<128, __half>(a, s) : score<64, __half>(a, s);
         if (e != cudaSuccess) return e;
     }
-    // A warp a row where its lanes hold the candidates (pages before the last `recent`) and rows fill the GPU, else a CTA.
+    // A warp a row where its lanes hold the candidates (pages before the last `recent`) and rows fill the GPU, else a CTA with
+    // the fewest keys a lane.  Picks by both forms, us, a warp and a CTA: 12288 rows of 250 pages 59 and 78, of 500 78 and 99, of
+    // 1000 124 and 170; 7168 rows of single tokens 93 and 103, 137 and 149, 232 and 257; 3584 42 and 45, 66 and 69, 112 and 124
+    // (already ahead, as it is from about 1800 on); 128 8.0 and 8.6, 11.5 and 10.6, 15.4 and 13.2.  1900 pages with 8 warps
+    // 8.4 (8 rows) and 402 (7168), with 32 10 and 512.
     const bool many = (long long)a.T * a.Hkv >= SMS * 24;
     const int width = a.max_pages - a.recent;
     if (many && width <= 256) return pick_rows<1, 8>(a, s);

@@ -19,7 +19,8 @@ inline cudaError_t allow_shared(const void *kernel, int bytes, std::atomic<uint6
 }
 
 // A launch that may come in before the end of the one ahead of it in the stream, if that one allows it
-// (let_later_kernels_in).  The kernel calls wait_for_earlier_kernels before it reads or writes anything.
+// (let_later_kernels_in).  The kernel calls wait_for_earlier_kernels before it reads or writes anything, whatever is ahead of
+// it: another thread may launch in between, and caches may hold what was there before.
 template <typename... A>
 cudaError_t launch_early(void (*kernel)(A...), dim3 grid, dim3 block, size_t shared, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t c = {};

@@ -8,8 +8,9 @@
 // and the scale are normal numbers; a row or block where they are not (faint or zero, NaN, products past fp32) goes by y.
 //
 // A row is one warp's or one CTA's, in registers from its one read on: bound by HBM (bf16: 4 bytes read, 3 or 4 written a
-// channel), and by the launch and two round trips for a row alone.  16384 rows of 8192 channels with a scale for 128: 148 us,
-// 6.4 TB/s (0.94 of the copy bandwidth measured); 5003 rows of 2560 in fp16: 15.9 us, 6.4 TB/s; one row: 3.1 us.
+// channel), and by the launch and two round trips for a row alone.  16384 rows of 8192 channels with a scale for 128: 139 us,
+// 6.8 TB/s (the copy bandwidth measured is 6.7; a twentieth of the bytes stays in L2); 5003 rows of 2560 in fp16: 17.2 us, 6.0
+// TB/s; one row: 3.1 us.
 #include "kda_async.cuh"
 #include "kda_internal.h"
 #include "kda_kv4_store.cuh"
@@ -245,8 +246,11 @@ cudaError_t go(const AddNormArgs &a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch(const AddNormArgs &a, cudaStream_t s) {
-    // a warp a row while its lanes hold it in four vectors, then as many warps as that takes: the loads of a row are all in
-    // flight at once
+    // A warp a row while its lanes hold it in four vectors, then as many warps as that takes: the loads of a row are all in
+    // flight at once, and what rows share is done by few warps.  Measured with scales of 128, us for 2^27 channels in bf16 and
+    // for one row, warps x vectors: 512 channels 1 x 2 141 and 2.0, 2 x 1 264 and 1.7; 1024 1 x 4 135 and 2.7, 2 x 2 139 and
+    // 2.0, 4 x 1 164 and 1.7; 2048 4 x 2 140 and 2.1, 2 x 4 139 and 2.7, 8 x 1 166 and 1.7; 4096 4 x 4 141 and 2.8, 8 x 2 142
+    // and 2.3, 16 x 4 298 and 2.5; 8192 8 x 4 140 and 3.1, 16 x 2 147 and 2.6; 16384 16 x 4 147 and 3.9, 32 x 2 191 and 3.7.
     const int v = a.C / 8;
     if (v <= 32) return go<T, 1, 1>(a, s);
     if (v <= 64) return go<T, 1, 2>(a, s);
