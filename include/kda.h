@@ -667,7 +667,9 @@ KDA_API size_t kda_kv4_pick_workspace_bytes(int total_tokens, int H_kv, int max_
  * at a negative position sees none; pages out of range come after all others
  * (KDA_DEVERR_PAGE_RANGE).  After KDA_DEVERR_TIMEOUT the picks are not valid, and the
  * error is fatal for the context as in the other calls.  Launches go with B times
- * max_q: single tokens and long pieces are faster in calls of their own.
+ * max_q: single tokens and long pieces are faster in calls of their own, and
+ * B x ceil(max_q / 8) up to 2^31 - 1 and 131070 kv heads (524280 with max_q 1) are
+ * taken where max_pages is above count.
  */
 KDA_API int kda_kv4_pick(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv, int D,
                          const void *q, long long q_stride, const int32_t *cu_seqlens,

